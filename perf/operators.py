@@ -103,7 +103,7 @@ def _w4_codes(x, g):
     q = torch.where(d > 0, xg / d, 0.0)
     a = q.abs()
     mag = ((a > 0.25).to(torch.uint8) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0))
-    return (mag + 8 * (q < 0)).view(M, K), s
+    return (mag | ((q < 0).to(torch.uint8) << 3)).view(M, K), s
 
 
 def _pack4(codes):
