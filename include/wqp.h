@@ -233,6 +233,66 @@ int w8a16_gemm_mma(const void* A, const void* W, const float* scales, void* C,
 int w8a16_gemm_mma_strided(const void* A, int lda, const void* W, const float* scales,
                            void* C, int ldc, int M, int N, int K, void* stream);
 
+/* --------------------------------------------- quantised activations ---
+ * The entries below make the packed formats and multiply rows of quantised
+ * activations with packed weights. X, residual, weight and the outputs of
+ * the norms have one element type, given as a wqp_dtype. X and the residuals
+ * have row pitches in elements (a multiple of 8, at least K) and 16-byte
+ * aligned bases; codes and scales are contiguous. M >= 0 (0 is a no-op) is
+ * unlimited, K % 128 == 0 and K <= 2^20. Stream, device and error behaviour
+ * are those of the GEMV entries.
+ */
+typedef enum wqp_dtype { WQP_BF16 = 0, WQP_F16 = 1, WQP_F32 = 2 } wqp_dtype;
+
+/* Rows of X to the W4A16 format: per group of 16,
+ *   scale = e4m3(amax / (6 * global_scale)),  d = scale * global_scale (FP32),
+ *   code  = e2m1(x / d), or 0 where d is 0,
+ * both rounded to nearest even and saturating. The quotients are the FP32
+ * ones, correctly rounded. A group that holds a NaN or an infinity gets a NaN
+ * scale (0x7F) and zero codes, so it dequantises to NaN. codes [M, K/2]
+ * (8-byte aligned) and scales [M, K/16] are laid out as w4a16_gemv reads
+ * them, so weights can be made with this entry too. 2^-100 <= global_scale
+ * <= 2^100. */
+int w4_quantize(const void* X, int ldx, int dtype, float global_scale, void* codes, void* scales,
+                int M, int K, void* stream);
+
+/* Rows of X to 8 bits: per group of 128, with amax at least 2^-100,
+ *   scale = amax / 448 (FP32),  code = e4m3(x * (448 / amax)).
+ * A group that holds a NaN or an infinity gets NaN codes and scale. codes
+ * [M, K] (8-byte aligned), scales float [M, K/128]. */
+int a8_quantize(const void* X, int ldx, int dtype, void* codes, float* scales, int M, int K, void* stream);
+
+/* Root-mean-square norm with the residual's addition: h = x + residual (or x,
+ * with residual NULL), y = (h * rsqrt(mean(h^2) + eps)) * weight, in FP32
+ * from the unrounded h. residual_out receives h rounded (it may be NULL, and
+ * may be the residual or X itself, with the same pitch); Y [M, ldy] receives
+ * y rounded (it may be X). eps >= 0. */
+int rms_norm(const void* X, int ldx, const void* residual, int ldr, const void* weight, float eps,
+             void* residual_out, int ldro, void* Y, int ldy, int dtype, int M, int K, void* stream);
+
+/* The same with y written as a8_quantize writes it, from its FP32 values. */
+int rms_norm_a8(const void* X, int ldx, const void* residual, int ldr, const void* weight, float eps,
+                void* residual_out, int ldro, void* codes, float* scales, int dtype, int M, int K,
+                void* stream);
+
+/* C[m, n] = bf16(a_global * w_global * sum_g sa[m, g] sw[n, g] sum_{k in g} a w),
+ * both operands in the W4A16 format, on the tensor core's 4-bit path (exact
+ * products, FP32 accumulation). A [M, K/2] and W [N, K/2] codes, a_scales
+ * [M, K/16] and w_scales [N, K/16], all contiguous and 16-byte aligned;
+ * K % 256 == 0, K <= 2^20, N <= 2^24, ldc >= N, C 2-byte aligned. Scales are
+ * magnitudes: a scale code with its sign bit set counts as NaN. Any M. */
+int w4a4_gemm(const void* A, const void* a_scales, float a_global, const void* W, const void* w_scales,
+              float w_global, void* C, int ldc, int M, int N, int K, void* stream);
+
+/* C[m, n] = bf16(sum_b sa[m, b] sw[n/128, b] sum_{k in block b} a w), with A
+ * [M, K] E4M3 and a_scales float [M, K/128] as a8_quantize writes them, and
+ * the W8A16 weights (E4M3 [N, K], float [ceil(N/128), K/128]). Each 128-K
+ * block is summed by the tensor core and scaled once, in FP32. A and W
+ * contiguous and 16-byte aligned, scales 4-byte aligned; otherwise as
+ * w4a4_gemm, with K % 128 == 0. */
+int w8a8_gemm(const void* A, const float* a_scales, const void* W, const float* w_scales, void* C, int ldc,
+              int M, int N, int K, void* stream);
+
 /* ------------------------------------------------------------ dequant ---
  * Unpack every weight to FP32: out is float [N, K] row-major, device memory,
  * 4-byte aligned. Each value is the one the GEMVs multiply by:

@@ -14,6 +14,7 @@ import threading
 __all__ = [
     "WqpError", "lib", "lib_path", "q2_gemv", "q2_gemm_tc", "q2_gemm_mma", "w4a16_gemv", "w4a16_gemm_tc",
     "w4a16_gemm_mma", "w8a16_gemm", "w8a16_gemm_tc", "w8a16_gemm_mma",
+    "w4_quantize", "a8_quantize", "rms_norm", "rms_norm_a8", "w4a4_gemm", "w8a8_gemm",
     "q2_dequant", "w4a16_dequant", "w8a16_dequant", "row_chunks", "set_pdl",
     "get_device_error", "selftest_wait_timeout", "status_string", "EXPORTS", "MAX_M_PER_LAUNCH",
 ]
@@ -46,6 +47,12 @@ EXPORTS = {
     "w8a16_gemm_tc_strided": [_P, _I, _P, _P, _P, _I, _I, _I, _I, _P],
     "w8a16_gemm_mma": [_P, _P, _P, _P, _I, _I, _I, _P],
     "w8a16_gemm_mma_strided": [_P, _I, _P, _P, _P, _I, _I, _I, _I, _P],
+    "w4_quantize": [_P, _I, _I, _F, _P, _P, _I, _I, _P],
+    "a8_quantize": [_P, _I, _I, _P, _P, _I, _I, _P],
+    "rms_norm": [_P, _I, _P, _I, _P, _F, _P, _I, _P, _I, _I, _I, _I, _P],
+    "rms_norm_a8": [_P, _I, _P, _I, _P, _F, _P, _I, _P, _P, _I, _I, _I, _P],
+    "w4a4_gemm": [_P, _P, _F, _P, _P, _F, _P, _I, _I, _I, _I, _P],
+    "w8a8_gemm": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P],
     "q2_dequant": [_P, _P, _I, _I, _P],
     "w4a16_dequant": [_P, _P, _F, _P, _I, _I, _P],
     "w8a16_dequant": [_P, _P, _P, _I, _I, _P],
@@ -245,6 +252,173 @@ def w8a16_gemm_tc(A, W, scales, N: int, K: int, out=None, stream=None):
     C = _out(A, M, N, out)
     _check(lib().w8a16_gemm_tc_strided(_ptr(A), lda, _ptr(W), _ptr(scales), _ptr(C), C.stride(0),
                                        M, N, K, _stream(stream)), "w8a16_gemm_tc")
+    return C
+
+
+_DTYPES = None           # torch dtype -> wqp_dtype, set on first use
+
+
+def _typed_rows(name, x, K=None, like=None):
+    """Rows [M, K] with unit column stride: their (pitch, wqp_dtype)."""
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+
+        _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be torch.bfloat16, float16 or float32")
+    if x.dim() != 2 or x.stride(1) != 1 or (K is not None and x.shape[1] != K):
+        raise ValueError(f"{name} must be [M, {'K' if K is None else K}] with unit column stride")
+    if like is not None and (x.shape != like.shape or x.dtype is not like.dtype):
+        raise ValueError(f"{name} must have the shape and type of x")
+    return (x.shape[1] if x.shape[0] <= 1 else x.stride(0)), _DTYPES[x.dtype]
+
+
+def _packed(name, t, shape, dtype):
+    """A contiguous tensor of a packed format."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor")
+
+
+def _weights(W, w_scales, codes, scales, dtype):
+    """Packed weights: their types and sizes (any shape, as the GEMV entries take them)."""
+    import torch
+
+    if W.dtype is not torch.uint8 or w_scales.dtype is not dtype:
+        raise TypeError(f"W must be torch.uint8 and w_scales {dtype}")
+    if W.numel() != codes or w_scales.numel() != scales or not (W.is_contiguous() and w_scales.is_contiguous()):
+        raise ValueError(f"W must hold {codes} contiguous bytes and w_scales {scales} contiguous values")
+
+
+def _codes_out(x, shapes, dtypes, out):
+    import torch
+
+    if out is None:
+        return tuple(torch.empty(s, dtype=d, device=x.device) for s, d in zip(shapes, dtypes))
+    codes, scales = out
+    _need_cuda(codes, scales)
+    _packed("out codes", codes, shapes[0], dtypes[0])
+    _packed("out scales", scales, shapes[1], dtypes[1])
+    return codes, scales
+
+
+def w4_quantize(x, global_scale: float = 1.0, out=None, stream=None):
+    """Rows x [M, K] (bfloat16, float16 or float32) to the W4A16 format: uint8 codes [M, K/2] and
+    uint8 E4M3 scales [M, K/16], under one global_scale. out: (codes, scales) to write to."""
+    import torch
+
+    _need_cuda(x)
+    ldx, dt = _typed_rows("x", x)
+    M, K = x.shape
+    codes, scales = _codes_out(x, ((M, K // 2), (M, K // 16)), (torch.uint8, torch.uint8), out)
+    _check(lib().w4_quantize(_ptr(x), ldx, dt, float(global_scale), _ptr(codes), _ptr(scales), M, K,
+                             _stream(stream)), "w4_quantize")
+    return codes, scales
+
+
+def a8_quantize(x, out=None, stream=None):
+    """Rows x [M, K] (bfloat16, float16 or float32) to uint8 E4M3 codes [M, K] with float32 scales
+    [M, K/128]. out: (codes, scales) to write to."""
+    import torch
+
+    _need_cuda(x)
+    ldx, dt = _typed_rows("x", x)
+    M, K = x.shape
+    codes, scales = _codes_out(x, ((M, K), (M, K // 128)), (torch.uint8, torch.float32), out)
+    _check(lib().a8_quantize(_ptr(x), ldx, dt, _ptr(codes), _ptr(scales), M, K, _stream(stream)), "a8_quantize")
+    return codes, scales
+
+
+def _norm_args(x, weight, residual, residual_out):
+    """(ldx, dtype, ldr, residual_out, ldro) of a norm call, its arguments checked."""
+    import torch
+
+    _need_cuda(x, weight, residual, residual_out)
+    ldx, dt = _typed_rows("x", x)
+    if weight.dtype is not x.dtype or tuple(weight.shape) != (x.shape[1],) or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous [{x.shape[1]}] tensor of x's type")
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out without residual")
+        return ldx, dt, 0, None, 0
+    ldr, _ = _typed_rows("residual", residual, like=x)
+    if residual_out is None:
+        residual_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    ldro, _ = _typed_rows("residual_out", residual_out, like=x)
+    return ldx, dt, ldr, residual_out, ldro
+
+
+def rms_norm(x, weight, eps: float, residual=None, residual_out=None, out=None, stream=None):
+    """(y, h): h = x + residual, y = h * rsqrt(mean(h^2) + eps) * weight, in x's type (bfloat16,
+    float16 or float32). Without a residual h is None. residual_out may be the residual itself."""
+    import torch
+
+    ldx, dt, ldr, h, ldh = _norm_args(x, weight, residual, residual_out)
+    M, K = x.shape
+    if out is None:
+        out = torch.empty((M, K), dtype=x.dtype, device=x.device)
+    _need_cuda(out)
+    ldy, _ = _typed_rows("out", out, like=x)
+    _check(lib().rms_norm(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), float(eps), _ptr(h), ldh, _ptr(out), ldy,
+                          dt, M, K, _stream(stream)), "rms_norm")
+    return out, h
+
+
+def rms_norm_a8(x, weight, eps: float, residual=None, residual_out=None, out=None, stream=None):
+    """(codes, scales, h): rms_norm with y written as a8_quantize writes it. out: (codes, scales)."""
+    import torch
+
+    ldx, dt, ldr, h, ldh = _norm_args(x, weight, residual, residual_out)
+    M, K = x.shape
+    codes, scales = _codes_out(x, ((M, K), (M, K // 128)), (torch.uint8, torch.float32), out)
+    _check(lib().rms_norm_a8(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), float(eps), _ptr(h), ldh, _ptr(codes),
+                             _ptr(scales), dt, M, K, _stream(stream)), "rms_norm_a8")
+    return codes, scales, h
+
+
+def _gemm_out(A, M, N, out):
+    import torch
+
+    if out is None:
+        return torch.empty((M, N), dtype=torch.bfloat16, device=A.device), N
+    _need_cuda(out)
+    if out.dtype is not torch.bfloat16:
+        raise TypeError("out must be torch.bfloat16")
+    if tuple(out.shape) != (M, N) or out.stride(1) != 1 and N > 1:
+        raise ValueError(f"out must be [{M}, {N}] with unit column stride")
+    return out, (N if M <= 1 else out.stride(0))
+
+
+def w4a4_gemm(A, a_scales, W, w_scales, N: int, K: int, a_global: float = 1.0, w_global: float = 1.0, out=None,
+              stream=None):
+    """C[M, N] = dequant(A) @ dequant(W)^T, both in the W4A16 format (w4_quantize), any M, K % 256 == 0."""
+    import torch
+
+    _need_cuda(A, a_scales, W, w_scales)
+    M = A.shape[0]
+    _packed("A", A, (M, K // 2), torch.uint8)
+    _packed("a_scales", a_scales, (M, K // 16), torch.uint8)
+    _weights(W, w_scales, N * (K // 2), N * (K // 16), torch.uint8)
+    C, ldc = _gemm_out(A, M, N, out)
+    _check(lib().w4a4_gemm(_ptr(A), _ptr(a_scales), float(a_global), _ptr(W), _ptr(w_scales), float(w_global), _ptr(C),
+                           ldc, M, N, K, _stream(stream)), "w4a4_gemm")
+    return C
+
+
+def w8a8_gemm(A, a_scales, W, w_scales, N: int, K: int, out=None, stream=None):
+    """C[M, N] = dequant(A) @ dequant(W)^T: A as a8_quantize and rms_norm_a8 write it, W8A16 weights, any M."""
+    import torch
+
+    _need_cuda(A, a_scales, W, w_scales)
+    M = A.shape[0]
+    _packed("A", A, (M, K), torch.uint8)
+    _packed("a_scales", a_scales, (M, K // 128), torch.float32)
+    _weights(W, w_scales, N * K, (N + 127) // 128 * (K // 128), torch.float32)
+    C, ldc = _gemm_out(A, M, N, out)
+    _check(lib().w8a8_gemm(_ptr(A), _ptr(a_scales), _ptr(W), _ptr(w_scales), _ptr(C), ldc, M, N, K,
+                           _stream(stream)), "w8a8_gemm")
     return C
 
 

@@ -200,6 +200,99 @@ int run_dequant(int fmt, const void* W, const void* scales, float gscale, float*
   return WQP_OK;
 }
 
+// Shape of the quantised-activation entries: M, K, and one operand with rows.
+int check_rows(const char* nm, int M, int K, int dtype) {
+  if (M < 0) return fail(WQP_ERR_INVALID_ARG, "%s: M=%d < 0", nm, M);
+  if (K < 128 || K > (1 << 20) || K % 128 != 0)
+    return fail(WQP_ERR_INVALID_ARG, "%s: K=%d must be a multiple of 128 in [128, 2^20]", nm, K);
+  if (dtype < WQP_BF16 || dtype > WQP_F32)
+    return fail(WQP_ERR_INVALID_ARG, "%s: dtype=%d is not a wqp_dtype", nm, dtype);
+  return WQP_OK;
+}
+
+int check_pitched(const char* nm, const char* what, const void* p, int ld, int K) {
+  if (!p) return fail(WQP_ERR_INVALID_ARG, "%s: NULL %s", nm, what);
+  if (!aligned(p, 16)) return fail(WQP_ERR_INVALID_ARG, "%s: %s must be 16-byte aligned", nm, what);
+  if (ld < K || ld % 8 != 0)
+    return fail(WQP_ERR_INVALID_ARG, "%s: pitch %d of %s must be >= K=%d and a multiple of 8", nm, ld, what, K);
+  return WQP_OK;
+}
+
+int check_codes(const char* nm, const void* codes, const void* scales, uintptr_t scale_align) {
+  if (!codes || !scales) return fail(WQP_ERR_INVALID_ARG, "%s: NULL codes or scales", nm);
+  if (!aligned(codes, 8)) return fail(WQP_ERR_INVALID_ARG, "%s: codes must be 8-byte aligned", nm);
+  if (!aligned(scales, scale_align))
+    return fail(WQP_ERR_INVALID_ARG, "%s: scales must be %d-byte aligned", nm, static_cast<int>(scale_align));
+  return WQP_OK;
+}
+
+int run_quantize(bool a8, const void* X, int ldx, int dtype, float gscale, void* codes, void* scales, int M, int K,
+                 void* stream) {
+  const char* nm = a8 ? "a8_quantize" : "w4_quantize";
+  int st = check_rows(nm, M, K, dtype);
+  if (st == WQP_OK && !(gscale >= 0x1p-100f && gscale <= 0x1p100f))
+    st = fail(WQP_ERR_INVALID_ARG, "%s: global_scale=%g outside 2^-100..2^100", nm, gscale);
+  if (st == WQP_OK && M == 0) return WQP_OK;
+  if (st == WQP_OK) st = check_pitched(nm, "X", X, ldx, K);
+  if (st == WQP_OK) st = check_codes(nm, codes, scales, a8 ? 4 : 1);
+  DeviceInfo* dev = nullptr;
+  if (st != WQP_OK || (st = device_setup(&dev)) != WQP_OK) return st;
+  const QuantArgs a = {X,     static_cast<uint8_t*>(codes), scales, gscale, dtype, M, K, ldx,
+                       g_pdl.load(std::memory_order_relaxed) != 0};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = a8 ? launch_a8_quantize(a, s) : launch_w4_quantize(a, s);
+  return e == cudaSuccess ? WQP_OK : cuda_fail(e, nm);
+}
+
+int run_norm(bool a8, const void* X, int ldx, const void* R, int ldr, const void* W, float eps, void* H, int ldh,
+             void* Y, int ldy, float* S, int dtype, int M, int K, void* stream) {
+  const char* nm = a8 ? "rms_norm_a8" : "rms_norm";
+  int st = check_rows(nm, M, K, dtype);
+  if (st == WQP_OK && !(eps >= 0.0f && eps <= 3.4e38f))
+    st = fail(WQP_ERR_INVALID_ARG, "%s: eps=%g must be finite and not negative", nm, eps);
+  if (st == WQP_OK && M == 0) return WQP_OK;
+  if (st == WQP_OK) st = check_pitched(nm, "X", X, ldx, K);
+  if (st == WQP_OK && R) st = check_pitched(nm, "residual", R, ldr, K);
+  if (st == WQP_OK && H) st = check_pitched(nm, "residual_out", H, ldh, K);
+  if (st == WQP_OK) st = check_pitched(nm, "weight", W, K, K);
+  if (st == WQP_OK) st = a8 ? check_codes(nm, Y, S, 4) : check_pitched(nm, "Y", Y, ldy, K);
+  DeviceInfo* dev = nullptr;
+  if (st != WQP_OK || (st = device_setup(&dev)) != WQP_OK) return st;
+  const NormArgs a = {X,   R,   W,   H,   Y,   S, eps, dtype, M, K, ldx, ldr, ldh, ldy, dev->num_sms,
+                      g_pdl.load(std::memory_order_relaxed) != 0};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = a8 ? launch_rms_norm_a8(a, s) : launch_rms_norm(a, s);
+  return e == cudaSuccess ? WQP_OK : cuda_fail(e, nm);
+}
+
+int run_act_gemm(bool w4, const void* A, const void* SA, float ga, const void* W, const void* SW, float gw, void* C,
+                 int ldc, int M, int N, int K, void* stream) {
+  const char* nm = w4 ? "w4a4_gemm" : "w8a8_gemm";
+  const int unit = w4 ? 256 : 128;
+  if (M < 0) return fail(WQP_ERR_INVALID_ARG, "%s: M=%d < 0", nm, M);
+  if (N < 1 || N > (1 << 24)) return fail(WQP_ERR_INVALID_ARG, "%s: N=%d outside 1..2^24", nm, N);
+  if (K < unit || K > (1 << 20) || K % unit != 0)
+    return fail(WQP_ERR_INVALID_ARG, "%s: K=%d must be a multiple of %d in [%d, 2^20]", nm, K, unit, unit);
+  if (!(ga == ga) || !(gw == gw)) return fail(WQP_ERR_INVALID_ARG, "%s: a global scale is NaN", nm);
+  if (M == 0) return WQP_OK;
+  if (!A || !SA || !W || !SW || !C) return fail(WQP_ERR_INVALID_ARG, "%s: NULL A, W, C or scales", nm);
+  if (!aligned(A, 16) || !aligned(W, 16))
+    return fail(WQP_ERR_INVALID_ARG, "%s: A and W must be 16-byte aligned", nm);
+  const uintptr_t sal = w4 ? 16 : 4;
+  if (!aligned(SA, sal) || !aligned(SW, sal))
+    return fail(WQP_ERR_INVALID_ARG, "%s: scales must be %d-byte aligned", nm, static_cast<int>(sal));
+  if (!aligned(C, 2)) return fail(WQP_ERR_INVALID_ARG, "%s: C must be 2-byte aligned", nm);
+  if (ldc < N) return fail(WQP_ERR_INVALID_ARG, "%s: ldc=%d must be >= N=%d", nm, ldc, N);
+  DeviceInfo* dev = nullptr;
+  const int st = device_setup(&dev);
+  if (st != WQP_OK) return st;
+  const ActGemmArgs a = {A, SA, W, SW, C, ga * gw, M, N, K, ldc, dev->err, dev->num_sms,
+                         g_pdl.load(std::memory_order_relaxed) != 0};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = w4 ? launch_w4a4_gemm(a, s) : launch_w8a8_gemm(a, s);
+  return e == cudaSuccess ? WQP_OK : cuda_fail(e, nm);
+}
+
 }  // namespace
 
 namespace wqp {
@@ -308,6 +401,35 @@ int w8a16_gemm_tc(const void* A, const void* W, const float* scales, void* C, in
 int w8a16_gemm_tc_strided(const void* A, int lda, const void* W, const float* scales, void* C,
                           int ldc, int M, int N, int K, void* stream) {
   return run_gemm(Fmt::W8TC, A, lda, W, scales, 1.0f, C, ldc, M, N, K, stream);
+}
+
+int w4_quantize(const void* X, int ldx, int dtype, float global_scale, void* codes, void* scales, int M, int K,
+                void* stream) {
+  return run_quantize(false, X, ldx, dtype, global_scale, codes, scales, M, K, stream);
+}
+
+int a8_quantize(const void* X, int ldx, int dtype, void* codes, float* scales, int M, int K, void* stream) {
+  return run_quantize(true, X, ldx, dtype, 1.0f, codes, scales, M, K, stream);
+}
+
+int rms_norm(const void* X, int ldx, const void* residual, int ldr, const void* weight, float eps, void* residual_out,
+             int ldro, void* Y, int ldy, int dtype, int M, int K, void* stream) {
+  return run_norm(false, X, ldx, residual, ldr, weight, eps, residual_out, ldro, Y, ldy, nullptr, dtype, M, K, stream);
+}
+
+int rms_norm_a8(const void* X, int ldx, const void* residual, int ldr, const void* weight, float eps,
+                void* residual_out, int ldro, void* codes, float* scales, int dtype, int M, int K, void* stream) {
+  return run_norm(true, X, ldx, residual, ldr, weight, eps, residual_out, ldro, codes, K, scales, dtype, M, K, stream);
+}
+
+int w4a4_gemm(const void* A, const void* a_scales, float a_global, const void* W, const void* w_scales,
+              float w_global, void* C, int ldc, int M, int N, int K, void* stream) {
+  return run_act_gemm(true, A, a_scales, a_global, W, w_scales, w_global, C, ldc, M, N, K, stream);
+}
+
+int w8a8_gemm(const void* A, const float* a_scales, const void* W, const float* w_scales, void* C, int ldc, int M,
+              int N, int K, void* stream) {
+  return run_act_gemm(false, A, a_scales, 1.0f, W, w_scales, 1.0f, C, ldc, M, N, K, stream);
 }
 
 int q2_dequant(const void* W, float* out, int N, int K, void* stream) {

@@ -1,0 +1,365 @@
+// Products of quantised activations with packed weights, few rows (the whole
+// call is a small number of column tiles): 4-bit by 4-bit with E4M3 scales
+// per 16 K, and 8-bit by 8-bit with FP32 scales per 128 K.
+//
+// Bound by the weights' bytes. Swap-AB: the 128 weight rows of a tile are the
+// MMA's M side and up to NT activation rows, zero-padded by the copies, its
+// N side, so one pass over the weights serves NT rows:
+//   D[n, m] = sum_k W[n, k] A[m, k]      (tcgen05.mma, FP32 accumulators)
+// Both operands go from global to shared memory as they lie (128-byte rows,
+// 128-byte swizzle) and into the tensor core undecoded.
+//  * 4 bits: the tensor core multiplies each 16-K product sum by both scales;
+//    two warps bring a stage's scales into the order it reads them in and the
+//    MMA warp copies them to tensor memory. One accumulator for all of K.
+//  * 8 bits: one MMA group per 128 K; the epilogue reads it and adds it, times
+//    its two scales, to FP32 accumulators in registers.
+// With few tiles, K is split over a cluster of up to 8 CTAs. Rank q owns the
+// activation rows q, q + splits, ...; the others push their partial sums of
+// those into its shared memory, and it adds them in rank order, so the result
+// does not depend on timing.
+//
+// Warps: 0 copies, 1 MMA (and tensor memory), 2..3 scales (4 bits), 4..7
+// epilogue (lane quarter = warp % 4).
+#include "act.cuh"
+
+namespace wqp {
+namespace act {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kEpiWarp0 = 4;
+
+struct FewParams {
+  const float* SA;      // 8 bits: float [M, K/128]
+  const float* SW;      // 8 bits: float [ceil(N/128), K/128]
+  float gscale;
+  uint16_t* C;
+  int M, N, K, ldc;
+  int splits, stages;
+  unsigned* err;
+};
+
+template <class F, int NT>
+struct FewLayout {
+  static constexpr int kS = NT <= 32 ? 4 : (NT <= 64 ? 4 : 3);            // stages
+  static constexpr int kAcc = F::kScaled ? 1 : (NT <= 64 ? 4 : 2);        // accumulator slots
+  static constexpr int kW = 0;
+  static constexpr int kA = kW + kS * 16384;
+  static constexpr int kRawW = kA + kS * NT * 128;
+  static constexpr int kRawA = kRawW + (F::kScaled ? kS * kScaleBlock : 0);
+  static constexpr int kSclW = kRawA + (F::kScaled ? kS * NT * 16 : 0);
+  static constexpr int kSclA = kSclW + (F::kScaled ? kS * kScaleBlock : 0);
+  static constexpr int kFac = kSclA + (F::kScaled ? kS * kScaleBlock : 0);
+  static constexpr int kRecv = kFac + (F::kScaled ? 0 : 4 * NT * 4);
+  static constexpr int kBytes = kRecv + (NT + 7) * 128 * 4;
+  static constexpr int kAlloc = kBytes + 1024;                            // slack for 1024-byte alignment
+  static constexpr int kStageBytes = 16384 + NT * 128 + (F::kScaled ? kScaleBlock + NT * 16 : 0);
+  // Tensor memory: the accumulators, then (4 bits) two sets of a stage's
+  // scales, 4 columns per step and operand.
+  static constexpr int kCols = F::kScaled ? (NT + 64 <= 128 ? 128 : 256) : (kAcc * NT <= 64 ? 64 : (kAcc * NT <= 128 ? 128 : 256));
+  static constexpr int kCtas = kAlloc + 2048 <= 114 * 1024 && kCols <= 256 ? 2 : 1;   // per SM
+  static_assert(kAlloc <= 227 * 1024, "shared memory");
+};
+
+template <class F, int NT>
+__global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
+    few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
+               const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSA, FewParams p) {
+  using L = FewLayout<F, NT>;
+  constexpr int S = L::kS, NACC = L::kAcc;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_sh[S], empty_sh[S], scaled_sh[S], acc_full_sh[NACC], acc_free_sh[NACC];
+  __shared__ uint32_t tmem_sh;
+  __shared__ int abort_sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = p.splits;
+  const int tile = blockIdx.x / splits, rank = blockIdx.x - tile * splits;
+  const int n0 = tile * 128, m0 = blockIdx.y * NT;
+  const int st0 = static_cast<int>(static_cast<long long>(rank) * p.stages / splits);
+  const int nst = static_cast<int>(static_cast<long long>(rank + 1) * p.stages / splits) - st0;
+  const uint32_t full = smem_u32(full_sh), empty = smem_u32(empty_sh), scaled = smem_u32(scaled_sh);
+  const uint32_t acc_full = smem_u32(acc_full_sh), acc_free = smem_u32(acc_free_sh);
+  volatile int* abort_flag = &abort_sh;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+      mbar_init(scaled + 8 * i, 2);
+    }
+    for (int i = 0; i < NACC; ++i) {
+      mbar_init(acc_full + 8 * i, 1);
+      mbar_init(acc_free + 8 * i, 4);
+    }
+    abort_sh = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_sh), L::kCols);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  pdl_launch_dependents();
+  if (splits > 1) cluster_arrive_relaxed();      // matched before the first push
+
+  int issued = 0;                                // stages whose copies lane 0 of warp 0 started
+  if (warp == 0) {
+    if (lane == 0) {
+      prefetch_tmap(&tmW);
+      prefetch_tmap(&tmA);
+      const uint64_t pol = policy_evict_first();
+      auto load_w = [&](int t) {
+        const int s = t % S;
+        mbar_arrive_expect_tx(full + 8 * s, L::kStageBytes);
+        tma_load_2d_hint(sb + L::kW + s * 16384, &tmW, (st0 + t) * 128, n0, full + 8 * s, pol);
+        if (F::kScaled) tma_load_2d_hint(sb + L::kRawW + s * kScaleBlock, &tmSW, (st0 + t) * 16, n0, full + 8 * s, pol);
+      };
+      auto load_a = [&](int t) {
+        const int s = t % S;
+        tma_load_2d(sb + L::kA + s * NT * 128, &tmA, (st0 + t) * 128, m0, full + 8 * s);
+        if (F::kScaled) tma_load_2d(sb + L::kRawA + s * NT * 16, &tmSA, (st0 + t) * 16, m0, full + 8 * s);
+      };
+      // The weights do not depend on the previous grid; the activations may.
+      const int ahead = min(S, nst);
+      for (int t = 0; t < ahead; ++t) load_w(t);
+      pdl_wait();
+      for (int t = 0; t < ahead; ++t) load_a(t);
+      issued = ahead;
+      for (int t = ahead; t < nst; ++t) {
+        if (!wait_or_abort(empty + 8 * (t % S), ((t / S) - 1) & 1, p.err, abort_flag)) break;
+        load_w(t);
+        load_a(t);
+        issued = t + 1;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = F::kScaled ? idesc_f4(128, NT) : idesc_f8(128, NT);
+    int last = -1;
+    for (int t = 0; t < nst; ++t) {
+      const int s = t % S, slot = t % NACC;
+      bool ok = wait_or_abort(full + 8 * s, (t / S) & 1, p.err, abort_flag);
+      if (F::kScaled) ok = ok && wait_or_abort(scaled + 8 * s, (t / S) & 1, p.err, abort_flag);
+      if (!F::kScaled && t >= NACC)
+        ok = ok && wait_or_abort(acc_free + 8 * slot, ((t / NACC) - 1) & 1, p.err, abort_flag);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t wd = tile_desc(sb + L::kW + s * 16384), ad = tile_desc(sb + L::kA + s * NT * 128);
+        if constexpr (F::kScaled) {
+          const uint32_t sw = tmem + NT + (t & 1) * 32, sa = sw + 16;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            copy_scales(sw + 4 * j, scale_desc(sb + L::kSclW + s * kScaleBlock + 512 * j));
+            copy_scales(sa + 4 * j, scale_desc(sb + L::kSclA + s * kScaleBlock + 512 * j));
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_f4(tmem, wd + 2 * j, ad + 2 * j, idesc, sw + 4 * j, sa + 4 * j, (t | j) ? 1u : 0u);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma_f8(tmem + slot * NT, wd + 2 * j, ad + 2 * j, idesc, j ? 1u : 0u);
+        }
+        mma_commit(empty + 8 * s);
+        if (!F::kScaled || t == nst - 1) mma_commit(acc_full + 8 * slot);
+      }
+      __syncwarp();
+      last = t;
+    }
+    // This warp's MMAs are done before tensor memory is freed.
+    if (last >= 0) mbar_wait(empty + 8 * (last % S), (last / S) & 1, p.err);
+  } else if (warp < kEpiWarp0) {
+    if constexpr (F::kScaled) {
+      for (int t = 0; t < nst; ++t) {
+        const int s = t % S;
+        const bool ok = wait_or_abort(full + 8 * s, (t / S) & 1, p.err, abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        rearrange_scales(smem + L::kRawW + s * kScaleBlock, smem + L::kSclW + s * kScaleBlock, warp - 2, lane, 128);
+        rearrange_scales(smem + L::kRawA + s * NT * 16, smem + L::kSclA + s * kScaleBlock, warp - 2, lane, NT);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(scaled + 8 * s);
+      }
+    }
+  } else {
+    const int q = warp & 3, r = q * 32 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    float acc[NT];
+#pragma unroll
+    for (int m = 0; m < NT; ++m) acc[m] = 0.0f;
+    bool live = true;
+    if constexpr (F::kScaled) {
+      live = __all_sync(0xFFFFFFFFu, wait_or_abort(acc_full, 0, p.err, abort_flag));
+      if (live) {
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < NT; c += 16) {
+          float v[16];
+          tmem_ld<16>(tl + c, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[c + i] = v[i] * p.gscale;
+        }
+      }
+    } else {
+      // Lane l brings the scales of activation rows l, l + 32, ...; each
+      // group's are fetched while the group before it is added.
+      constexpr int kPer = (NT + 31) / 32;
+      const int kb = p.K >> 7;
+      const float* sw = p.SW + static_cast<long long>(tile) * kb + st0;
+      const float* sa[kPer];
+      float next[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        sa[i] = p.SA + static_cast<long long>(min(m0 + 32 * i + lane, p.M - 1)) * kb + st0;
+      float* fac = reinterpret_cast<float*>(smem + L::kFac) + q * NT;
+      pdl_wait();
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) next[i] = sa[i][0] * __ldg(sw);
+      for (int t = 0; t < nst; ++t) {
+        const int slot = t % NACC;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          if (32 * i + lane < NT) fac[32 * i + lane] = next[i];
+          if (t + 1 < nst) next[i] = sa[i][t + 1] * __ldg(sw + t + 1);
+        }
+        __syncwarp();
+        live = __all_sync(0xFFFFFFFFu, wait_or_abort(acc_full + 8 * slot, (t / NACC) & 1, p.err, abort_flag));
+        if (!live) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < NT; c += 16) {
+          float v[16];
+          tmem_ld<16>(tl + slot * NT + c, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(v[i], fac[c + i], acc[c + i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_free + 8 * slot);
+      }
+    }
+    const int rows = min(NT, p.M - m0);
+    if (splits > 1) {
+      cluster_wait();
+      // Row m goes to rank m % splits, into [source rank][m / splits][weight row].
+      const int per = (NT + splits - 1) / splits;
+#pragma unroll
+      for (int m = 0; m < NT; ++m) {
+        if (m < rows && live) {
+          const uint32_t dst = sb + L::kRecv + 4 * ((rank * per + m / splits) * 128 + r);
+          st_dsmem_f32(mapa_shared(dst, m % splits), acc[m]);
+        }
+      }
+    } else if (live && n0 + r < p.N) {
+      uint16_t* c = p.C + static_cast<long long>(m0) * p.ldc + n0 + r;
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+        if (m < rows) c[static_cast<long long>(m) * p.ldc] = f32_to_bf16_rn(acc[m]);
+    }
+  }
+  if (splits > 1 && warp < kEpiWarp0) cluster_wait();
+
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kCols);
+  }
+  const bool failed = *abort_flag != 0;
+  if (failed && warp == 0 && lane == 0)          // no copy may still be in flight when the CTA exits
+    for (int t = max(0, issued - S); t < issued; ++t) mbar_wait(full + 8 * (t % S), (t / S) & 1, p.err);
+  if (splits > 1) {
+    __syncwarp();
+    cluster_sync();                              // the pushes are in place
+    const int per = (NT + splits - 1) / splits;
+    const int rows = min(NT, p.M - m0);
+    const float* recv = reinterpret_cast<const float*>(smem + L::kRecv);
+    const int r = threadIdx.x & 127;
+    if (!failed && n0 + r < p.N) {
+      for (int i = threadIdx.x >> 7; i * splits + rank < rows; i += kThreads / 128) {
+        float v = recv[i * 128 + r];
+        for (int src = 1; src < splits; ++src) v += recv[(src * per + i) * 128 + r];
+        p.C[static_cast<long long>(m0 + i * splits + rank) * p.ldc + n0 + r] = f32_to_bf16_rn(v);
+      }
+    }
+  }
+}
+
+template <class F, int NT>
+cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
+  using L = FewLayout<F, NT>;
+  const uint64_t row = F::kScaled ? static_cast<uint64_t>(a.K) / 2 : static_cast<uint64_t>(a.K);
+  CUtensorMap mw, ma, msw, msa;
+  cudaError_t e = cached_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.W, row, static_cast<uint64_t>(a.N), row, 128, 128,
+                                CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  e = make_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, row, static_cast<uint64_t>(a.M), row, 128, NT,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  msw = mw;
+  msa = ma;
+  if (F::kScaled) {
+    const uint64_t srow = static_cast<uint64_t>(a.K) / 16;
+    e = cached_map_2d(&msw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.SW, srow, static_cast<uint64_t>(a.N), srow, 16, 128,
+                      CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e != cudaSuccess) return e;
+    e = make_map_2d(&msa, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.SA, srow, static_cast<uint64_t>(a.M), srow, 16, NT,
+                    CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e != cudaSuccess) return e;
+  }
+  static AttrLatch latch;
+  if (e = set_smem_attrs(few_kernel<F, NT>, latch, L::kAlloc, true); e != cudaSuccess) return e;
+  FewParams p = {};
+  if (!F::kScaled) {
+    p.SA = static_cast<const float*>(a.SA);
+    p.SW = static_cast<const float*>(a.SW);
+  }
+  p.gscale = a.gscale;
+  p.C = static_cast<uint16_t*>(a.C);
+  p.M = a.M;
+  p.N = a.N;
+  p.K = a.K;
+  p.ldc = a.ldc;
+  p.stages = a.K / F::kStageK;
+  p.err = a.err;
+  const int tiles = (a.N + 127) / 128, mt = (a.M + NT - 1) / NT;
+  p.splits = 1;
+  for (int sp = 2; sp <= 8 && sp <= p.stages && static_cast<long long>(sp) * tiles * mt <= L::kCtas * a.num_sms; ++sp)
+    p.splits = sp;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles * p.splits, mt);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::kAlloc;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, few_kernel<F, NT>, mw, ma, msw, msa, p);
+}
+
+template <class F>
+cudaError_t launch_few(const ActGemmArgs& a, cudaStream_t s) {
+  if (a.M <= 16) return launch_few_nt<F, 16>(a, s);
+  if (a.M <= 32) return launch_few_nt<F, 32>(a, s);
+  if (a.M <= 64) return launch_few_nt<F, 64>(a, s);
+  return launch_few_nt<F, 128>(a, s);
+}
+
+}  // namespace
+}  // namespace act
+
+cudaError_t launch_w4a4_gemm(const ActGemmArgs& a, cudaStream_t s) { return act::launch_few<act::F4>(a, s); }
+cudaError_t launch_w8a8_gemm(const ActGemmArgs& a, cudaStream_t s) { return act::launch_few<act::F8>(a, s); }
+
+}  // namespace wqp

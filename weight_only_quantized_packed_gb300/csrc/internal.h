@@ -62,6 +62,54 @@ struct DequantArgs {
   bool pdl;
 };
 
+// Rows to quantise: X [M, ldx] of type dtype (wqp_dtype), codes and scales
+// contiguous.
+struct QuantArgs {
+  const void* X;
+  uint8_t* codes;
+  void* scales;
+  float gscale;         // 4-bit global scale
+  int dtype, M, K, ldx;
+  bool pdl;
+};
+
+// RMS norm of X (+ R) [M, K]; H (the sum) and R may be NULL. Y is of X's
+// type with pitch ldy, or contiguous E4M3 codes with scales S.
+struct NormArgs {
+  const void* X;
+  const void* R;
+  const void* W;
+  void* H;
+  void* Y;
+  float* S;
+  float eps;
+  int dtype, M, K;
+  int ldx, ldr, ldh, ldy;
+  int num_sms;
+  bool pdl;
+};
+
+// C [M, ldc] = rows of quantised activations times packed weights.
+struct ActGemmArgs {
+  const void* A;        // codes [M, K/2] (4-bit) or [M, K] (8-bit), contiguous
+  const void* SA;       // E4M3 [M, K/16] or float [M, K/128]
+  const void* W;
+  const void* SW;       // E4M3 [N, K/16] or float [ceil(N/128), K/128]
+  void* C;
+  float gscale;         // product of the two global scales (1 for 8-bit)
+  int M, N, K, ldc;
+  unsigned* err;
+  int num_sms;
+  bool pdl;
+};
+
+cudaError_t launch_w4_quantize(const QuantArgs& a, cudaStream_t s);
+cudaError_t launch_a8_quantize(const QuantArgs& a, cudaStream_t s);
+cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_rms_norm_a8(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_w4a4_gemm(const ActGemmArgs& a, cudaStream_t s);
+cudaError_t launch_w8a8_gemm(const ActGemmArgs& a, cudaStream_t s);
+
 cudaError_t launch_q2_gemv(const GemvArgs& a, cudaStream_t s);
 cudaError_t launch_w4a16_gemv(const GemvArgs& a, cudaStream_t s);
 cudaError_t launch_w8a16_gemm(const GemvArgs& a, cudaStream_t s);
