@@ -359,7 +359,28 @@ cudaError_t launch_few(const ActGemmArgs& a, cudaStream_t s) {
 }  // namespace
 }  // namespace act
 
-cudaError_t launch_w4a4_gemm(const ActGemmArgs& a, cudaStream_t s) { return act::launch_few<act::F4>(a, s); }
-cudaError_t launch_w8a8_gemm(const ActGemmArgs& a, cudaStream_t s) { return act::launch_few<act::F8>(a, s); }
+// Up to 128 rows one pass over the weights serves them all; more go to the
+// kernel whose tiles are wider in both directions. Calls of more than 2^20
+// rows go in pieces, so that tile counts stay within an int.
+template <class F>
+static cudaError_t launch_act_gemm(const ActGemmArgs& a, cudaStream_t s) {
+  constexpr int kPiece = 1 << 20;
+  cudaError_t e = cudaSuccess;
+  for (int r0 = 0; r0 < a.M && e == cudaSuccess; r0 += kPiece) {
+    ActGemmArgs b = a;
+    b.M = a.M - r0 < kPiece ? a.M - r0 : kPiece;
+    const size_t r = static_cast<size_t>(r0), K = static_cast<size_t>(a.K);
+    b.A = static_cast<const char*>(a.A) + r * (F::kScaled ? K / 2 : K);
+    b.SA = static_cast<const char*>(a.SA) + r * (F::kScaled ? K / 16 : K / 128 * 4);
+    b.C = static_cast<char*>(a.C) + r * a.ldc * 2;
+    if (b.M <= 128) e = act::launch_few<F>(b, s);
+    else e = F::kScaled ? launch_w4a4_many(b, s) : launch_w8a8_many(b, s);
+    if (a.M - r0 <= kPiece) break;
+  }
+  return e;
+}
+
+cudaError_t launch_w4a4_gemm(const ActGemmArgs& a, cudaStream_t s) { return launch_act_gemm<act::F4>(a, s); }
+cudaError_t launch_w8a8_gemm(const ActGemmArgs& a, cudaStream_t s) { return launch_act_gemm<act::F8>(a, s); }
 
 }  // namespace wqp

@@ -109,6 +109,9 @@ cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s);
 cudaError_t launch_rms_norm_a8(const NormArgs& a, cudaStream_t s);
 cudaError_t launch_w4a4_gemm(const ActGemmArgs& a, cudaStream_t s);
 cudaError_t launch_w8a8_gemm(const ActGemmArgs& a, cudaStream_t s);
+// The kernels for many rows (gemm_act_many.cu).
+cudaError_t launch_w4a4_many(const ActGemmArgs& a, cudaStream_t s);
+cudaError_t launch_w8a8_many(const ActGemmArgs& a, cudaStream_t s);
 
 cudaError_t launch_q2_gemv(const GemvArgs& a, cudaStream_t s);
 cudaError_t launch_w4a16_gemv(const GemvArgs& a, cudaStream_t s);
