@@ -36,23 +36,85 @@ __device__ __forceinline__ void mma_f4(uint32_t d, uint64_t ad, uint64_t bd, uin
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
-// mma_commit, arriving at the same barrier of every CTA of the cluster in mask.
-__device__ __forceinline__ void mma_commit_multicast(uint32_t bar, uint16_t mask) {
+
+// The pair forms: two CTAs of a cluster (ranks 2i and 2i + 1) work on one
+// 256-row tile. The even CTA issues for both: the same shared and tensor
+// memory addresses are meant in each. Each CTA holds its 128 rows of A and of
+// D, and half the rows of B.
+__device__ __forceinline__ void pair_mma_f8(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(mask)
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// tma_load_2d into the same place of every CTA of the cluster in mask, each
-// completing on its own barrier at that place.
-__device__ __forceinline__ void tma_load_2d_multicast(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
-                                                      uint16_t mask) {
+__device__ __forceinline__ void pair_mma_f4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sa,
+                                            uint32_t sb, uint32_t accumulate) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"(mask)
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
       : "memory");
 }
+__device__ __forceinline__ void pair_copy_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// Arrives at this barrier of both CTAs when this thread's earlier pair
+// operations are done.
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// The same, at a barrier of this CTA alone.
+__device__ __forceinline__ void pair_commit_own(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// A tile into this CTA's shared memory, completing on a barrier of either CTA
+// of the pair (bar is a shared::cluster address).
+__device__ __forceinline__ void pair_tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+// mbar_arrive and mbar_arrive_expect_tx at a shared::cluster address. They
+// order this CTA's own accesses only (a release at cluster scope costs about
+// a microsecond, a stage's whole time): what the arrival announces is in this
+// CTA's shared or tensor memory, complete behind a proxy or tcgen05 fence,
+// and only tcgen05 operations of the pair use it.
+__device__ __forceinline__ void pair_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void pair_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// A tile of this CTA's shared memory to global memory; rows and columns
+// outside the map are dropped. The thread that stored waits before the
+// shared memory is written again (read) or the CTA ends (all).
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Instruction descriptors: N >> 3 at bits 17..22, M >> 4 at bits 24..28; FP32
 // accumulation. E4M3 operands are format 0; E2M1 with block scales is format
@@ -64,8 +126,8 @@ __host__ __device__ constexpr uint32_t idesc_f4(int M, int N) {
   return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// 32 lanes x NC columns from tensor memory without waiting; the registers are
-// valid after tmem_ld_wait.
+// 32 lanes x 32 or 16 columns from tensor memory without waiting; the
+// registers are valid after tmem_ld_wait.
 __device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -78,35 +140,68 @@ __device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld16_start(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// Waits for this thread's tensor-memory loads; r stands for what they wrote,
+// so that no use of it moves above the wait.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Two FP32 values in one register pair, and (x, y) = (x, y) * f + (x, y)'.
+__device__ __forceinline__ uint64_t pair_f32(uint32_t lo, uint32_t hi) {
+  return static_cast<uint64_t>(lo) | (static_cast<uint64_t>(hi) << 32);
+}
+__device__ __forceinline__ void fma_f32x2(uint64_t& acc, uint64_t v, uint64_t f) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(f));
+}
+
 // ---------------------------------------------------------------- 4-bit scales
-// A raw stage holds a row's 16 scales (256 K) as 16 bytes. The tensor core
+// A stage arrives with a row's 16 scales (256 K) as 16 bytes. The tensor core
 // wants, per 64-K step, lane l of column i to hold the 4 scales of row
 // 32 i + l, and copy_scales takes that column group as 32 rows of 16 bytes:
-// step j of a 128-row block is the 512 bytes at dst + 512 j. `half` (0, 1)
-// does the steps 2 half and 2 half + 1; only the first `rows` rows exist. The
-// tensor core reads the scales as unsigned: a code with its sign bit set
-// becomes NaN, so that it cannot pass for a positive one.
-constexpr int kScaleBlock = 2048;      // bytes of a 128-row block, raw or rearranged
+// step j of a 128-row block is the 512 bytes at 512 j. A block is rearranged
+// in place by two warps: `half` (0, 1) does the steps 2 half and 2 half + 1,
+// and both have loaded (take) before either stores (put). Only the first
+// `rows` rows of a block exist. The tensor core reads the scales as unsigned:
+// a code with its sign bit set becomes NaN, so that it cannot pass for a
+// positive one.
+constexpr int kScaleBlock = 2048;      // bytes of a 128-row block
 
 __device__ __forceinline__ uint32_t scales_no_sign(uint32_t w) { return w | (((w & 0x80808080u) >> 7) * 0x7Fu); }
 
-__device__ __forceinline__ void rearrange_scales(const uint8_t* raw, uint8_t* dst, int half, int lane, int rows) {
-  uint2 v[4];
+__device__ __forceinline__ void take_scales(const uint8_t* block, int half, int lane, int rows, uint2 (&v)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[i] = make_uint2(0, 0);
-    if (32 * i + lane < rows) v[i] = *reinterpret_cast<const uint2*>(raw + (32 * i + lane) * 16 + 8 * half);
+    if (32 * i + lane < rows) v[i] = *reinterpret_cast<const uint2*>(block + (32 * i + lane) * 16 + 8 * half);
     v[i].x = scales_no_sign(v[i].x);
     v[i].y = scales_no_sign(v[i].y);
   }
-  uint8_t* d = dst + half * 1024 + lane * 16;
+}
+__device__ __forceinline__ void put_scales(uint8_t* block, int half, int lane, const uint2 (&v)[4]) {
+  uint8_t* d = block + half * 1024 + lane * 16;
   *reinterpret_cast<uint4*>(d) = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
   *reinterpret_cast<uint4*>(d + 512) = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
 }

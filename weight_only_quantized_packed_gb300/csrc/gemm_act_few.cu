@@ -45,9 +45,7 @@ struct FewLayout {
   static constexpr int kAcc = F::kScaled ? 1 : (NT <= 64 ? 4 : 2);        // accumulator slots
   static constexpr int kW = 0;
   static constexpr int kA = kW + kS * 16384;
-  static constexpr int kRawW = kA + kS * NT * 128;
-  static constexpr int kRawA = kRawW + (F::kScaled ? kS * kScaleBlock : 0);
-  static constexpr int kSclW = kRawA + (F::kScaled ? kS * NT * 16 : 0);
+  static constexpr int kSclW = kA + kS * NT * 128;
   static constexpr int kSclA = kSclW + (F::kScaled ? kS * kScaleBlock : 0);
   static constexpr int kFac = kSclA + (F::kScaled ? kS * kScaleBlock : 0);
   static constexpr int kRecv = kFac + (F::kScaled ? 0 : 4 * NT * 4);
@@ -117,12 +115,12 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
         const int s = t % S;
         mbar_arrive_expect_tx(full + 8 * s, L::kStageBytes);
         tma_load_2d_hint(sb + L::kW + s * 16384, &tmW, (st0 + t) * 128, n0, full + 8 * s, pol);
-        if (F::kScaled) tma_load_2d_hint(sb + L::kRawW + s * kScaleBlock, &tmSW, (st0 + t) * 16, n0, full + 8 * s, pol);
+        if (F::kScaled) tma_load_2d_hint(sb + L::kSclW + s * kScaleBlock, &tmSW, (st0 + t) * 16, n0, full + 8 * s, pol);
       };
       auto load_a = [&](int t) {
         const int s = t % S;
         tma_load_2d(sb + L::kA + s * NT * 128, &tmA, (st0 + t) * 128, m0, full + 8 * s);
-        if (F::kScaled) tma_load_2d(sb + L::kRawA + s * NT * 16, &tmSA, (st0 + t) * 16, m0, full + 8 * s);
+        if (F::kScaled) tma_load_2d(sb + L::kSclA + s * kScaleBlock, &tmSA, (st0 + t) * 16, m0, full + 8 * s);
       };
       // The weights do not depend on the previous grid; the activations may.
       const int ahead = min(S, nst);
@@ -179,8 +177,14 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
         const int s = t % S;
         const bool ok = wait_or_abort(full + 8 * s, (t / S) & 1, p.err, abort_flag);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        rearrange_scales(smem + L::kRawW + s * kScaleBlock, smem + L::kSclW + s * kScaleBlock, warp - 2, lane, 128);
-        rearrange_scales(smem + L::kRawA + s * NT * 16, smem + L::kSclA + s * kScaleBlock, warp - 2, lane, NT);
+        uint8_t* bw = smem + L::kSclW + s * kScaleBlock;
+        uint8_t* ba = smem + L::kSclA + s * kScaleBlock;
+        uint2 vw[4], va[4];
+        take_scales(bw, warp - 2, lane, 128, vw);
+        take_scales(ba, warp - 2, lane, NT, va);
+        asm volatile("bar.sync 1, 64;" ::: "memory");
+        put_scales(bw, warp - 2, lane, vw);
+        put_scales(ba, warp - 2, lane, va);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(scaled + 8 * s);
@@ -199,10 +203,11 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < NT; c += 16) {
-          float v[16];
-          tmem_ld<16>(tl + c, v);
+          uint32_t v[16];
+          tmem_ld16_start(tl + c, v);
+          tmem_ld_wait(v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[c + i] = v[i] * p.gscale;
+          for (int i = 0; i < 16; ++i) acc[c + i] = __uint_as_float(v[i]) * p.gscale;
         }
       }
     } else {
@@ -234,10 +239,11 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < NT; c += 16) {
-          float v[16];
-          tmem_ld<16>(tl + slot * NT + c, v);
+          uint32_t v[16];
+          tmem_ld16_start(tl + slot * NT + c, v);
+          tmem_ld_wait(v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(v[i], fac[c + i], acc[c + i]);
+          for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(__uint_as_float(v[i]), fac[c + i], acc[c + i]);
         }
         tc_fence_before();
         __syncwarp();

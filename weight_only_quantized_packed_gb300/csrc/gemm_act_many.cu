@@ -2,28 +2,28 @@
 // 4-bit with E4M3 scales per 16 K, and 8-bit by 8-bit with FP32 scales per
 // 128 K.
 //
-// Bound by the tensor core, so a tile is as wide as the MMA allows: 128
-// activation rows (the MMA's M side, one tensor-memory lane each) by BN weight
-// rows. Persistent CTAs, one per SM, walk over the tiles; with CL = 2 a
-// cluster of two takes two row tiles of the same weights, and each CTA loads
-// half of the weight tile for both.
-//  * 4 bits: the tensor core applies the scales (act.cuh: rearranged by two
-//    warps, copied to tensor memory by the MMA warp). One accumulator, drained
-//    into registers as BF16 before the next tile's first MMA.
+// Bound by the tensor core and, at its 8- and 4-bit rates, by the shared
+// memory that feeds it: a tile is 256 activation rows by BN weight rows, held
+// by a pair of CTAs on two SMs (act.cuh), so that each SM reads half of the
+// weight tile for all of its MMA's work. Persistent pairs walk over the tiles.
+//  * 4 bits: the tensor core applies the scales, rearranged by two warps of
+//    each CTA (its 128 activation rows, all BN weight rows) and copied to
+//    tensor memory by the MMA warp. One accumulator, drained into registers as
+//    BF16 before the next tile's first MMA.
 //  * 8 bits: two accumulators that take turns per 128 K; the epilogue adds each,
 //    times its activation row's and weight block's scale, to FP32 sums in
 //    registers while the tensor core fills the other.
+// Output goes through shared memory, 32 rows by 32 columns a warp at a time,
+// and leaves as bulk tensor stores (rows of C that are not 16-byte aligned: as
+// whole row segments from there).
 //
-// Warps: 0 copies, 1 MMA (and tensor memory), 2..3 scales (4 bits), 4..11
-// epilogue: lane quarter = warp % 4, column half = (warp - 4) / 4.
+// Warps: 0 copies, 1 MMA (even CTA; tensor memory in both), 4 bits: 2..3
+// scales; the rest epilogue, one per lane quarter (warp % 4) and 64 columns.
 #include "act.cuh"
 
 namespace wqp {
 namespace act {
 namespace {
-
-constexpr int kThreads = 384;
-constexpr int kEpiWarp0 = 4;
 
 constexpr uint32_t kScaleCol = 256;    // 4 bits: two sets of a stage's scales
 
@@ -33,26 +33,28 @@ struct ManyParams {
   float gscale;
   uint16_t* C;
   int M, N, K, ldc;
-  int mt, nt;           // row tiles in units of CL, weight tiles
+  int mt, nt;           // 256-row tiles, weight tiles
   int stages;           // per tile
   int vec;              // C rows are 16-byte aligned
   unsigned* err;
 };
 
-template <class F, int BN, int CL>
+template <class F, int BN>
 struct ManyLayout {
-  static constexpr int kAux = F::kScaled ? 2 * kScaleBlock * (1 + BN / 128) : 0;
-  static constexpr int kStageBytes = 16384 + BN * 128 + kAux;
-  static constexpr int kS = (220 * 1024) / kStageBytes;
+  static constexpr int kRoles = 4;
+  static constexpr int kCols = F::kScaled ? 64 : BN / 2;        // columns of an epilogue warp
+  static constexpr int kEpi = BN / kCols * 4;                   // epilogue warps
+  static constexpr int kThreads = (kRoles + kEpi) * 32;
+  static constexpr int kNB = (BN + 127) / 128;                  // 128-row blocks of the weights' scales
+  static constexpr int kStageBytes = 16384 + BN * 64 + (F::kScaled ? kScaleBlock * (1 + kNB) : 0);
+  static constexpr int kS = (225 * 1024 - kEpi * 2048) / kStageBytes;
   static constexpr int kA = 0;
   static constexpr int kB = kA + kS * 16384;
-  static constexpr int kRawA = kB + kS * BN * 128;
-  static constexpr int kRawB = kRawA + (F::kScaled ? kS * kScaleBlock : 0);
-  static constexpr int kSclA = kRawB + (F::kScaled ? kS * kScaleBlock * (BN / 128) : 0);
+  static constexpr int kOut = kB + kS * BN * 64;                // [epilogue warp][32 rows][64 bytes]
+  static constexpr int kSclA = kOut + kEpi * 2048;
   static constexpr int kSclB = kSclA + (F::kScaled ? kS * kScaleBlock : 0);
-  static constexpr int kBytes = kSclB + (F::kScaled ? kS * kScaleBlock * (BN / 128) : 0);
+  static constexpr int kBytes = kSclB + (F::kScaled ? kS * kScaleBlock * kNB : 0);
   static constexpr int kAlloc = kBytes + 1024;
-  static constexpr int kLoad = 16384 + BN * 128 + kAux / 2;     // bytes that arrive per stage
   static constexpr int kAcc = F::kScaled ? 1 : 2;
   static_assert(kAlloc <= 227 * 1024 - 1024, "shared memory");
 };
@@ -68,261 +70,318 @@ __device__ __forceinline__ void tile_at(int i, int mt, int nt, int& m, int& n) {
   m = g * G + (j - n * rows);
 }
 
-template <class F, int BN, int CL>
-__global__ void __launch_bounds__(kThreads, 1)
+template <class F, int BN>
+__global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
     many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, ManyParams p) {
-  using L = ManyLayout<F, BN, CL>;
-  constexpr int S = L::kS, NACC = L::kAcc, COLS = BN / 2;
+                const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                const __grid_constant__ CUtensorMap tmC, ManyParams p) {
+  using L = ManyLayout<F, BN>;
+  constexpr int S = L::kS, NACC = L::kAcc, COLS = L::kCols, NB = L::kNB;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full_sh[S], empty_sh[S], scaled_sh[S], acc_full_sh[NACC], acc_free_sh[NACC], drained_sh;
+  // full, scaled and acc_free count both CTAs' work and are used in the even
+  // CTA; raw_full is each CTA's own; empty and acc_full are told to both.
+  __shared__ __align__(8) uint64_t full_sh[S], raw_full_sh[S], empty_sh[S], scaled_sh[S], acc_full_sh[NACC],
+      acc_free_sh[NACC], drained_sh;
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = CL > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int first = blockIdx.x / CL, step = gridDim.x / CL, total = p.mt * p.nt;
-  const uint32_t full = smem_u32(full_sh), empty = smem_u32(empty_sh), scaled = smem_u32(scaled_sh);
-  const uint32_t acc_full = smem_u32(acc_full_sh), acc_free = smem_u32(acc_free_sh);
+  const int rank = static_cast<int>(cluster_rank());
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1, total = p.mt * p.nt;
+  const uint32_t full = smem_u32(full_sh), raw_full = smem_u32(raw_full_sh), empty = smem_u32(empty_sh);
+  const uint32_t scaled = smem_u32(scaled_sh), acc_full = smem_u32(acc_full_sh), acc_free = smem_u32(acc_free_sh);
+  const uint32_t drained = smem_u32(&drained_sh);
   volatile int* abort_flag = &abort_sh;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, CL);
-      mbar_init(scaled + 8 * i, 2);
+      mbar_init(full + 8 * i, 2);
+      mbar_init(raw_full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+      mbar_init(scaled + 8 * i, 4);
     }
     for (int i = 0; i < NACC; ++i) {
       mbar_init(acc_full + 8 * i, 1);
-      mbar_init(acc_free + 8 * i, 8);
+      mbar_init(acc_free + 8 * i, 2 * L::kEpi);
     }
-    mbar_init(smem_u32(&drained_sh), 1);
+    mbar_init(drained, 1);
     abort_sh = 0;
     mbar_fence_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&tmem_sh), 512);
-    tmem_relinquish();
+    pair_tmem_alloc(smem_u32(&tmem_sh), 512);
     tc_fence_before();
   }
   __syncthreads();
-  if (CL > 1) cluster_sync();                  // every barrier exists before a peer's copy or arrive
+  cluster_sync();                              // every barrier exists before a peer's copy or arrive
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
   pdl_launch_dependents();
 
-  if (warp < kEpiWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == 0) {
-      int it = 0;
-      if (lane == 0) {
-        prefetch_tmap(&tmA);
-        prefetch_tmap(&tmB);
-        pdl_wait();
-        bool live = true;
-        for (int i = first; i < total && live; i += step) {
-          int mi, ni;
-          tile_at(i, p.mt, p.nt, mi, ni);
-          const int m0 = (mi * CL + rank) * 128, n0 = ni * BN;
-          for (int k = 0; k < p.stages; ++k, ++it) {
-            const int s = it % S;
-            if (it >= S && !wait_or_abort(empty + 8 * s, ((it / S) - 1) & 1, p.err, abort_flag)) {
-              live = false;
-              break;
-            }
-            const uint32_t bar = full + 8 * s;
-            mbar_arrive_expect_tx(bar, L::kLoad);
-            tma_load_2d(sb + L::kA + s * 16384, &tmA, k * 128, m0, bar);
-            const uint32_t db = sb + L::kB + s * BN * 128;
-            if (F::kScaled) tma_load_2d(sb + L::kRawA + s * kScaleBlock, &tmSA, k * 16, m0, bar);
-            const uint32_t ds = sb + L::kRawB + s * kScaleBlock * (BN / 128);
-            if (CL == 1) {
-              tma_load_2d(db, &tmB, k * 128, n0, bar);
-              if (F::kScaled) tma_load_2d(ds, &tmSB, k * 16, n0, bar);
-            } else {
-              constexpr int R = BN / CL;
-              tma_load_2d_multicast(db + rank * R * 128, &tmB, k * 128, n0 + rank * R, bar, (1 << CL) - 1);
-              if (F::kScaled) tma_load_2d_multicast(ds + rank * R * 16, &tmSB, k * 16, n0 + rank * R, bar, (1 << CL) - 1);
-            }
+  // The loops below keep their place in a ring as an index and a parity: their
+  // instructions are on the path from one stage to the next. Copies, MMAs and
+  // stores are issued under elect.sync, whose one thread the compiler knows to
+  // be one: behind a test of the lane number the same instructions took twice
+  // the kernel's time (4096x34816x5120, 4 bits: 494 us against 261). When a
+  // wait has run out (abort_flag) the loops go on to their ends, waiting no
+  // more, and nothing is stored.
+  if (warp < L::kRoles) {
+    if (!F::kScaled) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0 && elect_one()) {
+      prefetch_tmap(&tmA);
+      prefetch_tmap(&tmB);
+      pdl_wait();
+      const uint32_t full0 = mapa_shared(full, 0);
+      int s = 0, used = 0;                     // stages used, up to S
+      uint32_t ph = 1;                         // parity of the stage's last consumption
+      for (int i = first; i < total && !*abort_flag; i += step) {
+        int mi, ni;
+        tile_at(i, p.mt, p.nt, mi, ni);
+        const int m0 = mi * 256 + rank * 128, n0 = ni * BN;
+        for (int k = 0; k < p.stages; ++k) {
+          if (used == S) {
+            if (!wait_or_abort(empty + 8 * s, ph, p.err, abort_flag)) break;
+          } else {
+            ++used;
           }
+          // The even CTA's barrier takes both CTAs' bytes; each announces its own.
+          pair_arrive_expect_tx(full0 + 8 * s, 16384 + BN * 64);
+          pair_tma_load_2d(sb + L::kA + s * 16384, &tmA, k * 128, m0, full0 + 8 * s);
+          pair_tma_load_2d(sb + L::kB + s * BN * 64, &tmB, k * 128, n0 + rank * (BN / 2), full0 + 8 * s);
+          if (F::kScaled) {
+            mbar_arrive_expect_tx(raw_full + 8 * s, (128 + BN) * 16);
+            tma_load_2d(sb + L::kSclA + s * kScaleBlock, &tmSA, k * 16, m0, raw_full + 8 * s);
+            tma_load_2d(sb + L::kSclB + s * kScaleBlock * NB, &tmSB, k * 16, n0, raw_full + 8 * s);
+          }
+          if (++s == S) s = 0, ph ^= 1;
         }
-        // Every stage has been consumed here and by the peer, and the peer's
-        // arrivals have come, before the CTA may exit.
-        for (int t = it > S ? it - S : 0; t < it; ++t)
-          if (!wait_or_abort(empty + 8 * (t % S), (t / S) & 1, p.err, abort_flag))
-            mbar_wait(full + 8 * (t % S), (t / S) & 1, p.err);
       }
-      __syncwarp();
-    } else if (warp == 1) {
-      constexpr uint32_t idesc = F::kScaled ? idesc_f4(128, BN) : idesc_f8(128, BN);
-      int it = 0, blk = 0;                     // stages, and accumulators handed over
-      bool live = true;
-      for (int i = first; i < total && live; i += step) {
-        for (int k = 0; k < p.stages; ++k, ++it) {
-          const int s = it % S, slot = blk % NACC;
-          bool ok = wait_or_abort(full + 8 * s, (it / S) & 1, p.err, abort_flag);
-          if (F::kScaled) ok = ok && wait_or_abort(scaled + 8 * s, (it / S) & 1, p.err, abort_flag);
-          if ((!F::kScaled || k == 0) && blk >= NACC)
-            ok = ok && wait_or_abort(acc_free + 8 * slot, ((blk / NACC) - 1) & 1, p.err, abort_flag);
-          live = __all_sync(0xFFFFFFFFu, ok);
-          if (!live) break;
+      // Every stage has been consumed, or (after an abort) has at least
+      // arrived, before the CTA may exit: the oldest first.
+      for (int t = 0; t < used; ++t) {
+        const int at = used < S ? t : s;
+        const uint32_t par = used < S ? 0u : ph;
+        if (!wait_or_abort(empty + 8 * at, par, p.err, abort_flag)) {
+          if (rank == 0) mbar_wait(full + 8 * at, par, p.err);
+          if (F::kScaled) mbar_wait(raw_full + 8 * at, par, p.err);
+        }
+        if (used == S && ++s == S) s = 0, ph ^= 1;
+      }
+    } else if (warp == 1 && rank == 0) {
+      constexpr uint32_t idesc = F::kScaled ? idesc_f4(256, BN) : idesc_f8(256, BN);
+      const uint64_t ad0 = tile_desc(sb + L::kA), bd0 = tile_desc(sb + L::kB);
+      const uint64_t sad0 = scale_desc(sb + L::kSclA), sbd0 = scale_desc(sb + L::kSclB);
+      int s = 0, slot = 0, handed = 0;         // accumulators handed over, up to NACC
+      uint32_t ph = 0, acc_ph = 1, set = 0;
+      for (int i = first; i < total; i += step) {
+        for (int k = 0; k < p.stages; ++k) {
+          if (!F::kScaled || k == 0) {
+            if (handed == NACC) wait_or_abort(acc_free + 8 * slot, acc_ph, p.err, abort_flag);
+            else ++handed;
+          }
+          wait_or_abort(full + 8 * s, ph, p.err, abort_flag);
+          if (F::kScaled) wait_or_abort(scaled + 8 * s, ph, p.err, abort_flag);
+          __syncwarp();
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t ad = tile_desc(sb + L::kA + s * 16384), bd = tile_desc(sb + L::kB + s * BN * 128);
+            // Addresses in a descriptor are in units of 16 bytes.
+            const uint64_t ad = ad0 + s * (16384 >> 4), bd = bd0 + s * ((BN * 64) >> 4);
             if constexpr (F::kScaled) {
-              constexpr int NB = BN / 128;
-              const uint32_t sa = tmem + kScaleCol + (it & 1) * 64, sw = sa + 16;
+              const uint64_t sad = sad0 + s * (kScaleBlock >> 4), sbd = sbd0 + s * ((NB * kScaleBlock) >> 4);
+              const uint32_t sa = tmem + kScaleCol + set * 64, sw = sa + 16;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                copy_scales(sa + 4 * j, scale_desc(sb + L::kSclA + s * kScaleBlock + 512 * j));
+                pair_copy_scales(sa + 4 * j, sad + 32 * j);
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-                  copy_scales(sw + (j * NB + b) * 4,
-                              scale_desc(sb + L::kSclB + (s * NB + b) * kScaleBlock + 512 * j));
+                for (int b = 0; b < NB; ++b) pair_copy_scales(sw + (j * NB + b) * 4, sbd + b * (kScaleBlock >> 4) + 32 * j);
               }
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                mma_f4(tmem, ad + 2 * j, bd + 2 * j, idesc, sa + 4 * j, sw + j * NB * 4, (k | j) ? 1u : 0u);
+                pair_mma_f4(tmem, ad + 2 * j, bd + 2 * j, idesc, sa + 4 * j, sw + j * NB * 4, (k | j) ? 1u : 0u);
             } else {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) mma_f8(tmem + slot * 256, ad + 2 * j, bd + 2 * j, idesc, j ? 1u : 0u);
+              for (int j = 0; j < 4; ++j) pair_mma_f8(tmem + slot * 256, ad + 2 * j, bd + 2 * j, idesc, j ? 1u : 0u);
             }
-            if (CL == 1) mma_commit(empty + 8 * s);
-            else mma_commit_multicast(empty + 8 * s, (1 << CL) - 1);
-            if (!F::kScaled || k == p.stages - 1) mma_commit(acc_full + 8 * slot);
+            if (!F::kScaled || k == p.stages - 1) pair_commit(acc_full + 8 * slot);
+            pair_commit(empty + 8 * s);
           }
           __syncwarp();
-          if (!F::kScaled || k == p.stages - 1) ++blk;
+          set ^= 1;
+          if ((!F::kScaled || k == p.stages - 1) && ++slot == NACC) slot = 0, acc_ph ^= 1;
+          if (++s == S) s = 0, ph ^= 1;
         }
       }
-      // This warp's MMAs are done before tensor memory is freed.
-      if (elect_one()) mma_commit(smem_u32(&drained_sh));
+      // The pair's MMAs are done before the cluster barrier below, and tensor
+      // memory is freed after it.
+      if (elect_one()) pair_commit_own(drained);
       __syncwarp();
-      mbar_wait(smem_u32(&drained_sh), 0, p.err);
-    } else if constexpr (F::kScaled) {
-      int it = 0;
-      bool live = true;
-      for (int i = first; i < total && live; i += step) {
-        for (int k = 0; k < p.stages; ++k, ++it) {
-          const int s = it % S;
-          live = __all_sync(0xFFFFFFFFu, wait_or_abort(full + 8 * s, (it / S) & 1, p.err, abort_flag));
-          if (!live) break;
-          rearrange_scales(smem + L::kRawA + s * kScaleBlock, smem + L::kSclA + s * kScaleBlock, warp - 2, lane, 128);
+      mbar_wait(drained, 0, p.err);
+    } else if (F::kScaled && warp >= 2) {
+      const uint32_t scaled0 = mapa_shared(scaled, 0);
+      int s = 0;
+      uint32_t ph = 0;
+      for (int i = first; i < total; i += step) {
+        for (int k = 0; k < p.stages; ++k) {
+          wait_or_abort(raw_full + 8 * s, ph, p.err, abort_flag);
+          uint8_t* ba = smem + L::kSclA + s * kScaleBlock;
+          uint8_t* bb = smem + L::kSclB + s * NB * kScaleBlock;
+          uint2 va[4], vb[NB][4];
+          take_scales(ba, warp - 2, lane, 128, va);
 #pragma unroll
-          for (int b = 0; b < BN / 128; ++b) {
-            const int at = (s * (BN / 128) + b) * kScaleBlock;
-            rearrange_scales(smem + L::kRawB + at, smem + L::kSclB + at, warp - 2, lane, 128);
-          }
+          for (int b = 0; b < NB; ++b) take_scales(bb + b * kScaleBlock, warp - 2, lane, min(128, BN - 128 * b), vb[b]);
+          asm volatile("bar.sync 1, 64;" ::: "memory");
+          put_scales(ba, warp - 2, lane, va);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) put_scales(bb + b * kScaleBlock, warp - 2, lane, vb[b]);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(scaled + 8 * s);
+          if (lane == 0) pair_arrive(scaled0 + 8 * s);
+          if (++s == S) s = 0, ph ^= 1;
         }
       }
     }
+    __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
+    if (!F::kScaled) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int q = warp & 3, ew = warp - L::kRoles, h = ew >> 2;
     const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * COLS;
+    const uint32_t acc_free0 = mapa_shared(acc_free, 0);
+    uint8_t* out = smem + L::kOut + ew * 2048;
     const int kb = p.K >> 7;
-    pdl_wait();                                // 8 bits: the activations' scales
-    int blk = 0;
-    bool live = true;
-    for (int i = first; i < total && live; i += step) {
+    if (!F::kScaled) pdl_wait();               // the activations' scales
+    int slot = 0;
+    uint32_t ph = 0;
+    for (int i = first; i < total; i += step) {
       int mi, ni;
       tile_at(i, p.mt, p.nt, mi, ni);
-      const int m = (mi * CL + rank) * 128 + q * 32 + lane, n0 = ni * BN + h * COLS;
+      const int m0 = mi * 256 + rank * 128 + q * 32, n0 = ni * BN + h * COLS;
       uint32_t packed[COLS / 2];
       if constexpr (F::kScaled) {
-        live = __all_sync(0xFFFFFFFFu, wait_or_abort(acc_full, blk & 1, p.err, abort_flag));
-        if (!live) break;
+        wait_or_abort(acc_full, ph, p.err, abort_flag);
+        ph ^= 1;
+        __syncwarp();
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < COLS; c += 32) {
           uint32_t v[32];
           tmem_ld32_start(tl + c, v);
-          tmem_ld_wait();
+          tmem_ld_wait(v);
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             packed[c / 2 + j] = pack_bf16(__uint_as_float(v[2 * j]) * p.gscale, __uint_as_float(v[2 * j + 1]) * p.gscale);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(acc_free);
-        ++blk;
+        if (lane == 0) pair_arrive(acc_free0);
       } else {
-        const float* sa = p.SA + static_cast<long long>(min(m, p.M - 1)) * kb;
-        const float* sw = p.SW + static_cast<long long>(min(n0, p.N - 1) >> 7) * kb;
-        float acc[COLS];
+        const float* sa = p.SA + static_cast<long long>(min(m0 + lane, p.M - 1)) * kb;
+        // The warp's columns lie in one or two weight blocks; `cross` is the
+        // first column of the second.
+        const int cross = 128 - (n0 & 127);
+        const float* sw0 = p.SW + static_cast<long long>(min(n0, p.N - 1) >> 7) * kb;
+        const float* sw1 = p.SW + static_cast<long long>(min(n0 + COLS - 1, p.N - 1) >> 7) * kb;
+        uint64_t acc[COLS / 2];
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) acc[c] = 0.0f;
-        float next = sa[0] * __ldg(sw);
-        for (int k = 0; k < kb; ++k, ++blk) {
-          const int slot = blk & 1;
-          const float f = next;
-          if (k + 1 < kb) next = sa[k + 1] * __ldg(sw + k + 1);
-          live = __all_sync(0xFFFFFFFFu, wait_or_abort(acc_full + 8 * slot, (blk >> 1) & 1, p.err, abort_flag));
-          if (!live) break;
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < COLS; c += 32) {
-            uint32_t v[32];
-            tmem_ld32_start(tl + slot * 256 + c, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(__uint_as_float(v[j]), f, acc[c + j]);
+        for (int c = 0; c < COLS / 2; ++c) acc[c] = 0;
+        float next0 = sa[0] * __ldg(sw0), next1 = sa[0] * __ldg(sw1);
+        for (int k = 0; k < kb; ++k) {
+          const uint64_t f0 = pair_f32(__float_as_uint(next0), __float_as_uint(next0));
+          const uint64_t f1 = pair_f32(__float_as_uint(next1), __float_as_uint(next1));
+          if (k + 1 < kb) {
+            const float a = sa[k + 1];
+            next0 = a * __ldg(sw0 + k + 1);
+            if (BN % 256 != 0) next1 = a * __ldg(sw1 + k + 1);
           }
-          tc_fence_before();
+          wait_or_abort(acc_full + 8 * slot, ph, p.err, abort_flag);
           __syncwarp();
-          if (lane == 0) mbar_arrive(acc_free + 8 * slot);
-        }
-        if (!live) break;
+          tc_fence_after();
+          // The next columns are on their way while these are added; the
+          // accumulator is free once the last have arrived.
+          constexpr int W = 16;
+          uint32_t v[2][W];
+          tmem_ld16_start(tl + slot * 256, v[0]);
 #pragma unroll
-        for (int j = 0; j < COLS / 2; ++j) packed[j] = pack_bf16(acc[2 * j], acc[2 * j + 1]);
-      }
-      if (m < p.M) {
-        uint16_t* c = p.C + static_cast<long long>(m) * p.ldc + n0;
-        if (p.vec && n0 + COLS <= p.N) {
+          for (int c = 0; c < COLS; c += W) {
+            uint32_t(&x)[W] = v[(c / W) & 1];
+            tmem_ld_wait(x);
+            if (c + W < COLS) {
+              tmem_ld16_start(tl + slot * 256 + c + W, v[(c / W + 1) & 1]);
+            } else {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) pair_arrive(acc_free0 + 8 * slot);
+            }
+            const uint64_t f = (BN % 256 == 0 || c < cross) ? f0 : f1;
 #pragma unroll
-          for (int j = 0; j < COLS / 8; ++j)
-            reinterpret_cast<uint4*>(c)[j] = make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < COLS / 2; ++j) {
-            if (n0 + 2 * j < p.N) c[2 * j] = static_cast<uint16_t>(packed[j] & 0xFFFFu);
-            if (n0 + 2 * j + 1 < p.N) c[2 * j + 1] = static_cast<uint16_t>(packed[j] >> 16);
+            for (int j = 0; j < W / 2; ++j) fma_f32x2(acc[c / 2 + j], pair_f32(x[2 * j], x[2 * j + 1]), f);
           }
+          if (++slot == NACC) slot = 0, ph ^= 1;
+        }
+#pragma unroll
+        for (int j = 0; j < COLS / 2; ++j)
+          packed[j] = pack_bf16(__uint_as_float(static_cast<uint32_t>(acc[j])), __uint_as_float(static_cast<uint32_t>(acc[j] >> 32)));
+      }
+      if (*abort_flag) continue;
+      // 32 rows of 64 bytes in the 64-byte swizzle (16-byte chunk j of row r at
+      // j ^ (r / 2 mod 4)): free of bank conflicts here, and the store map's own.
+#pragma unroll
+      for (int c = 0; c < COLS; c += 32) {
+        if (elect_one()) tma_store_wait_read();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(out + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(packed[c / 2 + 4 * j], packed[c / 2 + 4 * j + 1], packed[c / 2 + 4 * j + 2], packed[c / 2 + 4 * j + 3]);
+        if (p.vec) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (elect_one() && m0 < p.M && n0 + c < p.N) tma_store_2d(&tmC, n0 + c, m0, smem_u32(out));
+        } else {
+          __syncwarp();
+          const int n = n0 + c + lane;
+          for (int r = 0; r < 32 && m0 + r < p.M; ++r) {
+            const uint16_t v = *reinterpret_cast<const uint16_t*>(out + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+            if (n < p.N) p.C[static_cast<long long>(m0 + r) * p.ldc + n] = v;
+          }
+          __syncwarp();
         }
       }
     }
+    if (elect_one()) tma_store_wait_all();
   }
   __syncwarp();
   __syncthreads();
+  cluster_sync();                              // no arrive or copy of the pair is on its way any more
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    pair_tmem_dealloc(tmem, 512);
   }
-  if (CL > 1) cluster_sync();
 }
 
-template <class F, int BN, int CL>
+template <class F, int BN>
 cudaError_t launch_many_t(const ActGemmArgs& a, cudaStream_t s) {
-  using L = ManyLayout<F, BN, CL>;
+  using L = ManyLayout<F, BN>;
   const uint64_t row = F::kScaled ? static_cast<uint64_t>(a.K) / 2 : static_cast<uint64_t>(a.K);
   const uint64_t srow = static_cast<uint64_t>(a.K) / 16;
   const uint64_t M = static_cast<uint64_t>(a.M), N = static_cast<uint64_t>(a.N);
-  CUtensorMap ma, mb, msa, msb;
+  CUtensorMap ma, mb, msa, msb, mc;
   constexpr auto kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   cudaError_t e = make_map_2d(&ma, kU8, a.A, row, M, row, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (e == cudaSuccess) e = cached_map_2d(&mb, kU8, a.W, row, N, row, 128, BN / CL, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e == cudaSuccess) e = cached_map_2d(&mb, kU8, a.W, row, N, row, 128, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B);
   msa = ma;
   msb = mb;
   if (F::kScaled) {
     if (e == cudaSuccess) e = make_map_2d(&msa, kU8, a.SA, srow, M, srow, 16, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
-    if (e == cudaSuccess) e = cached_map_2d(&msb, kU8, a.SW, srow, N, srow, 16, BN / CL, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e == cudaSuccess) e = cached_map_2d(&msb, kU8, a.SW, srow, N, srow, 16, BN, CU_TENSOR_MAP_SWIZZLE_NONE);
   }
+  const bool vec = a.ldc % 8 == 0 && reinterpret_cast<uintptr_t>(a.C) % 16 == 0;
+  mc = ma;
+  if (e == cudaSuccess && vec)
+    e = make_map_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.C, N, M, static_cast<uint64_t>(a.ldc) * 2, 32, 32,
+                    CU_TENSOR_MAP_SWIZZLE_64B);
   static AttrLatch latch;
-  if (e == cudaSuccess) e = set_smem_attrs(many_kernel<F, BN, CL>, latch, L::kAlloc, true);
+  if (e == cudaSuccess) e = set_smem_attrs(many_kernel<F, BN>, latch, L::kAlloc, true);
   if (e != cudaSuccess) return e;
   ManyParams p = {};
   if (!F::kScaled) {
@@ -335,34 +394,33 @@ cudaError_t launch_many_t(const ActGemmArgs& a, cudaStream_t s) {
   p.N = a.N;
   p.K = a.K;
   p.ldc = a.ldc;
-  p.mt = (a.M + 128 * CL - 1) / (128 * CL);
+  p.mt = (a.M + 255) / 256;
   p.nt = (a.N + BN - 1) / BN;
   p.stages = a.K / F::kStageK;
-  p.vec = a.ldc % 8 == 0 && reinterpret_cast<uintptr_t>(a.C) % 16 == 0;
+  p.vec = vec;
   p.err = a.err;
   const long long total = static_cast<long long>(p.mt) * p.nt;
-  const int clusters = static_cast<int>(total < a.num_sms / CL ? total : a.num_sms / CL);
+  const int pairs = static_cast<int>(total < a.num_sms / 2 ? total : a.num_sms / 2);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(clusters * CL);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(pairs * 2);
+  cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kAlloc;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CL;
+  attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.pdl ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, many_kernel<F, BN, CL>, ma, mb, msa, msb, p);
+  return cudaLaunchKernelEx(&cfg, many_kernel<F, BN>, ma, mb, msa, msb, mc, p);
 }
 
 template <class F>
 cudaError_t launch_many(const ActGemmArgs& a, cudaStream_t s) {
-  if (a.M <= 128) return launch_many_t<F, 256, 1>(a, s);
-  return launch_many_t<F, 256, 2>(a, s);
+  return launch_many_t<F, 256>(a, s);
 }
 
 }  // namespace
