@@ -178,19 +178,20 @@ __device__ __forceinline__ void fma_f32x2(uint64_t& acc, uint64_t v, uint64_t f)
 }
 
 // ---------------------------------------------------------------- 4-bit scales
-// A stage arrives with a row's 16 scales (256 K) as 16 bytes. The tensor core
+// A stage takes 16 scales (256 K) of every row: 16 bytes. The tensor core
 // wants, per 64-K step, lane l of column i to hold the 4 scales of row
-// 32 i + l, and copy_scales takes that column group as 32 rows of 16 bytes:
-// step j of a 128-row block is the 512 bytes at 512 j. A block is rearranged
-// in place by two warps: `half` (0, 1) does the steps 2 half and 2 half + 1,
-// and both have loaded (take) before either stores (put). Only the first
-// `rows` rows of a block exist. The tensor core reads the scales as unsigned:
-// a code with its sign bit set becomes NaN, so that it cannot pass for a
-// positive one.
+// 32 i + l of a 128-row block, and copy_scales takes that column group as 32
+// rows of 16 bytes: step j of a block is the 512 bytes at 512 j. The tensor
+// core reads the scales as unsigned: a code with its sign bit set becomes NaN,
+// so that it cannot pass for a positive one.
 constexpr int kScaleBlock = 2048;      // bytes of a 128-row block
 
 __device__ __forceinline__ uint32_t scales_no_sign(uint32_t w) { return w | (((w & 0x80808080u) >> 7) * 0x7Fu); }
 
+// A block that a tensor copy brought as rows of 16 bytes, rearranged in place
+// by two warps: `half` (0, 1) does the steps 2 half and 2 half + 1, and both
+// have loaded (take) before either stores (put). Only the first `rows` rows
+// of the block exist.
 __device__ __forceinline__ void take_scales(const uint8_t* block, int half, int lane, int rows, uint2 (&v)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -204,6 +205,32 @@ __device__ __forceinline__ void put_scales(uint8_t* block, int half, int lane, c
   uint8_t* d = block + half * 1024 + lane * 16;
   *reinterpret_cast<uint4*>(d) = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
   *reinterpret_cast<uint4*>(d + 512) = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
+}
+
+// The same straight from global memory, through registers: warp `half` has
+// the columns 2 half and 2 half + 1, so two rows of a block per thread. Rows
+// that do not exist read the last one that does (their operand rows are
+// zero). Where the weights stream from HBM this beats the tensor copies, whose
+// 16-byte rows cost about as much time as 128-byte ones (1x34816x5120: 22.4 ->
+// 19.3 us); in the kernel for many rows its latency is in the way (258 -> 374
+// us at 4096x34816x5120).
+struct ScaleRows {
+  const uint8_t* p[2];
+  __device__ __forceinline__ void at(const uint8_t* scales, int row0, int rows, int pitch, int half, int lane) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      p[e] = scales + static_cast<long long>(min(row0 + 64 * half + 32 * e + lane, rows - 1)) * pitch;
+  }
+  __device__ __forceinline__ void load(int stage, uint4 (&v)[2]) const {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) v[e] = __ldg(reinterpret_cast<const uint4*>(p[e] + static_cast<long long>(stage) * 16));
+  }
+};
+__device__ __forceinline__ void put_scale_rows(uint8_t* block, int half, int lane, const uint4 (&v)[2]) {
+  const uint32_t a[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, b[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint2*>(block + 512 * j + lane * 16 + half * 8) = make_uint2(scales_no_sign(a[j]), scales_no_sign(b[j]));
 }
 // Copy one rearranged 64-K step (at saddr) into 4 columns.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) { return sdesc(saddr, 16, 128, 0); }

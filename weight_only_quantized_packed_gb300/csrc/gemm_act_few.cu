@@ -9,7 +9,7 @@
 // Both operands go from global to shared memory as they lie (128-byte rows,
 // 128-byte swizzle) and into the tensor core undecoded.
 //  * 4 bits: the tensor core multiplies each 16-K product sum by both scales;
-//    two warps bring a stage's scales into the order it reads them in and the
+//    two warps bring a stage's scales, in the order it reads them in, and the
 //    MMA warp copies them to tensor memory. One accumulator for all of K.
 //  * 8 bits: one MMA group per 128 K; the epilogue reads it and adds it, times
 //    its two scales, to FP32 accumulators in registers.
@@ -30,8 +30,8 @@ constexpr int kThreads = 256;
 constexpr int kEpiWarp0 = 4;
 
 struct FewParams {
-  const float* SA;      // 8 bits: float [M, K/128]
-  const float* SW;      // 8 bits: float [ceil(N/128), K/128]
+  const void* SA;
+  const void* SW;
   float gscale;
   uint16_t* C;
   int M, N, K, ldc;
@@ -51,7 +51,7 @@ struct FewLayout {
   static constexpr int kRecv = kFac + (F::kScaled ? 0 : 4 * NT * 4);
   static constexpr int kBytes = kRecv + (NT + 7) * 128 * 4;
   static constexpr int kAlloc = kBytes + 1024;                            // slack for 1024-byte alignment
-  static constexpr int kStageBytes = 16384 + NT * 128 + (F::kScaled ? kScaleBlock + NT * 16 : 0);
+  static constexpr int kStageBytes = 16384 + NT * 128;
   // Tensor memory: the accumulators, then (4 bits) two sets of a stage's
   // scales, 4 columns per step and operand.
   static constexpr int kCols = F::kScaled ? (NT + 64 <= 128 ? 128 : 256) : (kAcc * NT <= 64 ? 64 : (kAcc * NT <= 128 ? 128 : 256));
@@ -61,8 +61,7 @@ struct FewLayout {
 
 template <class F, int NT>
 __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
-    few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
-               const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSA, FewParams p) {
+    few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA, FewParams p) {
   using L = FewLayout<F, NT>;
   constexpr int S = L::kS, NACC = L::kAcc;
   extern __shared__ uint8_t smem_raw[];
@@ -105,9 +104,10 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
   pdl_launch_dependents();
   if (splits > 1) cluster_arrive_relaxed();      // matched before the first push
 
-  int issued = 0;                                // stages whose copies lane 0 of warp 0 started
+  // Copies and MMAs are issued under elect.sync (see gemm_act_many.cu).
+  int issued = 0;                                // stages whose copies this thread started
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       prefetch_tmap(&tmW);
       prefetch_tmap(&tmA);
       const uint64_t pol = policy_evict_first();
@@ -115,12 +115,10 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
         const int s = t % S;
         mbar_arrive_expect_tx(full + 8 * s, L::kStageBytes);
         tma_load_2d_hint(sb + L::kW + s * 16384, &tmW, (st0 + t) * 128, n0, full + 8 * s, pol);
-        if (F::kScaled) tma_load_2d_hint(sb + L::kSclW + s * kScaleBlock, &tmSW, (st0 + t) * 16, n0, full + 8 * s, pol);
       };
       auto load_a = [&](int t) {
         const int s = t % S;
         tma_load_2d(sb + L::kA + s * NT * 128, &tmA, (st0 + t) * 128, m0, full + 8 * s);
-        if (F::kScaled) tma_load_2d(sb + L::kSclA + s * kScaleBlock, &tmSA, (st0 + t) * 16, m0, full + 8 * s);
       };
       // The weights do not depend on the previous grid; the activations may.
       const int ahead = min(S, nst);
@@ -173,21 +171,38 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
     if (last >= 0) mbar_wait(empty + 8 * (last % S), (last / S) & 1, p.err);
   } else if (warp < kEpiWarp0) {
     if constexpr (F::kScaled) {
-      for (int t = 0; t < nst; ++t) {
-        const int s = t % S;
-        const bool ok = wait_or_abort(full + 8 * s, (t / S) & 1, p.err, abort_flag);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        uint8_t* bw = smem + L::kSclW + s * kScaleBlock;
-        uint8_t* ba = smem + L::kSclA + s * kScaleBlock;
-        uint2 vw[4], va[4];
-        take_scales(bw, warp - 2, lane, 128, vw);
-        take_scales(ba, warp - 2, lane, NT, va);
-        asm volatile("bar.sync 1, 64;" ::: "memory");
-        put_scales(bw, warp - 2, lane, vw);
-        put_scales(ba, warp - 2, lane, va);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(scaled + 8 * s);
+      // Four stages' scales are on their way at a time.
+      constexpr int D = 4;
+      const int half = warp - 2, pitch = p.K >> 4;
+      ScaleRows rw, ra;
+      rw.at(static_cast<const uint8_t*>(p.SW), n0, p.N, pitch, half, lane);
+      ra.at(static_cast<const uint8_t*>(p.SA), m0, p.M, pitch, half, lane);
+      const bool any = 64 * half < NT;           // this warp's activation columns exist
+      uint4 vw[D][2], va[D][2];
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        if (d < nst) rw.load(st0 + d, vw[d]);
+      pdl_wait();
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        if (d < nst && any) ra.load(st0 + d, va[d]);
+      for (int t0 = 0; t0 < nst; t0 += D) {        // after an abort: to the end, without waiting
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          const int t = t0 + d, s = t % S;
+          if (t < nst) {
+            if (t >= S) wait_or_abort(empty + 8 * s, ((t / S) - 1) & 1, p.err, abort_flag);
+            put_scale_rows(smem + L::kSclW + s * kScaleBlock, half, lane, vw[d]);
+            if (any) put_scale_rows(smem + L::kSclA + s * kScaleBlock, half, lane, va[d]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(scaled + 8 * s);
+            if (t + D < nst) {
+              rw.load(st0 + t + D, vw[d]);
+              if (any) ra.load(st0 + t + D, va[d]);
+            }
+          }
+        }
       }
     }
   } else {
@@ -215,12 +230,12 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
       // group's are fetched while the group before it is added.
       constexpr int kPer = (NT + 31) / 32;
       const int kb = p.K >> 7;
-      const float* sw = p.SW + static_cast<long long>(tile) * kb + st0;
+      const float* sw = static_cast<const float*>(p.SW) + static_cast<long long>(tile) * kb + st0;
       const float* sa[kPer];
       float next[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        sa[i] = p.SA + static_cast<long long>(min(m0 + 32 * i + lane, p.M - 1)) * kb + st0;
+        sa[i] = static_cast<const float*>(p.SA) + static_cast<long long>(min(m0 + 32 * i + lane, p.M - 1)) * kb + st0;
       float* fac = reinterpret_cast<float*>(smem + L::kFac) + q * NT;
       pdl_wait();
 #pragma unroll
@@ -277,10 +292,10 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
     tmem_dealloc(tmem, L::kCols);
   }
   const bool failed = *abort_flag != 0;
-  if (failed && warp == 0 && lane == 0)          // no copy may still be in flight when the CTA exits
+  if (failed)                                    // no copy may still be in flight when the CTA exits
     for (int t = max(0, issued - S); t < issued; ++t) mbar_wait(full + 8 * (t % S), (t / S) & 1, p.err);
+  __syncwarp();
   if (splits > 1) {
-    __syncwarp();
     cluster_sync();                              // the pushes are in place
     const int per = (NT + splits - 1) / splits;
     const int rows = min(NT, p.M - m0);
@@ -300,31 +315,18 @@ template <class F, int NT>
 cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
   using L = FewLayout<F, NT>;
   const uint64_t row = F::kScaled ? static_cast<uint64_t>(a.K) / 2 : static_cast<uint64_t>(a.K);
-  CUtensorMap mw, ma, msw, msa;
+  CUtensorMap mw, ma;
   cudaError_t e = cached_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.W, row, static_cast<uint64_t>(a.N), row, 128, 128,
                                 CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
   e = make_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, row, static_cast<uint64_t>(a.M), row, 128, NT,
                   CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
-  msw = mw;
-  msa = ma;
-  if (F::kScaled) {
-    const uint64_t srow = static_cast<uint64_t>(a.K) / 16;
-    e = cached_map_2d(&msw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.SW, srow, static_cast<uint64_t>(a.N), srow, 16, 128,
-                      CU_TENSOR_MAP_SWIZZLE_NONE);
-    if (e != cudaSuccess) return e;
-    e = make_map_2d(&msa, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.SA, srow, static_cast<uint64_t>(a.M), srow, 16, NT,
-                    CU_TENSOR_MAP_SWIZZLE_NONE);
-    if (e != cudaSuccess) return e;
-  }
   static AttrLatch latch;
   if (e = set_smem_attrs(few_kernel<F, NT>, latch, L::kAlloc, true); e != cudaSuccess) return e;
   FewParams p = {};
-  if (!F::kScaled) {
-    p.SA = static_cast<const float*>(a.SA);
-    p.SW = static_cast<const float*>(a.SW);
-  }
+  p.SA = a.SA;
+  p.SW = a.SW;
   p.gscale = a.gscale;
   p.C = static_cast<uint16_t*>(a.C);
   p.M = a.M;
@@ -335,7 +337,7 @@ cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
   p.err = a.err;
   const int tiles = (a.N + 127) / 128, mt = (a.M + NT - 1) / NT;
   p.splits = 1;
-  for (int sp = 2; sp <= 8 && sp <= p.stages && static_cast<long long>(sp) * tiles * mt <= L::kCtas * a.num_sms; ++sp)
+  for (int sp = 2; sp <= 4 && sp <= p.stages && static_cast<long long>(sp) * tiles * mt <= L::kCtas * a.num_sms; ++sp)
     p.splits = sp;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles * p.splits, mt);
@@ -351,7 +353,7 @@ cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.pdl ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, few_kernel<F, NT>, mw, ma, msw, msa, p);
+  return cudaLaunchKernelEx(&cfg, few_kernel<F, NT>, mw, ma, p);
 }
 
 template <class F>

@@ -59,10 +59,13 @@ struct ManyLayout {
   static_assert(kAlloc <= 227 * 1024 - 1024, "shared memory");
 };
 
-// Tile i of the walk: groups of 8 row tiles go through all weight tiles, row
-// tiles first, so that the tiles in flight share both operands in L2.
+// Tile i of the walk: groups of G row tiles go through all weight tiles, row
+// tiles first, so that the tiles in flight share both operands in L2. A group
+// is as many bytes in either format (4096x34816x5120, 4 bits: 261 us at G = 8,
+// 254 at 16; 4096x5120x17408, 8 bits: 305 us at 8, 310 at 16).
+template <class F>
 __device__ __forceinline__ void tile_at(int i, int mt, int nt, int& m, int& n) {
-  constexpr int G = 8;
+  constexpr int G = F::kScaled ? 16 : 8;
   const int per = G * nt;
   const int g = i / per, rows = min(G, mt - g * G);
   const int j = i - g * per;
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       uint32_t ph = 1;                         // parity of the stage's last consumption
       for (int i = first; i < total && !*abort_flag; i += step) {
         int mi, ni;
-        tile_at(i, p.mt, p.nt, mi, ni);
+        tile_at<F>(i, p.mt, p.nt, mi, ni);
         const int m0 = mi * 256 + rank * 128, n0 = ni * BN;
         for (int k = 0; k < p.stages; ++k) {
           if (used == S) {
@@ -254,7 +257,7 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
     uint32_t ph = 0;
     for (int i = first; i < total; i += step) {
       int mi, ni;
-      tile_at(i, p.mt, p.nt, mi, ni);
+      tile_at<F>(i, p.mt, p.nt, mi, ni);
       const int m0 = mi * 256 + rank * 128 + q * 32, n0 = ni * BN + h * COLS;
       uint32_t packed[COLS / 2];
       if constexpr (F::kScaled) {
@@ -418,9 +421,19 @@ cudaError_t launch_many_t(const ActGemmArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, many_kernel<F, BN>, ma, mb, msa, msb, mc, p);
 }
 
+// Width of the weight tiles: the pairs take whole rounds of tiles, and a round
+// takes a time proportional to BN + 200 (operand bytes go with BN + 256, MMAs
+// with BN). Measured, BN = 256 | 192 | 128, us: 4 bits 333x7168x5120 13.3 | 12.0
+// | 17.2, 2048x5120x5120 30.5 | 26.2 | 35.5, 4096x34816x5120 254 | 284 | 359;
+// 8 bits 333x7168x5120 20.3 | 18.2 | 27.8, 4096x5120x17408 299 | 316 | 395.
 template <class F>
 cudaError_t launch_many(const ActGemmArgs& a, cudaStream_t s) {
-  return launch_many_t<F, 256>(a, s);
+  const long long mt = (a.M + 255) / 256, pairs = a.num_sms / 2;
+  const auto cost = [&](int bn) { return (mt * ((a.N + bn - 1) / bn) + pairs - 1) / pairs * (bn + 200); };
+  const long long c256 = cost(256), c192 = cost(192), c128 = cost(128);
+  if (c256 <= c192 && c256 <= c128) return launch_many_t<F, 256>(a, s);
+  if (c192 <= c128) return launch_many_t<F, 192>(a, s);
+  return launch_many_t<F, 128>(a, s);
 }
 
 }  // namespace
