@@ -255,170 +255,177 @@ def w8a16_gemm_tc(A, W, scales, N: int, K: int, out=None, stream=None):
     return C
 
 
-_DTYPES = None           # torch dtype -> wqp_dtype, set on first use
+_DTYPES = {}             # torch dtype -> wqp_dtype, filled on first use
+_torch = None
 
 
-def _typed_rows(name, x, K=None, like=None):
-    """Rows [M, K] with unit column stride: their (pitch, wqp_dtype)."""
-    global _DTYPES
-    if _DTYPES is None:
+def _load_torch():
+    """torch, once: an import statement on every call costs a tenth of a launch."""
+    global _torch
+    if _torch is None:
         import torch
 
-        _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-    if x.dtype not in _DTYPES:
+        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+        _torch = torch
+    return _torch
+
+
+def _typed_rows(name, x):
+    """Rows [M, K] with unit column stride: (pitch, wqp_dtype, M, K)."""
+    if not x.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
+    dt = _DTYPES.get(x.dtype)
+    if dt is None:
         raise TypeError(f"{name} must be torch.bfloat16, float16 or float32")
-    if x.dim() != 2 or x.stride(1) != 1 or (K is not None and x.shape[1] != K):
-        raise ValueError(f"{name} must be [M, {'K' if K is None else K}] with unit column stride")
-    if like is not None and (x.shape != like.shape or x.dtype is not like.dtype):
-        raise ValueError(f"{name} must have the shape and type of x")
-    return (x.shape[1] if x.shape[0] <= 1 else x.stride(0)), _DTYPES[x.dtype]
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be [M, K] with unit column stride")
+    return (stride[0] if shape[0] > 1 else shape[1]), dt, shape[0], shape[1]
+
+
+def _rows_like(name, t, x):
+    """The pitch of rows with the shape and type of x."""
+    if not t.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not x.dtype or shape != x.shape or (stride[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must have the shape and type of x, with unit column stride")
+    return stride[0] if shape[0] > 1 else shape[1]
 
 
 def _packed(name, t, shape, dtype):
-    """A contiguous tensor of a packed format."""
+    """A contiguous tensor of a packed format; its address."""
+    if not t.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} tensor")
+    return t.data_ptr()
 
 
-def _weights(W, w_scales, codes, scales, dtype):
-    """Packed weights: their types and sizes (any shape, as the GEMV entries take them)."""
-    import torch
+def _weights(name, t, count, dtype):
+    """Packed weights or their scales (any shape, as the GEMV entries take them); their address."""
+    if not t.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.numel() != count or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {count} contiguous values")
+    return t.data_ptr()
 
-    if W.dtype is not torch.uint8 or w_scales.dtype is not dtype:
-        raise TypeError(f"W must be torch.uint8 and w_scales {dtype}")
-    if W.numel() != codes or w_scales.numel() != scales or not (W.is_contiguous() and w_scales.is_contiguous()):
-        raise ValueError(f"W must hold {codes} contiguous bytes and w_scales {scales} contiguous values")
 
-
-def _codes_out(x, shapes, dtypes, out):
-    import torch
-
+def _codes_out(x, codes_shape, scales_shape, scales_dtype, out):
+    """(codes, scales) and their addresses, new or the caller's."""
     if out is None:
-        return tuple(torch.empty(s, dtype=d, device=x.device) for s, d in zip(shapes, dtypes))
+        codes = _torch.empty(codes_shape, dtype=_torch.uint8, device=x.device)
+        scales = _torch.empty(scales_shape, dtype=scales_dtype, device=x.device)
+        return codes, scales, codes.data_ptr(), scales.data_ptr()
     codes, scales = out
-    _need_cuda(codes, scales)
-    _packed("out codes", codes, shapes[0], dtypes[0])
-    _packed("out scales", scales, shapes[1], dtypes[1])
-    return codes, scales
+    return (codes, scales, _packed("out codes", codes, codes_shape, _torch.uint8),
+            _packed("out scales", scales, scales_shape, scales_dtype))
 
 
 def w4_quantize(x, global_scale: float = 1.0, out=None, stream=None):
     """Rows x [M, K] (bfloat16, float16 or float32) to the W4A16 format: uint8 codes [M, K/2] and
     uint8 E4M3 scales [M, K/16], under one global_scale. out: (codes, scales) to write to."""
-    import torch
-
-    _need_cuda(x)
-    ldx, dt = _typed_rows("x", x)
-    M, K = x.shape
-    codes, scales = _codes_out(x, ((M, K // 2), (M, K // 16)), (torch.uint8, torch.uint8), out)
-    _check(lib().w4_quantize(_ptr(x), ldx, dt, float(global_scale), _ptr(codes), _ptr(scales), M, K,
-                             _stream(stream)), "w4_quantize")
+    torch = _torch or _load_torch()
+    ldx, dt, M, K = _typed_rows("x", x)
+    codes, scales, pc, ps = _codes_out(x, (M, K // 2), (M, K // 16), torch.uint8, out)
+    _check(lib().w4_quantize(x.data_ptr(), ldx, dt, global_scale, pc, ps, M, K, _stream(stream)), "w4_quantize")
     return codes, scales
 
 
 def a8_quantize(x, out=None, stream=None):
     """Rows x [M, K] (bfloat16, float16 or float32) to uint8 E4M3 codes [M, K] with float32 scales
     [M, K/128]. out: (codes, scales) to write to."""
-    import torch
-
-    _need_cuda(x)
-    ldx, dt = _typed_rows("x", x)
-    M, K = x.shape
-    codes, scales = _codes_out(x, ((M, K), (M, K // 128)), (torch.uint8, torch.float32), out)
-    _check(lib().a8_quantize(_ptr(x), ldx, dt, _ptr(codes), _ptr(scales), M, K, _stream(stream)), "a8_quantize")
+    torch = _torch or _load_torch()
+    ldx, dt, M, K = _typed_rows("x", x)
+    codes, scales, pc, ps = _codes_out(x, (M, K), (M, K // 128), torch.float32, out)
+    _check(lib().a8_quantize(x.data_ptr(), ldx, dt, pc, ps, M, K, _stream(stream)), "a8_quantize")
     return codes, scales
 
 
 def _norm_args(x, weight, residual, residual_out):
-    """(ldx, dtype, ldr, residual_out, ldro) of a norm call, its arguments checked."""
-    import torch
-
-    _need_cuda(x, weight, residual, residual_out)
-    ldx, dt = _typed_rows("x", x)
-    if weight.dtype is not x.dtype or tuple(weight.shape) != (x.shape[1],) or not weight.is_contiguous():
-        raise ValueError(f"weight must be a contiguous [{x.shape[1]}] tensor of x's type")
+    """(residual's address and pitch, residual_out, its address and pitch, weight's address)."""
+    K = x.shape[1]
+    if not weight.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
+    if weight.dtype is not x.dtype or weight.shape != (K,) or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous [{K}] tensor of x's type")
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out without residual")
-        return ldx, dt, 0, None, 0
-    ldr, _ = _typed_rows("residual", residual, like=x)
+        return None, 0, None, None, 0, weight.data_ptr()
+    ldr = _rows_like("residual", residual, x)
     if residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    ldro, _ = _typed_rows("residual_out", residual_out, like=x)
-    return ldx, dt, ldr, residual_out, ldro
+        residual_out, ldh = _torch.empty(x.shape, dtype=x.dtype, device=x.device), K
+    else:
+        ldh = ldr if residual_out is residual else _rows_like("residual_out", residual_out, x)
+    return residual.data_ptr(), ldr, residual_out, residual_out.data_ptr(), ldh, weight.data_ptr()
 
 
 def rms_norm(x, weight, eps: float, residual=None, residual_out=None, out=None, stream=None):
     """(y, h): h = x + residual, y = h * rsqrt(mean(h^2) + eps) * weight, in x's type (bfloat16,
     float16 or float32). Without a residual h is None. residual_out may be the residual itself."""
-    import torch
-
-    ldx, dt, ldr, h, ldh = _norm_args(x, weight, residual, residual_out)
-    M, K = x.shape
+    torch = _torch or _load_torch()
+    ldx, dt, M, K = _typed_rows("x", x)
+    pr, ldr, h, ph, ldh, pw = _norm_args(x, weight, residual, residual_out)
     if out is None:
-        out = torch.empty((M, K), dtype=x.dtype, device=x.device)
-    _need_cuda(out)
-    ldy, _ = _typed_rows("out", out, like=x)
-    _check(lib().rms_norm(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), float(eps), _ptr(h), ldh, _ptr(out), ldy,
-                          dt, M, K, _stream(stream)), "rms_norm")
+        out, ldy = torch.empty((M, K), dtype=x.dtype, device=x.device), K
+    else:
+        ldy = _rows_like("out", out, x)
+    _check(lib().rms_norm(x.data_ptr(), ldx, pr, ldr, pw, eps, ph, ldh, out.data_ptr(), ldy, dt, M, K,
+                          _stream(stream)), "rms_norm")
     return out, h
 
 
 def rms_norm_a8(x, weight, eps: float, residual=None, residual_out=None, out=None, stream=None):
     """(codes, scales, h): rms_norm with y written as a8_quantize writes it. out: (codes, scales)."""
-    import torch
-
-    ldx, dt, ldr, h, ldh = _norm_args(x, weight, residual, residual_out)
-    M, K = x.shape
-    codes, scales = _codes_out(x, ((M, K), (M, K // 128)), (torch.uint8, torch.float32), out)
-    _check(lib().rms_norm_a8(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), float(eps), _ptr(h), ldh, _ptr(codes),
-                             _ptr(scales), dt, M, K, _stream(stream)), "rms_norm_a8")
+    torch = _torch or _load_torch()
+    ldx, dt, M, K = _typed_rows("x", x)
+    pr, ldr, h, ph, ldh, pw = _norm_args(x, weight, residual, residual_out)
+    codes, scales, pc, ps = _codes_out(x, (M, K), (M, K // 128), torch.float32, out)
+    _check(lib().rms_norm_a8(x.data_ptr(), ldx, pr, ldr, pw, eps, ph, ldh, pc, ps, dt, M, K, _stream(stream)),
+           "rms_norm_a8")
     return codes, scales, h
 
 
 def _gemm_out(A, M, N, out):
-    import torch
-
     if out is None:
-        return torch.empty((M, N), dtype=torch.bfloat16, device=A.device), N
-    _need_cuda(out)
-    if out.dtype is not torch.bfloat16:
+        return _torch.empty((M, N), dtype=_torch.bfloat16, device=A.device), N
+    if not out.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
+    if out.dtype is not _torch.bfloat16:
         raise TypeError("out must be torch.bfloat16")
-    if tuple(out.shape) != (M, N) or out.stride(1) != 1 and N > 1:
+    stride = out.stride()
+    if out.shape != (M, N) or (stride[1] != 1 and N > 1):
         raise ValueError(f"out must be [{M}, {N}] with unit column stride")
-    return out, (N if M <= 1 else out.stride(0))
+    return out, (stride[0] if M > 1 else N)
 
 
 def w4a4_gemm(A, a_scales, W, w_scales, N: int, K: int, a_global: float = 1.0, w_global: float = 1.0, out=None,
               stream=None):
     """C[M, N] = dequant(A) @ dequant(W)^T, both in the W4A16 format (w4_quantize), any M, K % 256 == 0."""
-    import torch
-
-    _need_cuda(A, a_scales, W, w_scales)
-    M = A.shape[0]
-    _packed("A", A, (M, K // 2), torch.uint8)
-    _packed("a_scales", a_scales, (M, K // 16), torch.uint8)
-    _weights(W, w_scales, N * (K // 2), N * (K // 16), torch.uint8)
+    torch = _torch or _load_torch()
+    M, u8 = A.shape[0], torch.uint8
+    pa, psa = _packed("A", A, (M, K // 2), u8), _packed("a_scales", a_scales, (M, K // 16), u8)
+    pw, psw = _weights("W", W, N * (K // 2), u8), _weights("w_scales", w_scales, N * (K // 16), u8)
     C, ldc = _gemm_out(A, M, N, out)
-    _check(lib().w4a4_gemm(_ptr(A), _ptr(a_scales), float(a_global), _ptr(W), _ptr(w_scales), float(w_global), _ptr(C),
-                           ldc, M, N, K, _stream(stream)), "w4a4_gemm")
+    _check(lib().w4a4_gemm(pa, psa, a_global, pw, psw, w_global, C.data_ptr(), ldc, M, N, K, _stream(stream)),
+           "w4a4_gemm")
     return C
 
 
 def w8a8_gemm(A, a_scales, W, w_scales, N: int, K: int, out=None, stream=None):
     """C[M, N] = dequant(A) @ dequant(W)^T: A as a8_quantize and rms_norm_a8 write it, W8A16 weights, any M."""
-    import torch
-
-    _need_cuda(A, a_scales, W, w_scales)
+    torch = _torch or _load_torch()
     M = A.shape[0]
-    _packed("A", A, (M, K), torch.uint8)
-    _packed("a_scales", a_scales, (M, K // 128), torch.float32)
-    _weights(W, w_scales, N * K, (N + 127) // 128 * (K // 128), torch.float32)
+    pa, psa = _packed("A", A, (M, K), torch.uint8), _packed("a_scales", a_scales, (M, K // 128), torch.float32)
+    pw = _weights("W", W, N * K, torch.uint8)
+    psw = _weights("w_scales", w_scales, (N + 127) // 128 * (K // 128), torch.float32)
     C, ldc = _gemm_out(A, M, N, out)
-    _check(lib().w8a8_gemm(_ptr(A), _ptr(a_scales), _ptr(W), _ptr(w_scales), _ptr(C), ldc, M, N, K,
-                           _stream(stream)), "w8a8_gemm")
+    _check(lib().w8a8_gemm(pa, psa, pw, psw, C.data_ptr(), ldc, M, N, K, _stream(stream)), "w8a8_gemm")
     return C
 
 

@@ -258,7 +258,7 @@ int run_norm(bool a8, const void* X, int ldx, const void* R, int ldr, const void
   if (st == WQP_OK) st = a8 ? check_codes(nm, Y, S, 4) : check_pitched(nm, "Y", Y, ldy, K);
   DeviceInfo* dev = nullptr;
   if (st != WQP_OK || (st = device_setup(&dev)) != WQP_OK) return st;
-  const NormArgs a = {X,   R,   W,   H,   Y,   S, eps, dtype, M, K, ldx, ldr, ldh, ldy, dev->num_sms,
+  const NormArgs a = {X,   R,   W,   H,   Y,   S, eps, dtype, M, K, ldx, ldr, ldh, ldy, dev->err, dev->num_sms,
                       g_pdl.load(std::memory_order_relaxed) != 0};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = a8 ? launch_rms_norm_a8(a, s) : launch_rms_norm(a, s);

@@ -85,6 +85,7 @@ struct NormArgs {
   float eps;
   int dtype, M, K;
   int ldx, ldr, ldh, ldy;
+  unsigned* err;        // device error word
   int num_sms;
   bool pdl;
 };
