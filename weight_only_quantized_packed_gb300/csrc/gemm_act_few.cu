@@ -1,10 +1,10 @@
-// Products of quantised activations with packed weights, few rows (the whole
-// call is a small number of column tiles): 4-bit by 4-bit with E4M3 scales
-// per 16 K, and 8-bit by 8-bit with FP32 scales per 128 K.
+// Products of quantised activations with packed weights, few rows: 4-bit by
+// 4-bit with E4M3 scales per 16 K, and 8-bit by 8-bit with FP32 scales per
+// 128 K.
 //
 // Bound by the weights' bytes. Swap-AB: the 128 weight rows of a tile are the
-// MMA's M side and up to NT activation rows, zero-padded by the copies, its
-// N side, so one pass over the weights serves NT rows:
+// MMA's M side and the call's activation rows, zero-padded to NT by the
+// copies, its N side, so one pass over the weights serves them all:
 //   D[n, m] = sum_k W[n, k] A[m, k]      (tcgen05.mma, FP32 accumulators)
 // Both operands go from global to shared memory as they lie (128-byte rows,
 // 128-byte swizzle) and into the tensor core undecoded.
@@ -13,7 +13,7 @@
 //    MMA warp copies them to tensor memory. One accumulator for all of K.
 //  * 8 bits: one MMA group per 128 K; the epilogue reads it and adds it, times
 //    its two scales, to FP32 accumulators in registers.
-// With few tiles, K is split over a cluster of up to 8 CTAs. Rank q owns the
+// With few tiles, K is split over a cluster of up to 4 CTAs. Rank q owns the
 // activation rows q, q + splits, ...; the others push their partial sums of
 // those into its shared memory, and it adds them in rank order, so the result
 // does not depend on timing.
@@ -28,6 +28,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kEpiWarp0 = 4;
+// CTAs of a tile. More than 4 do not all become resident at once (clusters lie
+// within a GPC): 1x5120x5120, 4 bits, up to 8 | 4 | 3 | 2 | 1: 9.4 | 7.5 | 7.3 |
+// 8.0 | 10.3 us.
+constexpr int kMaxSplits = 4;
 
 struct FewParams {
   const void* SA;
@@ -41,7 +45,9 @@ struct FewParams {
 
 template <class F, int NT>
 struct FewLayout {
-  static constexpr int kS = NT <= 32 ? 4 : (NT <= 64 ? 4 : 3);            // stages
+  // Stages: two CTAs of an SM share its memory up to NT = 32, wider ones have
+  // it to themselves.
+  static constexpr int kS = NT == 64 ? 6 : 4;
   static constexpr int kAcc = F::kScaled ? 1 : (NT <= 64 ? 4 : 2);        // accumulator slots
   static constexpr int kW = 0;
   static constexpr int kA = kW + kS * 16384;
@@ -73,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int splits = p.splits;
   const int tile = blockIdx.x / splits, rank = blockIdx.x - tile * splits;
-  const int n0 = tile * 128, m0 = blockIdx.y * NT;
+  const int n0 = tile * 128;
   const int st0 = static_cast<int>(static_cast<long long>(rank) * p.stages / splits);
   const int nst = static_cast<int>(static_cast<long long>(rank + 1) * p.stages / splits) - st0;
   const uint32_t full = smem_u32(full_sh), empty = smem_u32(empty_sh), scaled = smem_u32(scaled_sh);
@@ -118,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
       };
       auto load_a = [&](int t) {
         const int s = t % S;
-        tma_load_2d(sb + L::kA + s * NT * 128, &tmA, (st0 + t) * 128, m0, full + 8 * s);
+        tma_load_2d(sb + L::kA + s * NT * 128, &tmA, (st0 + t) * 128, 0, full + 8 * s);
       };
       // The weights do not depend on the previous grid; the activations may.
       const int ahead = min(S, nst);
@@ -176,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
       const int half = warp - 2, pitch = p.K >> 4;
       ScaleRows rw, ra;
       rw.at(static_cast<const uint8_t*>(p.SW), n0, p.N, pitch, half, lane);
-      ra.at(static_cast<const uint8_t*>(p.SA), m0, p.M, pitch, half, lane);
+      ra.at(static_cast<const uint8_t*>(p.SA), 0, p.M, pitch, half, lane);
       const bool any = 64 * half < NT;           // this warp's activation columns exist
       uint4 vw[D][2], va[D][2];
 #pragma unroll
@@ -226,62 +232,85 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
         }
       }
     } else {
-      // Lane l brings the scales of activation rows l, l + 32, ...; each
-      // group's are fetched while the group before it is added.
-      constexpr int kPer = (NT + 31) / 32;
+      // Lane l brings the scales of activation rows l, l + 32, ..., D groups
+      // ahead of their use: a fetch takes longer than a group.
+      constexpr int kPer = (NT + 31) / 32, D = 4;
       const int kb = p.K >> 7;
       const float* sw = static_cast<const float*>(p.SW) + static_cast<long long>(tile) * kb + st0;
       const float* sa[kPer];
-      float next[kPer];
+      float fa[D][kPer], fw[D];
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        sa[i] = static_cast<const float*>(p.SA) + static_cast<long long>(min(m0 + 32 * i + lane, p.M - 1)) * kb + st0;
+        sa[i] = static_cast<const float*>(p.SA) + static_cast<long long>(min(32 * i + lane, p.M - 1)) * kb + st0;
       float* fac = reinterpret_cast<float*>(smem + L::kFac) + q * NT;
+#pragma unroll
+      for (int d = 0; d < D; ++d) fw[d] = d < nst ? __ldg(sw + d) : 0.0f;
       pdl_wait();
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) next[i] = sa[i][0] * __ldg(sw);
-      for (int t = 0; t < nst; ++t) {
-        const int slot = t % NACC;
-        __syncwarp();
+      for (int d = 0; d < D; ++d)
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          if (32 * i + lane < NT) fac[32 * i + lane] = next[i];
-          if (t + 1 < nst) next[i] = sa[i][t + 1] * __ldg(sw + t + 1);
+        for (int i = 0; i < kPer; ++i) fa[d][i] = d < nst ? sa[i][d] : 0.0f;
+      for (int t0 = 0; t0 < nst && live; t0 += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          const int t = t0 + d, slot = t % NACC;
+          if (t < nst && live) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+              if (32 * i + lane < NT) fac[32 * i + lane] = fa[d][i] * fw[d];
+              if (t + D < nst) fa[d][i] = sa[i][t + D];
+            }
+            if (t + D < nst) fw[d] = __ldg(sw + t + D);
+            __syncwarp();
+            live = __all_sync(0xFFFFFFFFu, wait_or_abort(acc_full + 8 * slot, (t / NACC) & 1, p.err, abort_flag));
+            if (live) {
+              tc_fence_after();
+              // The next 16 columns are on their way while these are added; the
+              // accumulator is free once the last have arrived.
+              uint32_t v[2][16];
+              tmem_ld16_start(tl + slot * NT, v[0]);
+#pragma unroll
+              for (int c = 0; c < NT; c += 16) {
+                uint32_t(&x)[16] = v[(c / 16) & 1];
+                tmem_ld_wait(x);
+                if (c + 16 < NT) {
+                  tmem_ld16_start(tl + slot * NT + c + 16, v[(c / 16 + 1) & 1]);
+                } else {
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(acc_free + 8 * slot);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(__uint_as_float(x[i]), fac[c + i], acc[c + i]);
+              }
+            }
+          }
         }
-        __syncwarp();
-        live = __all_sync(0xFFFFFFFFu, wait_or_abort(acc_full + 8 * slot, (t / NACC) & 1, p.err, abort_flag));
-        if (!live) break;
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < NT; c += 16) {
-          uint32_t v[16];
-          tmem_ld16_start(tl + slot * NT + c, v);
-          tmem_ld_wait(v);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(__uint_as_float(v[i]), fac[c + i], acc[c + i]);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_free + 8 * slot);
       }
     }
-    const int rows = min(NT, p.M - m0);
     if (splits > 1) {
       cluster_wait();
       // Row m goes to rank m % splits, into [source rank][m / splits][weight row].
       const int per = (NT + splits - 1) / splits;
+      const uint32_t dst = sb + L::kRecv + 4 * (rank * per * 128 + r);
+      uint32_t at = 0, to[kMaxSplits];
+#pragma unroll
+      for (int o = 0; o < kMaxSplits; ++o) to[o] = mapa_shared(dst, min(o, splits - 1));
+      int owner = 0;
 #pragma unroll
       for (int m = 0; m < NT; ++m) {
-        if (m < rows && live) {
-          const uint32_t dst = sb + L::kRecv + 4 * ((rank * per + m / splits) * 128 + r);
-          st_dsmem_f32(mapa_shared(dst, m % splits), acc[m]);
+        if (m < p.M && live) {
+          const uint32_t base = owner < 2 ? (owner == 0 ? to[0] : to[1]) : (owner == 2 ? to[2] : to[3]);
+          st_dsmem_f32(base + at, acc[m]);
         }
+        if (++owner == splits) owner = 0, at += 512;
       }
     } else if (live && n0 + r < p.N) {
-      uint16_t* c = p.C + static_cast<long long>(m0) * p.ldc + n0 + r;
+      uint16_t* c = p.C + n0 + r;
 #pragma unroll
       for (int m = 0; m < NT; ++m)
-        if (m < rows) c[static_cast<long long>(m) * p.ldc] = f32_to_bf16_rn(acc[m]);
+        if (m < p.M) c[static_cast<long long>(m) * p.ldc] = f32_to_bf16_rn(acc[m]);
     }
   }
   if (splits > 1 && warp < kEpiWarp0) cluster_wait();
@@ -298,14 +327,13 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
   if (splits > 1) {
     cluster_sync();                              // the pushes are in place
     const int per = (NT + splits - 1) / splits;
-    const int rows = min(NT, p.M - m0);
     const float* recv = reinterpret_cast<const float*>(smem + L::kRecv);
     const int r = threadIdx.x & 127;
     if (!failed && n0 + r < p.N) {
-      for (int i = threadIdx.x >> 7; i * splits + rank < rows; i += kThreads / 128) {
+      for (int i = threadIdx.x >> 7; i * splits + rank < p.M; i += kThreads / 128) {
         float v = recv[i * 128 + r];
         for (int src = 1; src < splits; ++src) v += recv[(src * per + i) * 128 + r];
-        p.C[static_cast<long long>(m0 + i * splits + rank) * p.ldc + n0 + r] = f32_to_bf16_rn(v);
+        p.C[static_cast<long long>(i * splits + rank) * p.ldc + n0 + r] = f32_to_bf16_rn(v);
       }
     }
   }
@@ -335,12 +363,11 @@ cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
   p.ldc = a.ldc;
   p.stages = a.K / F::kStageK;
   p.err = a.err;
-  const int tiles = (a.N + 127) / 128, mt = (a.M + NT - 1) / NT;
+  const int tiles = (a.N + 127) / 128;
   p.splits = 1;
-  for (int sp = 2; sp <= 4 && sp <= p.stages && static_cast<long long>(sp) * tiles * mt <= L::kCtas * a.num_sms; ++sp)
-    p.splits = sp;
+  for (int sp = 2; sp <= kMaxSplits && sp <= p.stages && sp * tiles <= L::kCtas * a.num_sms; ++sp) p.splits = sp;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles * p.splits, mt);
+  cfg.gridDim = dim3(tiles * p.splits);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = L::kAlloc;
   cfg.stream = s;
@@ -356,20 +383,33 @@ cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, few_kernel<F, NT>, mw, ma, p);
 }
 
+// Whether a call is this kernel's. It is where K can be split over the SMs
+// that few tiles leave idle, and always for the fewest rows; else
+// gemm_act_many.cu's wide tiles win. Measured, here | there, us:
+//  * 4 bits: 40x5120x5120 10.5 | 12.3, 64x5120x5120 11.1 | 10.7, 64x34816x5120
+//    29.9 | 26.2, 128x7168x5120 16.8 | 12.0;
+//  * 8 bits: 61x5120x17408 25.2 | 44.6, 64x34816x5120 39.5 | 39.2, 128x5120x17408
+//    34.9 | 46.0, 128x7168x5120 22.3 | 16.8.
+template <class F>
+bool few_fits(const ActGemmArgs& a) {
+  constexpr int kAlways = F::kScaled ? 32 : 64;
+  return a.M <= kAlways || (a.M <= 2 * kAlways && 3 * ((a.N + 127) / 128) <= a.num_sms);
+}
+
 template <class F>
 cudaError_t launch_few(const ActGemmArgs& a, cudaStream_t s) {
   if (a.M <= 16) return launch_few_nt<F, 16>(a, s);
   if (a.M <= 32) return launch_few_nt<F, 32>(a, s);
-  if (a.M <= 64) return launch_few_nt<F, 64>(a, s);
-  return launch_few_nt<F, 128>(a, s);
+  if constexpr (!F::kScaled)
+    if (a.M > 64) return launch_few_nt<F, 128>(a, s);
+  return launch_few_nt<F, 64>(a, s);
 }
 
 }  // namespace
 }  // namespace act
 
-// Up to 128 rows one pass over the weights serves them all; more go to the
-// kernel whose tiles are wider in both directions. Calls of more than 2^20
-// rows go in pieces, so that tile counts stay within an int.
+// Calls of more than 2^20 rows go in pieces, so that tile counts stay within
+// an int.
 template <class F>
 static cudaError_t launch_act_gemm(const ActGemmArgs& a, cudaStream_t s) {
   constexpr int kPiece = 1 << 20;
@@ -381,7 +421,7 @@ static cudaError_t launch_act_gemm(const ActGemmArgs& a, cudaStream_t s) {
     b.A = static_cast<const char*>(a.A) + r * (F::kScaled ? K / 2 : K);
     b.SA = static_cast<const char*>(a.SA) + r * (F::kScaled ? K / 16 : K / 128 * 4);
     b.C = static_cast<char*>(a.C) + r * a.ldc * 2;
-    if (b.M <= 128) e = act::launch_few<F>(b, s);
+    if (act::few_fits<F>(b)) e = act::launch_few<F>(b, s);
     else e = F::kScaled ? launch_w4a4_many(b, s) : launch_w8a8_many(b, s);
     if (a.M - r0 <= kPiece) break;
   }
