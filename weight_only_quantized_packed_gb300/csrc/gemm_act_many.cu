@@ -336,11 +336,21 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
         for (int j = 0; j < 4; ++j)
           *reinterpret_cast<uint4*>(out + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
               make_uint4(packed[c / 2 + 4 * j], packed[c / 2 + 4 * j + 1], packed[c / 2 + 4 * j + 2], packed[c / 2 + 4 * j + 3]);
-        if (p.vec) {
+        // A tensor store writes whole 16-byte units, past the end of the row too:
+        // its map ends at the last whole unit, and the few columns after that are
+        // stored by themselves.
+        if (p.vec && n0 + c < p.N) {
           fence_proxy_async_smem();
           __syncwarp();
-          if (elect_one() && m0 < p.M && n0 + c < p.N) tma_store_2d(&tmC, n0 + c, m0, smem_u32(out));
-        } else {
+          const int whole = p.N & ~7;
+          if (elect_one() && m0 < p.M && n0 + c < whole) tma_store_2d(&tmC, n0 + c, m0, smem_u32(out));
+          const int rest = whole - (n0 + c);   // column of the chunk where they begin
+          if (rest >= 0 && rest < 32 && m0 + lane < p.M)
+            for (int e = 0; whole + e < p.N; ++e)
+              p.C[static_cast<long long>(m0 + lane) * p.ldc + whole + e] =
+                  *reinterpret_cast<const uint16_t*>(out + lane * 64 + (((rest >> 3) ^ ((lane >> 1) & 3)) << 4) + e * 2);
+          __syncwarp();
+        } else if (n0 + c < p.N) {
           __syncwarp();
           const int n = n0 + c + lane;
           for (int r = 0; r < 32 && m0 + r < p.M; ++r) {
@@ -378,10 +388,10 @@ cudaError_t launch_many_t(const ActGemmArgs& a, cudaStream_t s) {
     if (e == cudaSuccess) e = make_map_2d(&msa, kU8, a.SA, srow, M, srow, 16, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e == cudaSuccess) e = cached_map_2d(&msb, kU8, a.SW, srow, N, srow, 16, BN, CU_TENSOR_MAP_SWIZZLE_NONE);
   }
-  const bool vec = a.ldc % 8 == 0 && reinterpret_cast<uintptr_t>(a.C) % 16 == 0;
+  const bool vec = a.N >= 8 && a.ldc % 8 == 0 && reinterpret_cast<uintptr_t>(a.C) % 16 == 0;
   mc = ma;
   if (e == cudaSuccess && vec)
-    e = make_map_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.C, N, M, static_cast<uint64_t>(a.ldc) * 2, 32, 32,
+    e = make_map_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.C, N & ~uint64_t(7), M, static_cast<uint64_t>(a.ldc) * 2, 32, 32,
                     CU_TENSOR_MAP_SWIZZLE_64B);
   static AttrLatch latch;
   if (e == cudaSuccess) e = set_smem_attrs(many_kernel<F, BN>, latch, L::kAlloc, true);
