@@ -424,3 +424,12 @@ def test_binding_refuses():
             call()
     assert wqp.w4a4_gemm(c[:0], s[:0], c, s, 4, 256).shape == (0, 4)
     assert wqp.rms_norm(x[:0], w, 1e-6)[0].shape == (0, 256) and wqp.w4_quantize(x[:0])[0].shape == (0, 128)
+
+
+def test_example_runs():
+    """The example's block with quantised activations is near the one without: E2M1 rows and weights keep about
+    three significant bits, so their product over many K is a few percent to a tenth off."""
+    import examples.quantised_ffn as ex
+
+    found = ex.main(["--hidden", "512", "--ffn", "1024", "--rows", "1,200"])
+    assert [f[0] for f in found] == [1, 200] and all(f[1] < 0.25 for f in found)
