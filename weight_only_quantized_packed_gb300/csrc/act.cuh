@@ -189,22 +189,24 @@ constexpr int kScaleBlock = 2048;      // bytes of a 128-row block
 __device__ __forceinline__ uint32_t scales_no_sign(uint32_t w) { return w | (((w & 0x80808080u) >> 7) * 0x7Fu); }
 
 // A block that a tensor copy brought as rows of 16 bytes, rearranged in place
-// by two warps: `half` (0, 1) does the steps 2 half and 2 half + 1, and both
-// have loaded (take) before either stores (put). Only the first `rows` rows
-// of the block exist.
-__device__ __forceinline__ void take_scales(const uint8_t* block, int half, int lane, int rows, uint2 (&v)[4]) {
+// by one warp. Only the first `rows` rows of the block exist.
+__device__ __forceinline__ void rearrange_scales(uint8_t* block, int lane, int rows) {
+  uint4 v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[i] = make_uint2(0, 0);
-    if (32 * i + lane < rows) v[i] = *reinterpret_cast<const uint2*>(block + (32 * i + lane) * 16 + 8 * half);
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (32 * i + lane < rows) v[i] = *reinterpret_cast<const uint4*>(block + (32 * i + lane) * 16);
     v[i].x = scales_no_sign(v[i].x);
     v[i].y = scales_no_sign(v[i].y);
+    v[i].z = scales_no_sign(v[i].z);
+    v[i].w = scales_no_sign(v[i].w);
   }
-}
-__device__ __forceinline__ void put_scales(uint8_t* block, int half, int lane, const uint2 (&v)[4]) {
-  uint8_t* d = block + half * 1024 + lane * 16;
+  __syncwarp();
+  uint8_t* d = block + lane * 16;
   *reinterpret_cast<uint4*>(d) = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
   *reinterpret_cast<uint4*>(d + 512) = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
+  *reinterpret_cast<uint4*>(d + 1024) = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
+  *reinterpret_cast<uint4*>(d + 1536) = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
 }
 
 // The same straight from global memory, through registers: warp `half` has

@@ -18,7 +18,7 @@
 // those into its shared memory, and it adds them in rank order, so the result
 // does not depend on timing.
 //
-// Warps: 0 copies, 1 MMA (and tensor memory), 2..3 scales (4 bits), 4..7
+// Warps: 0 copies, 1 MMA (and tensor memory), 2..3 scales (4 bits), the rest
 // epilogue (lane quarter = warp % 4).
 #include "act.cuh"
 
@@ -26,7 +26,6 @@ namespace wqp {
 namespace act {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kEpiWarp0 = 4;
 // CTAs of a tile. More than 4 do not all become resident at once (clusters lie
 // within a GPC): 1x5120x5120, 4 bits, up to 8 | 4 | 3 | 2 | 1: 9.4 | 7.5 | 7.3 |
@@ -43,11 +42,18 @@ struct FewParams {
   unsigned* err;
 };
 
-template <class F, int NT>
+// kShared: two CTAs of an SM share its memory (NT = 16, 8 bits NT = 32, and 8
+// bits NT = 64 where there are more tiles than SMs: 64x34816x5120 33.1 us against
+// 39.5); otherwise a CTA has it to itself.
+template <class F, int NT, bool kShared>
 struct FewLayout {
-  // Stages: two CTAs of an SM share its memory up to NT = 32, wider ones have
-  // it to themselves.
-  static constexpr int kS = NT == 64 ? 6 : 4;
+  // Epilogue warps: one per lane quarter, or two with half the columns each
+  // where one's time per 128 K would be the longest (61x5120x17408: 25.2 us
+  // with one).
+  static constexpr int kEpi = NT >= 64 ? 8 : 4;
+  static constexpr int kCols = NT * 4 / kEpi;
+  static constexpr int kThreads = (kEpiWarp0 + kEpi) * 32;
+  static constexpr int kS = kShared ? (NT == 64 ? 3 : 4) : (NT == 128 ? 4 : 6);   // stages
   static constexpr int kAcc = F::kScaled ? 1 : (NT <= 64 ? 4 : 2);        // accumulator slots
   static constexpr int kW = 0;
   static constexpr int kA = kW + kS * 16384;
@@ -60,15 +66,16 @@ struct FewLayout {
   static constexpr int kStageBytes = 16384 + NT * 128;
   // Tensor memory: the accumulators, then (4 bits) two sets of a stage's
   // scales, 4 columns per step and operand.
-  static constexpr int kCols = F::kScaled ? (NT + 64 <= 128 ? 128 : 256) : (kAcc * NT <= 64 ? 64 : (kAcc * NT <= 128 ? 128 : 256));
-  static constexpr int kCtas = kAlloc + 2048 <= 114 * 1024 && kCols <= 256 ? 2 : 1;   // per SM
+  static constexpr int kTmem = F::kScaled ? (NT + 64 <= 128 ? 128 : 256) : (kAcc * NT <= 64 ? 64 : (kAcc * NT <= 128 ? 128 : 256));
+  static constexpr int kCtas = kShared ? 2 : 1;                           // per SM
+  static_assert(!kShared || (kAlloc + 2048 <= 114 * 1024 && kTmem <= 256), "two CTAs of an SM");
   static_assert(kAlloc <= 227 * 1024, "shared memory");
 };
 
-template <class F, int NT>
-__global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
+template <class F, int NT, bool kShared>
+__global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout<F, NT, kShared>::kCtas)
     few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA, FewParams p) {
-  using L = FewLayout<F, NT>;
+  using L = FewLayout<F, NT, kShared>;
   constexpr int S = L::kS, NACC = L::kAcc;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_sh[S], empty_sh[S], scaled_sh[S], acc_full_sh[NACC], acc_free_sh[NACC];
@@ -94,13 +101,13 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
     }
     for (int i = 0; i < NACC; ++i) {
       mbar_init(acc_full + 8 * i, 1);
-      mbar_init(acc_free + 8 * i, 4);
+      mbar_init(acc_free + 8 * i, L::kEpi);
     }
     abort_sh = 0;
     mbar_fence_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&tmem_sh), L::kCols);
+    tmem_alloc(smem_u32(&tmem_sh), L::kTmem);
     tmem_relinquish();
     tc_fence_before();
   }
@@ -212,18 +219,19 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
       }
     }
   } else {
-    const int q = warp & 3, r = q * 32 + lane;
-    const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    float acc[NT];
+    constexpr int COLS = L::kCols;
+    const int q = warp & 3, r = q * 32 + lane, c0 = (warp - kEpiWarp0) / 4 * COLS;   // its first activation row
+    const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + c0;
+    float acc[COLS];
 #pragma unroll
-    for (int m = 0; m < NT; ++m) acc[m] = 0.0f;
+    for (int m = 0; m < COLS; ++m) acc[m] = 0.0f;
     bool live = true;
     if constexpr (F::kScaled) {
       live = __all_sync(0xFFFFFFFFu, wait_or_abort(acc_full, 0, p.err, abort_flag));
       if (live) {
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < NT; c += 16) {
+        for (int c = 0; c < COLS; c += 16) {
           uint32_t v[16];
           tmem_ld16_start(tl + c, v);
           tmem_ld_wait(v);
@@ -234,15 +242,15 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
     } else {
       // Lane l brings the scales of activation rows l, l + 32, ..., D groups
       // ahead of their use: a fetch takes longer than a group.
-      constexpr int kPer = (NT + 31) / 32, D = 4;
+      constexpr int kPer = (COLS + 31) / 32, D = 4;
       const int kb = p.K >> 7;
       const float* sw = static_cast<const float*>(p.SW) + static_cast<long long>(tile) * kb + st0;
       const float* sa[kPer];
       float fa[D][kPer], fw[D];
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        sa[i] = static_cast<const float*>(p.SA) + static_cast<long long>(min(32 * i + lane, p.M - 1)) * kb + st0;
-      float* fac = reinterpret_cast<float*>(smem + L::kFac) + q * NT;
+        sa[i] = static_cast<const float*>(p.SA) + static_cast<long long>(min(c0 + 32 * i + lane, p.M - 1)) * kb + st0;
+      float* fac = reinterpret_cast<float*>(smem + L::kFac) + (warp - kEpiWarp0) * COLS;
 #pragma unroll
       for (int d = 0; d < D; ++d) fw[d] = d < nst ? __ldg(sw + d) : 0.0f;
       pdl_wait();
@@ -258,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-              if (32 * i + lane < NT) fac[32 * i + lane] = fa[d][i] * fw[d];
+              if (32 * i + lane < COLS) fac[32 * i + lane] = fa[d][i] * fw[d];
               if (t + D < nst) fa[d][i] = sa[i][t + D];
             }
             if (t + D < nst) fw[d] = __ldg(sw + t + D);
@@ -271,10 +279,10 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
               uint32_t v[2][16];
               tmem_ld16_start(tl + slot * NT, v[0]);
 #pragma unroll
-              for (int c = 0; c < NT; c += 16) {
+              for (int c = 0; c < COLS; c += 16) {
                 uint32_t(&x)[16] = v[(c / 16) & 1];
                 tmem_ld_wait(x);
-                if (c + 16 < NT) {
+                if (c + 16 < COLS) {
                   tmem_ld16_start(tl + slot * NT + c + 16, v[(c / 16 + 1) & 1]);
                 } else {
                   tc_fence_before();
@@ -294,23 +302,23 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
       // Row m goes to rank m % splits, into [source rank][m / splits][weight row].
       const int per = (NT + splits - 1) / splits;
       const uint32_t dst = sb + L::kRecv + 4 * (rank * per * 128 + r);
-      uint32_t at = 0, to[kMaxSplits];
+      uint32_t at = c0 / splits * 512, to[kMaxSplits];
 #pragma unroll
       for (int o = 0; o < kMaxSplits; ++o) to[o] = mapa_shared(dst, min(o, splits - 1));
-      int owner = 0;
+      int owner = c0 % splits;
 #pragma unroll
-      for (int m = 0; m < NT; ++m) {
-        if (m < p.M && live) {
+      for (int m = 0; m < COLS; ++m) {
+        if (c0 + m < p.M && live) {
           const uint32_t base = owner < 2 ? (owner == 0 ? to[0] : to[1]) : (owner == 2 ? to[2] : to[3]);
           st_dsmem_f32(base + at, acc[m]);
         }
         if (++owner == splits) owner = 0, at += 512;
       }
     } else if (live && n0 + r < p.N) {
-      uint16_t* c = p.C + n0 + r;
+      uint16_t* c = p.C + static_cast<long long>(c0) * p.ldc + n0 + r;
 #pragma unroll
-      for (int m = 0; m < NT; ++m)
-        if (m < p.M) c[static_cast<long long>(m) * p.ldc] = f32_to_bf16_rn(acc[m]);
+      for (int m = 0; m < COLS; ++m)
+        if (c0 + m < p.M) c[static_cast<long long>(m) * p.ldc] = f32_to_bf16_rn(acc[m]);
     }
   }
   if (splits > 1 && warp < kEpiWarp0) cluster_wait();
@@ -318,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, L::kCols);
+    tmem_dealloc(tmem, L::kTmem);
   }
   const bool failed = *abort_flag != 0;
   if (failed)                                    // no copy may still be in flight when the CTA exits
@@ -330,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
     const float* recv = reinterpret_cast<const float*>(smem + L::kRecv);
     const int r = threadIdx.x & 127;
     if (!failed && n0 + r < p.N) {
-      for (int i = threadIdx.x >> 7; i * splits + rank < p.M; i += kThreads / 128) {
+      for (int i = threadIdx.x >> 7; i * splits + rank < p.M; i += L::kThreads / 128) {
         float v = recv[i * 128 + r];
         for (int src = 1; src < splits; ++src) v += recv[(src * per + i) * 128 + r];
         p.C[static_cast<long long>(i * splits + rank) * p.ldc + n0 + r] = f32_to_bf16_rn(v);
@@ -339,9 +347,9 @@ __global__ void __launch_bounds__(kThreads, FewLayout<F, NT>::kCtas)
   }
 }
 
-template <class F, int NT>
+template <class F, int NT, bool kShared>
 cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
-  using L = FewLayout<F, NT>;
+  using L = FewLayout<F, NT, kShared>;
   const uint64_t row = F::kScaled ? static_cast<uint64_t>(a.K) / 2 : static_cast<uint64_t>(a.K);
   CUtensorMap mw, ma;
   cudaError_t e = cached_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.W, row, static_cast<uint64_t>(a.N), row, 128, 128,
@@ -351,7 +359,7 @@ cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
                   CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
   static AttrLatch latch;
-  if (e = set_smem_attrs(few_kernel<F, NT>, latch, L::kAlloc, true); e != cudaSuccess) return e;
+  if (e = set_smem_attrs(few_kernel<F, NT, kShared>, latch, L::kAlloc, true); e != cudaSuccess) return e;
   FewParams p = {};
   p.SA = a.SA;
   p.SW = a.SW;
@@ -368,7 +376,7 @@ cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
   for (int sp = 2; sp <= kMaxSplits && sp <= p.stages && sp * tiles <= L::kCtas * a.num_sms; ++sp) p.splits = sp;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles * p.splits);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kAlloc;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -380,7 +388,7 @@ cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.pdl ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, few_kernel<F, NT>, mw, ma, p);
+  return cudaLaunchKernelEx(&cfg, few_kernel<F, NT, kShared>, mw, ma, p);
 }
 
 // Whether a call is this kernel's. It is where K can be split over the SMs
@@ -398,11 +406,13 @@ bool few_fits(const ActGemmArgs& a) {
 
 template <class F>
 cudaError_t launch_few(const ActGemmArgs& a, cudaStream_t s) {
-  if (a.M <= 16) return launch_few_nt<F, 16>(a, s);
-  if (a.M <= 32) return launch_few_nt<F, 32>(a, s);
-  if constexpr (!F::kScaled)
-    if (a.M > 64) return launch_few_nt<F, 128>(a, s);
-  return launch_few_nt<F, 64>(a, s);
+  if (a.M <= 16) return launch_few_nt<F, 16, true>(a, s);
+  if (a.M <= 32) return launch_few_nt<F, 32, !F::kScaled>(a, s);
+  if constexpr (!F::kScaled) {
+    if (a.M > 64) return launch_few_nt<F, 128, false>(a, s);
+    if ((a.N + 127) / 128 > a.num_sms) return launch_few_nt<F, 64, true>(a, s);
+  }
+  return launch_few_nt<F, 64, false>(a, s);
 }
 
 }  // namespace

@@ -41,9 +41,12 @@ struct ManyParams {
 
 template <class F, int BN>
 struct ManyLayout {
-  static constexpr int kRoles = 4;
-  static constexpr int kCols = F::kScaled ? 64 : BN / 2;        // columns of an epilogue warp
-  static constexpr int kEpi = BN / kCols * 4;                   // epilogue warps
+  // Warps before the epilogue's: copies and MMA, then 4 bits: two sets of
+  // three that rearrange scales, 8 bits: two idle ones (register shares are
+  // set by four warps at a time).
+  static constexpr int kRoles = F::kScaled ? 8 : 4;
+  static constexpr int kCols = BN / 2;                          // columns of an epilogue warp
+  static constexpr int kEpi = 8;                                // epilogue warps
   static constexpr int kThreads = (kRoles + kEpi) * 32;
   static constexpr int kNB = (BN + 127) / 128;                  // 128-row blocks of the weights' scales
   static constexpr int kStageBytes = 16384 + BN * 64 + (F::kScaled ? kScaleBlock * (1 + kNB) : 0);
@@ -102,7 +105,7 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       mbar_init(full + 8 * i, 2);
       mbar_init(raw_full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
-      mbar_init(scaled + 8 * i, 4);
+      mbar_init(scaled + 8 * i, 2 * (1 + NB));
     }
     for (int i = 0; i < NACC; ++i) {
       mbar_init(acc_full + 8 * i, 1);
@@ -221,26 +224,23 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       __syncwarp();
       mbar_wait(drained, 0, p.err);
     } else if (F::kScaled && warp >= 2) {
-      const uint32_t scaled0 = mapa_shared(scaled, 0);
-      int s = 0;
-      uint32_t ph = 0;
-      for (int i = first; i < total; i += step) {
-        for (int k = 0; k < p.stages; ++k) {
+      // Two sets of warps take the stages in turn, one 128-row block a warp.
+      const int set = (warp - 2) / 3, b = (warp - 2) % 3;
+      if (b < 1 + NB) {
+        const uint32_t scaled0 = mapa_shared(scaled, 0);
+        const long long stages = static_cast<long long>((total - first + step - 1) / step) * p.stages;
+        int s = set;
+        uint32_t ph = 0;
+        for (long long it = set; it < stages; it += 2) {
           wait_or_abort(raw_full + 8 * s, ph, p.err, abort_flag);
-          uint8_t* ba = smem + L::kSclA + s * kScaleBlock;
-          uint8_t* bb = smem + L::kSclB + s * NB * kScaleBlock;
-          uint2 va[4], vb[NB][4];
-          take_scales(ba, warp - 2, lane, 128, va);
-#pragma unroll
-          for (int b = 0; b < NB; ++b) take_scales(bb + b * kScaleBlock, warp - 2, lane, min(128, BN - 128 * b), vb[b]);
-          asm volatile("bar.sync 1, 64;" ::: "memory");
-          put_scales(ba, warp - 2, lane, va);
-#pragma unroll
-          for (int b = 0; b < NB; ++b) put_scales(bb + b * kScaleBlock, warp - 2, lane, vb[b]);
+          __syncwarp();
+          if (b == 0) rearrange_scales(smem + L::kSclA + s * kScaleBlock, lane, 128);
+          else rearrange_scales(smem + L::kSclB + (s * NB + b - 1) * kScaleBlock, lane, min(128, BN - 128 * (b - 1)));
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) pair_arrive(scaled0 + 8 * s);
-          if (++s == S) s = 0, ph ^= 1;
+          s += 2;
+          if (s >= S) s -= S, ph ^= 1;
         }
       }
     }
