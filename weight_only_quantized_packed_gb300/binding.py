@@ -316,14 +316,19 @@ def _weights(name, t, count, dtype):
 
 
 def _codes_out(x, codes_shape, scales_shape, scales_dtype, out):
-    """(codes, scales) and their addresses, new or the caller's."""
+    """(codes, scales), new or the caller's."""
     if out is None:
-        codes = _torch.empty(codes_shape, dtype=_torch.uint8, device=x.device)
-        scales = _torch.empty(scales_shape, dtype=scales_dtype, device=x.device)
-        return codes, scales, codes.data_ptr(), scales.data_ptr()
+        return (_torch.empty(codes_shape, dtype=_torch.uint8, device=x.device),
+                _torch.empty(scales_shape, dtype=scales_dtype, device=x.device))
     codes, scales = out
-    return (codes, scales, _packed("out codes", codes, codes_shape, _torch.uint8),
-            _packed("out scales", scales, scales_shape, scales_dtype))
+    if not (codes.is_cuda and scales.is_cuda):
+        raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
+    if codes.dtype is not _torch.uint8 or scales.dtype is not scales_dtype:
+        raise TypeError(f"out must be torch.uint8 codes and {scales_dtype} scales")
+    if (codes.shape != codes_shape or scales.shape != scales_shape
+            or not (codes.is_contiguous() and scales.is_contiguous())):
+        raise ValueError(f"out must be contiguous {list(codes_shape)} codes and {list(scales_shape)} scales")
+    return codes, scales
 
 
 def w4_quantize(x, global_scale: float = 1.0, out=None, stream=None):
@@ -331,8 +336,11 @@ def w4_quantize(x, global_scale: float = 1.0, out=None, stream=None):
     uint8 E4M3 scales [M, K/16], under one global_scale. out: (codes, scales) to write to."""
     torch = _torch or _load_torch()
     ldx, dt, M, K = _typed_rows("x", x)
-    codes, scales, pc, ps = _codes_out(x, (M, K // 2), (M, K // 16), torch.uint8, out)
-    _check(lib().w4_quantize(x.data_ptr(), ldx, dt, global_scale, pc, ps, M, K, _stream(stream)), "w4_quantize")
+    codes, scales = _codes_out(x, (M, K // 2), (M, K // 16), torch.uint8, out)
+    status = (_lib or lib()).w4_quantize(x.data_ptr(), ldx, dt, float(global_scale), codes.data_ptr(),
+                                         scales.data_ptr(), M, K, _stream(stream))
+    if status:
+        _check(status, "w4_quantize")
     return codes, scales
 
 
@@ -341,8 +349,11 @@ def a8_quantize(x, out=None, stream=None):
     [M, K/128]. out: (codes, scales) to write to."""
     torch = _torch or _load_torch()
     ldx, dt, M, K = _typed_rows("x", x)
-    codes, scales, pc, ps = _codes_out(x, (M, K), (M, K // 128), torch.float32, out)
-    _check(lib().a8_quantize(x.data_ptr(), ldx, dt, pc, ps, M, K, _stream(stream)), "a8_quantize")
+    codes, scales = _codes_out(x, (M, K), (M, K // 128), torch.float32, out)
+    status = (_lib or lib()).a8_quantize(x.data_ptr(), ldx, dt, codes.data_ptr(), scales.data_ptr(), M, K,
+                                         _stream(stream))
+    if status:
+        _check(status, "a8_quantize")
     return codes, scales
 
 
@@ -375,8 +386,11 @@ def rms_norm(x, weight, eps: float, residual=None, residual_out=None, out=None, 
         out, ldy = torch.empty((M, K), dtype=x.dtype, device=x.device), K
     else:
         ldy = _rows_like("out", out, x)
-    _check(lib().rms_norm(x.data_ptr(), ldx, pr, ldr, pw, eps, ph, ldh, out.data_ptr(), ldy, dt, M, K,
-                          _stream(stream)), "rms_norm")
+    status = (_lib or lib()).rms_norm(x.data_ptr(), ldx, pr, ldr, pw, float(eps), ph, ldh, out.data_ptr(), ldy,
+                                      dt, M, K,
+                                      _stream(stream))
+    if status:
+        _check(status, "rms_norm")
     return out, h
 
 
@@ -385,9 +399,12 @@ def rms_norm_a8(x, weight, eps: float, residual=None, residual_out=None, out=Non
     torch = _torch or _load_torch()
     ldx, dt, M, K = _typed_rows("x", x)
     pr, ldr, h, ph, ldh, pw = _norm_args(x, weight, residual, residual_out)
-    codes, scales, pc, ps = _codes_out(x, (M, K), (M, K // 128), torch.float32, out)
-    _check(lib().rms_norm_a8(x.data_ptr(), ldx, pr, ldr, pw, eps, ph, ldh, pc, ps, dt, M, K, _stream(stream)),
-           "rms_norm_a8")
+    codes, scales = _codes_out(x, (M, K), (M, K // 128), torch.float32, out)
+    status = (_lib or lib()).rms_norm_a8(x.data_ptr(), ldx, pr, ldr, pw, float(eps), ph, ldh, codes.data_ptr(),
+                                         scales.data_ptr(), dt, M, K,
+                                         _stream(stream))
+    if status:
+        _check(status, "rms_norm_a8")
     return codes, scales, h
 
 
@@ -412,8 +429,10 @@ def w4a4_gemm(A, a_scales, W, w_scales, N: int, K: int, a_global: float = 1.0, w
     pa, psa = _packed("A", A, (M, K // 2), u8), _packed("a_scales", a_scales, (M, K // 16), u8)
     pw, psw = _weights("W", W, N * (K // 2), u8), _weights("w_scales", w_scales, N * (K // 16), u8)
     C, ldc = _gemm_out(A, M, N, out)
-    _check(lib().w4a4_gemm(pa, psa, a_global, pw, psw, w_global, C.data_ptr(), ldc, M, N, K, _stream(stream)),
-           "w4a4_gemm")
+    status = (_lib or lib()).w4a4_gemm(pa, psa, float(a_global), pw, psw, float(w_global), C.data_ptr(), ldc, M, N, K,
+                                       _stream(stream))
+    if status:
+        _check(status, "w4a4_gemm")
     return C
 
 
@@ -425,7 +444,9 @@ def w8a8_gemm(A, a_scales, W, w_scales, N: int, K: int, out=None, stream=None):
     pw = _weights("W", W, N * K, torch.uint8)
     psw = _weights("w_scales", w_scales, (N + 127) // 128 * (K // 128), torch.float32)
     C, ldc = _gemm_out(A, M, N, out)
-    _check(lib().w8a8_gemm(pa, psa, pw, psw, C.data_ptr(), ldc, M, N, K, _stream(stream)), "w8a8_gemm")
+    status = (_lib or lib()).w8a8_gemm(pa, psa, pw, psw, C.data_ptr(), ldc, M, N, K, _stream(stream))
+    if status:
+        _check(status, "w8a8_gemm")
     return C
 
 
