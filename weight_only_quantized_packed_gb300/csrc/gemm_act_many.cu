@@ -6,26 +6,31 @@
 // memory that feeds it: a tile is 256 activation rows by BN weight rows, held
 // by a pair of CTAs on two SMs (act.cuh), so that each SM reads half of the
 // weight tile for all of its MMA's work. Persistent pairs walk over the tiles.
-//  * 4 bits: the tensor core applies the scales, rearranged by two warps of
-//    each CTA (its 128 activation rows, all BN weight rows) and copied to
-//    tensor memory by the MMA warp. One accumulator, drained into registers as
-//    BF16 before the next tile's first MMA.
-//  * 8 bits: two accumulators that take turns per 128 K; the epilogue adds each,
-//    times its activation row's and weight block's scale, to FP32 sums in
-//    registers while the tensor core fills the other.
+//  * 4 bits: the tensor core applies the scales, rearranged by warps of each CTA
+//    (its 128 activation rows, all BN weight rows) and copied to tensor memory
+//    by the MMA warp. One or two accumulators, drained into registers as BF16.
+//    4096x34816x5120: 248 us, 5.9 PFLOP/s until the power cap slows the clock.
+//    Tensor pipe 61 % busy (ncu); next are the bytes into an SM (38 KB a stage,
+//    at 64 a clock 83 % of a stage's time) and the drains between tiles.
+//  * 8 bits: two to four accumulators that take turns per 128 K; the epilogue
+//    adds each, times its activation row's and weight block's scale, to FP32
+//    sums in registers while the tensor core fills the others.
+//    4096x5120x17408: 277 us, 2.6 PFLOP/s. Bound by that reading and adding: 773
+//    clocks per 128 K of a 256-column tile, of which the MMAs are 544; without
+//    the additions 238 us.
 // Output goes through shared memory, 32 rows by 32 columns a warp at a time,
 // and leaves as bulk tensor stores (rows of C that are not 16-byte aligned: as
 // whole row segments from there).
 //
-// Warps: 0 copies, 1 MMA (even CTA; tensor memory in both), 4 bits: 2..3
-// scales; the rest epilogue, one per lane quarter (warp % 4) and 64 columns.
+// Warps: 0 copies, 1 MMA (even CTA; tensor memory in both), 4 bits: 2..7
+// scales; then 8 epilogue warps, one per lane quarter (warp % 4) and half of the
+// columns (16 with a quarter each read tensor memory no faster and have too few
+// registers: 348 us at 4096x5120x17408).
 #include "act.cuh"
 
 namespace wqp {
 namespace act {
 namespace {
-
-constexpr uint32_t kScaleCol = 256;    // 4 bits: two sets of a stage's scales
 
 struct ManyParams {
   const float* SA;
@@ -41,24 +46,29 @@ struct ManyParams {
 
 template <class F, int BN>
 struct ManyLayout {
-  // Warps before the epilogue's: copies and MMA, then 4 bits: two sets of
-  // three that rearrange scales, 8 bits: two idle ones (register shares are
-  // set by four warps at a time).
+  // Warps before the epilogue's: copies and MMA, then 4 bits: two sets of three
+  // that rearrange scales, 8 bits: two idle ones (register shares are set by
+  // four warps at a time).
   static constexpr int kRoles = F::kScaled ? 8 : 4;
   static constexpr int kCols = BN / 2;                          // columns of an epilogue warp
   static constexpr int kEpi = 8;                                // epilogue warps
   static constexpr int kThreads = (kRoles + kEpi) * 32;
   static constexpr int kNB = (BN + 127) / 128;                  // 128-row blocks of the weights' scales
   static constexpr int kStageBytes = 16384 + BN * 64 + (F::kScaled ? kScaleBlock * (1 + kNB) : 0);
-  static constexpr int kS = (225 * 1024 - kEpi * 2048) / kStageBytes;
+  static constexpr int kOutBytes = 32 * 64;                     // what an epilogue warp stores at a time
+  static constexpr int kS = (225 * 1024 - kEpi * kOutBytes) / kStageBytes;
   static constexpr int kA = 0;
   static constexpr int kB = kA + kS * 16384;
-  static constexpr int kOut = kB + kS * BN * 64;                // [epilogue warp][32 rows][64 bytes]
-  static constexpr int kSclA = kOut + kEpi * 2048;
+  static constexpr int kOut = kB + kS * BN * 64;                // [epilogue warp][32 rows][32 columns]
+  static constexpr int kSclA = kOut + kEpi * kOutBytes;
   static constexpr int kSclB = kSclA + (F::kScaled ? kS * kScaleBlock : 0);
   static constexpr int kBytes = kSclB + (F::kScaled ? kS * kScaleBlock * kNB : 0);
   static constexpr int kAlloc = kBytes + 1024;
-  static constexpr int kAcc = F::kScaled ? 1 : 2;
+  // Accumulators of BN columns in tensor memory, and (4 bits) behind them two
+  // sets of a stage's scales.
+  static constexpr int kAcc = F::kScaled ? (BN <= 192 ? 2 : 1) : 512 / BN;
+  static constexpr uint32_t kScaleCol = kAcc * BN;
+  static_assert(kScaleCol + (F::kScaled ? 64 + 16 + 16 * kNB : 0) <= 512, "tensor memory");
   static_assert(kAlloc <= 227 * 1024 - 1024, "shared memory");
 };
 
@@ -178,45 +188,58 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       constexpr uint32_t idesc = F::kScaled ? idesc_f4(256, BN) : idesc_f8(256, BN);
       const uint64_t ad0 = tile_desc(sb + L::kA), bd0 = tile_desc(sb + L::kB);
       const uint64_t sad0 = scale_desc(sb + L::kSclA), sbd0 = scale_desc(sb + L::kSclB);
-      int s = 0, slot = 0, handed = 0;         // accumulators handed over, up to NACC
+      // A wait that follows MMAs costs the tensor core a pause (the warp comes
+      // back from it only when the MMAs have been taken), so what the next
+      // stage needs is looked up before this stage's are issued, and waited for
+      // only if it was not there yet.
+      int s = 0, slot = 0, k = 0;
       uint32_t ph = 0, acc_ph = 1, set = 0;
-      for (int i = first; i < total; i += step) {
-        for (int k = 0; k < p.stages; ++k) {
-          if (!F::kScaled || k == 0) {
-            if (handed == NACC) wait_or_abort(acc_free + 8 * slot, acc_ph, p.err, abort_flag);
-            else ++handed;
-          }
+      bool loaded = false, freed = true;       // of the next stage; accumulators start free
+      const long long stages = static_cast<long long>((total - first + step - 1) / step) * p.stages;
+      for (long long it = 0; it < stages; ++it) {
+        if (!freed) wait_or_abort(acc_free + 8 * slot, acc_ph, p.err, abort_flag);
+        if (!loaded) {
           wait_or_abort(full + 8 * s, ph, p.err, abort_flag);
           if (F::kScaled) wait_or_abort(scaled + 8 * s, ph, p.err, abort_flag);
-          __syncwarp();
-          tc_fence_after();
-          if (elect_one()) {
-            // Addresses in a descriptor are in units of 16 bytes.
-            const uint64_t ad = ad0 + s * (16384 >> 4), bd = bd0 + s * ((BN * 64) >> 4);
-            if constexpr (F::kScaled) {
-              const uint64_t sad = sad0 + s * (kScaleBlock >> 4), sbd = sbd0 + s * ((NB * kScaleBlock) >> 4);
-              const uint32_t sa = tmem + kScaleCol + set * 64, sw = sa + 16;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                pair_copy_scales(sa + 4 * j, sad + 32 * j);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) pair_copy_scales(sw + (j * NB + b) * 4, sbd + b * (kScaleBlock >> 4) + 32 * j);
-              }
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                pair_mma_f4(tmem, ad + 2 * j, bd + 2 * j, idesc, sa + 4 * j, sw + j * NB * 4, (k | j) ? 1u : 0u);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) pair_mma_f8(tmem + slot * 256, ad + 2 * j, bd + 2 * j, idesc, j ? 1u : 0u);
-            }
-            if (!F::kScaled || k == p.stages - 1) pair_commit(acc_full + 8 * slot);
-            pair_commit(empty + 8 * s);
-          }
-          __syncwarp();
-          set ^= 1;
-          if ((!F::kScaled || k == p.stages - 1) && ++slot == NACC) slot = 0, acc_ph ^= 1;
-          if (++s == S) s = 0, ph ^= 1;
         }
+        __syncwarp();
+        tc_fence_after();
+        const int s1 = s + 1 == S ? 0 : s + 1, k1 = k + 1 == p.stages ? 0 : k + 1;
+        const uint32_t ph1 = s1 ? ph : ph ^ 1;
+        const bool hand = !F::kScaled || k1 == 0;                    // this stage completes an accumulator
+        const int slot1 = !hand ? slot : (slot + 1 == NACC ? 0 : slot + 1);
+        const uint32_t acc_ph1 = hand && slot1 == 0 ? acc_ph ^ 1 : acc_ph;
+        bool l1 = mbar_test(full + 8 * s1, ph1);
+        if (F::kScaled) l1 = l1 && mbar_test(scaled + 8 * s1, ph1);
+        // Parity 1 of a barrier that has completed no phase counts as complete.
+        const bool f1 = !hand || mbar_test(acc_free + 8 * slot1, acc_ph1);
+        if (elect_one()) {
+          // Addresses in a descriptor are in units of 16 bytes.
+          const uint64_t ad = ad0 + s * (16384 >> 4), bd = bd0 + s * ((BN * 64) >> 4);
+          if constexpr (F::kScaled) {
+            const uint64_t sad = sad0 + s * (kScaleBlock >> 4), sbd = sbd0 + s * ((NB * kScaleBlock) >> 4);
+            const uint32_t sa = tmem + L::kScaleCol + set * 64, sw = sa + 16;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              pair_copy_scales(sa + 4 * j, sad + 32 * j);
+#pragma unroll
+              for (int b = 0; b < NB; ++b) pair_copy_scales(sw + (j * NB + b) * 4, sbd + b * (kScaleBlock >> 4) + 32 * j);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              pair_mma_f4(tmem + slot * BN, ad + 2 * j, bd + 2 * j, idesc, sa + 4 * j, sw + j * NB * 4, (k | j) ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pair_mma_f8(tmem + slot * BN, ad + 2 * j, bd + 2 * j, idesc, j ? 1u : 0u);
+          }
+          if (hand) pair_commit(acc_full + 8 * slot);
+          pair_commit(empty + 8 * s);
+        }
+        __syncwarp();
+        loaded = __all_sync(0xFFFFFFFFu, l1);
+        freed = __all_sync(0xFFFFFFFFu, f1);
+        set ^= 1;
+        s = s1, ph = ph1, k = k1, slot = slot1, acc_ph = acc_ph1;
       }
       // The pair's MMAs are done before the cluster barrier below, and tensor
       // memory is freed after it.
@@ -250,7 +273,7 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
     const int q = warp & 3, ew = warp - L::kRoles, h = ew >> 2;
     const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * COLS;
     const uint32_t acc_free0 = mapa_shared(acc_free, 0);
-    uint8_t* out = smem + L::kOut + ew * 2048;
+    uint8_t* out = smem + L::kOut + ew * L::kOutBytes;
     const int kb = p.K >> 7;
     if (!F::kScaled) pdl_wait();               // the activations' scales
     int slot = 0;
@@ -261,14 +284,13 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       const int m0 = mi * 256 + rank * 128 + q * 32, n0 = ni * BN + h * COLS;
       uint32_t packed[COLS / 2];
       if constexpr (F::kScaled) {
-        wait_or_abort(acc_full, ph, p.err, abort_flag);
-        ph ^= 1;
+        wait_or_abort(acc_full + 8 * slot, ph, p.err, abort_flag);
         __syncwarp();
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < COLS; c += 32) {
           uint32_t v[32];
-          tmem_ld32_start(tl + c, v);
+          tmem_ld32_start(tl + slot * BN + c, v);
           tmem_ld_wait(v);
 #pragma unroll
           for (int j = 0; j < 16; ++j)
@@ -276,7 +298,8 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) pair_arrive(acc_free0);
+        if (lane == 0) pair_arrive(acc_free0 + 8 * slot);
+        if (++slot == NACC) slot = 0, ph ^= 1;
       } else {
         const float* sa = p.SA + static_cast<long long>(min(m0 + lane, p.M - 1)) * kb;
         // The warp's columns lie in one or two weight blocks; `cross` is the
@@ -287,39 +310,64 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
         uint64_t acc[COLS / 2];
 #pragma unroll
         for (int c = 0; c < COLS / 2; ++c) acc[c] = 0;
-        float next0 = sa[0] * __ldg(sw0), next1 = sa[0] * __ldg(sw1);
-        for (int k = 0; k < kb; ++k) {
-          const uint64_t f0 = pair_f32(__float_as_uint(next0), __float_as_uint(next0));
-          const uint64_t f1 = pair_f32(__float_as_uint(next1), __float_as_uint(next1));
-          if (k + 1 < kb) {
-            const float a = sa[k + 1];
-            next0 = a * __ldg(sw0 + k + 1);
-            if (BN % 256 != 0) next1 = a * __ldg(sw1 + k + 1);
-          }
-          wait_or_abort(acc_full + 8 * slot, ph, p.err, abort_flag);
-          __syncwarp();
-          tc_fence_after();
-          // The next columns are on their way while these are added; the
-          // accumulator is free once the last have arrived.
-          constexpr int W = 16;
-          uint32_t v[2][W];
-          tmem_ld16_start(tl + slot * 256, v[0]);
+        // Scales are fetched D blocks ahead of their use: a fetch may take longer
+        // than a block.
+        constexpr int D = 4;
+        constexpr bool kTwo = BN % 256 != 0;
+        float fa[D], fw0[D], fw1[D];
 #pragma unroll
-          for (int c = 0; c < COLS; c += W) {
-            uint32_t(&x)[W] = v[(c / W) & 1];
-            tmem_ld_wait(x);
-            if (c + W < COLS) {
-              tmem_ld16_start(tl + slot * 256 + c + W, v[(c / W + 1) & 1]);
-            } else {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) pair_arrive(acc_free0 + 8 * slot);
+        for (int d = 0; d < D; ++d) {
+          fa[d] = d < kb ? sa[d] : 0.0f;
+          fw0[d] = d < kb ? __ldg(sw0 + d) : 0.0f;
+          fw1[d] = kTwo && d < kb ? __ldg(sw1 + d) : 0.0f;
+        }
+        for (int k0 = 0; k0 < kb; k0 += D) {
+#pragma unroll
+          for (int d = 0; d < D; ++d) {
+            const int k = k0 + d;
+            if (k >= kb) break;
+            const float s0 = fa[d] * fw0[d], s1 = kTwo ? fa[d] * fw1[d] : s0;
+            const uint64_t f0 = pair_f32(__float_as_uint(s0), __float_as_uint(s0));
+            const uint64_t f1 = pair_f32(__float_as_uint(s1), __float_as_uint(s1));
+            if (k + D < kb) {
+              fa[d] = sa[k + D];
+              fw0[d] = __ldg(sw0 + k + D);
+              if (kTwo) fw1[d] = __ldg(sw1 + k + D);
             }
-            const uint64_t f = (BN % 256 == 0 || c < cross) ? f0 : f1;
+            wait_or_abort(acc_full + 8 * slot, ph, p.err, abort_flag);
+            __syncwarp();
+            tc_fence_after();
+            // The next 32 columns are on their way while these are added; the
+            // accumulator is free once the last have arrived.
+            const uint32_t at = tl + slot * BN;
+            uint32_t v[2][2][16];
+            tmem_ld16_start(at, v[0][0]);
+            tmem_ld16_start(at + 16, v[0][1]);
 #pragma unroll
-            for (int j = 0; j < W / 2; ++j) fma_f32x2(acc[c / 2 + j], pair_f32(x[2 * j], x[2 * j + 1]), f);
+            for (int c0 = 0; c0 < COLS; c0 += 32) {
+              uint32_t(&x)[2][16] = v[(c0 / 32) & 1];
+              uint32_t(&y)[2][16] = v[(c0 / 32 + 1) & 1];
+              tmem_ld_wait(x[0]);
+              if (c0 + 16 < COLS) tmem_ld_after(x[1]);
+              if (c0 + 32 < COLS) tmem_ld16_start(at + c0 + 32, y[0]);
+              if (c0 + 48 < COLS) tmem_ld16_start(at + c0 + 48, y[1]);
+              if (c0 + 32 >= COLS) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) pair_arrive(acc_free0 + 8 * slot);
+              }
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int c = c0 + 16 * u;
+                if (c < COLS) {
+                  const uint64_t f = (!kTwo || c < cross) ? f0 : f1;
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) fma_f32x2(acc[c / 2 + j], pair_f32(x[u][2 * j], x[u][2 * j + 1]), f);
+                }
+              }
+            }
+            if (++slot == NACC) slot = 0, ph ^= 1;
           }
-          if (++slot == NACC) slot = 0, ph ^= 1;
         }
 #pragma unroll
         for (int j = 0; j < COLS / 2; ++j)
@@ -328,13 +376,14 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       if (*abort_flag) continue;
       // 32 rows of 64 bytes in the 64-byte swizzle (16-byte chunk j of row r at
       // j ^ (r / 2 mod 4)): free of bank conflicts here, and the store map's own.
+      const auto chunk_at = [&](int r, int j) { return out + r * 64 + ((j ^ ((r >> 1) & 3)) << 4); };
 #pragma unroll
       for (int c = 0; c < COLS; c += 32) {
         if (elect_one()) tma_store_wait_read();
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4*>(out + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+          *reinterpret_cast<uint4*>(chunk_at(lane, j)) =
               make_uint4(packed[c / 2 + 4 * j], packed[c / 2 + 4 * j + 1], packed[c / 2 + 4 * j + 2], packed[c / 2 + 4 * j + 3]);
         // A tensor store writes whole 16-byte units, past the end of the row too:
         // its map ends at the last whole unit, and the few columns after that are
@@ -348,15 +397,14 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
           if (rest >= 0 && rest < 32 && m0 + lane < p.M)
             for (int e = 0; whole + e < p.N; ++e)
               p.C[static_cast<long long>(m0 + lane) * p.ldc + whole + e] =
-                  *reinterpret_cast<const uint16_t*>(out + lane * 64 + (((rest >> 3) ^ ((lane >> 1) & 3)) << 4) + e * 2);
+                  *reinterpret_cast<const uint16_t*>(chunk_at(lane, rest >> 3) + e * 2);
           __syncwarp();
         } else if (n0 + c < p.N) {
           __syncwarp();
           const int n = n0 + c + lane;
-          for (int r = 0; r < 32 && m0 + r < p.M; ++r) {
-            const uint16_t v = *reinterpret_cast<const uint16_t*>(out + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
-            if (n < p.N) p.C[static_cast<long long>(m0 + r) * p.ldc + n] = v;
-          }
+          for (int r = 0; r < 32 && m0 + r < p.M; ++r)
+            if (n < p.N)
+              p.C[static_cast<long long>(m0 + r) * p.ldc + n] = *reinterpret_cast<const uint16_t*>(chunk_at(r, lane >> 3) + (lane & 7) * 2);
           __syncwarp();
         }
       }
@@ -432,14 +480,16 @@ cudaError_t launch_many_t(const ActGemmArgs& a, cudaStream_t s) {
 }
 
 // Width of the weight tiles: the pairs take whole rounds of tiles, and a round
-// takes a time proportional to BN + 200 (operand bytes go with BN + 256, MMAs
-// with BN). Measured, BN = 256 | 192 | 128, us: 4 bits 333x7168x5120 13.3 | 12.0
-// | 17.2, 2048x5120x5120 30.5 | 26.2 | 35.5, 4096x34816x5120 254 | 284 | 359;
-// 8 bits 333x7168x5120 20.3 | 18.2 | 27.8, 4096x5120x17408 299 | 316 | 395.
+// takes a time proportional to BN + 140 (4 bits) or BN + 100 (8 bits). Measured,
+// BN = 256 | 192 | 128, us: 4 bits 333x7168x5120 13.3 | 12.2 | 16.9, 2048x5120x5120
+// 30.2 | 25.9 | 34.2, 4096x34816x5120 248 | 274 | 336; 8 bits 333x7168x5120 20.2 |
+// 18.3 | 24.4, 2048x7168x5120 55.8 | 63.0 | 68.3, 4096x5120x17408 277 | 284 | 310.
 template <class F>
 cudaError_t launch_many(const ActGemmArgs& a, cudaStream_t s) {
   const long long mt = (a.M + 255) / 256, pairs = a.num_sms / 2;
-  const auto cost = [&](int bn) { return (mt * ((a.N + bn - 1) / bn) + pairs - 1) / pairs * (bn + 200); };
+  const auto cost = [&](int bn) {
+    return (mt * ((a.N + bn - 1) / bn) + pairs - 1) / pairs * (bn + (F::kScaled ? 140 : 100));
+  };
   const long long c256 = cost(256), c192 = cost(192), c128 = cost(128);
   if (c256 <= c192 && c256 <= c128) return launch_many_t<F, 256>(a, s);
   if (c192 <= c128) return launch_many_t<F, 192>(a, s);
