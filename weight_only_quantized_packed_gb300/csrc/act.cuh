@@ -103,6 +103,13 @@ __device__ __forceinline__ void pair_arrive_expect_tx(uint32_t bar, uint32_t byt
   asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
+// One float into a CTA's shared memory through a shared::cluster address,
+// completing as 4 bytes on that CTA's mbarrier.
+__device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(addr), "f"(v), "r"(bar)
+               : "memory");
+}
+
 // A tile of this CTA's shared memory to global memory; rows and columns
 // outside the map are dropped. The thread that stored waits before the
 // shared memory is written again (read) or the CTA ends (all).

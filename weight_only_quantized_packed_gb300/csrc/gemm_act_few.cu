@@ -15,8 +15,9 @@
 //    its two scales, to FP32 accumulators in registers.
 // With few tiles, K is split over a cluster of up to 4 CTAs. Rank q owns the
 // activation rows q, q + splits, ...; the others push their partial sums of
-// those into its shared memory, and it adds them in rank order, so the result
-// does not depend on timing.
+// those into its shared memory (asynchronous stores that complete on its
+// barrier), and it adds them in rank order, so the result does not depend on
+// timing.
 //
 // Warps: 0 copies, 1 MMA (and tensor memory), 2..3 scales (4 bits), the rest
 // epilogue (lane quarter = warp % 4).
@@ -78,7 +79,8 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
   using L = FewLayout<F, NT, kShared>;
   constexpr int S = L::kS, NACC = L::kAcc;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full_sh[S], empty_sh[S], scaled_sh[S], acc_full_sh[NACC], acc_free_sh[NACC];
+  __shared__ __align__(8) uint64_t full_sh[S], empty_sh[S], scaled_sh[S], acc_full_sh[NACC], acc_free_sh[NACC],
+      recv_sh;
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -90,21 +92,48 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
   const int st0 = static_cast<int>(static_cast<long long>(rank) * p.stages / splits);
   const int nst = static_cast<int>(static_cast<long long>(rank + 1) * p.stages / splits) - st0;
   const uint32_t full = smem_u32(full_sh), empty = smem_u32(empty_sh), scaled = smem_u32(scaled_sh);
-  const uint32_t acc_full = smem_u32(acc_full_sh), acc_free = smem_u32(acc_free_sh);
+  const uint32_t acc_full = smem_u32(acc_full_sh), acc_free = smem_u32(acc_free_sh), recv_bar = smem_u32(&recv_sh);
+  const int own = (p.M - rank + splits - 1) / splits;      // activation rows rank, rank + splits, ...
   volatile int* abort_flag = &abort_sh;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < S; ++i) {
-      mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 1);
-      mbar_init(scaled + 8 * i, 2);
+  // The thread that copies: sets up the barriers and starts the first stages'
+  // weights, which do not depend on the previous grid, before the CTA meets.
+  // (Prefetching later stages into L2 on top: 17.1 -> 18.3..20.1 us at
+  // 1x17408x5120.) Copies and MMAs are issued under elect.sync (see
+  // gemm_act_many.cu).
+  const int ahead = min(S, nst);
+  int issued = 0;                                // stages whose copies this thread started
+  const uint64_t pol = policy_evict_first();
+  const auto load_w = [&](int t) {
+    const int s = t % S;
+    mbar_arrive_expect_tx(full + 8 * s, L::kStageBytes);
+    tma_load_2d_hint(sb + L::kW + s * 16384, &tmW, (st0 + t) * 128, n0, full + 8 * s, pol);
+  };
+  const auto load_a = [&](int t) {
+    const int s = t % S;
+    tma_load_2d(sb + L::kA + s * NT * 128, &tmA, (st0 + t) * 128, 0, full + 8 * s);
+  };
+  if (warp == 0) {
+    if (elect_one()) {
+      prefetch_tmap(&tmW);
+      prefetch_tmap(&tmA);
+      for (int i = 0; i < S; ++i) {
+        mbar_init(full + 8 * i, 1);
+        mbar_init(empty + 8 * i, 1);
+        mbar_init(scaled + 8 * i, 2);
+      }
+      for (int i = 0; i < NACC; ++i) {
+        mbar_init(acc_full + 8 * i, 1);
+        mbar_init(acc_free + 8 * i, L::kEpi);
+      }
+      mbar_init(recv_bar, 1);
+      abort_sh = 0;
+      mbar_fence_init();
+      // Every rank's share of this rank's rows, its own among them.
+      if (splits > 1) mbar_arrive_expect_tx(recv_bar, static_cast<uint32_t>(own) * 512u * splits);
+      for (int t = 0; t < ahead; ++t) load_w(t);
     }
-    for (int i = 0; i < NACC; ++i) {
-      mbar_init(acc_full + 8 * i, 1);
-      mbar_init(acc_free + 8 * i, L::kEpi);
-    }
-    abort_sh = 0;
-    mbar_fence_init();
+    __syncwarp();
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&tmem_sh), L::kTmem);
@@ -117,25 +146,8 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
   pdl_launch_dependents();
   if (splits > 1) cluster_arrive_relaxed();      // matched before the first push
 
-  // Copies and MMAs are issued under elect.sync (see gemm_act_many.cu).
-  int issued = 0;                                // stages whose copies this thread started
   if (warp == 0) {
     if (elect_one()) {
-      prefetch_tmap(&tmW);
-      prefetch_tmap(&tmA);
-      const uint64_t pol = policy_evict_first();
-      auto load_w = [&](int t) {
-        const int s = t % S;
-        mbar_arrive_expect_tx(full + 8 * s, L::kStageBytes);
-        tma_load_2d_hint(sb + L::kW + s * 16384, &tmW, (st0 + t) * 128, n0, full + 8 * s, pol);
-      };
-      auto load_a = [&](int t) {
-        const int s = t % S;
-        tma_load_2d(sb + L::kA + s * NT * 128, &tmA, (st0 + t) * 128, 0, full + 8 * s);
-      };
-      // The weights do not depend on the previous grid; the activations may.
-      const int ahead = min(S, nst);
-      for (int t = 0; t < ahead; ++t) load_w(t);
       pdl_wait();
       for (int t = 0; t < ahead; ++t) load_a(t);
       issued = ahead;
@@ -149,15 +161,26 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
     __syncwarp();
   } else if (warp == 1) {
     constexpr uint32_t idesc = F::kScaled ? idesc_f4(128, NT) : idesc_f8(128, NT);
-    int last = -1;
+    // 8 bits: what the next stage needs is looked up before this stage's MMAs are
+    // issued (see gemm_act_many.cu; 61x5120x17408: 23.3 -> 21.1 us). With 4 bits
+    // the scales of the next stage are hardly ever there yet, and it costs 2 %.
+    int last = -1, s = 0, slot = 0;
+    uint32_t ph = 0, acc_ph = 1;
+    bool loaded = false, freed = true;
     for (int t = 0; t < nst; ++t) {
-      const int s = t % S, slot = t % NACC;
-      bool ok = wait_or_abort(full + 8 * s, (t / S) & 1, p.err, abort_flag);
-      if (F::kScaled) ok = ok && wait_or_abort(scaled + 8 * s, (t / S) & 1, p.err, abort_flag);
-      if (!F::kScaled && t >= NACC)
-        ok = ok && wait_or_abort(acc_free + 8 * slot, ((t / NACC) - 1) & 1, p.err, abort_flag);
+      bool ok = true;
+      if (!loaded) {
+        ok = wait_or_abort(full + 8 * s, ph, p.err, abort_flag);
+        if (F::kScaled) ok = ok && wait_or_abort(scaled + 8 * s, ph, p.err, abort_flag);
+      }
+      if (!F::kScaled && !freed) ok = ok && wait_or_abort(acc_free + 8 * slot, acc_ph, p.err, abort_flag);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
+      const int s1 = s + 1 == S ? 0 : s + 1, slot1 = slot + 1 == NACC ? 0 : slot + 1;
+      const uint32_t ph1 = s1 ? ph : ph ^ 1, acc_ph1 = slot1 ? acc_ph : acc_ph ^ 1;
+      const bool l1 = !F::kScaled && mbar_test(full + 8 * s1, ph1);
+      // Parity 1 of a barrier that has completed no phase counts as complete.
+      const bool f1 = F::kScaled || mbar_test(acc_free + 8 * slot1, acc_ph1);
       if (elect_one()) {
         const uint64_t wd = tile_desc(sb + L::kW + s * 16384), ad = tile_desc(sb + L::kA + s * NT * 128);
         if constexpr (F::kScaled) {
@@ -175,10 +198,14 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
           for (int j = 0; j < 4; ++j) mma_f8(tmem + slot * NT, wd + 2 * j, ad + 2 * j, idesc, j ? 1u : 0u);
         }
         mma_commit(empty + 8 * s);
-        if (!F::kScaled || t == nst - 1) mma_commit(acc_full + 8 * slot);
+        if (!F::kScaled || t == nst - 1) mma_commit(acc_full + 8 * (F::kScaled ? 0 : slot));
       }
       __syncwarp();
       last = t;
+      loaded = __all_sync(0xFFFFFFFFu, l1);
+      freed = __all_sync(0xFFFFFFFFu, f1);
+      s = s1, ph = ph1;
+      if (!F::kScaled) slot = slot1, acc_ph = acc_ph1;
     }
     // This warp's MMAs are done before tensor memory is freed.
     if (last >= 0) mbar_wait(empty + 8 * (last % S), (last / S) & 1, p.err);
@@ -300,17 +327,22 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
     if (splits > 1) {
       cluster_wait();
       // Row m goes to rank m % splits, into [source rank][m / splits][weight row].
+      // After an abort too: the owner counts on it.
       const int per = (NT + splits - 1) / splits;
       const uint32_t dst = sb + L::kRecv + 4 * (rank * per * 128 + r);
-      uint32_t at = c0 / splits * 512, to[kMaxSplits];
+      uint32_t at = c0 / splits * 512, to[kMaxSplits], bars[kMaxSplits];
 #pragma unroll
-      for (int o = 0; o < kMaxSplits; ++o) to[o] = mapa_shared(dst, min(o, splits - 1));
+      for (int o = 0; o < kMaxSplits; ++o) {
+        to[o] = mapa_shared(dst, min(o, splits - 1));
+        bars[o] = mapa_shared(recv_bar, min(o, splits - 1));
+      }
       int owner = c0 % splits;
 #pragma unroll
       for (int m = 0; m < COLS; ++m) {
-        if (c0 + m < p.M && live) {
+        if (c0 + m < p.M) {
           const uint32_t base = owner < 2 ? (owner == 0 ? to[0] : to[1]) : (owner == 2 ? to[2] : to[3]);
-          st_dsmem_f32(base + at, acc[m]);
+          const uint32_t bar = owner < 2 ? (owner == 0 ? bars[0] : bars[1]) : (owner == 2 ? bars[2] : bars[3]);
+          st_async_f32(base + at, acc[m], bar);
         }
         if (++owner == splits) owner = 0, at += 512;
       }
@@ -331,14 +363,15 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
   const bool failed = *abort_flag != 0;
   if (failed)                                    // no copy may still be in flight when the CTA exits
     for (int t = max(0, issued - S); t < issued; ++t) mbar_wait(full + 8 * (t % S), (t / S) & 1, p.err);
-  __syncwarp();
-  if (splits > 1) {
-    cluster_sync();                              // the pushes are in place
+  if (splits > 1 && own > 0) {
+    // No one writes into this CTA once its rows' sums are complete. A peer may
+    // use up two waits of its own before it sends them.
+    const bool complete = mbar_wait_ns(recv_bar, 0, p.err, 3 * kWaitLimitNs);
     const int per = (NT + splits - 1) / splits;
     const float* recv = reinterpret_cast<const float*>(smem + L::kRecv);
     const int r = threadIdx.x & 127;
-    if (!failed && n0 + r < p.N) {
-      for (int i = threadIdx.x >> 7; i * splits + rank < p.M; i += L::kThreads / 128) {
+    if (complete && !failed && n0 + r < p.N) {
+      for (int i = threadIdx.x >> 7; i < own; i += L::kThreads / 128) {
         float v = recv[i * 128 + r];
         for (int src = 1; src < splits; ++src) v += recv[(src * per + i) * 128 + r];
         p.C[static_cast<long long>(i * splits + rank) * p.ldc + n0 + r] = f32_to_bf16_rn(v);
