@@ -400,6 +400,25 @@ def test_chain_under_pdl_and_on_a_side_stream(M):
     assert wqp.get_device_error() == 0
 
 
+@pytest.mark.parametrize("M", [3, 200])
+def test_chain_in_a_cuda_graph(M):
+    """Captured once, replayed on new inputs in the same buffers."""
+    K, N = 1024, 512
+    x, r = rows(M, K, torch.bfloat16, 0, 1), rows(M, K, torch.bfloat16, 0, 2)
+    w = torch.ones(K, dtype=torch.bfloat16, device=DEV)
+    w8, s8, _ = w8_operand(N, K, 3, False, True)
+    w4, s4, _ = w4_operand(K, N, 4, False)
+    layer(x, r, w, w8, s8, w4, s4)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = layer(x, r, w, w8, s8, w4, s4)
+    for seed in (11, 12):
+        x.copy_(rows(M, K, torch.bfloat16, 0, seed))
+        graph.replay()
+        want = layer(x, r, w, w8, s8, w4, s4)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_binding_refuses():
     x = torch.zeros(4, 256, dtype=torch.bfloat16, device=DEV)
     w = torch.ones(256, dtype=torch.bfloat16, device=DEV)

@@ -139,9 +139,9 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
   // instructions are on the path from one stage to the next. Copies, MMAs and
   // stores are issued under elect.sync, whose one thread the compiler knows to
   // be one: behind a test of the lane number the same instructions took twice
-  // the kernel's time (4096x34816x5120, 4 bits: 494 us against 261). When a
-  // wait has run out (abort_flag) the loops go on to their ends, waiting no
-  // more, and nothing is stored.
+  // the kernel's time (4096x34816x5120, 4 bits: 494 us against 261). A wait that
+  // runs out ends its warp's loop (the epilogue's: at the end of the tile, with
+  // nothing stored), and the others' with it.
   if (warp < L::kRoles) {
     if (!F::kScaled) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && elect_one()) {
@@ -197,12 +197,13 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       bool loaded = false, freed = true;       // of the next stage; accumulators start free
       const long long stages = static_cast<long long>((total - first + step - 1) / step) * p.stages;
       for (long long it = 0; it < stages; ++it) {
-        if (!freed) wait_or_abort(acc_free + 8 * slot, acc_ph, p.err, abort_flag);
+        bool ok = true;
+        if (!freed) ok = wait_or_abort(acc_free + 8 * slot, acc_ph, p.err, abort_flag);
         if (!loaded) {
-          wait_or_abort(full + 8 * s, ph, p.err, abort_flag);
-          if (F::kScaled) wait_or_abort(scaled + 8 * s, ph, p.err, abort_flag);
+          ok = ok && wait_or_abort(full + 8 * s, ph, p.err, abort_flag);
+          if (F::kScaled) ok = ok && wait_or_abort(scaled + 8 * s, ph, p.err, abort_flag);
         }
-        __syncwarp();
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
         tc_fence_after();
         const int s1 = s + 1 == S ? 0 : s + 1, k1 = k + 1 == p.stages ? 0 : k + 1;
         const uint32_t ph1 = s1 ? ph : ph ^ 1;
@@ -255,8 +256,7 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
         int s = set;
         uint32_t ph = 0;
         for (long long it = set; it < stages; it += 2) {
-          wait_or_abort(raw_full + 8 * s, ph, p.err, abort_flag);
-          __syncwarp();
+          if (!__all_sync(0xFFFFFFFFu, wait_or_abort(raw_full + 8 * s, ph, p.err, abort_flag))) break;
           if (b == 0) rearrange_scales(smem + L::kSclA + s * kScaleBlock, lane, 128);
           else rearrange_scales(smem + L::kSclB + (s * NB + b - 1) * kScaleBlock, lane, min(128, BN - 128 * (b - 1)));
           fence_proxy_async_smem();
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
         for (int j = 0; j < COLS / 2; ++j)
           packed[j] = pack_bf16(__uint_as_float(static_cast<uint32_t>(acc[j])), __uint_as_float(static_cast<uint32_t>(acc[j] >> 32)));
       }
-      if (*abort_flag) continue;
+      if (__any_sync(0xFFFFFFFFu, *abort_flag)) break;
       // 32 rows of 64 bytes in the 64-byte swizzle (16-byte chunk j of row r at
       // j ^ (r / 2 mod 4)): free of bank conflicts here, and the store map's own.
       const auto chunk_at = [&](int r, int j) { return out + r * 64 + ((j ^ ((r >> 1) & 3)) << 4); };
