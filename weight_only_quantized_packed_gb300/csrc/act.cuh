@@ -111,17 +111,20 @@ __device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t ba
 }
 
 // A tile of this CTA's shared memory to global memory; rows and columns
-// outside the map are dropped. The thread that stored waits before the
-// shared memory is written again (read) or the CTA ends (all).
+// outside the map are dropped. One thread stores, closes a group after each
+// place where a store may have been, and waits until all but the last N groups
+// have been read before their shared memory is written again, or the CTA ends.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
                "r"(x), "r"(y), "r"(src)
                : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_close() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void tma_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
 
 // Whether a barrier's phase is complete, without waiting.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {

@@ -56,11 +56,11 @@ struct ManyLayout {
   static constexpr int kNB = (BN + 127) / 128;                  // 128-row blocks of the weights' scales
   static constexpr int kStageBytes = 16384 + BN * 64 + (F::kScaled ? kScaleBlock * (1 + kNB) : 0);
   static constexpr int kOutBytes = 32 * 64;                     // what an epilogue warp stores at a time
-  static constexpr int kS = (225 * 1024 - kEpi * kOutBytes) / kStageBytes;
+  static constexpr int kS = (225 * 1024 - 2 * kEpi * kOutBytes) / kStageBytes;
   static constexpr int kA = 0;
   static constexpr int kB = kA + kS * 16384;
-  static constexpr int kOut = kB + kS * BN * 64;                // [epilogue warp][32 rows][32 columns]
-  static constexpr int kSclA = kOut + kEpi * kOutBytes;
+  static constexpr int kOut = kB + kS * BN * 64;                // [epilogue warp][2][32 rows][32 columns]
+  static constexpr int kSclA = kOut + 2 * kEpi * kOutBytes;
   static constexpr int kSclB = kSclA + (F::kScaled ? kS * kScaleBlock : 0);
   static constexpr int kBytes = kSclB + (F::kScaled ? kS * kScaleBlock * kNB : 0);
   static constexpr int kAlloc = kBytes + 1024;
@@ -125,14 +125,23 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
     abort_sh = 0;
     mbar_fence_init();
   }
+  // The copying warp goes on as soon as every barrier of the pair exists (no
+  // peer's copy or arrive may come before); the others meet for the tensor
+  // memory's address first. The cluster barriers only order execution: the
+  // barriers' set-up is published by its own fence, and a release here costs
+  // half a microsecond.
+  __syncwarp();
+  cluster_arrive_relaxed();
   if (warp == 1) {
     pair_tmem_alloc(smem_u32(&tmem_sh), 512);
     tc_fence_before();
   }
-  __syncthreads();
-  cluster_sync();                              // every barrier exists before a peer's copy or arrive
-  tc_fence_after();
-  const uint32_t tmem = tmem_sh;
+  if (warp != 0) {
+    asm volatile("bar.sync 1, %0;" ::"n"(L::kThreads - 32) : "memory");
+    tc_fence_after();
+  }
+  cluster_wait();
+  const uint32_t tmem = warp != 0 ? tmem_sh : 0u;
   pdl_launch_dependents();
 
   // The loops below keep their place in a ring as an index and a parity: their
@@ -273,7 +282,8 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
     const int q = warp & 3, ew = warp - L::kRoles, h = ew >> 2;
     const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * COLS;
     const uint32_t acc_free0 = mapa_shared(acc_free, 0);
-    uint8_t* out = smem + L::kOut + ew * L::kOutBytes;
+    uint8_t* const outs = smem + L::kOut + ew * 2 * L::kOutBytes;   // two, in turn
+    uint8_t* out = outs;
     const int kb = p.K >> 7;
     if (!F::kScaled) pdl_wait();               // the activations' scales
     int slot = 0;
@@ -282,6 +292,9 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       int mi, ni;
       tile_at<F>(i, p.mt, p.nt, mi, ni);
       const int m0 = mi * 256 + rank * 128 + q * 32, n0 = ni * BN + h * COLS;
+      // Tiles after this one, as far as it matters: an accumulator that no later
+      // one takes over is not announced as free.
+      const int left = min((total - 1 - i) / step, NACC);
       uint32_t packed[COLS / 2];
       if constexpr (F::kScaled) {
         wait_or_abort(acc_full + 8 * slot, ph, p.err, abort_flag);
@@ -298,7 +311,7 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) pair_arrive(acc_free0 + 8 * slot);
+        if (lane == 0 && i + NACC * step < total) pair_arrive(acc_free0 + 8 * slot);
         if (++slot == NACC) slot = 0, ph ^= 1;
       } else {
         const float* sa = p.SA + static_cast<long long>(min(m0 + lane, p.M - 1)) * kb;
@@ -354,7 +367,7 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
               if (c0 + 32 >= COLS) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) pair_arrive(acc_free0 + 8 * slot);
+                if (lane == 0 && (k + NACC < kb || i + step < total)) pair_arrive(acc_free0 + 8 * slot);
               }
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
@@ -379,7 +392,8 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       const auto chunk_at = [&](int r, int j) { return out + r * 64 + ((j ^ ((r >> 1) & 3)) << 4); };
 #pragma unroll
       for (int c = 0; c < COLS; c += 32) {
-        if (elect_one()) tma_store_wait_read();
+        out = out == outs ? outs + L::kOutBytes : outs;
+        if (elect_one()) tma_store_wait_read<1>();
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -407,13 +421,18 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
               p.C[static_cast<long long>(m0 + r) * p.ldc + n] = *reinterpret_cast<const uint16_t*>(chunk_at(r, lane >> 3) + (lane & 7) * 2);
           __syncwarp();
         }
+        if (elect_one()) tma_store_close();
       }
     }
-    if (elect_one()) tma_store_wait_all();
+    if (elect_one()) tma_store_wait_read<0>();  // the grid ends with the writes
   }
+  // Both CTAs are done with the pair's tensor memory. Nothing of the pair is on
+  // its way any more: every copy and commit has been waited for, and no arrive
+  // was sent that nobody waits for.
   __syncwarp();
   __syncthreads();
-  cluster_sync();                              // no arrive or copy of the pair is on its way any more
+  cluster_arrive_relaxed();
+  cluster_wait();
   if (warp == 1) {
     tc_fence_after();
     pair_tmem_dealloc(tmem, 512);
