@@ -216,25 +216,33 @@ constexpr int kScaleBlock = 2048;      // bytes of a 128-row block
 
 __device__ __forceinline__ uint32_t scales_no_sign(uint32_t w) { return w | (((w & 0x80808080u) >> 7) * 0x7Fu); }
 
-// A block that a tensor copy brought as rows of 16 bytes, rearranged in place
-// by one warp. Only the first `rows` rows of the block exist.
+// A block of two stages that a tensor copy brought as rows of 32 bytes, made
+// into the blocks of the two (2048 bytes each) in place by one warp. Only the
+// first `rows` rows of the block exist. (Copied a stage at a time, as rows of 16
+// bytes, the scales take twice the copies' time.)
 __device__ __forceinline__ void rearrange_scales(uint8_t* block, int lane, int rows) {
-  uint4 v[4];
+  uint4 v[2][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (32 * i + lane < rows) v[i] = *reinterpret_cast<const uint4*>(block + (32 * i + lane) * 16);
-    v[i].x = scales_no_sign(v[i].x);
-    v[i].y = scales_no_sign(v[i].y);
-    v[i].z = scales_no_sign(v[i].z);
-    v[i].w = scales_no_sign(v[i].w);
+    const uint4* p = reinterpret_cast<const uint4*>(block + (32 * i + lane) * 32);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      v[e][i] = 32 * i + lane < rows ? p[e] : make_uint4(0, 0, 0, 0);
+      v[e][i].x = scales_no_sign(v[e][i].x);
+      v[e][i].y = scales_no_sign(v[e][i].y);
+      v[e][i].z = scales_no_sign(v[e][i].z);
+      v[e][i].w = scales_no_sign(v[e][i].w);
+    }
   }
   __syncwarp();
-  uint8_t* d = block + lane * 16;
-  *reinterpret_cast<uint4*>(d) = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
-  *reinterpret_cast<uint4*>(d + 512) = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
-  *reinterpret_cast<uint4*>(d + 1024) = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
-  *reinterpret_cast<uint4*>(d + 1536) = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    uint8_t* d = block + e * kScaleBlock + lane * 16;
+    *reinterpret_cast<uint4*>(d) = make_uint4(v[e][0].x, v[e][1].x, v[e][2].x, v[e][3].x);
+    *reinterpret_cast<uint4*>(d + 512) = make_uint4(v[e][0].y, v[e][1].y, v[e][2].y, v[e][3].y);
+    *reinterpret_cast<uint4*>(d + 1024) = make_uint4(v[e][0].z, v[e][1].z, v[e][2].z, v[e][3].z);
+    *reinterpret_cast<uint4*>(d + 1536) = make_uint4(v[e][0].w, v[e][1].w, v[e][2].w, v[e][3].w);
+  }
 }
 
 // The same straight from global memory, through registers: warp `half` has

@@ -9,9 +9,10 @@
 //  * 4 bits: the tensor core applies the scales, rearranged by warps of each CTA
 //    (its 128 activation rows, all BN weight rows) and copied to tensor memory
 //    by the MMA warp. One or two accumulators, drained into registers as BF16.
-//    4096x34816x5120: 248 us, 5.9 PFLOP/s until the power cap slows the clock.
-//    Tensor pipe 61 % busy (ncu); next are the bytes into an SM (38 KB a stage,
-//    at 64 a clock 83 % of a stage's time) and the drains between tiles.
+//    4096x34816x5120: 233 us, 6.3 PFLOP/s until the power cap slows the clock.
+//    The tensor pipe is busy for two thirds of it; next are the bytes into an
+//    SM (38 KB a stage, at 64 a clock nine tenths of a stage's time) and the
+//    drains between tiles.
 //  * 8 bits: two to four accumulators that take turns per 128 K; the epilogue
 //    adds each, times its activation row's and weight block's scale, to FP32
 //    sums in registers while the tensor core fills the others.
@@ -54,15 +55,20 @@ struct ManyLayout {
   static constexpr int kEpi = 8;                                // epilogue warps
   static constexpr int kThreads = (kRoles + kEpi) * 32;
   static constexpr int kNB = (BN + 127) / 128;                  // 128-row blocks of the weights' scales
-  static constexpr int kStageBytes = 16384 + BN * 64 + (F::kScaled ? kScaleBlock * (1 + kNB) : 0);
+  static constexpr int kStageBytes = 16384 + BN * 64;
+  // 4 bits: the scales of two stages at a time, in a ring of their own (three
+  // slots: 236 us at 4096x34816x5120, four 233; a stage at a time 245).
+  static constexpr int kR = 4;
+  static constexpr int kSclBytes = F::kScaled ? kR * 2 * kScaleBlock * (1 + kNB) : 0;
+  static constexpr int kOutBufs = F::kScaled && BN == 256 ? 1 : 2;   // two there would cost a stage
   static constexpr int kOutBytes = 32 * 64;                     // what an epilogue warp stores at a time
-  static constexpr int kS = (225 * 1024 - 2 * kEpi * kOutBytes) / kStageBytes;
+  static constexpr int kS = (225 * 1024 - kOutBufs * kEpi * kOutBytes - kSclBytes) / kStageBytes;
   static constexpr int kA = 0;
   static constexpr int kB = kA + kS * 16384;
-  static constexpr int kOut = kB + kS * BN * 64;                // [epilogue warp][2][32 rows][32 columns]
-  static constexpr int kSclA = kOut + 2 * kEpi * kOutBytes;
-  static constexpr int kSclB = kSclA + (F::kScaled ? kS * kScaleBlock : 0);
-  static constexpr int kBytes = kSclB + (F::kScaled ? kS * kScaleBlock * kNB : 0);
+  static constexpr int kOut = kB + kS * BN * 64;                // [epilogue warp][buffer][32 rows][32 columns]
+  static constexpr int kSclA = kOut + kOutBufs * kEpi * kOutBytes;   // [kR][2 stages]
+  static constexpr int kSclB = kSclA + (F::kScaled ? kR * 2 * kScaleBlock : 0);   // [kR][block][2 stages]
+  static constexpr int kBytes = kSclA + kSclBytes;
   static constexpr int kAlloc = kBytes + 1024;
   // Accumulators of BN columns in tensor memory, and (4 bits) behind them two
   // sets of a stage's scales.
@@ -92,11 +98,12 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
                 const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                 const __grid_constant__ CUtensorMap tmC, ManyParams p) {
   using L = ManyLayout<F, BN>;
-  constexpr int S = L::kS, NACC = L::kAcc, COLS = L::kCols, NB = L::kNB;
+  constexpr int S = L::kS, R = L::kR, NACC = L::kAcc, COLS = L::kCols, NB = L::kNB;
   extern __shared__ uint8_t smem_raw[];
   // full, scaled and acc_free count both CTAs' work and are used in the even
-  // CTA; raw_full is each CTA's own; empty and acc_full are told to both.
-  __shared__ __align__(8) uint64_t full_sh[S], raw_full_sh[S], empty_sh[S], scaled_sh[S], acc_full_sh[NACC],
+  // CTA; raw_full is each CTA's own; empty, scl_empty and acc_full are told to
+  // both.
+  __shared__ __align__(8) uint64_t full_sh[S], empty_sh[S], raw_full_sh[R], scaled_sh[R], scl_empty_sh[R], acc_full_sh[NACC],
       acc_free_sh[NACC], drained_sh;
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
@@ -106,16 +113,19 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
   const int rank = static_cast<int>(cluster_rank());
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1, total = p.mt * p.nt;
   const uint32_t full = smem_u32(full_sh), raw_full = smem_u32(raw_full_sh), empty = smem_u32(empty_sh);
-  const uint32_t scaled = smem_u32(scaled_sh), acc_full = smem_u32(acc_full_sh), acc_free = smem_u32(acc_free_sh);
+  const uint32_t scaled = smem_u32(scaled_sh), scl_empty = smem_u32(scl_empty_sh), acc_full = smem_u32(acc_full_sh), acc_free = smem_u32(acc_free_sh);
   const uint32_t drained = smem_u32(&drained_sh);
   volatile int* abort_flag = &abort_sh;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(full + 8 * i, 2);
-      mbar_init(raw_full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < R; ++i) {
+      mbar_init(raw_full + 8 * i, 1);
       mbar_init(scaled + 8 * i, 2 * (1 + NB));
+      mbar_init(scl_empty + 8 * i, 1);
     }
     for (int i = 0; i < NACC; ++i) {
       mbar_init(acc_full + 8 * i, 1);
@@ -158,13 +168,24 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       prefetch_tmap(&tmB);
       pdl_wait();
       const uint32_t full0 = mapa_shared(full, 0);
-      int s = 0, used = 0;                     // stages used, up to S
-      uint32_t ph = 1;                         // parity of the stage's last consumption
+      int s = 0, used = 0, r = 0, rused = 0;   // stages and scale slots used, up to S and R
+      uint32_t ph = 1, rph = 1;                // parity of the stage's (slot's) last consumption
       for (int i = first; i < total && !*abort_flag; i += step) {
         int mi, ni;
         tile_at<F>(i, p.mt, p.nt, mi, ni);
         const int m0 = mi * 256 + rank * 128, n0 = ni * BN;
         for (int k = 0; k < p.stages; ++k) {
+          if (F::kScaled && k % 2 == 0) {
+            if (rused == R) {
+              if (!wait_or_abort(scl_empty + 8 * r, rph, p.err, abort_flag)) break;
+            } else {
+              ++rused;
+            }
+            mbar_arrive_expect_tx(raw_full + 8 * r, (128 + BN) * 32);
+            tma_load_2d(sb + L::kSclA + r * 2 * kScaleBlock, &tmSA, k * 16, m0, raw_full + 8 * r);
+            tma_load_2d(sb + L::kSclB + r * 2 * kScaleBlock * NB, &tmSB, k * 16, n0, raw_full + 8 * r);
+            if (++r == R) r = 0, rph ^= 1;
+          }
           if (used == S) {
             if (!wait_or_abort(empty + 8 * s, ph, p.err, abort_flag)) break;
           } else {
@@ -174,11 +195,6 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
           pair_arrive_expect_tx(full0 + 8 * s, 16384 + BN * 64);
           pair_tma_load_2d(sb + L::kA + s * 16384, &tmA, k * 128, m0, full0 + 8 * s);
           pair_tma_load_2d(sb + L::kB + s * BN * 64, &tmB, k * 128, n0 + rank * (BN / 2), full0 + 8 * s);
-          if (F::kScaled) {
-            mbar_arrive_expect_tx(raw_full + 8 * s, (128 + BN) * 16);
-            tma_load_2d(sb + L::kSclA + s * kScaleBlock, &tmSA, k * 16, m0, raw_full + 8 * s);
-            tma_load_2d(sb + L::kSclB + s * kScaleBlock * NB, &tmSB, k * 16, n0, raw_full + 8 * s);
-          }
           if (++s == S) s = 0, ph ^= 1;
         }
       }
@@ -187,11 +203,14 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       for (int t = 0; t < used; ++t) {
         const int at = used < S ? t : s;
         const uint32_t par = used < S ? 0u : ph;
-        if (!wait_or_abort(empty + 8 * at, par, p.err, abort_flag)) {
-          if (rank == 0) mbar_wait(full + 8 * at, par, p.err);
-          if (F::kScaled) mbar_wait(raw_full + 8 * at, par, p.err);
-        }
+        if (!wait_or_abort(empty + 8 * at, par, p.err, abort_flag) && rank == 0) mbar_wait(full + 8 * at, par, p.err);
         if (used == S && ++s == S) s = 0, ph ^= 1;
+      }
+      for (int t = 0; t < rused; ++t) {
+        const int at = rused < R ? t : r;
+        const uint32_t par = rused < R ? 0u : rph;
+        if (!wait_or_abort(scl_empty + 8 * at, par, p.err, abort_flag)) mbar_wait(raw_full + 8 * at, par, p.err);
+        if (rused == R && ++r == R) r = 0, rph ^= 1;
       }
     } else if (warp == 1 && rank == 0) {
       constexpr uint32_t idesc = F::kScaled ? idesc_f4(256, BN) : idesc_f8(256, BN);
@@ -201,8 +220,8 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       // back from it only when the MMAs have been taken), so what the next
       // stage needs is looked up before this stage's are issued, and waited for
       // only if it was not there yet.
-      int s = 0, slot = 0, k = 0;
-      uint32_t ph = 0, acc_ph = 1, set = 0;
+      int s = 0, slot = 0, k = 0, r = 0;
+      uint32_t ph = 0, acc_ph = 1, rph = 0, set = 0;
       bool loaded = false, freed = true;       // of the next stage; accumulators start free
       const long long stages = static_cast<long long>((total - first + step - 1) / step) * p.stages;
       for (long long it = 0; it < stages; ++it) {
@@ -210,7 +229,7 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
         if (!freed) ok = wait_or_abort(acc_free + 8 * slot, acc_ph, p.err, abort_flag);
         if (!loaded) {
           ok = ok && wait_or_abort(full + 8 * s, ph, p.err, abort_flag);
-          if (F::kScaled) ok = ok && wait_or_abort(scaled + 8 * s, ph, p.err, abort_flag);
+          if (F::kScaled && k % 2 == 0) ok = ok && wait_or_abort(scaled + 8 * r, rph, p.err, abort_flag);
         }
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         tc_fence_after();
@@ -219,21 +238,25 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
         const bool hand = !F::kScaled || k1 == 0;                    // this stage completes an accumulator
         const int slot1 = !hand ? slot : (slot + 1 == NACC ? 0 : slot + 1);
         const uint32_t acc_ph1 = hand && slot1 == 0 ? acc_ph ^ 1 : acc_ph;
+        const bool next = k1 % 2 == 0;                               // it is the last that uses its scale slot
+        const int r1 = !next ? r : (r + 1 == R ? 0 : r + 1);
+        const uint32_t rph1 = next && r1 == 0 ? rph ^ 1 : rph;
         bool l1 = mbar_test(full + 8 * s1, ph1);
-        if (F::kScaled) l1 = l1 && mbar_test(scaled + 8 * s1, ph1);
+        if (F::kScaled && next) l1 = l1 && mbar_test(scaled + 8 * r1, rph1);
         // Parity 1 of a barrier that has completed no phase counts as complete.
         const bool f1 = !hand || mbar_test(acc_free + 8 * slot1, acc_ph1);
         if (elect_one()) {
           // Addresses in a descriptor are in units of 16 bytes.
           const uint64_t ad = ad0 + s * (16384 >> 4), bd = bd0 + s * ((BN * 64) >> 4);
           if constexpr (F::kScaled) {
-            const uint64_t sad = sad0 + s * (kScaleBlock >> 4), sbd = sbd0 + s * ((NB * kScaleBlock) >> 4);
+            const uint64_t sad = sad0 + (r * 2 + k % 2) * (kScaleBlock >> 4);
+            const uint64_t sbd = sbd0 + (r * 2 * NB + k % 2) * (kScaleBlock >> 4);
             const uint32_t sa = tmem + L::kScaleCol + set * 64, sw = sa + 16;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               pair_copy_scales(sa + 4 * j, sad + 32 * j);
 #pragma unroll
-              for (int b = 0; b < NB; ++b) pair_copy_scales(sw + (j * NB + b) * 4, sbd + b * (kScaleBlock >> 4) + 32 * j);
+              for (int b = 0; b < NB; ++b) pair_copy_scales(sw + (j * NB + b) * 4, sbd + 2 * b * (kScaleBlock >> 4) + 32 * j);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -243,13 +266,14 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
             for (int j = 0; j < 4; ++j) pair_mma_f8(tmem + slot * BN, ad + 2 * j, bd + 2 * j, idesc, j ? 1u : 0u);
           }
           if (hand) pair_commit(acc_full + 8 * slot);
+          if (F::kScaled && next) pair_commit(scl_empty + 8 * r);
           pair_commit(empty + 8 * s);
         }
         __syncwarp();
         loaded = __all_sync(0xFFFFFFFFu, l1);
         freed = __all_sync(0xFFFFFFFFu, f1);
         set ^= 1;
-        s = s1, ph = ph1, k = k1, slot = slot1, acc_ph = acc_ph1;
+        s = s1, ph = ph1, k = k1, slot = slot1, acc_ph = acc_ph1, r = r1, rph = rph1;
       }
       // The pair's MMAs are done before the cluster barrier below, and tensor
       // memory is freed after it.
@@ -257,22 +281,22 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       __syncwarp();
       mbar_wait(drained, 0, p.err);
     } else if (F::kScaled && warp >= 2) {
-      // Two sets of warps take the stages in turn, one 128-row block a warp.
+      // Two sets of warps take the scale slots in turn, one 128-row block a warp.
       const int set = (warp - 2) / 3, b = (warp - 2) % 3;
       if (b < 1 + NB) {
         const uint32_t scaled0 = mapa_shared(scaled, 0);
-        const long long stages = static_cast<long long>((total - first + step - 1) / step) * p.stages;
-        int s = set;
-        uint32_t ph = 0;
-        for (long long it = set; it < stages; it += 2) {
-          if (!__all_sync(0xFFFFFFFFu, wait_or_abort(raw_full + 8 * s, ph, p.err, abort_flag))) break;
-          if (b == 0) rearrange_scales(smem + L::kSclA + s * kScaleBlock, lane, 128);
-          else rearrange_scales(smem + L::kSclB + (s * NB + b - 1) * kScaleBlock, lane, min(128, BN - 128 * (b - 1)));
+        const long long slots = static_cast<long long>((total - first + step - 1) / step) * ((p.stages + 1) / 2);
+        int r = set;
+        uint32_t rph = 0;
+        for (long long it = set; it < slots; it += 2) {
+          if (!__all_sync(0xFFFFFFFFu, wait_or_abort(raw_full + 8 * r, rph, p.err, abort_flag))) break;
+          if (b == 0) rearrange_scales(smem + L::kSclA + r * 2 * kScaleBlock, lane, 128);
+          else rearrange_scales(smem + L::kSclB + (r * NB + b - 1) * 2 * kScaleBlock, lane, min(128, BN - 128 * (b - 1)));
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) pair_arrive(scaled0 + 8 * s);
-          s += 2;
-          if (s >= S) s -= S, ph ^= 1;
+          if (lane == 0) pair_arrive(scaled0 + 8 * r);
+          r += 2;
+          if (r >= R) r -= R, rph ^= 1;
         }
       }
     }
@@ -282,7 +306,7 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
     const int q = warp & 3, ew = warp - L::kRoles, h = ew >> 2;
     const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * COLS;
     const uint32_t acc_free0 = mapa_shared(acc_free, 0);
-    uint8_t* const outs = smem + L::kOut + ew * 2 * L::kOutBytes;   // two, in turn
+    uint8_t* const outs = smem + L::kOut + ew * L::kOutBufs * L::kOutBytes;   // one, or two in turn
     uint8_t* out = outs;
     const int kb = p.K >> 7;
     if (!F::kScaled) pdl_wait();               // the activations' scales
@@ -392,8 +416,8 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       const auto chunk_at = [&](int r, int j) { return out + r * 64 + ((j ^ ((r >> 1) & 3)) << 4); };
 #pragma unroll
       for (int c = 0; c < COLS; c += 32) {
-        out = out == outs ? outs + L::kOutBytes : outs;
-        if (elect_one()) tma_store_wait_read<1>();
+        if (L::kOutBufs == 2) out = out == outs ? outs + L::kOutBytes : outs;
+        if (elect_one()) tma_store_wait_read<L::kOutBufs - 1>();
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -452,8 +476,8 @@ cudaError_t launch_many_t(const ActGemmArgs& a, cudaStream_t s) {
   msa = ma;
   msb = mb;
   if (F::kScaled) {
-    if (e == cudaSuccess) e = make_map_2d(&msa, kU8, a.SA, srow, M, srow, 16, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
-    if (e == cudaSuccess) e = cached_map_2d(&msb, kU8, a.SW, srow, N, srow, 16, BN, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e == cudaSuccess) e = make_map_2d(&msa, kU8, a.SA, srow, M, srow, 32, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e == cudaSuccess) e = cached_map_2d(&msb, kU8, a.SW, srow, N, srow, 32, BN, CU_TENSOR_MAP_SWIZZLE_NONE);
   }
   const bool vec = a.N >= 8 && a.ldc % 8 == 0 && reinterpret_cast<uintptr_t>(a.C) % 16 == 0;
   mc = ma;
