@@ -21,7 +21,7 @@
 //    the additions 238 us.
 // Output goes through shared memory, 32 rows by 32 columns a warp at a time,
 // and leaves as bulk tensor stores (rows of C that are not 16-byte aligned: as
-// whole row segments from there).
+// stores of 8, 4 or 2 bytes a lane from there).
 //
 // Warps: 0 copies, 1 MMA (even CTA; tensor memory in both), 4 bits: 2..7
 // scales; then 8 epilogue warps, one per lane quarter (warp % 4) and half of the
@@ -41,7 +41,7 @@ struct ManyParams {
   int M, N, K, ldc;
   int mt, nt;           // 256-row tiles, weight tiles
   int stages;           // per tile
-  int vec;              // C rows are 16-byte aligned
+  int align;            // of C's rows, bytes: 16, 8, 4 or 2
   unsigned* err;
 };
 
@@ -90,6 +90,30 @@ __device__ __forceinline__ void tile_at(int i, int mt, int nt, int& m, int& n) {
   const int j = i - g * per;
   n = j / rows;
   m = g * G + (j - n * rows);
+}
+
+// A 32 x 32 chunk at columns n.. of rows m0.. of C, whose rows are 2 E-byte
+// aligned, E elements a lane: chunk_at(r, j) is 16-byte piece j of row r.
+template <int E, class At>
+__device__ __forceinline__ void store_rows(const At& chunk_at, const ManyParams& p, int m0, int n, int lane) {
+  constexpr int kLanes = 32 / E, kRows = 32 / kLanes;        // lanes of a row, rows at a time
+  const int r0 = lane / kLanes, col = lane % kLanes * E, left = p.N - n - col;
+  const int rows = min(32, p.M - m0) - r0;
+  uint16_t* c = p.C + static_cast<long long>(m0 + r0) * p.ldc + n + col;
+#pragma unroll 8
+  for (int r = 0; r < 32; r += kRows, c += static_cast<long long>(kRows) * p.ldc) {
+    if (r >= rows) break;
+    const uint8_t* v = chunk_at(r0 + r, col >> 3) + (col & 7) * 2;
+    if (E == 4 && left >= 4) {
+      *reinterpret_cast<uint2*>(c) = *reinterpret_cast<const uint2*>(v);
+    } else if (E == 2 && left >= 2) {
+      *reinterpret_cast<uint32_t*>(c) = *reinterpret_cast<const uint32_t*>(v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (e < left) c[e] = reinterpret_cast<const uint16_t*>(v)[e];
+    }
+  }
 }
 
 template <class F, int BN>
@@ -426,7 +450,7 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
         // A tensor store writes whole 16-byte units, past the end of the row too:
         // its map ends at the last whole unit, and the few columns after that are
         // stored by themselves.
-        if (p.vec && n0 + c < p.N) {
+        if (p.align == 16 && n0 + c < p.N) {
           fence_proxy_async_smem();
           __syncwarp();
           const int whole = p.N & ~7;
@@ -439,10 +463,9 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
           __syncwarp();
         } else if (n0 + c < p.N) {
           __syncwarp();
-          const int n = n0 + c + lane;
-          for (int r = 0; r < 32 && m0 + r < p.M; ++r)
-            if (n < p.N)
-              p.C[static_cast<long long>(m0 + r) * p.ldc + n] = *reinterpret_cast<const uint16_t*>(chunk_at(r, lane >> 3) + (lane & 7) * 2);
+          if (p.align >= 8) store_rows<4>(chunk_at, p, m0, n0 + c, lane);
+          else if (p.align >= 4) store_rows<2>(chunk_at, p, m0, n0 + c, lane);
+          else store_rows<1>(chunk_at, p, m0, n0 + c, lane);
           __syncwarp();
         }
         if (elect_one()) tma_store_close();
@@ -479,9 +502,10 @@ cudaError_t launch_many_t(const ActGemmArgs& a, cudaStream_t s) {
     if (e == cudaSuccess) e = make_map_2d(&msa, kU8, a.SA, srow, M, srow, 32, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e == cudaSuccess) e = cached_map_2d(&msb, kU8, a.SW, srow, N, srow, 32, BN, CU_TENSOR_MAP_SWIZZLE_NONE);
   }
-  const bool vec = a.N >= 8 && a.ldc % 8 == 0 && reinterpret_cast<uintptr_t>(a.C) % 16 == 0;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.C) | static_cast<uintptr_t>(a.ldc) * 2;
+  const int align = at % 16 == 0 && a.N >= 8 ? 16 : (at % 8 == 0 ? 8 : (at % 4 == 0 ? 4 : 2));
   mc = ma;
-  if (e == cudaSuccess && vec)
+  if (e == cudaSuccess && align == 16)
     e = make_map_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.C, N & ~uint64_t(7), M, static_cast<uint64_t>(a.ldc) * 2, 32, 32,
                     CU_TENSOR_MAP_SWIZZLE_64B);
   static AttrLatch latch;
@@ -501,7 +525,7 @@ cudaError_t launch_many_t(const ActGemmArgs& a, cudaStream_t s) {
   p.mt = (a.M + 255) / 256;
   p.nt = (a.N + BN - 1) / BN;
   p.stages = a.K / F::kStageK;
-  p.vec = vec;
+  p.align = align;
   p.err = a.err;
   const long long total = static_cast<long long>(p.mt) * p.nt;
   const int pairs = static_cast<int>(total < a.num_sms / 2 ? total : a.num_sms / 2);
