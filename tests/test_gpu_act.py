@@ -306,6 +306,21 @@ def test_products_long_and_short_k(fmt, K, M):
 
 
 @pytest.mark.parametrize("fmt", [4, 8])
+@pytest.mark.parametrize("M,N,K", [(3, 2, 15616), (20, 1100, 5120), (53, 5, 16896), (65, 300, 10240), (129, 100, 5120), (257, 145, 11264),
+                                   (300, 640, 10240), (1000, 256, 5120), (1146, 21, 14336), (1985, 39, 12800)])
+def test_products_with_k_split(fmt, M, N, K):
+    """Few tiles and a long K, with one and with many rows per tile, into rows that are 13 elements longer."""
+    buf = torch.full((M + 2, N + 13), 7.0, dtype=torch.bfloat16, device=DEV).view(-1)
+    out = torch.as_strided(buf, (M, N), (N + 13, 1), N + 14)
+    for ints in (True, False):
+        C, av, wv = run(fmt, M, N, K, seed=M + N, ints=ints, out=out)
+        check(C, av, wv, K, ints)
+    out.fill_(7.0)
+    assert (buf == 7.0).all()
+    assert wqp.get_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", [4, 8])
 @pytest.mark.parametrize("M,N,pad,shift", [(3, 131, 5, 0), (40, 256, 8, 8), (300, 256, 8, 0), (300, 260, 4, 0), (300, 256, 1, 0),
                                            (300, 256, 8, 1), (300, 256, 8, 3), (270, 131, 13, 0)])
 def test_products_into_pitched_rows(fmt, M, N, pad, shift):

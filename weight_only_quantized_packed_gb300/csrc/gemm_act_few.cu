@@ -4,7 +4,7 @@
 //
 // Bound by the weights' bytes. Swap-AB: the 128 weight rows of a tile are the
 // MMA's M side and the call's activation rows, zero-padded to NT by the
-// copies, its N side, so one pass over the weights serves them all:
+// copies, its N side, so one pass over the weights serves NT of them:
 //   D[n, m] = sum_k W[n, k] A[m, k]      (tcgen05.mma, FP32 accumulators)
 // Both operands go from global to shared memory as they lie (128-byte rows,
 // 128-byte swizzle) and into the tensor core undecoded.
@@ -13,8 +13,8 @@
 //    MMA warp copies them to tensor memory. One accumulator for all of K.
 //  * 8 bits: one MMA group per 128 K; the epilogue reads it and adds it, times
 //    its two scales, to FP32 accumulators in registers.
-// With few tiles, K is split over a cluster of up to 4 CTAs. Rank q owns the
-// activation rows q, q + splits, ...; the others push their partial sums of
+// With few tiles, K is split over a cluster of up to 8 CTAs. Rank q owns the
+// tile's activation rows q, q + splits, ...; the others push their partial sums of
 // those into its shared memory (asynchronous stores that complete on its
 // barrier), and it adds them in rank order, so the result does not depend on
 // timing.
@@ -28,10 +28,8 @@ namespace act {
 namespace {
 
 constexpr int kEpiWarp0 = 4;
-// CTAs of a tile. More than 4 do not all become resident at once (clusters lie
-// within a GPC): 1x5120x5120, 4 bits, up to 8 | 4 | 3 | 2 | 1: 9.4 | 7.5 | 7.3 |
-// 8.0 | 10.3 us.
-constexpr int kMaxSplits = 4;
+// CTAs of a tile, at most: a portable cluster.
+constexpr int kMaxSplits = 8;
 
 struct FewParams {
   const void* SA;
@@ -88,12 +86,12 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int splits = p.splits;
   const int tile = blockIdx.x / splits, rank = blockIdx.x - tile * splits;
-  const int n0 = tile * 128;
+  const int n0 = tile * 128, m0 = blockIdx.y * NT, rows = min(NT, p.M - m0);   // activation rows m0..
   const int st0 = static_cast<int>(static_cast<long long>(rank) * p.stages / splits);
   const int nst = static_cast<int>(static_cast<long long>(rank + 1) * p.stages / splits) - st0;
   const uint32_t full = smem_u32(full_sh), empty = smem_u32(empty_sh), scaled = smem_u32(scaled_sh);
   const uint32_t acc_full = smem_u32(acc_full_sh), acc_free = smem_u32(acc_free_sh), recv_bar = smem_u32(&recv_sh);
-  const int own = (p.M - rank + splits - 1) / splits;      // activation rows rank, rank + splits, ...
+  const int own = (rows - rank + splits - 1) / splits;     // of them: rank, rank + splits, ...
   volatile int* abort_flag = &abort_sh;
 
   // The thread that copies: sets up the barriers and starts the first stages'
@@ -111,7 +109,7 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
   };
   const auto load_a = [&](int t) {
     const int s = t % S;
-    tma_load_2d(sb + L::kA + s * NT * 128, &tmA, (st0 + t) * 128, 0, full + 8 * s);
+    tma_load_2d(sb + L::kA + s * NT * 128, &tmA, (st0 + t) * 128, m0, full + 8 * s);
   };
   if (warp == 0) {
     if (elect_one()) {
@@ -216,7 +214,7 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
       const int half = warp - 2, pitch = p.K >> 4;
       ScaleRows rw, ra;
       rw.at(static_cast<const uint8_t*>(p.SW), n0, p.N, pitch, half, lane);
-      ra.at(static_cast<const uint8_t*>(p.SA), 0, p.M, pitch, half, lane);
+      ra.at(static_cast<const uint8_t*>(p.SA), m0, p.M, pitch, half, lane);
       const bool any = 64 * half < NT;           // this warp's activation columns exist
       uint4 vw[D][2], va[D][2];
 #pragma unroll
@@ -276,7 +274,7 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
       float fa[D][kPer], fw[D];
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        sa[i] = static_cast<const float*>(p.SA) + static_cast<long long>(min(c0 + 32 * i + lane, p.M - 1)) * kb + st0;
+        sa[i] = static_cast<const float*>(p.SA) + static_cast<long long>(min(m0 + c0 + 32 * i + lane, p.M - 1)) * kb + st0;
       float* fac = reinterpret_cast<float*>(smem + L::kFac) + (warp - kEpiWarp0) * COLS;
 #pragma unroll
       for (int d = 0; d < D; ++d) fw[d] = d < nst ? __ldg(sw + d) : 0.0f;
@@ -330,27 +328,18 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
       // After an abort too: the owner counts on it.
       const int per = (NT + splits - 1) / splits;
       const uint32_t dst = sb + L::kRecv + 4 * (rank * per * 128 + r);
-      uint32_t at = c0 / splits * 512, to[kMaxSplits], bars[kMaxSplits];
-#pragma unroll
-      for (int o = 0; o < kMaxSplits; ++o) {
-        to[o] = mapa_shared(dst, min(o, splits - 1));
-        bars[o] = mapa_shared(recv_bar, min(o, splits - 1));
-      }
+      uint32_t at = c0 / splits * 512;
       int owner = c0 % splits;
 #pragma unroll
       for (int m = 0; m < COLS; ++m) {
-        if (c0 + m < p.M) {
-          const uint32_t base = owner < 2 ? (owner == 0 ? to[0] : to[1]) : (owner == 2 ? to[2] : to[3]);
-          const uint32_t bar = owner < 2 ? (owner == 0 ? bars[0] : bars[1]) : (owner == 2 ? bars[2] : bars[3]);
-          st_async_f32(base + at, acc[m], bar);
-        }
+        if (c0 + m < rows) st_async_f32(mapa_shared(dst + at, owner), acc[m], mapa_shared(recv_bar, owner));
         if (++owner == splits) owner = 0, at += 512;
       }
     } else if (live && n0 + r < p.N) {
-      uint16_t* c = p.C + static_cast<long long>(c0) * p.ldc + n0 + r;
+      uint16_t* c = p.C + static_cast<long long>(m0 + c0) * p.ldc + n0 + r;
 #pragma unroll
       for (int m = 0; m < COLS; ++m)
-        if (c0 + m < p.M) c[static_cast<long long>(m) * p.ldc] = f32_to_bf16_rn(acc[m]);
+        if (c0 + m < rows) c[static_cast<long long>(m) * p.ldc] = f32_to_bf16_rn(acc[m]);
     }
   }
   if (splits > 1 && warp < kEpiWarp0) cluster_wait();
@@ -374,10 +363,52 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
       for (int i = threadIdx.x >> 7; i < own; i += L::kThreads / 128) {
         float v = recv[i * 128 + r];
         for (int src = 1; src < splits; ++src) v += recv[(src * per + i) * 128 + r];
-        p.C[static_cast<long long>(i * splits + rank) * p.ldc + n0 + r] = f32_to_bf16_rn(v);
+        p.C[static_cast<long long>(m0 + i * splits + rank) * p.ldc + n0 + r] = f32_to_bf16_rn(v);
       }
     }
   }
+}
+
+// How many clusters of `size` CTAs, each with an SM to itself, are resident at
+// once. It depends on how the device's SMs are spread over its GPCs, so it is
+// asked for, once per device.
+cudaError_t resident_clusters(int size, int* n) {
+  using L = FewLayout<F8, 128, false>;
+  static_assert(L::kAlloc > 114 * 1024, "one CTA an SM");
+  const auto kern = few_kernel<F8, 128, false>;
+  static AttrLatch attrs, found[kMaxSplits + 1];         // the number and 1
+  if (cudaError_t e = set_smem_attrs(kern, attrs, L::kAlloc, true); e != cudaSuccess) return e;
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+  *n = found[size].done[dev].load(std::memory_order_acquire) - 1;
+  if (*n >= 0) return cudaSuccess;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = size;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::kAlloc;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(n, kern, &cfg);
+  if (e == cudaSuccess) found[size].done[dev].store(*n + 1, std::memory_order_release);
+  return e;
+}
+
+// CTAs of a tile: as many as leave every cluster resident, with `ctas` CTAs an
+// SM. (Of 2..8 CTAs, with an SM each, 76, 46, 36, 28, 23, 15 and 15 clusters are.
+// One wave too many costs most: 600x1280x5120, 8 bits, 50 tiles of 3 | 2 CTAs:
+// 26.0 | 17.1 us; 1000x256x5120, 16 of 7 | 6: 18.4 | 10.5.)
+cudaError_t few_splits(long long tiles, int stages, int ctas, int* splits) {
+  *splits = 1;
+  for (int sp = 2; sp <= kMaxSplits && sp <= stages; ++sp) {
+    int n = 0;
+    if (cudaError_t e = resident_clusters(sp, &n); e != cudaSuccess) return e;
+    if (tiles <= static_cast<long long>(n) * ctas) *splits = sp;
+  }
+  return cudaSuccess;
 }
 
 template <class F, int NT, bool kShared>
@@ -404,11 +435,11 @@ cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
   p.ldc = a.ldc;
   p.stages = a.K / F::kStageK;
   p.err = a.err;
-  const int tiles = (a.N + 127) / 128;
-  p.splits = 1;
-  for (int sp = 2; sp <= kMaxSplits && sp <= p.stages && sp * tiles <= L::kCtas * a.num_sms; ++sp) p.splits = sp;
+  const int tiles = (a.N + 127) / 128, mt = (a.M + NT - 1) / NT;
+  e = few_splits(static_cast<long long>(tiles) * mt, p.stages, L::kCtas, &p.splits);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles * p.splits);
+  cfg.gridDim = dim3(tiles * p.splits, mt);
   cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kAlloc;
   cfg.stream = s;
@@ -424,27 +455,40 @@ cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, few_kernel<F, NT, kShared>, mw, ma, p);
 }
 
-// Whether a call is this kernel's. It is where K can be split over the SMs
-// that few tiles leave idle, and always for the fewest rows; else
-// gemm_act_many.cu's wide tiles win. Measured, here | there, us:
-//  * 4 bits: 40x5120x5120 10.5 | 12.3, 64x5120x5120 11.1 | 10.7, 64x34816x5120
-//    29.9 | 26.2, 128x7168x5120 16.8 | 12.0;
-//  * 8 bits: 61x5120x17408 25.2 | 44.6, 64x34816x5120 39.5 | 39.2, 128x5120x17408
-//    34.9 | 46.0, 128x7168x5120 22.3 | 16.8.
+// Whether a call is this kernel's: always for the fewest rows, and where K can
+// be split over the SMs that few tiles leave idle and that saves more time than
+// the sums of the parts cost; else gemm_act_many.cu's wide tiles win. Measured,
+// here | there, us:
+//  * 4 bits: 40x5120x5120 9.1 | 10.8, 64x5120x5120 9.4 | 10.2, 100x640x5120 8.5 |
+//    10.0, 100x5120x5120 11.5 | 10.3, 128x7168x5120 14.0 | 10.6, 300x640x10240 10.3 |
+//    15.6, 300x256x1024 8.2 | 5.7, 1000x256x5120 9.5 | 10.1;
+//  * 8 bits: 128x5120x17408 27.8 | 40.4, 128x7168x5120 17.3 | 14.8, 100x1280x1280
+//    8.0 | 6.4, 300x640x2560 8.7 | 9.0, 800x640x5120 12.6 | 14.6, 1146x21x14336
+//    14.0 | 34.0.
 template <class F>
-bool few_fits(const ActGemmArgs& a) {
+cudaError_t few_fits(const ActGemmArgs& a, bool* fits) {
   constexpr int kAlways = F::kScaled ? 32 : 64;
-  return a.M <= kAlways || (a.M <= 2 * kAlways && 3 * ((a.N + 127) / 128) <= a.num_sms);
+  *fits = a.M <= kAlways;
+  if (*fits) return cudaSuccess;
+  const int rows = a.M <= 64 ? 64 : 128, stages = a.K / F::kStageK;
+  const long long tiles = static_cast<long long>((a.N + 127) / 128) * ((a.M + rows - 1) / rows);
+  if (2 * tiles > a.num_sms) return cudaSuccess;
+  int splits;
+  const cudaError_t e = few_splits(tiles, stages, 1, &splits);
+  // Of an eighth of a microsecond: a stage here, with 64 and with 128 rows, and
+  // there, and what a call costs more here.
+  const int here = (stages + splits - 1) / splits * (rows == 64 ? 3 : 4) + (F::kScaled ? (rows == 64 ? 8 : 22) : 32);
+  *fits = splits > 1 && 4 * here < 9 * stages;
+  return e;
 }
 
 template <class F>
 cudaError_t launch_few(const ActGemmArgs& a, cudaStream_t s) {
   if (a.M <= 16) return launch_few_nt<F, 16, true>(a, s);
   if (a.M <= 32) return launch_few_nt<F, 32, !F::kScaled>(a, s);
-  if constexpr (!F::kScaled) {
-    if (a.M > 64) return launch_few_nt<F, 128, false>(a, s);
+  if (a.M > 64) return launch_few_nt<F, 128, false>(a, s);
+  if constexpr (!F::kScaled)
     if ((a.N + 127) / 128 > a.num_sms) return launch_few_nt<F, 64, true>(a, s);
-  }
   return launch_few_nt<F, 64, false>(a, s);
 }
 
@@ -464,7 +508,10 @@ static cudaError_t launch_act_gemm(const ActGemmArgs& a, cudaStream_t s) {
     b.A = static_cast<const char*>(a.A) + r * (F::kScaled ? K / 2 : K);
     b.SA = static_cast<const char*>(a.SA) + r * (F::kScaled ? K / 16 : K / 128 * 4);
     b.C = static_cast<char*>(a.C) + r * a.ldc * 2;
-    if (act::few_fits<F>(b)) e = act::launch_few<F>(b, s);
+    bool few = false;
+    e = act::few_fits<F>(b, &few);
+    if (e != cudaSuccess) return e;
+    if (few) e = act::launch_few<F>(b, s);
     else e = F::kScaled ? launch_w4a4_many(b, s) : launch_w8a8_many(b, s);
     if (a.M - r0 <= kPiece) break;
   }
