@@ -41,17 +41,20 @@ struct FewParams {
   unsigned* err;
 };
 
-// kShared: two CTAs of an SM share its memory (NT = 16, 8 bits NT = 32, and 8
-// bits NT = 64 where there are more tiles than SMs: 64x34816x5120 33.1 us against
-// 39.5); otherwise a CTA has it to itself.
+// kShared: two CTAs of an SM share its memory; otherwise a CTA has it to itself.
+// NT = 16, and 8 bits NT = 32, share it always. Wider tiles share it where there
+// are more tiles than SMs, and then have no room to receive parts of a split K
+// in: 64x34816x5120, 8 bits, 32.3 us against 39.5; 32x34816x5120, 4 bits, 17.2
+// against 24.8.
 template <class F, int NT, bool kShared>
 struct FewLayout {
   // Epilogue warps: one per lane quarter, or two with half the columns each
   // where one's time per 128 K would be the longest (61x5120x17408: 25.2 us
-  // with one).
+  // with one, 21.1 with two).
   static constexpr int kEpi = NT >= 64 ? 8 : 4;
   static constexpr int kCols = NT * 4 / kEpi;
   static constexpr int kThreads = (kEpiWarp0 + kEpi) * 32;
+  static constexpr bool kWhole = kShared && NT >= (F::kScaled ? 32 : 64);  // a tile's K is not split
   static constexpr int kS = kShared ? (NT == 64 ? 3 : 4) : (NT == 128 ? 4 : 6);   // stages
   static constexpr int kAcc = F::kScaled ? 1 : (NT <= 64 ? 4 : 2);        // accumulator slots
   static constexpr int kW = 0;
@@ -60,7 +63,7 @@ struct FewLayout {
   static constexpr int kSclA = kSclW + (F::kScaled ? kS * kScaleBlock : 0);
   static constexpr int kFac = kSclA + (F::kScaled ? kS * kScaleBlock : 0);
   static constexpr int kRecv = kFac + (F::kScaled ? 0 : 4 * NT * 4);
-  static constexpr int kBytes = kRecv + (NT + 7) * 128 * 4;
+  static constexpr int kBytes = kRecv + (kWhole ? 0 : (NT + 7) * 128 * 4);
   static constexpr int kAlloc = kBytes + 1024;                            // slack for 1024-byte alignment
   static constexpr int kStageBytes = 16384 + NT * 128;
   // Tensor memory: the accumulators, then (4 bits) two sets of a stage's
@@ -84,7 +87,7 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int splits = p.splits;
+  const int splits = L::kWhole ? 1 : p.splits;
   const int tile = blockIdx.x / splits, rank = blockIdx.x - tile * splits;
   const int n0 = tile * 128, m0 = blockIdx.y * NT, rows = min(NT, p.M - m0);   // activation rows m0..
   const int st0 = static_cast<int>(static_cast<long long>(rank) * p.stages / splits);
@@ -398,12 +401,15 @@ cudaError_t resident_clusters(int size, int* n) {
 }
 
 // CTAs of a tile: as many as leave every cluster resident, with `ctas` CTAs an
-// SM. (Of 2..8 CTAs, with an SM each, 76, 46, 36, 28, 23, 15 and 15 clusters are.
+// SM; more than 4 only with two stages each, and CTAs with an SM each only from 4
+// stages on, as less work saved does not pay for the sums (1x2560x2560, 4 bits,
+// by 7 | 5: 4.7 | 4.3 us; 64x2560x256, 8 bits, by 2 | not: 6.2 | 4.7). (Of 2..8 CTAs, with an SM each, 76, 46, 36, 28, 23, 15 and 15 clusters are.
 // One wave too many costs most: 600x1280x5120, 8 bits, 50 tiles of 3 | 2 CTAs:
 // 26.0 | 17.1 us; 1000x256x5120, 16 of 7 | 6: 18.4 | 10.5.)
 cudaError_t few_splits(long long tiles, int stages, int ctas, int* splits) {
   *splits = 1;
-  for (int sp = 2; sp <= kMaxSplits && sp <= stages; ++sp) {
+  if (ctas == 1 && stages < 4) return cudaSuccess;
+  for (int sp = 2; sp <= kMaxSplits && sp <= (sp <= 4 ? stages : stages / 2); ++sp) {
     int n = 0;
     if (cudaError_t e = resident_clusters(sp, &n); e != cudaSuccess) return e;
     if (tiles <= static_cast<long long>(n) * ctas) *splits = sp;
@@ -436,7 +442,8 @@ cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
   p.stages = a.K / F::kStageK;
   p.err = a.err;
   const int tiles = (a.N + 127) / 128, mt = (a.M + NT - 1) / NT;
-  e = few_splits(static_cast<long long>(tiles) * mt, p.stages, L::kCtas, &p.splits);
+  p.splits = 1;
+  if (!L::kWhole) e = few_splits(static_cast<long long>(tiles) * mt, p.stages, L::kCtas, &p.splits);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles * p.splits, mt);
@@ -455,41 +462,42 @@ cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, few_kernel<F, NT, kShared>, mw, ma, p);
 }
 
-// Whether a call is this kernel's: always for the fewest rows, and where K can
-// be split over the SMs that few tiles leave idle and that saves more time than
-// the sums of the parts cost; else gemm_act_many.cu's wide tiles win. Measured,
+// Whether a call is this kernel's: always up to 64 rows, and where K can be
+// split over the SMs that few tiles leave idle and that saves more time than the
+// sums of the parts cost; else gemm_act_many.cu's wide tiles win. Measured,
 // here | there, us:
-//  * 4 bits: 40x5120x5120 9.1 | 10.8, 64x5120x5120 9.4 | 10.2, 100x640x5120 8.5 |
-//    10.0, 100x5120x5120 11.5 | 10.3, 128x7168x5120 14.0 | 10.6, 300x640x10240 10.3 |
-//    15.6, 300x256x1024 8.2 | 5.7, 1000x256x5120 9.5 | 10.1;
-//  * 8 bits: 128x5120x17408 27.8 | 40.4, 128x7168x5120 17.3 | 14.8, 100x1280x1280
-//    8.0 | 6.4, 300x640x2560 8.7 | 9.0, 800x640x5120 12.6 | 14.6, 1146x21x14336
-//    14.0 | 34.0.
+//  * 4 bits: 40x10240x5120 12.1 | 13.0, 49x17408x5120 13.7 | 18.2, 64x10240x5120
+//    12.6 | 11.2, 64x17408x2560 8.8 | 11.5, 64x34816x5120 19.5 | 25.1,
+//    64x2560x10240 9.0 | 15.6; 100x640x5120 8.5 | 10.0, 100x5120x5120 11.5 | 10.3,
+//    128x7168x5120 14.0 | 10.6, 300x640x10240 10.3 | 15.6, 300x256x1024 8.2 | 5.7,
+//    1000x256x5120 9.5 | 10.1;
+//  * 8 bits: 64x10240x5120 16.8 | 18.3, 64x34816x5120 32.3 | 40.9, 64x2560x10240
+//    10.2 | 25.4; 128x5120x17408 27.8 | 40.4, 128x7168x5120 17.3 | 14.8,
+//    100x1280x1280 8.0 | 6.4, 300x640x2560 8.7 | 9.0, 800x640x5120 12.6 | 14.6,
+//    1146x21x14336 14.0 | 34.0.
 template <class F>
 cudaError_t few_fits(const ActGemmArgs& a, bool* fits) {
-  constexpr int kAlways = F::kScaled ? 32 : 64;
-  *fits = a.M <= kAlways;
+  *fits = a.M <= 64;
   if (*fits) return cudaSuccess;
-  const int rows = a.M <= 64 ? 64 : 128, stages = a.K / F::kStageK;
-  const long long tiles = static_cast<long long>((a.N + 127) / 128) * ((a.M + rows - 1) / rows);
+  const int stages = a.K / F::kStageK;
+  const long long tiles = static_cast<long long>((a.N + 127) / 128) * ((a.M + 127) / 128);
   if (2 * tiles > a.num_sms) return cudaSuccess;
   int splits;
   const cudaError_t e = few_splits(tiles, stages, 1, &splits);
-  // Of an eighth of a microsecond: a stage here, with 64 and with 128 rows, and
-  // there, and what a call costs more here.
-  const int here = (stages + splits - 1) / splits * (rows == 64 ? 3 : 4) + (F::kScaled ? (rows == 64 ? 8 : 22) : 32);
+  // In eighths of a microsecond: a stage here 4 and there 9 / 4, and what a call
+  // costs more here.
+  const int here = (stages + splits - 1) / splits * 4 + (F::kScaled ? 22 : 32);
   *fits = splits > 1 && 4 * here < 9 * stages;
   return e;
 }
 
 template <class F>
 cudaError_t launch_few(const ActGemmArgs& a, cudaStream_t s) {
+  const bool wide = (a.N + 127) / 128 > a.num_sms;
   if (a.M <= 16) return launch_few_nt<F, 16, true>(a, s);
-  if (a.M <= 32) return launch_few_nt<F, 32, !F::kScaled>(a, s);
-  if (a.M > 64) return launch_few_nt<F, 128, false>(a, s);
-  if constexpr (!F::kScaled)
-    if ((a.N + 127) / 128 > a.num_sms) return launch_few_nt<F, 64, true>(a, s);
-  return launch_few_nt<F, 64, false>(a, s);
+  if (a.M <= 32) return wide || !F::kScaled ? launch_few_nt<F, 32, true>(a, s) : launch_few_nt<F, 32, false>(a, s);
+  if (a.M <= 64) return wide ? launch_few_nt<F, 64, true>(a, s) : launch_few_nt<F, 64, false>(a, s);
+  return launch_few_nt<F, 128, false>(a, s);
 }
 
 }  // namespace
