@@ -48,15 +48,20 @@ struct FewParams {
 // against 24.8.
 template <class F, int NT, bool kShared>
 struct FewLayout {
-  // Epilogue warps: one per lane quarter, or two with half the columns each
-  // where one's time per 128 K would be the longest (61x5120x17408: 25.2 us
-  // with one, 21.1 with two).
-  static constexpr int kEpi = NT >= 64 ? 8 : 4;
+  // Epilogue warps: one to four per lane quarter, with NT, NT / 2 or NT / 4 columns
+  // each: as many as registers allow, for a shorter time per 128 K (8 bits) and
+  // at the end (with two at NT = 64, 128: 61x5120x17408, 8 bits, 20.8 us against
+  // 20.0, 800x640x5120 12.6 against 11.4; 128x640x5120, 4 bits, 8.8 against 7.9).
+  static constexpr int kEpi = NT >= 64 ? (kShared ? 8 : 16) : (NT == 32 && !(F::kScaled && kShared) ? 8 : 4);
   static constexpr int kCols = NT * 4 / kEpi;
   static constexpr int kThreads = (kEpiWarp0 + kEpi) * 32;
   static constexpr bool kWhole = kShared && NT >= (F::kScaled ? 32 : 64);  // a tile's K is not split
   static constexpr int kS = kShared ? (NT == 64 ? 3 : 4) : (NT == 128 ? 4 : 6);   // stages
   static constexpr int kAcc = F::kScaled ? 1 : (NT <= 64 ? 4 : 2);        // accumulator slots
+  // Stages of a hand-over between copies, MMAs and epilogue: a hand-over takes the
+  // MMA warp about as long as 64 columns of MMAs (64x10240x5120, 8 bits, one stage
+  // | two: 16.9 | 15.7 us). With 128 columns and two: 28.2 | 28.9 at 128x5120x17408.
+  static constexpr int kB = !F::kScaled && NT == 64 && !kShared ? 2 : 1;
   static constexpr int kW = 0;
   static constexpr int kA = kW + kS * 16384;
   static constexpr int kSclW = kA + kS * NT * 128;
@@ -78,7 +83,7 @@ template <class F, int NT, bool kShared>
 __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout<F, NT, kShared>::kCtas)
     few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA, FewParams p) {
   using L = FewLayout<F, NT, kShared>;
-  constexpr int S = L::kS, NACC = L::kAcc;
+  constexpr int B = L::kB, S = L::kS / B, NACC = L::kAcc / B;   // ring and accumulators, in hand-overs
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_sh[S], empty_sh[S], scaled_sh[S], acc_full_sh[NACC], acc_free_sh[NACC],
       recv_sh;
@@ -102,17 +107,18 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
   // (Prefetching later stages into L2 on top: 17.1 -> 18.3..20.1 us at
   // 1x17408x5120.) Copies and MMAs are issued under elect.sync (see
   // gemm_act_many.cu).
-  const int ahead = min(S, nst);
+  const int ahead = min(L::kS, nst), nu = (nst + B - 1) / B;   // nu: hand-overs
   int issued = 0;                                // stages whose copies this thread started
   const uint64_t pol = policy_evict_first();
   const auto load_w = [&](int t) {
-    const int s = t % S;
-    mbar_arrive_expect_tx(full + 8 * s, L::kStageBytes);
-    tma_load_2d_hint(sb + L::kW + s * 16384, &tmW, (st0 + t) * 128, n0, full + 8 * s, pol);
+    const int i = t % L::kS;
+    const uint32_t bar = full + 8 * (i / B);
+    if (t % B == 0) mbar_arrive_expect_tx(bar, min(B, nst - t) * L::kStageBytes);
+    tma_load_2d_hint(sb + L::kW + i * 16384, &tmW, (st0 + t) * 128, n0, bar, pol);
   };
   const auto load_a = [&](int t) {
-    const int s = t % S;
-    tma_load_2d(sb + L::kA + s * NT * 128, &tmA, (st0 + t) * 128, m0, full + 8 * s);
+    const int i = t % L::kS;
+    tma_load_2d(sb + L::kA + i * NT * 128, &tmA, (st0 + t) * 128, m0, full + 8 * (i / B));
   };
   if (warp == 0) {
     if (elect_one()) {
@@ -153,7 +159,8 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
       for (int t = 0; t < ahead; ++t) load_a(t);
       issued = ahead;
       for (int t = ahead; t < nst; ++t) {
-        if (!wait_or_abort(empty + 8 * (t % S), ((t / S) - 1) & 1, p.err, abort_flag)) break;
+        const int u = t / B;
+        if (t % B == 0 && !wait_or_abort(empty + 8 * (u % S), ((u / S) - 1) & 1, p.err, abort_flag)) break;
         load_w(t);
         load_a(t);
         issued = t + 1;
@@ -168,7 +175,7 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
     int last = -1, s = 0, slot = 0;
     uint32_t ph = 0, acc_ph = 1;
     bool loaded = false, freed = true;
-    for (int t = 0; t < nst; ++t) {
+    for (int t = 0; t < nu; ++t) {
       bool ok = true;
       if (!loaded) {
         ok = wait_or_abort(full + 8 * s, ph, p.err, abort_flag);
@@ -183,7 +190,7 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
       // Parity 1 of a barrier that has completed no phase counts as complete.
       const bool f1 = F::kScaled || mbar_test(acc_free + 8 * slot1, acc_ph1);
       if (elect_one()) {
-        const uint64_t wd = tile_desc(sb + L::kW + s * 16384), ad = tile_desc(sb + L::kA + s * NT * 128);
+        const uint64_t wd = tile_desc(sb + L::kW + s * B * 16384), ad = tile_desc(sb + L::kA + s * B * NT * 128);
         if constexpr (F::kScaled) {
           const uint32_t sw = tmem + NT + (t & 1) * 32, sa = sw + 16;
 #pragma unroll
@@ -196,7 +203,12 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
             mma_f4(tmem, wd + 2 * j, ad + 2 * j, idesc, sw + 4 * j, sa + 4 * j, (t | j) ? 1u : 0u);
         } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma_f8(tmem + slot * NT, wd + 2 * j, ad + 2 * j, idesc, j ? 1u : 0u);
+          for (int b = 0; b < B; ++b) {
+            if (b && t * B + b >= nst) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma_f8(tmem + (slot * B + b) * NT, wd + b * 1024 + 2 * j, ad + b * NT * 8 + 2 * j, idesc, j ? 1u : 0u);
+          }
         }
         mma_commit(empty + 8 * s);
         if (!F::kScaled || t == nst - 1) mma_commit(acc_full + 8 * (F::kScaled ? 0 : slot));
@@ -289,7 +301,7 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
       for (int t0 = 0; t0 < nst && live; t0 += D) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-          const int t = t0 + d, slot = t % NACC;
+          const int t = t0 + d, u = t / B, slot = u % NACC;
           if (t < nst && live) {
             __syncwarp();
 #pragma unroll
@@ -299,23 +311,25 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
             }
             if (t + D < nst) fw[d] = __ldg(sw + t + D);
             __syncwarp();
-            live = __all_sync(0xFFFFFFFFu, wait_or_abort(acc_full + 8 * slot, (t / NACC) & 1, p.err, abort_flag));
+            if (t % B == 0)
+              live = __all_sync(0xFFFFFFFFu, wait_or_abort(acc_full + 8 * slot, (u / NACC) & 1, p.err, abort_flag));
             if (live) {
               tc_fence_after();
               // The next 16 columns are on their way while these are added; the
               // accumulator is free once the last have arrived.
               uint32_t v[2][16];
-              tmem_ld16_start(tl + slot * NT, v[0]);
+              const uint32_t ta = tl + (slot * B + t % B) * NT;
+              tmem_ld16_start(ta, v[0]);
 #pragma unroll
               for (int c = 0; c < COLS; c += 16) {
                 uint32_t(&x)[16] = v[(c / 16) & 1];
                 tmem_ld_wait(x);
                 if (c + 16 < COLS) {
-                  tmem_ld16_start(tl + slot * NT + c + 16, v[(c / 16 + 1) & 1]);
+                  tmem_ld16_start(ta + c + 16, v[(c / 16 + 1) & 1]);
                 } else {
                   tc_fence_before();
                   __syncwarp();
-                  if (lane == 0) mbar_arrive(acc_free + 8 * slot);
+                  if (lane == 0 && (t % B == B - 1 || t == nst - 1)) mbar_arrive(acc_free + 8 * slot);
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(__uint_as_float(x[i]), fac[c + i], acc[c + i]);
@@ -354,7 +368,7 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
   }
   const bool failed = *abort_flag != 0;
   if (failed)                                    // no copy may still be in flight when the CTA exits
-    for (int t = max(0, issued - S); t < issued; ++t) mbar_wait(full + 8 * (t % S), (t / S) & 1, p.err);
+    for (int n = (issued + B - 1) / B, u = max(0, n - S); u < n; ++u) mbar_wait(full + 8 * (u % S), (u / S) & 1, p.err);
   if (splits > 1 && own > 0) {
     // No one writes into this CTA once its rows' sums are complete. A peer may
     // use up two waits of its own before it sends them.
@@ -466,15 +480,15 @@ cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
 // split over the SMs that few tiles leave idle and that saves more time than the
 // sums of the parts cost; else gemm_act_many.cu's wide tiles win. Measured,
 // here | there, us:
-//  * 4 bits: 40x10240x5120 12.1 | 13.0, 49x17408x5120 13.7 | 18.2, 64x10240x5120
-//    12.6 | 11.2, 64x17408x2560 8.8 | 11.5, 64x34816x5120 19.5 | 25.1,
-//    64x2560x10240 9.0 | 15.6; 100x640x5120 8.5 | 10.0, 100x5120x5120 11.5 | 10.3,
-//    128x7168x5120 14.0 | 10.6, 300x640x10240 10.3 | 15.6, 300x256x1024 8.2 | 5.7,
-//    1000x256x5120 9.5 | 10.1;
-//  * 8 bits: 64x10240x5120 16.8 | 18.3, 64x34816x5120 32.3 | 40.9, 64x2560x10240
-//    10.2 | 25.4; 128x5120x17408 27.8 | 40.4, 128x7168x5120 17.3 | 14.8,
-//    100x1280x1280 8.0 | 6.4, 300x640x2560 8.7 | 9.0, 800x640x5120 12.6 | 14.6,
-//    1146x21x14336 14.0 | 34.0.
+//  * 4 bits: 40x10240x5120 12.1 | 12.9, 49x17408x5120 13.7 | 18.5, 64x10240x5120
+//    12.7 | 11.3, 64x17408x2560 8.8 | 11.5, 64x34816x5120 19.7 | 25.0,
+//    64x2560x10240 8.7 | 15.7; 100x640x5120 7.5 | 10.1, 100x5120x5120 10.3 | 10.4,
+//    128x7168x5120 12.6 | 10.6, 200x1280x2560 7.6 | 7.4, 300x640x10240 9.7 | 15.7,
+//    300x256x1024 7.1 | 5.8, 1000x256x5120 8.7 | 10.2;
+//  * 8 bits: 64x10240x5120 15.3 | 18.3, 64x34816x5120 32.3 | 40.4, 64x2560x10240
+//    9.8 | 25.4; 128x5120x17408 26.9 | 41.0, 128x7168x5120 16.1 | 14.9,
+//    100x1280x1280 6.9 | 6.5, 300x640x2560 7.8 | 9.1, 800x640x5120 11.4 | 14.6,
+//    1146x21x14336 13.3 | 34.0.
 template <class F>
 cudaError_t few_fits(const ActGemmArgs& a, bool* fits) {
   *fits = a.M <= 64;
@@ -486,7 +500,7 @@ cudaError_t few_fits(const ActGemmArgs& a, bool* fits) {
   const cudaError_t e = few_splits(tiles, stages, 1, &splits);
   // In eighths of a microsecond: a stage here 4 and there 9 / 4, and what a call
   // costs more here.
-  const int here = (stages + splits - 1) / splits * 4 + (F::kScaled ? 22 : 32);
+  const int here = (stages + splits - 1) / splits * 4 + (F::kScaled ? 17 : 26);
   *fits = splits > 1 && 4 * here < 9 * stages;
   return e;
 }
