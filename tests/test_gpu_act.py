@@ -308,7 +308,8 @@ def test_products_long_and_short_k(fmt, K, M):
 @pytest.mark.parametrize("fmt", [4, 8])
 @pytest.mark.parametrize("M,N,K", [(3, 2, 15616), (20, 1100, 5120), (53, 5, 16896), (65, 300, 10240), (129, 100, 5120), (257, 145, 11264),
                                    (300, 640, 10240), (1000, 256, 5120), (1146, 21, 14336), (1985, 39, 12800), (17, 19999, 768),
-                                   (32, 20000, 2560), (49, 19510, 768), (64, 34816, 1280)])
+                                   (32, 20000, 2560), (49, 19510, 768), (64, 34816, 1280), (100, 20002, 768), (128, 34816, 2560),
+                                   (384, 34817, 512)])
 def test_products_with_k_split_and_with_many_tiles(fmt, M, N, K):
     """Few tiles with a long K, with one and with many rows per tile, and more tiles than SMs, into rows that are 13
     elements longer."""

@@ -39,7 +39,7 @@ struct ManyParams {
   float gscale;
   uint16_t* C;
   int M, N, K, ldc;
-  int mt, nt;           // 256-row tiles, weight tiles
+  int mt, nt;           // tiles of 256 rows of the first operand, of BN rows of the second
   int stages;           // per tile
   int align;            // of C's rows, bytes: 16, 8, 4 or 2
   unsigned* err;
@@ -116,7 +116,8 @@ __device__ __forceinline__ void store_rows(const At& chunk_at, const ManyParams&
   }
 }
 
-template <class F, int BN>
+// kSwap: the weights are the first operand, and a tile is stored transposed.
+template <class F, int BN, bool kSwap>
 __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
     many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
     for (int i = first; i < total; i += step) {
       int mi, ni;
       tile_at<F>(i, p.mt, p.nt, mi, ni);
-      const int m0 = mi * 256 + rank * 128 + q * 32, n0 = ni * BN + h * COLS;
+      const int a0 = mi * 256 + rank * 128 + q * 32, b0 = ni * BN + h * COLS;   // the warp's rows of either operand
       // Tiles after this one, as far as it matters: an accumulator that no later
       // one takes over is not announced as free.
       const int left = min((total - 1 - i) / step, NACC);
@@ -362,12 +363,12 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
         if (lane == 0 && i + NACC * step < total) pair_arrive(acc_free0 + 8 * slot);
         if (++slot == NACC) slot = 0, ph ^= 1;
       } else {
-        const float* sa = p.SA + static_cast<long long>(min(m0 + lane, p.M - 1)) * kb;
+        const float* sa = p.SA + static_cast<long long>(min(a0 + lane, p.M - 1)) * kb;
         // The warp's columns lie in one or two weight blocks; `cross` is the
         // first column of the second.
-        const int cross = 128 - (n0 & 127);
-        const float* sw0 = p.SW + static_cast<long long>(min(n0, p.N - 1) >> 7) * kb;
-        const float* sw1 = p.SW + static_cast<long long>(min(n0 + COLS - 1, p.N - 1) >> 7) * kb;
+        const int cross = 128 - (b0 & 127);
+        const float* sw0 = p.SW + static_cast<long long>(min(b0, p.N - 1) >> 7) * kb;
+        const float* sw1 = p.SW + static_cast<long long>(min(b0 + COLS - 1, p.N - 1) >> 7) * kb;
         uint64_t acc[COLS / 2];
 #pragma unroll
         for (int c = 0; c < COLS / 2; ++c) acc[c] = 0;
@@ -443,29 +444,39 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
         if (L::kOutBufs == 2) out = out == outs ? outs + L::kOutBytes : outs;
         if (elect_one()) tma_store_wait_read<L::kOutBufs - 1>();
         __syncwarp();
+        if constexpr (kSwap) {                 // the lane has a column of the chunk
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4*>(chunk_at(lane, j)) =
-              make_uint4(packed[c / 2 + 4 * j], packed[c / 2 + 4 * j + 1], packed[c / 2 + 4 * j + 2], packed[c / 2 + 4 * j + 3]);
+          for (int j = 0; j < 16; ++j) {
+            uint16_t* v = reinterpret_cast<uint16_t*>(chunk_at(2 * j, lane >> 3)) + (lane & 7);
+            v[0] = static_cast<uint16_t>(packed[c / 2 + j]);
+            v[32] = static_cast<uint16_t>(packed[c / 2 + j] >> 16);   // row 2j + 1, in the same swizzle
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(chunk_at(lane, j)) =
+                make_uint4(packed[c / 2 + 4 * j], packed[c / 2 + 4 * j + 1], packed[c / 2 + 4 * j + 2], packed[c / 2 + 4 * j + 3]);
+        }
+        const int m0 = kSwap ? b0 + c : a0, n0 = kSwap ? a0 : b0 + c;   // the chunk's place in C
         // A tensor store writes whole 16-byte units, past the end of the row too:
         // its map ends at the last whole unit, and the few columns after that are
         // stored by themselves.
-        if (p.align == 16 && n0 + c < p.N) {
+        if (p.align == 16 && n0 < p.N) {
           fence_proxy_async_smem();
           __syncwarp();
           const int whole = p.N & ~7;
-          if (elect_one() && m0 < p.M && n0 + c < whole) tma_store_2d(&tmC, n0 + c, m0, smem_u32(out));
-          const int rest = whole - (n0 + c);   // column of the chunk where they begin
+          if (elect_one() && m0 < p.M && n0 < whole) tma_store_2d(&tmC, n0, m0, smem_u32(out));
+          const int rest = whole - (n0);   // column of the chunk where they begin
           if (rest >= 0 && rest < 32 && m0 + lane < p.M)
             for (int e = 0; whole + e < p.N; ++e)
               p.C[static_cast<long long>(m0 + lane) * p.ldc + whole + e] =
                   *reinterpret_cast<const uint16_t*>(chunk_at(lane, rest >> 3) + e * 2);
           __syncwarp();
-        } else if (n0 + c < p.N) {
+        } else if (n0 < p.N) {
           __syncwarp();
-          if (p.align >= 8) store_rows<4>(chunk_at, p, m0, n0 + c, lane);
-          else if (p.align >= 4) store_rows<2>(chunk_at, p, m0, n0 + c, lane);
-          else store_rows<1>(chunk_at, p, m0, n0 + c, lane);
+          if (p.align >= 8) store_rows<4>(chunk_at, p, m0, n0, lane);
+          else if (p.align >= 4) store_rows<2>(chunk_at, p, m0, n0, lane);
+          else store_rows<1>(chunk_at, p, m0, n0, lane);
           __syncwarp();
         }
         if (elect_one()) tma_store_close();
@@ -486,30 +497,32 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
   }
 }
 
-template <class F, int BN>
+template <class F, int BN, bool kSwap>
 cudaError_t launch_many_t(const ActGemmArgs& a, cudaStream_t s) {
   using L = ManyLayout<F, BN>;
   const uint64_t row = F::kScaled ? static_cast<uint64_t>(a.K) / 2 : static_cast<uint64_t>(a.K);
   const uint64_t srow = static_cast<uint64_t>(a.K) / 16;
   const uint64_t M = static_cast<uint64_t>(a.M), N = static_cast<uint64_t>(a.N);
-  CUtensorMap ma, mb, msa, msb, mc;
+  CUtensorMap ma = {}, mb = {}, msa = {}, msb = {}, mc = {};
+  CUtensorMap &mx = kSwap ? mb : ma, &mw = kSwap ? ma : mb, &msx = kSwap ? msb : msa, &msw = kSwap ? msa : msb;
   constexpr auto kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  cudaError_t e = make_map_2d(&ma, kU8, a.A, row, M, row, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (e == cudaSuccess) e = cached_map_2d(&mb, kU8, a.W, row, N, row, 128, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B);
-  msa = ma;
-  msb = mb;
+  // Rows of a copy: a CTA's own 128 of the first operand and half the tile's of
+  // the second, but the scales of all of those.
+  constexpr int kX = kSwap ? BN : 128, kXHalf = kSwap ? BN / 2 : 128;
+  constexpr int kW = kSwap ? 128 : BN, kWHalf = kSwap ? 128 : BN / 2;
+  cudaError_t e = make_map_2d(&mx, kU8, a.A, row, M, row, 128, kXHalf, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e == cudaSuccess) e = cached_map_2d(&mw, kU8, a.W, row, N, row, 128, kWHalf, CU_TENSOR_MAP_SWIZZLE_128B);
   if (F::kScaled) {
-    if (e == cudaSuccess) e = make_map_2d(&msa, kU8, a.SA, srow, M, srow, 32, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
-    if (e == cudaSuccess) e = cached_map_2d(&msb, kU8, a.SW, srow, N, srow, 32, BN, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e == cudaSuccess) e = make_map_2d(&msx, kU8, a.SA, srow, M, srow, 32, kX, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e == cudaSuccess) e = cached_map_2d(&msw, kU8, a.SW, srow, N, srow, 32, kW, CU_TENSOR_MAP_SWIZZLE_NONE);
   }
   const uintptr_t at = reinterpret_cast<uintptr_t>(a.C) | static_cast<uintptr_t>(a.ldc) * 2;
   const int align = at % 16 == 0 && a.N >= 8 ? 16 : (at % 8 == 0 ? 8 : (at % 4 == 0 ? 4 : 2));
-  mc = ma;
   if (e == cudaSuccess && align == 16)
     e = make_map_2d(&mc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.C, N & ~uint64_t(7), M, static_cast<uint64_t>(a.ldc) * 2, 32, 32,
                     CU_TENSOR_MAP_SWIZZLE_64B);
   static AttrLatch latch;
-  if (e == cudaSuccess) e = set_smem_attrs(many_kernel<F, BN>, latch, L::kAlloc, true);
+  if (e == cudaSuccess) e = set_smem_attrs(many_kernel<F, BN, kSwap>, latch, L::kAlloc, true);
   if (e != cudaSuccess) return e;
   ManyParams p = {};
   if (!F::kScaled) {
@@ -522,8 +535,8 @@ cudaError_t launch_many_t(const ActGemmArgs& a, cudaStream_t s) {
   p.N = a.N;
   p.K = a.K;
   p.ldc = a.ldc;
-  p.mt = (a.M + 255) / 256;
-  p.nt = (a.N + BN - 1) / BN;
+  p.mt = ((kSwap ? a.N : a.M) + 255) / 256;
+  p.nt = ((kSwap ? a.M : a.N) + BN - 1) / BN;
   p.stages = a.K / F::kStageK;
   p.align = align;
   p.err = a.err;
@@ -543,7 +556,7 @@ cudaError_t launch_many_t(const ActGemmArgs& a, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.pdl ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, many_kernel<F, BN>, ma, mb, msa, msb, mc, p);
+  return cudaLaunchKernelEx(&cfg, many_kernel<F, BN, kSwap>, ma, mb, msa, msb, mc, p);
 }
 
 // Width of the weight tiles: the pairs take whole rounds of tiles, and a round
@@ -551,16 +564,26 @@ cudaError_t launch_many_t(const ActGemmArgs& a, cudaStream_t s) {
 // BN = 256 | 192 | 128, us: 4 bits 333x7168x5120 13.3 | 12.2 | 16.9, 2048x5120x5120
 // 30.2 | 25.9 | 34.2, 4096x34816x5120 248 | 274 | 336; 8 bits 333x7168x5120 20.2 |
 // 18.3 | 24.4, 2048x7168x5120 55.8 | 63.0 | 68.3, 4096x5120x17408 277 | 284 | 310.
+// With 4 bits the operands change places where the activation rows then leave
+// less of a tile empty: 128x34816x5120 26.1 us as they are | 22.4 changed,
+// 192x34816x5120 26.4 | 25.1, 384x17408x5120 22.8 | 21.0. (256 columns changed do
+// not fit the registers: 33.5 us at 256x34816x5120 against 26.7. With 8 bits every
+// column would have a factor of its own: 128x34816x5120 41.1 | 43.2.)
 template <class F>
 cudaError_t launch_many(const ActGemmArgs& a, cudaStream_t s) {
-  const long long mt = (a.M + 255) / 256, pairs = a.num_sms / 2;
-  const auto cost = [&](int bn) {
-    return (mt * ((a.N + bn - 1) / bn) + pairs - 1) / pairs * (bn + (F::kScaled ? 140 : 100));
+  const long long M = a.M, N = a.N, pairs = a.num_sms / 2;
+  const auto cost = [&](long long first, long long second, int bn) {
+    return ((first + 255) / 256 * ((second + bn - 1) / bn) + pairs - 1) / pairs * (bn + (F::kScaled ? 140 : 100));
   };
-  const long long c256 = cost(256), c192 = cost(192), c128 = cost(128);
-  if (c256 <= c192 && c256 <= c128) return launch_many_t<F, 256>(a, s);
-  if (c192 <= c128) return launch_many_t<F, 192>(a, s);
-  return launch_many_t<F, 128>(a, s);
+  const long long c256 = cost(M, N, 256), c192 = cost(M, N, 192), c128 = cost(M, N, 128);
+  const long long best = c256 < c192 ? (c256 < c128 ? c256 : c128) : (c192 < c128 ? c192 : c128);
+  if constexpr (F::kScaled) {
+    const long long s192 = cost(N, M, 192), s128 = cost(N, M, 128);
+    if (s192 < best && s192 < s128) return launch_many_t<F, 192, true>(a, s);
+    if (s128 < best) return launch_many_t<F, 128, true>(a, s);
+  }
+  if (c256 == best) return launch_many_t<F, 256, false>(a, s);
+  return c192 == best ? launch_many_t<F, 192, false>(a, s) : launch_many_t<F, 128, false>(a, s);
 }
 
 }  // namespace
