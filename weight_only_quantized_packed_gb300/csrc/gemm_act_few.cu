@@ -386,48 +386,54 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
   }
 }
 
-// How many clusters of `size` CTAs, each with an SM to itself, are resident at
-// once. It depends on how the device's SMs are spread over its GPCs, so it is
-// asked for, once per device.
-cudaError_t resident_clusters(int size, int* n) {
+// How many clusters of 2, 3, ... CTAs, each with an SM to itself, are resident
+// at once, as (*found)[size]. It depends on how the device's SMs are spread over
+// its GPCs, so it is asked for, once per device.
+cudaError_t resident_clusters(const std::atomic<int>** found) {
   using L = FewLayout<F8, 128, false>;
   static_assert(L::kAlloc > 114 * 1024, "one CTA an SM");
-  const auto kern = few_kernel<F8, 128, false>;
-  static AttrLatch attrs, found[kMaxSplits + 1];         // the number and 1
-  if (cudaError_t e = set_smem_attrs(kern, attrs, L::kAlloc, true); e != cudaSuccess) return e;
+  static std::atomic<int> table[kMaxDevices][kMaxSplits + 1];
+  static AttrLatch latch, attrs;
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
-  *n = found[size].done[dev].load(std::memory_order_acquire) - 1;
-  if (*n >= 0) return cudaSuccess;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  *found = table[dev];
+  if (latch.done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const auto kern = few_kernel<F8, 128, false>;
+  if (cudaError_t e = set_smem_attrs(kern, attrs, L::kAlloc, true); e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = size;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(size);
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kAlloc;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaOccupancyMaxActiveClusters(n, kern, &cfg);
-  if (e == cudaSuccess) found[size].done[dev].store(*n + 1, std::memory_order_release);
-  return e;
+  for (int size = 2; size <= kMaxSplits; ++size) {
+    int n = 0;
+    attr.val.clusterDim.x = size;
+    cfg.gridDim = dim3(size);
+    if (cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg); e != cudaSuccess) return e;
+    table[dev][size].store(n, std::memory_order_relaxed);
+  }
+  latch.done[dev].store(1, std::memory_order_release);
+  return cudaSuccess;
 }
 
 // CTAs of a tile: as many as leave every cluster resident, with `ctas` CTAs an
-// SM; more than 4 only with two stages each, and CTAs with an SM each only from 4
-// stages on, as less work saved does not pay for the sums (1x2560x2560, 4 bits,
-// by 7 | 5: 4.7 | 4.3 us; 64x2560x256, 8 bits, by 2 | not: 6.2 | 4.7). (Of 2..8 CTAs, with an SM each, 76, 46, 36, 28, 23, 15 and 15 clusters are.
-// One wave too many costs most: 600x1280x5120, 8 bits, 50 tiles of 3 | 2 CTAs:
-// 26.0 | 17.1 us; 1000x256x5120, 16 of 7 | 6: 18.4 | 10.5.)
+// SM (of 2..8 CTAs with an SM each, 76, 46, 36, 28, 23, 15 and 15 clusters are; one
+// wave too many costs most: 600x1280x5120, 8 bits, 50 tiles of 3 | 2 CTAs 26.0 |
+// 17.1 us, 1000x256x5120, 16 of 7 | 6 18.4 | 10.5). More than 4 only with two
+// stages each, and CTAs with an SM each only from 4 stages on, as less work saved
+// does not pay for the sums (1x2560x2560, 4 bits, by 7 | 5: 4.7 | 4.3 us;
+// 64x2560x256, 8 bits, by 2 | not: 6.2 | 4.7).
 cudaError_t few_splits(long long tiles, int stages, int ctas, int* splits) {
   *splits = 1;
-  if (ctas == 1 && stages < 4) return cudaSuccess;
-  for (int sp = 2; sp <= kMaxSplits && sp <= (sp <= 4 ? stages : stages / 2); ++sp) {
-    int n = 0;
-    if (cudaError_t e = resident_clusters(sp, &n); e != cudaSuccess) return e;
-    if (tiles <= static_cast<long long>(n) * ctas) *splits = sp;
-  }
+  if (stages < 2 || (ctas == 1 && stages < 4)) return cudaSuccess;
+  const std::atomic<int>* resident;
+  if (cudaError_t e = resident_clusters(&resident); e != cudaSuccess) return e;
+  for (int sp = 2; sp <= kMaxSplits && sp <= (sp <= 4 ? stages : stages / 2); ++sp)
+    if (tiles <= static_cast<long long>(resident[sp].load(std::memory_order_relaxed)) * ctas) *splits = sp;
   return cudaSuccess;
 }
 
