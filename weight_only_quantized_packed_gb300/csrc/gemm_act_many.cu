@@ -9,16 +9,18 @@
 //  * 4 bits: the tensor core applies the scales, rearranged by warps of each CTA
 //    (its 128 activation rows, all BN weight rows) and copied to tensor memory
 //    by the MMA warp. One or two accumulators, drained into registers as BF16.
-//    4096x34816x5120: 233 us, 6.3 PFLOP/s until the power cap slows the clock.
+//    4096x34816x5120: 236 us, 6.2 PFLOP/s until the power cap slows the clock.
 //    The tensor pipe is busy for two thirds of it; next are the bytes into an
 //    SM (38 KB a stage, at 64 a clock nine tenths of a stage's time) and the
 //    drains between tiles.
 //  * 8 bits: two to four accumulators that take turns per 128 K; the epilogue
 //    adds each, times its activation row's and weight block's scale, to FP32
 //    sums in registers while the tensor core fills the others.
-//    4096x5120x17408: 277 us, 2.6 PFLOP/s. Bound by that reading and adding: 773
+//    4096x5120x17408: 277 to 290 us, 2.5 PFLOP/s. Bound by that reading and adding: 773
 //    clocks per 128 K of a 256-column tile, of which the MMAs are 544; without
 //    the additions 238 us.
+// With 4 bits the operands may change places (kSwap): 256 weight rows by BN
+// activation rows, where that leaves less of the tiles empty.
 // Output goes through shared memory, 32 rows by 32 columns a warp at a time,
 // and leaves as bulk tensor stores (rows of C that are not 16-byte aligned: as
 // stores of 8, 4 or 2 bytes a lane from there).
