@@ -321,7 +321,10 @@ int wqp_row_chunks(int M, int K, int N, int max_rows, long long* out, int cap);
  * on the stream is finishing. It prefetches W (and the scales) before it
  * waits for that kernel, and reads A only after the wait. So with PDL
  * enabled, W must not be written by the kernel launched just before on the
- * same stream. Off by default. The setting is process-wide. Returns the
+ * same stream; nor, as each kernel lets the next one start before it has itself
+ * waited, by earlier ones since the last launch without PDL. Where weights are
+ * made on the stream (w4_quantize, a copy), turn PDL off for the first launch
+ * after that. Off by default. The setting is process-wide. Returns the
  * previous setting. */
 int wqp_set_pdl(int enable);
 

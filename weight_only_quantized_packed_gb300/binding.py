@@ -492,7 +492,8 @@ def row_chunks(M: int, K: int, N: int, max_rows: int):
 
 
 def set_pdl(enable: bool) -> bool:
-    """Process-wide programmatic-dependent-launch policy; returns the old one."""
+    """Process-wide programmatic-dependent-launch policy; returns the old one. With it on, weights may be
+    read before earlier launches have finished: make the first launch after writing weights without it."""
     return bool(lib().wqp_set_pdl(1 if enable else 0))
 
 
