@@ -323,6 +323,15 @@ def test_products_with_k_split_and_with_many_tiles(fmt, M, N, K):
     assert wqp.get_device_error() == 0
 
 
+# A pair of CTAs takes two or three tiles of 128, 256 and 192 columns, with fewer 128-K blocks a tile than it has accumulators.
+@pytest.mark.parametrize("M,N", [(7680, 640), (9728, 1024), (2560, 2048), (7681, 2050)])
+@pytest.mark.parametrize("K", [128, 256, 384])
+def test_w8a8_tiles_shorter_than_the_accumulators(M, N, K):
+    C, av, wv = run(8, M, N, K, seed=M + K, ints=True)
+    check(C, av, wv, K, True)
+    assert wqp.get_device_error() == 0
+
+
 @pytest.mark.parametrize("fmt", [4, 8])
 @pytest.mark.parametrize("M,N,pad,shift", [(3, 131, 5, 0), (40, 256, 8, 8), (300, 256, 8, 0), (300, 260, 4, 0), (300, 256, 1, 0),
                                            (300, 256, 8, 1), (300, 256, 8, 3), (270, 131, 13, 0)])

@@ -343,9 +343,6 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       int mi, ni;
       tile_at<F>(i, p.mt, p.nt, mi, ni);
       const int a0 = mi * 256 + rank * 128 + q * 32, b0 = ni * BN + h * COLS;   // the warp's rows of either operand
-      // Tiles after this one, as far as it matters: an accumulator that no later
-      // one takes over is not announced as free.
-      const int left = min((total - 1 - i) / step, NACC);
       uint32_t packed[COLS / 2];
       if constexpr (F::kScaled) {
         wait_or_abort(acc_full + 8 * slot, ph, p.err, abort_flag);
@@ -365,6 +362,12 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
         if (lane == 0 && i + NACC * step < total) pair_arrive(acc_free0 + 8 * slot);
         if (++slot == NACC) slot = 0, ph ^= 1;
       } else {
+        // Tiles after this one, as far as it matters: a use of an accumulator is
+        // announced as over where NACC uses later another one follows, as only that
+        // one waits for it. (An arrive at the other CTA that nobody waits for could
+        // come after that CTA's end. With K = 128 there are fewer uses a tile than
+        // accumulators, so that a following tile alone does not mean one.)
+        const int left = min((total - 1 - i) / step, NACC);
         const float* sa = p.SA + static_cast<long long>(min(a0 + lane, p.M - 1)) * kb;
         // The warp's columns lie in one or two weight blocks; `cross` is the
         // first column of the second.
@@ -418,7 +421,7 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
               if (c0 + 32 >= COLS) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && (k + NACC < kb || i + step < total)) pair_arrive(acc_free0 + 8 * slot);
+                if (lane == 0 && k + NACC < (left + 1) * kb) pair_arrive(acc_free0 + 8 * slot);
               }
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
