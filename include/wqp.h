@@ -299,7 +299,8 @@ int w8a8_gemm(const void* A, const float* a_scales, const void* W, const float* 
  *   q2:  ((code & 3) - 1) * d
  *   w4:  (e2m1 * e4m3(scale)) * global_scale
  *   w8:  e4m3(W) * s[n/128, k/128]           (one FP32 multiply)
- * These are debugging and verification aids, not part of the hot path.
+ * These are debugging and verification aids, not part of the hot path. They are
+ * launched without PDL (see wqp_set_pdl), so they may follow what writes W.
  */
 int q2_dequant(const void* W, float* out, int N, int K, void* stream);
 int w4a16_dequant(const void* W, const void* scales, float global_scale, float* out,

@@ -1,0 +1,79 @@
+"""The quantised-activation entries launched with programmatic dependent launch: every call of a chain reads what the
+call before it wrote, into the same buffers with other inputs each time, so that a value left from the pass before
+shows. Each pass is compared, bit for bit, with the same calls made without PDL."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import weight_only_quantized_packed_gb300 as wqp
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+PASSES = 6
+
+
+@pytest.fixture(autouse=True)
+def _pdl_off():
+    old = wqp.set_pdl(False)
+    yield
+    wqp.set_pdl(old)
+    assert wqp.get_device_error() == 0
+
+
+def passes(M, K):
+    g = torch.Generator(device=DEV).manual_seed(M + K)
+    return [torch.randn((M, K), generator=g, device=DEV).mul_(2.0 ** (i % 3)).bfloat16() for i in range(PASSES)]
+
+
+def w8_weights(N, K, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    w = (torch.randn((N, K), generator=g, device=DEV) * 20).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    return w, torch.rand(((N + 127) // 128, K // 128), generator=g, device=DEV) + 0.5
+
+
+def assert_same_under_pdl(chain, inputs):
+    """chain(x) -> tensors, its own buffers."""
+    want = [[t.clone() for t in chain(x)] for x in inputs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for x, w in zip(inputs, want):
+            wqp.set_pdl(True)
+            got = chain(x)
+            wqp.set_pdl(False)
+            got = [t.clone() for t in got]
+            assert all(torch.equal(a, b) for a, b in zip(got, w))
+
+
+@pytest.mark.parametrize("M", [1, 40, 3000])
+def test_quantise_then_unpack(M):
+    K = 5120
+    codes, scales = wqp.w4_quantize(torch.zeros(M, K, device=DEV))
+    values = torch.empty((M, K), device=DEV)
+
+    def chain(x):
+        wqp.w4_quantize(x, 0.03, out=(codes, scales))
+        return codes, scales, wqp.w4a16_dequant(codes, scales, M, K, 0.03, out=values)
+
+    assert_same_under_pdl(chain, passes(M, K))
+
+
+@pytest.mark.parametrize("M", [1, 40, 700])
+def test_norm_then_unpack_then_product(M):
+    """The unpacking in between has nothing to do with the rows: the product has to wait for the norm all the same."""
+    N, K = 640, 5120
+    w = torch.ones(K, dtype=torch.bfloat16, device=DEV)
+    w8, s8 = w8_weights(N, K, 1)
+    small, ss = w8_weights(128, 128, 2)
+    q2 = torch.zeros(8 * 34 * 8, dtype=torch.uint8, device=DEV)
+    codes, scales, h = wqp.rms_norm_a8(passes(M, K)[0], w, 1e-6, residual=passes(M, K)[1])
+    u = torch.empty((M, N), dtype=torch.bfloat16, device=DEV)
+    v, v2 = torch.empty((128, 128), device=DEV), torch.empty((8, 1024), device=DEV)
+
+    def chain(x):
+        wqp.rms_norm_a8(x, w, 1e-6, residual=x, residual_out=h, out=(codes, scales))
+        wqp.w8a16_dequant(small, ss, 128, 128, out=v)
+        wqp.q2_dequant(q2, 8, 1024, out=v2)
+        return wqp.w8a8_gemm(codes, scales, w8, s8, N, K, out=u), h, v
+
+    assert_same_under_pdl(chain, passes(M, K))

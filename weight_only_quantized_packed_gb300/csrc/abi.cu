@@ -191,7 +191,7 @@ int run_dequant(int fmt, const void* W, const void* scales, float gscale, float*
   DeviceInfo* dev = nullptr;
   int st = device_setup(&dev);
   if (st != WQP_OK) return st;
-  DequantArgs a = {W, scales, out, N, K, gscale, g_pdl.load(std::memory_order_relaxed) != 0};
+  DequantArgs a = {W, scales, out, N, K, gscale};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = fmt == 0   ? launch_q2_dequant(a, s)
                   : fmt == 1 ? launch_w4a16_dequant(a, s)

@@ -1,5 +1,8 @@
 // Dequant entry points: unpack every weight to FP32 with the GEMV kernels'
-// own decoders. A verification aid, not part of the hot path.
+// own decoders. A verification aid, not part of the hot path. Launched without
+// PDL whatever the policy: codes and scales come through the read-only path and
+// may be the previous kernel's (w4_quantize), and a grid that did not wait for
+// it would also end the chain of waits that later kernels rely on.
 #include "decode.cuh"
 
 namespace wqp {
@@ -88,17 +91,17 @@ dim3 grid_for(long long items) {
 
 cudaError_t launch_q2_dequant(const DequantArgs& a, cudaStream_t s) {
   return launch(q2_dequant_kernel, grid_for(static_cast<long long>(a.N) * (a.K / 128) * 8), dim3(256), 0, s,
-                a.pdl, static_cast<const uint8_t*>(a.W), a.out, a.N, a.K);
+                false, static_cast<const uint8_t*>(a.W), a.out, a.N, a.K);
 }
 cudaError_t launch_w4a16_dequant(const DequantArgs& a, cudaStream_t s) {
   const bool vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
   return launch(vec ? w4_dequant_kernel<true> : w4_dequant_kernel<false>,
-                grid_for((static_cast<long long>(a.N) * (a.K / 4) + 3) / 4), dim3(256), 0, s, a.pdl,
+                grid_for((static_cast<long long>(a.N) * (a.K / 4) + 3) / 4), dim3(256), 0, s, false,
                 static_cast<const uint8_t*>(a.W), static_cast<const uint8_t*>(a.scales), a.gscale,
                 a.out, a.N, a.K);
 }
 cudaError_t launch_w8a16_dequant(const DequantArgs& a, cudaStream_t s) {
-  return launch(w8_dequant_kernel, grid_for(static_cast<long long>(a.N) * a.K), dim3(256), 0, s, a.pdl,
+  return launch(w8_dequant_kernel, grid_for(static_cast<long long>(a.N) * a.K), dim3(256), 0, s, false,
                 static_cast<const uint8_t*>(a.W), static_cast<const float*>(a.scales), a.out, a.N,
                 a.K);
 }

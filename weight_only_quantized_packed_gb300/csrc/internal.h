@@ -59,7 +59,6 @@ struct DequantArgs {
   float* out;           // f32 [N, K]
   int N, K;
   float gscale;
-  bool pdl;
 };
 
 // Rows to quantise: X [M, ldx] of type dtype (wqp_dtype), codes and scales
