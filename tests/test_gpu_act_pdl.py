@@ -77,3 +77,30 @@ def test_norm_then_unpack_then_product(M):
         return wqp.w8a8_gemm(codes, scales, w8, s8, N, K, out=u), h, v
 
     assert_same_under_pdl(chain, passes(M, K))
+
+
+@pytest.mark.parametrize("M", [1, 24, 64, 100, 300])
+@pytest.mark.parametrize("fmt", [4, 8])
+def test_quantise_then_product(fmt, M):
+    """The rows' codes and scales are written by the kernel just before, over those of the pass before; M over the
+    kernels' ranges, with K split (640 columns) and not."""
+    K = 5120
+    first = passes(M, K)[0]
+    for N in (640, 20480):
+        u = torch.empty((M, N), dtype=torch.bfloat16, device=DEV)
+        if fmt == 4:
+            w, sw = wqp.w4_quantize(torch.randn((N, K), generator=torch.Generator(device=DEV).manual_seed(N), device=DEV), 0.002)
+            codes, scales = wqp.w4_quantize(first, 0.01)
+
+            def chain(x):
+                wqp.w4_quantize(x, 0.01, out=(codes, scales))
+                return codes, scales, wqp.w4a4_gemm(codes, scales, w, sw, N, K, 0.01, 0.002, out=u)
+        else:
+            w, sw = w8_weights(N, K, N)
+            codes, scales = wqp.a8_quantize(first)
+
+            def chain(x):
+                wqp.a8_quantize(x, out=(codes, scales))
+                return codes, scales, wqp.w8a8_gemm(codes, scales, w, sw, N, K, out=u)
+
+        assert_same_under_pdl(chain, passes(M, K))

@@ -259,9 +259,16 @@ struct ScaleRows {
     for (int e = 0; e < 2; ++e)
       p[e] = scales + static_cast<long long>(min(row0 + 64 * half + 32 * e + lane, rows - 1)) * pitch;
   }
+  // kWeights: through the read-only path. The activations' scales may have been
+  // written while this grid was already there (PDL), which that path does not
+  // allow for.
+  template <bool kWeights>
   __device__ __forceinline__ void load(int stage, uint4 (&v)[2]) const {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) v[e] = __ldg(reinterpret_cast<const uint4*>(p[e] + static_cast<long long>(stage) * 16));
+    for (int e = 0; e < 2; ++e) {
+      const uint4* q = reinterpret_cast<const uint4*>(p[e] + static_cast<long long>(stage) * 16);
+      v[e] = kWeights ? __ldg(q) : *q;
+    }
   }
 };
 __device__ __forceinline__ void put_scale_rows(uint8_t* block, int half, int lane, const uint4 (&v)[2]) {

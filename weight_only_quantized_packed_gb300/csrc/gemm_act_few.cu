@@ -234,11 +234,11 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
       uint4 vw[D][2], va[D][2];
 #pragma unroll
       for (int d = 0; d < D; ++d)
-        if (d < nst) rw.load(st0 + d, vw[d]);
+        if (d < nst) rw.load<true>(st0 + d, vw[d]);
       pdl_wait();
 #pragma unroll
       for (int d = 0; d < D; ++d)
-        if (d < nst && any) ra.load(st0 + d, va[d]);
+        if (d < nst && any) ra.load<false>(st0 + d, va[d]);
       for (int t0 = 0; t0 < nst; t0 += D) {        // after an abort: to the end, without waiting
 #pragma unroll
         for (int d = 0; d < D; ++d) {
@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
             __syncwarp();
             if (lane == 0) mbar_arrive(scaled + 8 * s);
             if (t + D < nst) {
-              rw.load(st0 + t + D, vw[d]);
-              if (any) ra.load(st0 + t + D, va[d]);
+              rw.load<true>(st0 + t + D, vw[d]);
+              if (any) ra.load<false>(st0 + t + D, va[d]);
             }
           }
         }
