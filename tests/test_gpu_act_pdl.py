@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import weight_only_quantized_packed_gb300 as wqp
+from tests import _gpu as G
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -104,3 +105,31 @@ def test_quantise_then_product(fmt, M):
                 return codes, scales, wqp.w8a8_gemm(codes, scales, w, sw, N, K, out=u)
 
         assert_same_under_pdl(chain, passes(M, K))
+
+
+WEIGHT_ONLY = {
+    "q2": (wqp.q2_gemv, wqp.q2_gemm_tc, wqp.q2_gemm_mma),
+    "w4": (wqp.w4a16_gemv, wqp.w4a16_gemm_tc, wqp.w4a16_gemm_mma),
+    "w8": (wqp.w8a16_gemm, wqp.w8a16_gemm_tc, wqp.w8a16_gemm_mma),
+}
+
+
+@pytest.mark.parametrize("M", [1, 5, 16])
+@pytest.mark.parametrize("N,K", [(640, 5120), (1000, 1024)])
+@pytest.mark.parametrize("fmt", sorted(WEIGHT_ONLY))
+def test_norm_then_weight_only_products(fmt, N, K, M):
+    """The norm's BF16 rows are the next kernel's activations, which it has to read as they were just written."""
+    d = G.make(fmt, 1, N, K, seed=77)
+    weights = (d["dW"],) if fmt == "q2" else (d["dW"], d["dS"])
+    w = torch.ones(K, dtype=torch.bfloat16, device=DEV)
+    y = torch.empty((M, K), dtype=torch.bfloat16, device=DEV)
+    outs = [torch.empty((M, N), dtype=torch.bfloat16, device=DEV) for _ in WEIGHT_ONLY[fmt]]
+
+    def chain(x):
+        for call, out in zip(WEIGHT_ONLY[fmt], outs):
+            wqp.rms_norm(x, w, 1e-6, out=y)
+            call(y, *weights, N, K, out=out)
+            x = x * 1.5 - 0.25
+        return outs
+
+    assert_same_under_pdl(chain, passes(M, K))

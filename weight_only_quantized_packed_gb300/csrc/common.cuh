@@ -99,9 +99,12 @@ __device__ __forceinline__ uint64_t policy_evict_first() {
 }
 
 // ------------------------------------------------------------------ loads
-__device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
+// 16 bytes of activations that this SM reads once. Not through the read-only
+// path (.nc): under PDL the previous kernel may write them while this grid is
+// already there. Volatile, so it stays behind the wait for that kernel.
+__device__ __forceinline__ uint4 ld_act_v4(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, kOcc)
         if constexpr (kMulti) {
           if (g + 8 * mt < p.M) cp_async16(abuf + (mt * 4 + q) * 32 + lane, act_src(t, mt, q));
         } else {
-          if (!bulk_act) act[mt][q] = ld_nc_v4(act_src(t, mt, q));
+          if (!bulk_act) act[mt][q] = ld_act_v4(act_src(t, mt, q));
         }
       }
     if constexpr (kMulti) cp_async_commit();

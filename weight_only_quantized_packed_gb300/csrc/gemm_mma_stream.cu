@@ -185,7 +185,7 @@ __device__ __forceinline__ void load_bact(const StreamParams& p, int kb, int mt,
   const uint16_t* src = p.A + static_cast<size_t>(m) * p.lda + kb + 32 * t4;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const uint4 v = ld_nc_v4(src + 8 * q);
+    const uint4 v = ld_act_v4(src + 8 * q);
     r[4 * q] = v.x;
     r[4 * q + 1] = v.y;
     r[4 * q + 2] = v.z;

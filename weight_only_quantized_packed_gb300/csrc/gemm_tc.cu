@@ -612,8 +612,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       if (j < ng && m < p.M) {
         const uint16_t* src = p.A + static_cast<size_t>(m) * p.lda + static_cast<size_t>(g_begin + j) * GK +
                               ((it >> 2) & 1) * 64 + (it & 3) * 16;
-        x = ld_nc_v4(src);
-        y = ld_nc_v4(src + 8);
+        x = ld_act_v4(src);
+        y = ld_act_v4(src + 8);
       }
     };
     uint4 cx = make_uint4(0, 0, 0, 0), cy = cx;

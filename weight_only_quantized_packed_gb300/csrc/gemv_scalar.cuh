@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, (ScalarCfg<F, M, ARES>::kMinBlocks))
       const int m = u / segK;
       const int sg = u - m * segK;
       const uint4* src = reinterpret_cast<const uint4*>(p.A + static_cast<size_t>(m) * p.lda + sg * 16);
-      const uint4 v0 = __ldg(src), v1 = __ldg(src + 1);
+      const uint4 v0 = src[0], v1 = src[1];     // not __ldg: the previous kernel's, see ld_act_v4
       widen_segment<F>(v0, v1, fA + m * ldfa, sg);
       if constexpr (F::kOffset) fOff[m * ldoff + sg] = F::seg_offset(v0, v1);
     }

@@ -94,7 +94,7 @@ __device__ __forceinline__ void build_bfrag(const uint16_t* A, int lda, int M, i
   uint32_t r[16];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const uint4 v = ld_nc_v4(src + 8 * q);
+    const uint4 v = ld_act_v4(src + 8 * q);
     r[4 * q] = v.x;
     r[4 * q + 1] = v.y;
     r[4 * q + 2] = v.z;
