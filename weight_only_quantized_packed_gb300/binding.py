@@ -4,6 +4,12 @@ Argument marshalling only. torch supplies device memory and the current
 stream, and every step of the computation runs in the library's CUDA
 kernels. There is no CPU or PyTorch fallback: if libwqp.so is missing or a
 call fails, an exception is raised.
+
+Every call takes ``stream`` (a stream object or a handle; the current stream
+without one). Outputs it makes belong to that stream, as if made under
+``torch.cuda.stream(stream)``, and may be read on the stream that is current
+after that one has been waited for. Operands are the caller's: complete before
+the call runs, and kept (or given to ``Tensor.record_stream``) until it has.
 """
 from __future__ import annotations
 
@@ -144,11 +150,27 @@ def _need_cuda(*ts):
             raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
 
 
-def _out(A, M, N, out):
-    import torch
+def _empty(shape, dtype, device, stream):
+    """A new output for a call on `stream` (its argument, not the handle)."""
+    torch = _torch
+    if stream is None or _stream(stream) == _stream(None):
+        return torch.empty(shape, dtype=dtype, device=device)
+    # From the pool of the call's stream: a block of the current stream's may
+    # still be in use by work queued there. The current stream is recorded, so
+    # that the block is not handed out again while it is read there.
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle > 1 else torch.cuda.default_stream(device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(current)
+    return out
 
+
+def _out(A, M, N, out, stream):
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        out = _empty((M, N), (_torch or _load_torch()).bfloat16, A.device, stream)
     return out
 
 
@@ -169,7 +191,7 @@ def q2_gemv(A, W, N: int, K: int, out=None, stream=None):
     """C[M, N] = A @ dequant_q2(W)^T. W is uint8 Q2_0 blocks (34*K/128 B per row)."""
     _need_cuda(A, W, out)
     M, lda = _rows(A, K)
-    C = _out(A, M, N, out)
+    C = _out(A, M, N, out, stream)
     _check(lib().q2_gemv_strided(_ptr(A), lda, _ptr(W), _ptr(C), C.stride(0), M, N, K,
                                  _stream(stream)), "q2_gemv")
     return C
@@ -179,7 +201,7 @@ def q2_gemm_tc(A, W, N: int, K: int, out=None, stream=None):
     """Tensor-core (tcgen05 swap-AB) form of q2_gemv, 1 <= M <= 16, K % 1024 == 0."""
     _need_cuda(A, W, out)
     M, lda = _rows(A, K)
-    C = _out(A, M, N, out)
+    C = _out(A, M, N, out, stream)
     _check(lib().q2_gemm_tc_strided(_ptr(A), lda, _ptr(W), _ptr(C), C.stride(0), M, N, K,
                                     _stream(stream)), "q2_gemm_tc")
     return C
@@ -189,7 +211,7 @@ def q2_gemm_mma(A, W, N: int, K: int, out=None, stream=None):
     """Warp-level tensor-core (mma.sync swap-AB) form of q2_gemv, 1 <= M <= 16, K % 1024 == 0."""
     _need_cuda(A, W, out)
     M, lda = _rows(A, K)
-    C = _out(A, M, N, out)
+    C = _out(A, M, N, out, stream)
     _check(lib().q2_gemm_mma_strided(_ptr(A), lda, _ptr(W), _ptr(C), C.stride(0), M, N, K,
                                      _stream(stream)), "q2_gemm_mma")
     return C
@@ -199,7 +221,7 @@ def w4a16_gemv(A, W, scales, N: int, K: int, global_scale: float = 1.0, out=None
     """C = A @ dequant_w4(W, scales, global_scale)^T."""
     _need_cuda(A, W, scales, out)
     M, lda = _rows(A, K)
-    C = _out(A, M, N, out)
+    C = _out(A, M, N, out, stream)
     _check(lib().w4a16_gemv_ex(_ptr(A), lda, _ptr(W), _ptr(scales), float(global_scale), _ptr(C),
                                C.stride(0), M, N, K, _stream(stream)), "w4a16_gemv")
     return C
@@ -209,7 +231,7 @@ def w4a16_gemm_tc(A, W, scales, N: int, K: int, global_scale: float = 1.0, out=N
     """Tensor-core (tcgen05 swap-AB) form of w4a16_gemv, 1 <= M <= 16, K % 256 == 0."""
     _need_cuda(A, W, scales, out)
     M, lda = _rows(A, K)
-    C = _out(A, M, N, out)
+    C = _out(A, M, N, out, stream)
     _check(lib().w4a16_gemm_tc_ex(_ptr(A), lda, _ptr(W), _ptr(scales), float(global_scale), _ptr(C),
                                   C.stride(0), M, N, K, _stream(stream)), "w4a16_gemm_tc")
     return C
@@ -219,7 +241,7 @@ def w4a16_gemm_mma(A, W, scales, N: int, K: int, global_scale: float = 1.0, out=
     """Warp-level tensor-core (mma.sync swap-AB) form of w4a16_gemv, K % 1024 == 0."""
     _need_cuda(A, W, scales, out)
     M, lda = _rows(A, K)
-    C = _out(A, M, N, out)
+    C = _out(A, M, N, out, stream)
     _check(lib().w4a16_gemm_mma_ex(_ptr(A), lda, _ptr(W), _ptr(scales), float(global_scale), _ptr(C),
                                    C.stride(0), M, N, K, _stream(stream)), "w4a16_gemm_mma")
     return C
@@ -229,7 +251,7 @@ def w8a16_gemm_mma(A, W, scales, N: int, K: int, out=None, stream=None):
     """Warp-level tensor-core (mma.sync swap-AB) form of w8a16_gemm, K % 1024 == 0."""
     _need_cuda(A, W, scales, out)
     M, lda = _rows(A, K)
-    C = _out(A, M, N, out)
+    C = _out(A, M, N, out, stream)
     _check(lib().w8a16_gemm_mma_strided(_ptr(A), lda, _ptr(W), _ptr(scales), _ptr(C), C.stride(0),
                                         M, N, K, _stream(stream)), "w8a16_gemm_mma")
     return C
@@ -239,7 +261,7 @@ def w8a16_gemm(A, W, scales, N: int, K: int, out=None, stream=None):
     """C = A @ (e4m3(W) * block_scales)^T, scalar-FMA kernels."""
     _need_cuda(A, W, scales, out)
     M, lda = _rows(A, K)
-    C = _out(A, M, N, out)
+    C = _out(A, M, N, out, stream)
     _check(lib().w8a16_gemm_strided(_ptr(A), lda, _ptr(W), _ptr(scales), _ptr(C), C.stride(0),
                                     M, N, K, _stream(stream)), "w8a16_gemm")
     return C
@@ -249,7 +271,7 @@ def w8a16_gemm_tc(A, W, scales, N: int, K: int, out=None, stream=None):
     """Tensor-core (tcgen05 swap-AB) form of w8a16_gemm, 1 <= M <= 16."""
     _need_cuda(A, W, scales, out)
     M, lda = _rows(A, K)
-    C = _out(A, M, N, out)
+    C = _out(A, M, N, out, stream)
     _check(lib().w8a16_gemm_tc_strided(_ptr(A), lda, _ptr(W), _ptr(scales), _ptr(C), C.stride(0),
                                        M, N, K, _stream(stream)), "w8a16_gemm_tc")
     return C
@@ -315,11 +337,11 @@ def _weights(name, t, count, dtype):
     return t.data_ptr()
 
 
-def _codes_out(x, codes_shape, scales_shape, scales_dtype, out):
+def _codes_out(x, codes_shape, scales_shape, scales_dtype, out, stream):
     """(codes, scales), new or the caller's."""
     if out is None:
-        return (_torch.empty(codes_shape, dtype=_torch.uint8, device=x.device),
-                _torch.empty(scales_shape, dtype=scales_dtype, device=x.device))
+        return (_empty(codes_shape, _torch.uint8, x.device, stream),
+                _empty(scales_shape, scales_dtype, x.device, stream))
     codes, scales = out
     if not (codes.is_cuda and scales.is_cuda):
         raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
@@ -336,7 +358,7 @@ def w4_quantize(x, global_scale: float = 1.0, out=None, stream=None):
     uint8 E4M3 scales [M, K/16], under one global_scale. out: (codes, scales) to write to."""
     torch = _torch or _load_torch()
     ldx, dt, M, K = _typed_rows("x", x)
-    codes, scales = _codes_out(x, (M, K // 2), (M, K // 16), torch.uint8, out)
+    codes, scales = _codes_out(x, (M, K // 2), (M, K // 16), torch.uint8, out, stream)
     status = (_lib or lib()).w4_quantize(x.data_ptr(), ldx, dt, float(global_scale), codes.data_ptr(),
                                          scales.data_ptr(), M, K, _stream(stream))
     if status:
@@ -349,7 +371,7 @@ def a8_quantize(x, out=None, stream=None):
     [M, K/128]. out: (codes, scales) to write to."""
     torch = _torch or _load_torch()
     ldx, dt, M, K = _typed_rows("x", x)
-    codes, scales = _codes_out(x, (M, K), (M, K // 128), torch.float32, out)
+    codes, scales = _codes_out(x, (M, K), (M, K // 128), torch.float32, out, stream)
     status = (_lib or lib()).a8_quantize(x.data_ptr(), ldx, dt, codes.data_ptr(), scales.data_ptr(), M, K,
                                          _stream(stream))
     if status:
@@ -357,7 +379,7 @@ def a8_quantize(x, out=None, stream=None):
     return codes, scales
 
 
-def _norm_args(x, weight, residual, residual_out):
+def _norm_args(x, weight, residual, residual_out, stream):
     """(residual's address and pitch, residual_out, its address and pitch, weight's address)."""
     K = x.shape[1]
     if not weight.is_cuda:
@@ -370,7 +392,7 @@ def _norm_args(x, weight, residual, residual_out):
         return None, 0, None, None, 0, weight.data_ptr()
     ldr = _rows_like("residual", residual, x)
     if residual_out is None:
-        residual_out, ldh = _torch.empty(x.shape, dtype=x.dtype, device=x.device), K
+        residual_out, ldh = _empty(x.shape, x.dtype, x.device, stream), K
     else:
         ldh = ldr if residual_out is residual else _rows_like("residual_out", residual_out, x)
     return residual.data_ptr(), ldr, residual_out, residual_out.data_ptr(), ldh, weight.data_ptr()
@@ -381,9 +403,9 @@ def rms_norm(x, weight, eps: float, residual=None, residual_out=None, out=None, 
     float16 or float32). Without a residual h is None. residual_out may be the residual itself."""
     torch = _torch or _load_torch()
     ldx, dt, M, K = _typed_rows("x", x)
-    pr, ldr, h, ph, ldh, pw = _norm_args(x, weight, residual, residual_out)
+    pr, ldr, h, ph, ldh, pw = _norm_args(x, weight, residual, residual_out, stream)
     if out is None:
-        out, ldy = torch.empty((M, K), dtype=x.dtype, device=x.device), K
+        out, ldy = _empty((M, K), x.dtype, x.device, stream), K
     else:
         ldy = _rows_like("out", out, x)
     status = (_lib or lib()).rms_norm(x.data_ptr(), ldx, pr, ldr, pw, float(eps), ph, ldh, out.data_ptr(), ldy,
@@ -398,8 +420,8 @@ def rms_norm_a8(x, weight, eps: float, residual=None, residual_out=None, out=Non
     """(codes, scales, h): rms_norm with y written as a8_quantize writes it. out: (codes, scales)."""
     torch = _torch or _load_torch()
     ldx, dt, M, K = _typed_rows("x", x)
-    pr, ldr, h, ph, ldh, pw = _norm_args(x, weight, residual, residual_out)
-    codes, scales = _codes_out(x, (M, K), (M, K // 128), torch.float32, out)
+    pr, ldr, h, ph, ldh, pw = _norm_args(x, weight, residual, residual_out, stream)
+    codes, scales = _codes_out(x, (M, K), (M, K // 128), torch.float32, out, stream)
     status = (_lib or lib()).rms_norm_a8(x.data_ptr(), ldx, pr, ldr, pw, float(eps), ph, ldh, codes.data_ptr(),
                                          scales.data_ptr(), dt, M, K,
                                          _stream(stream))
@@ -408,9 +430,9 @@ def rms_norm_a8(x, weight, eps: float, residual=None, residual_out=None, out=Non
     return codes, scales, h
 
 
-def _gemm_out(A, M, N, out):
+def _gemm_out(A, M, N, out, stream):
     if out is None:
-        return _torch.empty((M, N), dtype=_torch.bfloat16, device=A.device), N
+        return _empty((M, N), _torch.bfloat16, A.device, stream), N
     if not out.is_cuda:
         raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
     if out.dtype is not _torch.bfloat16:
@@ -428,7 +450,7 @@ def w4a4_gemm(A, a_scales, W, w_scales, N: int, K: int, a_global: float = 1.0, w
     M, u8 = A.shape[0], torch.uint8
     pa, psa = _packed("A", A, (M, K // 2), u8), _packed("a_scales", a_scales, (M, K // 16), u8)
     pw, psw = _weights("W", W, N * (K // 2), u8), _weights("w_scales", w_scales, N * (K // 16), u8)
-    C, ldc = _gemm_out(A, M, N, out)
+    C, ldc = _gemm_out(A, M, N, out, stream)
     status = (_lib or lib()).w4a4_gemm(pa, psa, float(a_global), pw, psw, float(w_global), C.data_ptr(), ldc, M, N, K,
                                        _stream(stream))
     if status:
@@ -443,31 +465,29 @@ def w8a8_gemm(A, a_scales, W, w_scales, N: int, K: int, out=None, stream=None):
     pa, psa = _packed("A", A, (M, K), torch.uint8), _packed("a_scales", a_scales, (M, K // 128), torch.float32)
     pw = _weights("W", W, N * K, torch.uint8)
     psw = _weights("w_scales", w_scales, (N + 127) // 128 * (K // 128), torch.float32)
-    C, ldc = _gemm_out(A, M, N, out)
+    C, ldc = _gemm_out(A, M, N, out, stream)
     status = (_lib or lib()).w8a8_gemm(pa, psa, pw, psw, C.data_ptr(), ldc, M, N, K, _stream(stream))
     if status:
         _check(status, "w8a8_gemm")
     return C
 
 
-def _deq_out(W, N, K, out):
-    import torch
-
+def _deq_out(W, N, K, out, stream):
     if out is None:
-        out = torch.empty((N, K), dtype=torch.float32, device=W.device)
+        out = _empty((N, K), (_torch or _load_torch()).float32, W.device, stream)
     return out
 
 
 def q2_dequant(W, N: int, K: int, out=None, stream=None):
     _need_cuda(W, out)
-    o = _deq_out(W, N, K, out)
+    o = _deq_out(W, N, K, out, stream)
     _check(lib().q2_dequant(_ptr(W), _ptr(o), N, K, _stream(stream)), "q2_dequant")
     return o
 
 
 def w4a16_dequant(W, scales, N: int, K: int, global_scale: float = 1.0, out=None, stream=None):
     _need_cuda(W, scales, out)
-    o = _deq_out(W, N, K, out)
+    o = _deq_out(W, N, K, out, stream)
     _check(lib().w4a16_dequant(_ptr(W), _ptr(scales), float(global_scale), _ptr(o), N, K,
                                _stream(stream)), "w4a16_dequant")
     return o
@@ -475,7 +495,7 @@ def w4a16_dequant(W, scales, N: int, K: int, global_scale: float = 1.0, out=None
 
 def w8a16_dequant(W, scales, N: int, K: int, out=None, stream=None):
     _need_cuda(W, scales, out)
-    o = _deq_out(W, N, K, out)
+    o = _deq_out(W, N, K, out, stream)
     _check(lib().w8a16_dequant(_ptr(W), _ptr(scales), _ptr(o), N, K, _stream(stream)),
            "w8a16_dequant")
     return o
