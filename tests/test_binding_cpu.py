@@ -140,3 +140,59 @@ def test_outputs_on_the_current_stream_are_plain(world, name, given):
     call(stream=given)
     assert [(t.pool, t.recorded) for t in world.made] == [(CURRENT, [])] * count
     assert world.calls[-1][1][-1] == CURRENT
+
+
+# Pitches: (entry, call with rows of the given strides, position of the pitch in the library's arguments, pitch of contiguous rows).
+def _gemm4(C):
+    return binding.w4a4_gemm(u8(2, K // 2), u8(2, K // 16), u8(N, K // 2), u8(N, K // 16), N, K, out=C)
+
+
+def _gemm8(C):
+    return binding.w8a8_gemm(u8(2, K), f32(2, K // 128), u8(N, K), f32(N // 128, K // 128), N, K, out=C)
+
+
+def _norm(x=None, r=None, h=None, y=None, m=2):
+    return binding.rms_norm(x or bf16(m, K), bf16(K), 1e-6, residual=r or bf16(m, K), residual_out=h, out=y)
+
+
+def _norm8(x=None, r=None, h=None, m=2):
+    return binding.rms_norm_a8(x or bf16(m, K), bf16(K), 1e-6, residual=r or bf16(m, K), residual_out=h)
+
+
+PITCHED = [
+    ("w4_quantize x", K, 1, lambda t: binding.w4_quantize(t, 1.0)), ("a8_quantize x", K, 1, binding.a8_quantize),
+    ("rms_norm x", K, 1, lambda t: _norm(x=t, m=t.shape[0])), ("rms_norm residual", K, 3, lambda t: _norm(r=t, m=t.shape[0])),
+    ("rms_norm residual_out", K, 7, lambda t: _norm(h=t, m=t.shape[0])), ("rms_norm out", K, 9, lambda t: _norm(y=t, m=t.shape[0])),
+    ("rms_norm_a8 x", K, 1, lambda t: _norm8(x=t, m=t.shape[0])), ("rms_norm_a8 residual", K, 3, lambda t: _norm8(r=t, m=t.shape[0])),
+    ("rms_norm_a8 residual_out", K, 7, lambda t: _norm8(h=t, m=t.shape[0])),
+]
+for _n, _w in [("q2_gemv", (u8(N, K * 34 // 128),)), ("q2_gemm_tc", (u8(N, K * 34 // 128),)), ("q2_gemm_mma", (u8(N, K * 34 // 128),))] + [
+        (n, (u8(N, K), u8(N, K // 16)))
+        for n in ("w4a16_gemv", "w4a16_gemm_tc", "w4a16_gemm_mma", "w8a16_gemm", "w8a16_gemm_tc", "w8a16_gemm_mma")]:
+    PITCHED += [(_n + " A", K, 1, lambda t, n=_n, w=_w: getattr(binding, n)(t, *w, N, K)),
+                (_n + " out", N, {1: 4, 2: 5}[len(_w)] + _n.startswith("w4"),
+                 lambda t, n=_n, w=_w: getattr(binding, n)(bf16(t.shape[0], K), *w, N, K, out=t))]
+PITCHED_OUT = [("w4a4_gemm out", N, 7, _gemm4), ("w8a8_gemm out", N, 5, _gemm8)]
+
+
+@pytest.mark.parametrize("pitch", [2 ** 31, 2 ** 32 + 2048, 5 * 2 ** 30])
+@pytest.mark.parametrize("name,cols,at,call", PITCHED + PITCHED_OUT, ids=[p[0] for p in PITCHED + PITCHED_OUT])
+def test_pitches_beyond_an_int_are_refused(world, name, cols, at, call, pitch):
+    """The C ABI takes a pitch as an int: a larger one would arrive as another pitch."""
+    with pytest.raises(ValueError, match="pitch"):
+        call(bf16(2, cols, strides=(pitch, 1)))
+    assert not world.calls
+
+
+@pytest.mark.parametrize("name,cols,at,call", PITCHED + PITCHED_OUT, ids=[p[0] for p in PITCHED + PITCHED_OUT])
+def test_the_largest_pitch_arrives(world, name, cols, at, call):
+    call(bf16(2, cols, strides=(2 ** 31 - 8, 1)))
+    assert world.calls[-1][1][at] == 2 ** 31 - 8
+
+
+@pytest.mark.parametrize("pitch", [5, 5 * 2 ** 30, 2 ** 32 + 2048])
+@pytest.mark.parametrize("name,cols,at,call", PITCHED, ids=[p[0] for p in PITCHED])
+def test_one_row_has_no_pitch(world, name, cols, at, call, pitch):
+    """The last token of one long sequence: [1, T, K][:, -1] is T * K apart from nothing."""
+    call(bf16(1, cols, strides=(pitch, 1)))
+    assert world.calls[-1][1][at] == cols

@@ -472,6 +472,22 @@ def test_binding_refuses():
     assert wqp.rms_norm(x[:0], w, 1e-6)[0].shape == (0, 256) and wqp.w4_quantize(x[:0])[0].shape == (0, 128)
 
 
+@pytest.mark.parametrize("pitch", [5, 5 * 2 ** 30, 2 ** 32 + 2048])
+def test_a_single_row_of_any_stride(pitch):
+    """[1, T, K][:, -1] has one row, T * K elements from the next: the stride means nothing."""
+    N, K = 256, 1024
+    x, r = rows(1, K, torch.bfloat16, 0, 1), rows(1, K, torch.bfloat16, 0, 2)
+    w = torch.ones(K, dtype=torch.bfloat16, device=DEV)
+    w8, s8, _ = w8_operand(N, K, 3, True, True)
+    one = lambda t: torch.as_strided(t, t.shape, (pitch, 1))
+    assert all(torch.equal(a, b) for a, b in zip(wqp.w4_quantize(x), wqp.w4_quantize(one(x))))
+    assert all(torch.equal(a, b) for a, b in zip(wqp.rms_norm(x, w, 1e-6, residual=r),
+                                                 wqp.rms_norm(one(x), w, 1e-6, residual=one(r), residual_out=one(r.clone()), out=one(x.clone()))))
+    out = torch.empty(1, N, dtype=torch.bfloat16, device=DEV)
+    want = wqp.w8a16_gemm(x, w8, s8, N, K)
+    assert torch.equal(wqp.w8a16_gemm(one(x), w8, s8, N, K, out=one(out)), want) and torch.equal(out, want)
+
+
 def test_example_runs():
     """The example's block with quantised activations is near the one without: E2M1 rows and weights keep about
     three significant bits, so their product over many K is a few percent to a tenth off."""
