@@ -152,20 +152,29 @@ __device__ __forceinline__ uint32_t quantise4(const float (&v)[8], float g, floa
   const float d = e4m3_to_f32(s) * g;
   const bool fin = finite(m);
   const float inv = (d > 0.0f && fin) ? 1.0f / d : 0.0f;
-  float q[8];
   // x / d, correctly rounded, from the correctly rounded reciprocal by one
   // residual step (P. Markstein, "Computation of elementary functions on the
   // IBM RISC System/6000 processor", 1990): a quotient that falls on the
   // middle between two codes has to be recognised as such, which x * inv
-  // alone misses for 3 of the 8 scale mantissas. Groups whose scale saturates
-  // may overflow there and take the product as it is: they end at +-6.
+  // alone misses for 3 of the 8 scale mantissas. A quotient may overflow where
+  // the scale saturates by far; elements beyond 8 d, which end at +-6, are
+  // brought to 8 d there.
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = v[i];
+  const bool far = t > 0x1p100f;
+  if (__any_sync(0xFFFFFFFFu, far)) {
+    const float lim = far ? 8.0f * d : __uint_as_float(0x7F7FFFFFu);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -lim), lim);
+  }
+  float q[8];
   const uint64_t inv2 = pack2(inv, inv), nd2 = pack2(-d, -d);
-  const bool fix = t <= 448.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint64_t x2 = pack2(v[2 * i], v[2 * i + 1]);
+    const uint64_t x2 = pack2(x[2 * i], x[2 * i + 1]);
     uint64_t q2 = mul2(x2, inv2);
-    if (fix) q2 = fma2(fma2(q2, nd2, x2), inv2, q2);
+    q2 = fma2(fma2(q2, nd2, x2), inv2, q2);
     q[2 * i] = lo2(q2);
     q[2 * i + 1] = hi2(q2);
   }
