@@ -34,19 +34,25 @@ def near_middles(d, groups, dtype, seed):
     return torch.where(torch.rand((groups, 16), generator=g) < 0.5, -v, v)
 
 
-# Global scales with few and with many bits, tiny and large.
-@pytest.mark.parametrize("g", [0.53125, 0.00059581938, 1.0, 0.3, 1.1 * 2.0 ** -20, 1.37 * 2.0 ** -100, 1.9 * 2.0 ** 60])
-@pytest.mark.parametrize("over", [0.0, 1.0004, 1.7, 1000.0, 2.0 ** 95, 2.0 ** 103, 2.0 ** 120])
-@pytest.mark.parametrize("dtype", TYPES)
-def test_w4_quantize_rounds_the_quotient_in_every_group(dtype, g, over):
-    """Groups whose amax / (6 g) is `over` times the largest scale (0: exactly the largest scale), with elements around
-    the middles between two codes."""
-    g = float(torch.tensor(g))
+def saturating(dtype, g, over):
+    """(d, amax) of groups whose amax / (6 g) is `over` times the largest scale."""
     d = float(torch.tensor(448.0) * torch.tensor(g))
-    amax = torch.tensor(max(over, 1.0) * 6 * d, dtype=torch.float64).to(dtype)
-    if not (amax.isfinite() and float(amax) > 5.2 * d and torch.tensor(d / 4).to(dtype) > 0):
-        pytest.skip("outside the type's range")
-    groups = 512
+    return d, torch.tensor(over * 6 * d, dtype=torch.float64).to(dtype)
+
+
+def in_range(dtype, g, over):
+    d, amax = saturating(dtype, g, over)
+    return bool(amax.isfinite()) and float(amax) > 5.2 * d and bool(torch.tensor(d / 4).to(dtype) > 0)
+
+
+# Global scales with few and with many bits, tiny and large; what of them the type can hold.
+@pytest.mark.parametrize("dtype,g,over", [
+    (t, g, over) for t in TYPES for g in [0.53125, 0.00059581938, 1.0, 0.3, 1.1 * 2.0 ** -20, 1.37 * 2.0 ** -100, 1.9 * 2.0 ** 60]
+    for over in [1.0, 1.0004, 1.7, 1000.0, 2.0 ** 95, 2.0 ** 103, 2.0 ** 120] if in_range(t, g, over)])
+def test_w4_quantize_rounds_the_quotient_in_every_group(dtype, g, over):
+    """Elements around the middles between two codes, of groups at and beyond the largest scale."""
+    g, groups = float(torch.tensor(g)), 512
+    d, amax = saturating(dtype, g, over)
     x = near_middles(d, groups, dtype, seed=int(over) % 97 + 1)
     x[:, 3] = torch.where(torch.arange(groups) % 2 == 0, amax, -amax)
     codes, scales = wqp.w4_quantize(x.view(8, -1).to(DEV), g)
@@ -68,3 +74,15 @@ def test_w4_quantize_calibrated_global_scale():
         assert torch.equal(unpack4(codes).view(groups, 16), codes_of(x.float(), d))
         hit += bool(torch.tensor(amax) / (torch.tensor(6.0) * torch.tensor(g)) > 448)
     assert hit
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_w4_quantize_codes_under_a_zero_scale_are_zero(dtype):
+    """Elements of either sign in groups whose scale rounds to nothing."""
+    x = torch.zeros(4, 128)
+    x[1] = 2.0 ** -14
+    x[2] = -(2.0 ** -14)
+    x[3, ::3] = -0.0
+    x[3, 1::3] = -(2.0 ** -15)
+    codes, scales = wqp.w4_quantize(x.to(dtype).to(DEV), 1.0)
+    assert not scales.any() and not codes.any()

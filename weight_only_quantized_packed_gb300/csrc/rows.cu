@@ -179,7 +179,7 @@ __device__ __forceinline__ uint32_t quantise4(const float (&v)[8], float g, floa
     q[2 * i + 1] = hi2(q2);
   }
   scale = fin ? s : 0x7Fu;
-  return fin ? f32x8_to_e2m1(q) : 0u;
+  return inv > 0.0f ? f32x8_to_e2m1(q) : 0u;     // not the sign of x where d is 0
 }
 
 // This lane's 8 elements of a 128-group (16 lanes): their codes, and the
