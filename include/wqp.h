@@ -280,7 +280,8 @@ int rms_norm_a8(const void* X, int ldx, const void* residual, int ldr, const voi
  * products, FP32 accumulation). A [M, K/2] and W [N, K/2] codes, a_scales
  * [M, K/16] and w_scales [N, K/16], all contiguous and 16-byte aligned;
  * K % 256 == 0, K <= 2^20, N <= 2^24, ldc >= N, C 2-byte aligned. Scales are
- * magnitudes: a scale code with its sign bit set counts as NaN. Any M. */
+ * magnitudes: a scale code with its sign bit set counts as NaN. The global scales
+ * multiply whole sums, and their product may itself pass FP32's range. Any M. */
 int w4a4_gemm(const void* A, const void* a_scales, float a_global, const void* W, const void* w_scales,
               float w_global, void* C, int ldc, int M, int N, int K, void* stream);
 

@@ -265,6 +265,24 @@ int run_norm(bool a8, const void* X, int ldx, const void* R, int ldr, const void
   return e == cudaSuccess ? WQP_OK : cuda_fail(e, nm);
 }
 
+// a * b as a power of two times a factor. The power is 1 unless FP32 has the
+// product as infinity, as 0 or with fewer bits, though a sum times it may be in
+// BF16's range: the 4-bit sums are 0 or between 2^-20 and 2^43 in magnitude, so
+// their product with the power is in FP32's normal range, and the factor takes
+// it out of that only where the result is.
+void split_scale(float a, float b, float* pow, float* factor) {
+  const double p = static_cast<double>(a) * b, m = p < 0.0 ? -p : p;     // exact
+  *pow = 1.0f;
+  *factor = a * b;
+  if (m > 0.0 && m < 0x1p-126) {
+    *pow = 0x1p-84f;
+    *factor = static_cast<float>(p * 0x1p84);
+  } else if (m >= 0x1p128 && m < 0x1p256) {      // from 2^148 on only zeros stay finite
+    *pow = 0x1p60f;
+    *factor = m < 0x1p187 ? static_cast<float>(p * 0x1p-60) : (p < 0.0 ? -0x1p127f : 0x1p127f);
+  }
+}
+
 int run_act_gemm(bool w4, const void* A, const void* SA, float ga, const void* W, const void* SW, float gw, void* C,
                  int ldc, int M, int N, int K, void* stream) {
   const char* nm = w4 ? "w4a4_gemm" : "w8a8_gemm";
@@ -286,7 +304,9 @@ int run_act_gemm(bool w4, const void* A, const void* SA, float ga, const void* W
   DeviceInfo* dev = nullptr;
   const int st = device_setup(&dev);
   if (st != WQP_OK) return st;
-  const ActGemmArgs a = {A, SA, W, SW, C, ga * gw, M, N, K, ldc, dev->err, dev->num_sms,
+  float gpow, gscale;
+  split_scale(ga, gw, &gpow, &gscale);
+  const ActGemmArgs a = {A, SA, W, SW, C, gpow, gscale, M, N, K, ldc, dev->err, dev->num_sms,
                          g_pdl.load(std::memory_order_relaxed) != 0};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = w4 ? launch_w4a4_gemm(a, s) : launch_w8a8_gemm(a, s);

@@ -197,12 +197,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Two FP32 values in one register pair, and (x, y) = (x, y) * f + (x, y)'.
+// Two FP32 values in one register pair, (x, y) = (x, y) * f + (x, y)' and (x, y) * f.
 __device__ __forceinline__ uint64_t pair_f32(uint32_t lo, uint32_t hi) {
   return static_cast<uint64_t>(lo) | (static_cast<uint64_t>(hi) << 32);
 }
 __device__ __forceinline__ void fma_f32x2(uint64_t& acc, uint64_t v, uint64_t f) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(f));
+}
+__device__ __forceinline__ void mul_f32x2(uint64_t& v, uint64_t f) {
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(f));
 }
 
 // ---------------------------------------------------------------- 4-bit scales

@@ -34,7 +34,7 @@ constexpr int kMaxSplits = 8;
 struct FewParams {
   const void* SA;
   const void* SW;
-  float gscale;
+  float gpow, gscale;
   uint16_t* C;
   int M, N, K, ldc;
   int splits, stages;
@@ -101,6 +101,9 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
   const uint32_t acc_full = smem_u32(acc_full_sh), acc_free = smem_u32(acc_free_sh), recv_bar = smem_u32(&recv_sh);
   const int own = (rows - rank + splits - 1) / splits;     // of them: rank, rank + splits, ...
   volatile int* abort_flag = &abort_sh;
+  // A whole sum to C: the global scales come last, as parts of a sum could pass
+  // FP32's range with them where the sum does not.
+  const auto rounded = [&](float v) { return f32_to_bf16_rn(F::kScaled ? (v * p.gpow) * p.gscale : v); };
 
   // The thread that copies: sets up the barriers and starts the first stages'
   // weights, which do not depend on the previous grid, before the CTA meets.
@@ -276,7 +279,7 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
           tmem_ld16_start(tl + c, v);
           tmem_ld_wait(v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[c + i] = __uint_as_float(v[i]) * p.gscale;
+          for (int i = 0; i < 16; ++i) acc[c + i] = __uint_as_float(v[i]);
         }
       }
     } else {
@@ -356,7 +359,7 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
       uint16_t* c = p.C + static_cast<long long>(m0 + c0) * p.ldc + n0 + r;
 #pragma unroll
       for (int m = 0; m < COLS; ++m)
-        if (c0 + m < rows) c[static_cast<long long>(m) * p.ldc] = f32_to_bf16_rn(acc[m]);
+        if (c0 + m < rows) c[static_cast<long long>(m) * p.ldc] = rounded(acc[m]);
     }
   }
   if (splits > 1 && warp < kEpiWarp0) cluster_wait();
@@ -380,7 +383,7 @@ __global__ void __launch_bounds__(FewLayout<F, NT, kShared>::kThreads, FewLayout
       for (int i = threadIdx.x >> 7; i < own; i += L::kThreads / 128) {
         float v = recv[i * 128 + r];
         for (int src = 1; src < splits; ++src) v += recv[(src * per + i) * 128 + r];
-        p.C[static_cast<long long>(m0 + i * splits + rank) * p.ldc + n0 + r] = f32_to_bf16_rn(v);
+        p.C[static_cast<long long>(m0 + i * splits + rank) * p.ldc + n0 + r] = rounded(v);
       }
     }
   }
@@ -453,6 +456,7 @@ cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
   FewParams p = {};
   p.SA = a.SA;
   p.SW = a.SW;
+  p.gpow = a.gpow;
   p.gscale = a.gscale;
   p.C = static_cast<uint16_t*>(a.C);
   p.M = a.M;

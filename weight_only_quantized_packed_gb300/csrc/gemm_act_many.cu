@@ -38,7 +38,7 @@ namespace {
 struct ManyParams {
   const float* SA;
   const float* SW;
-  float gscale;
+  float gpow, gscale;
   uint16_t* C;
   int M, N, K, ldc;
   int mt, nt;           // tiles of 256 rows of the first operand, of BN rows of the second
@@ -345,6 +345,8 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       const int a0 = mi * 256 + rank * 128 + q * 32, b0 = ni * BN + h * COLS;   // the warp's rows of either operand
       uint32_t packed[COLS / 2];
       if constexpr (F::kScaled) {
+        const uint64_t gp = pair_f32(__float_as_uint(p.gpow), __float_as_uint(p.gpow));
+        const uint64_t gs = pair_f32(__float_as_uint(p.gscale), __float_as_uint(p.gscale));
         wait_or_abort(acc_full + 8 * slot, ph, p.err, abort_flag);
         __syncwarp();
         tc_fence_after();
@@ -354,8 +356,12 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
           tmem_ld32_start(tl + slot * BN + c, v);
           tmem_ld_wait(v);
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            packed[c / 2 + j] = pack_bf16(__uint_as_float(v[2 * j]) * p.gscale, __uint_as_float(v[2 * j + 1]) * p.gscale);
+          for (int j = 0; j < 16; ++j) {
+            uint64_t x = pair_f32(v[2 * j], v[2 * j + 1]);
+            mul_f32x2(x, gp);
+            mul_f32x2(x, gs);
+            packed[c / 2 + j] = pack_bf16(__uint_as_float(static_cast<uint32_t>(x)), __uint_as_float(static_cast<uint32_t>(x >> 32)));
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -534,6 +540,7 @@ cudaError_t launch_many_t(const ActGemmArgs& a, cudaStream_t s) {
     p.SA = static_cast<const float*>(a.SA);
     p.SW = static_cast<const float*>(a.SW);
   }
+  p.gpow = a.gpow;
   p.gscale = a.gscale;
   p.C = static_cast<uint16_t*>(a.C);
   p.M = a.M;

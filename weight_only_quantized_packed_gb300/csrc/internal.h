@@ -96,7 +96,9 @@ struct ActGemmArgs {
   const void* W;
   const void* SW;       // E4M3 [N, K/16] or float [ceil(N/128), K/128]
   void* C;
-  float gscale;         // product of the two global scales (1 for 8-bit)
+  // The product of the two global scales (1 for 8-bit) is gpow * gscale: the sums
+  // are multiplied by the power of two first, which is 1 where FP32 has the product.
+  float gpow, gscale;
   int M, N, K, ldc;
   unsigned* err;
   int num_sms;
