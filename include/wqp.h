@@ -266,7 +266,8 @@ int a8_quantize(const void* X, int ldx, int dtype, void* codes, float* scales, i
  * with residual NULL), y = (h * rsqrt(mean(h^2) + eps)) * weight, in FP32
  * from the unrounded h. residual_out receives h rounded (it may be NULL, and
  * may be the residual or X itself, with the same pitch); Y [M, ldy] receives
- * y rounded (it may be X). eps >= 0. */
+ * y rounded (it may be X). eps >= 0. The sum of squares is FP32's too: where it
+ * passes that range (elements around 2^60), y is 0. */
 int rms_norm(const void* X, int ldx, const void* residual, int ldr, const void* weight, float eps,
              void* residual_out, int ldro, void* Y, int ldy, int dtype, int M, int K, void* stream);
 
@@ -288,7 +289,8 @@ int w4a4_gemm(const void* A, const void* a_scales, float a_global, const void* W
 /* C[m, n] = bf16(sum_b sa[m, b] sw[n/128, b] sum_{k in block b} a w), with A
  * [M, K] E4M3 and a_scales float [M, K/128] as a8_quantize writes them, and
  * the W8A16 weights (E4M3 [N, K], float [ceil(N/128), K/128]). Each 128-K
- * block is summed by the tensor core and scaled once, in FP32. A and W
+ * block is summed by the tensor core and scaled once, by the FP32 product of
+ * its two scales (which has to be in FP32's normal range). A and W
  * contiguous and 16-byte aligned, scales 4-byte aligned; otherwise as
  * w4a4_gemm, with K % 128 == 0. */
 int w8a8_gemm(const void* A, const float* a_scales, const void* W, const float* w_scales, void* C, int ldc,
@@ -320,8 +322,9 @@ int wqp_row_chunks(int M, int K, int N, int max_rows, long long* out, int cap);
 
 /* Launch policy: when enabled, kernels are launched with programmatic
  * dependent launch (PDL). A kernel may then start while the previous kernel
- * on the stream is finishing. It prefetches W (and the scales) before it
- * waits for that kernel, and reads A only after the wait. So with PDL
+ * on the stream is finishing. It prefetches W (and W's scales) before it
+ * waits for that kernel, and reads A (and A's scales) only after the wait. The
+ * dequant entries and the launches without PDL start after it. So with PDL
  * enabled, W must not be written by the kernel launched just before on the
  * same stream; nor, as each kernel lets the next one start before it has itself
  * waited, by earlier ones since the last launch without PDL. Where weights are

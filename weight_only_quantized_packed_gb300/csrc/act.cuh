@@ -1,5 +1,5 @@
-// Primitives and formats of the quantised-activation GEMMs (gemm_act_rows.cu,
-// gemm_act_cols.cu): tcgen05 with 8-bit operands, and with 4-bit operands
+// Primitives and formats of the quantised-activation GEMMs (gemm_act_few.cu,
+// gemm_act_many.cu): tcgen05 with 8-bit operands, and with 4-bit operands
 // whose scales the tensor core applies itself.
 #pragma once
 #include "decode.cuh"

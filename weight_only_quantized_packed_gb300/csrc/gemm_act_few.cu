@@ -486,10 +486,11 @@ cudaError_t launch_few_nt(const ActGemmArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, few_kernel<F, NT, kShared>, mw, ma, p);
 }
 
-// Whether a call is this kernel's: always up to 64 rows, and where K can be
-// split over the SMs that few tiles leave idle and that saves more time than the
-// sums of the parts cost; else gemm_act_many.cu's wide tiles win. Measured,
-// here | there, us:
+// Whether a call is this kernel's: always up to 64 rows (with 4 bits a fixed
+// choice that costs a tenth where nearly every SM has one tile whose K is not
+// split: 64x10240x5120 below), and where K can be split over the SMs that few
+// tiles leave idle and that saves more time than the sums of the parts cost;
+// else gemm_act_many.cu's wide tiles win. Measured, here | there, us:
 //  * 4 bits: 40x10240x5120 12.1 | 12.9, 49x17408x5120 13.7 | 18.5, 64x10240x5120
 //    12.7 | 11.3, 64x17408x2560 8.8 | 11.5, 64x34816x5120 19.7 | 25.0,
 //    64x2560x10240 8.7 | 15.7; 100x640x5120 7.5 | 10.1, 100x5120x5120 10.3 | 10.4,

@@ -9,14 +9,16 @@
 //  * 4 bits: the tensor core applies the scales, rearranged by warps of each CTA
 //    (its 128 activation rows, all BN weight rows) and copied to tensor memory
 //    by the MMA warp. One or two accumulators, drained into registers as BF16.
-//    4096x34816x5120: 236 us, 6.2 PFLOP/s until the power cap slows the clock.
+//    4096x34816x5120: 236 us, 6.2 PFLOP/s until the power cap slows the clock,
+//    264 to 272 us, 5.4 PFLOP/s, in steady use.
 //    The tensor pipe is busy for two thirds of it; next are the bytes into an
 //    SM (38 KB a stage, at 64 a clock nine tenths of a stage's time) and the
 //    drains between tiles.
 //  * 8 bits: two to four accumulators that take turns per 128 K; the epilogue
 //    adds each, times its activation row's and weight block's scale, to FP32
 //    sums in registers while the tensor core fills the others.
-//    4096x5120x17408: 277 to 290 us, 2.5 PFLOP/s. Bound by that reading and adding: 773
+//    4096x5120x17408: 277 to 290 us, 2.5 PFLOP/s, until the power cap slows the
+//    clock, 315 to 324 us in steady use. Bound by that reading and adding: 773
 //    clocks per 128 K of a 256-column tile, of which the MMAs are 544; without
 //    the additions 238 us.
 // With 4 bits the operands may change places (kSwap): 256 weight rows by BN
@@ -345,6 +347,8 @@ __global__ void __launch_bounds__(ManyLayout<F, BN>::kThreads, 1)
       const int a0 = mi * 256 + rank * 128 + q * 32, b0 = ni * BN + h * COLS;   // the warp's rows of either operand
       uint32_t packed[COLS / 2];
       if constexpr (F::kScaled) {
+        // Both factors always, two values an instruction: a branch on the power (1
+        // but for extreme global scales) costs registers that there are not.
         const uint64_t gp = pair_f32(__float_as_uint(p.gpow), __float_as_uint(p.gpow));
         const uint64_t gs = pair_f32(__float_as_uint(p.gscale), __float_as_uint(p.gscale));
         wait_or_abort(acc_full + 8 * slot, ph, p.err, abort_flag);

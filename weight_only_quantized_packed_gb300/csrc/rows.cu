@@ -6,7 +6,7 @@
 // under the time of its bytes.
 //
 // w4_quantize, per group of 16 (amax = largest magnitude, g = global scale):
-//   s = e4m3(amax / (6 g)), d = s * g, code = e2m1(x / d)
+//   s = e4m3(amax / (6 g)), d = s * g, code = e2m1(x / d), or 0 where d is 0
 // a8_quantize, per group of 128 (amax floored at 2^-100):
 //   s = amax / 448, code = e4m3(x * (448 / amax))
 // rms_norm: h = x + r, y = (h * rsqrt(mean h^2 + eps)) * w, in FP32 from the

@@ -1,5 +1,6 @@
-// tcgen05 / TMA / cluster primitives (inline PTX, sm_103a) for the
-// tensor-core GEMM. Only what gemm_tc.cu uses.
+// tcgen05 / TMA / cluster primitives (inline PTX, sm_103a): what gemm_tc.cu and
+// the quantised-activation GEMMs share, and the bounded waits of every kernel
+// that copies into shared memory.
 #pragma once
 #include <cuda.h>
 
