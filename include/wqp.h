@@ -296,6 +296,71 @@ int w4a4_gemm(const void* A, const void* a_scales, float a_global, const void* W
 int w8a8_gemm(const void* A, const float* a_scales, const void* W, const float* w_scales, void* C, int ldc,
               int M, int N, int K, void* stream);
 
+/* --------------------------------------------------- experts ---
+ * A feed-forward part whose weights are a set of E experts (1..1024), of which
+ * each of T tokens uses top_k (1..32, the slots): routing, grouping the
+ * (token, slot) pairs by expert, the experts' products with packed W4A16
+ * matrices, and adding a token's rows up. Pair p = t * top_k + s is slot s of
+ * token t; at most 2^30 pairs. A pair whose id is not in 0..E-1 has no expert
+ * (padding, or an expert that is kept elsewhere): it is not in the order, not
+ * computed, and not added. T >= 0 (0 is a no-op). No size is read back to the
+ * host: the calls may be captured in a graph and replayed for other tokens.
+ * Stream, device and error behaviour are those of the GEMV entries.
+ */
+typedef enum wqp_scoring { WQP_SOFTMAX = 0, WQP_SIGMOID = 1 } wqp_scoring;
+
+/* Each token's experts from its logits l [E] (logits [T, ldl] of a wqp_dtype,
+ * ldl >= E): s = softmax(l) or sigmoid(l), and the choice c = s + bias (float
+ * [E]), or l itself where bias is NULL.
+ * Groups (1..32, E a multiple): of consecutive, equally large groups of
+ * experts the top_groups (1..groups) with the largest scores stay, a group's
+ * score being the sum of its group_best (1 or 2) largest choices (of s for
+ * group_best = 2 without a bias). top_k <= E / groups * top_groups.
+ * ids int [T, top_k]: the experts with the largest choices, in that order;
+ * equal ones, and equal groups, in the order of their index. The order is that
+ * of exact choices (those that lie too close for FP32 are taken again in FP64).
+ * weights float [T, top_k] = s, divided by the sum over the token's top_k with
+ * renormalise, times scale (finite).
+ * An expert whose logit is -inf (or whose choice is -inf or NaN) is never
+ * taken; slots that find none have id -1 and weight 0. A token with a NaN
+ * logit (or, softmax, one of +inf) gets its largest logits without bias and
+ * groups, and NaN weights. */
+int expert_route(const void* logits, int ldl, int dtype, const float* bias, int* ids, float* weights, int T, int E,
+                 int top_k, int scoring, int groups, int top_groups, int group_best, int renormalise, float scale,
+                 void* stream);
+
+/* The pairs by expert: ids int [R] (R = T * top_k); rows int [R] receives the
+ * pairs of expert 0 in rising order, then those of expert 1, and so on, and -1
+ * behind the last; offsets int [E + 1] where each expert's begin (offsets[E]:
+ * the pairs that have one). R = 0 still writes offsets. */
+int expert_order(const int* ids, int* rows, int* offsets, int R, int E, void* stream);
+
+/* Every pair's row times its expert's matrix:
+ *   C[p, n] = bf16(g[e] * sum_k A[p / slots, k] * e2m1(W[e, n, k]) * e4m3(scales[e, n, k / 16]))
+ * or, gated, with u that value in FP32 and F = N / 2 (N even),
+ *   C[p, n] = bf16(silu(u[n]) * u[F + n]),  n < F.
+ * A is BF16 [T, lda] (slots = 1: a row of its own for each pair), W uint8
+ * [E, N, K/2] and scales [E, N, K/16] as w4a16_gemv has them, contiguous;
+ * global_scales float [E] or NULL (1). rows [T * slots] and offsets [E + 1] are
+ * expert_order's. C is BF16 [T * slots, ldc]; rows of pairs without an expert are
+ * left as they were. Alignment, K, N, lda and ldc as for w4a16_gemv.
+ * Numerics: the operands are exact (FP16 with activations scaled per 128 K as
+ * w4a16_gemm_mma has them, or BF16), the sums FP32. A row does not depend on the
+ * others, but which kernel runs (and with it the order of the sums) on T * slots
+ * and E. */
+int w4a16_experts(const void* A, int lda, const void* W, const void* scales, const float* global_scales, const int* rows,
+                  const int* offsets, void* C, int ldc, int T, int slots, int E, int N, int K, int gated, void* stream);
+
+/* out[t] = residual[t] + sum_s weights[t, s] * Y[t * slots + s], over the slots
+ * whose id is in 0..E-1 (other rows of Y are not read), in FP32 and in the
+ * order of the slots, the residual (which may be NULL) last, rounded once. Y
+ * [T * slots, ldy], residual [T, ldr] and out [T, ldo] are of one wqp_dtype,
+ * with 16-byte aligned bases and pitches in elements, multiples of 8; weights
+ * float and ids int [T, slots]. H % 8 == 0, H <= 2^20. out may be the
+ * residual, with the same pitch. */
+int expert_combine(const void* Y, int ldy, const float* weights, const int* ids, int E, const void* residual, int ldr,
+                   void* out, int ldo, int dtype, int T, int slots, int H, void* stream);
+
 /* ------------------------------------------------------------ dequant ---
  * Unpack every weight to FP32: out is float [N, K] row-major, device memory,
  * 4-byte aligned. Each value is the one the GEMVs multiply by:

@@ -21,6 +21,7 @@ __all__ = [
     "WqpError", "lib", "lib_path", "q2_gemv", "q2_gemm_tc", "q2_gemm_mma", "w4a16_gemv", "w4a16_gemm_tc",
     "w4a16_gemm_mma", "w8a16_gemm", "w8a16_gemm_tc", "w8a16_gemm_mma",
     "w4_quantize", "a8_quantize", "rms_norm", "rms_norm_a8", "w4a4_gemm", "w8a8_gemm",
+    "expert_route", "expert_order", "w4a16_experts", "expert_combine",
     "q2_dequant", "w4a16_dequant", "w8a16_dequant", "row_chunks", "set_pdl",
     "get_device_error", "selftest_wait_timeout", "status_string", "EXPORTS", "MAX_M_PER_LAUNCH",
 ]
@@ -59,6 +60,10 @@ EXPORTS = {
     "rms_norm_a8": [_P, _I, _P, _I, _P, _F, _P, _I, _P, _P, _I, _I, _I, _P],
     "w4a4_gemm": [_P, _P, _F, _P, _P, _F, _P, _I, _I, _I, _I, _P],
     "w8a8_gemm": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P],
+    "expert_route": [_P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P],
+    "expert_order": [_P, _P, _P, _I, _I, _P],
+    "w4a16_experts": [_P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P],
+    "expert_combine": [_P, _I, _P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _P],
     "q2_dequant": [_P, _P, _I, _I, _P],
     "w4a16_dequant": [_P, _P, _F, _P, _I, _I, _P],
     "w8a16_dequant": [_P, _P, _P, _I, _I, _P],
@@ -499,6 +504,105 @@ def w8a8_gemm(A, a_scales, W, w_scales, N: int, K: int, out=None, stream=None):
     if status:
         _check(status, "w8a8_gemm")
     return C
+
+
+_SCORING = {"softmax": 0, "sigmoid": 1}
+
+
+def expert_route(logits, top_k: int, scoring: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+                 group_best: int = 2, renormalise: bool = True, scale: float = 1.0, out=None, stream=None):
+    """(ids, weights): each token's top_k experts from its logits [T, E] (bfloat16, float16 or float32) by score
+    ("softmax" or "sigmoid") plus bias (float32 [E]), of the top_groups best of `groups` groups of experts; int32 ids and
+    float32 weights [T, top_k], the scores, renormalised to sum to 1 and times scale. Id -1: no expert was left (logits
+    of -inf). out: (ids, weights) to write to."""
+    torch = _torch or _load_torch()
+    ldl, dt, T, E = _typed_rows("logits", logits)
+    if scoring not in _SCORING:
+        raise ValueError("scoring must be 'softmax' or 'sigmoid'")
+    pb = None if bias is None else _packed("bias", bias, (E,), torch.float32)
+    if out is None:
+        ids, weights = (_empty((T, top_k), torch.int32, logits.device, stream),
+                        _empty((T, top_k), torch.float32, logits.device, stream))
+    else:
+        ids, weights = out
+        _packed("ids", ids, (T, top_k), torch.int32)
+        _packed("weights", weights, (T, top_k), torch.float32)
+    status = (_lib or lib()).expert_route(logits.data_ptr(), ldl, dt, pb, ids.data_ptr(), weights.data_ptr(), T, E, top_k,
+                                          _SCORING[scoring], groups, top_groups, group_best, 1 if renormalise else 0,
+                                          float(scale), _stream(stream))
+    if status:
+        _check(status, "expert_route")
+    return ids, weights
+
+
+def expert_order(ids, E: int, out=None, stream=None):
+    """(rows, offsets): the pairs (elements of the int32 ids [T, top_k]) by expert, int32 [T * top_k] with -1 behind the
+    last, and where each expert's begin, int32 [E + 1]. Ids outside 0..E-1 have no expert. out: (rows, offsets) to write to."""
+    torch = _torch or _load_torch()
+    R = ids.numel()
+    pi = _weights("ids", ids, R, torch.int32)
+    if out is None:
+        rows, offsets = (_empty((R,), torch.int32, ids.device, stream), _empty((E + 1,), torch.int32, ids.device, stream))
+    else:
+        rows, offsets = out
+        _packed("rows", rows, (R,), torch.int32)
+        _packed("offsets", offsets, (E + 1,), torch.int32)
+    status = (_lib or lib()).expert_order(pi, rows.data_ptr(), offsets.data_ptr(), R, E, _stream(stream))
+    if status:
+        _check(status, "expert_order")
+    return rows, offsets
+
+
+def w4a16_experts(A, W, scales, rows, offsets, N: int, K: int, global_scales=None, gated: bool = False, out=None,
+                  stream=None):
+    """C[p] = A[p / slots] @ dequant(W[e])^T for every pair p of each expert e, bfloat16 [R, N]; gated: silu(gate) * up of
+    its two halves, [R, N / 2]. A is bfloat16 [R, K], or [T, K] with R = T * slots; W and scales hold E W4A16 matrices
+    [N, K], global_scales their float32 scales [E]; rows and offsets are expert_order's. Rows of pairs without an expert
+    are not written: a new out holds anything there."""
+    torch = _torch or _load_torch()
+    T, lda = _rows(A, K)
+    if not A.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
+    E, R = offsets.numel() - 1, rows.numel()
+    if E < 1:
+        raise ValueError("offsets must hold E + 1 values")
+    slots = R // T if T else 1
+    if R != T * slots or slots < 1 and T:
+        raise ValueError(f"{R} pairs are not a multiple of the {T} rows of A")
+    pr, po = _packed("rows", rows, (R,), torch.int32), _packed("offsets", offsets, (E + 1,), torch.int32)
+    pw, ps = _weights("W", W, E * N * (K // 2), torch.uint8), _weights("scales", scales, E * N * (K // 16), torch.uint8)
+    pg = None if global_scales is None else _packed("global_scales", global_scales, (E,), torch.float32)
+    if gated and N % 2:
+        raise ValueError(f"N={N} must be even, gate and up")
+    C, ldc = _gemm_out(A, R, N // 2 if gated else N, out, stream)
+    status = (_lib or lib()).w4a16_experts(A.data_ptr(), lda, pw, ps, pg, pr, po, C.data_ptr(), ldc, T, slots, E, N, K,
+                                           1 if gated else 0, _stream(stream))
+    if status:
+        _check(status, "w4a16_experts")
+    return C
+
+
+def expert_combine(y, weights, ids, E: int, residual=None, out=None, stream=None):
+    """[T, H]: residual + the sum over the slots of weights[t, s] * y[t * slots + s], in y's type (bfloat16, float16 or
+    float32); y [T * slots, H], float32 weights and int32 ids [T, slots]. Rows whose id is outside 0..E-1 are not read.
+    out may be the residual."""
+    torch = _torch or _load_torch()
+    ldy, dt, R, H = _typed_rows("y", y)
+    if weights.dim() != 2 or weights.shape[0] * weights.shape[1] != R:
+        raise ValueError(f"weights must be [T, slots] with T * slots = {R}")
+    T, slots = weights.shape
+    pw, pi = _packed("weights", weights, (T, slots), torch.float32), _packed("ids", ids, (T, slots), torch.int32)
+    like = y[:T]
+    ldr = _rows_like("residual", residual, like) if residual is not None else 0
+    if out is None:
+        out, ldo = _empty((T, H), y.dtype, y.device, stream), H
+    else:
+        ldo = _rows_like("out", out, like)
+    status = (_lib or lib()).expert_combine(y.data_ptr(), ldy, pw, pi, E, None if residual is None else residual.data_ptr(),
+                                            ldr, out.data_ptr(), ldo, dt, T, slots, H, _stream(stream))
+    if status:
+        _check(status, "expert_combine")
+    return out
 
 
 def _deq_out(W, N, K, out, stream):

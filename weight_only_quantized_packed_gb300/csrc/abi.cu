@@ -313,6 +313,117 @@ int run_act_gemm(bool w4, const void* A, const void* SA, float ga, const void* W
   return e == cudaSuccess ? WQP_OK : cuda_fail(e, nm);
 }
 
+// Experts, the slots of a token, and their pairs.
+int check_pairs(const char* nm, int T, int slots, int E) {
+  if (T < 0) return fail(WQP_ERR_INVALID_ARG, "%s: T=%d < 0", nm, T);
+  if (slots < 1 || slots > kMaxTopK) return fail(WQP_ERR_INVALID_ARG, "%s: %d slots outside 1..%d", nm, slots, kMaxTopK);
+  if (E < 1 || E > kMaxExperts) return fail(WQP_ERR_INVALID_ARG, "%s: E=%d outside 1..%d", nm, E, kMaxExperts);
+  if (static_cast<long long>(T) * slots > (1 << 30))
+    return fail(WQP_ERR_INVALID_ARG, "%s: %d tokens of %d slots are more than 2^30 pairs", nm, T, slots);
+  return WQP_OK;
+}
+
+int check_words(const char* nm, const char* what, const void* p) {
+  if (!p) return fail(WQP_ERR_INVALID_ARG, "%s: NULL %s", nm, what);
+  if (!aligned(p, 4)) return fail(WQP_ERR_INVALID_ARG, "%s: %s must be 4-byte aligned", nm, what);
+  return WQP_OK;
+}
+
+int run_route(const void* X, int ldl, int dtype, const float* bias, int* ids, float* weights, int T, int E, int top_k,
+              int scoring, int groups, int top_groups, int group_best, int renormalise, float scale, void* stream) {
+  const char* nm = "expert_route";
+  int st = check_pairs(nm, T, top_k, E);
+  if (st != WQP_OK) return st;
+  if (dtype < WQP_BF16 || dtype > WQP_F32) return fail(WQP_ERR_INVALID_ARG, "%s: dtype=%d is not a wqp_dtype", nm, dtype);
+  if (scoring != WQP_SOFTMAX && scoring != WQP_SIGMOID)
+    return fail(WQP_ERR_INVALID_ARG, "%s: scoring=%d is not a wqp_scoring", nm, scoring);
+  if (groups < 1 || groups > kMaxGroups || E % groups != 0)
+    return fail(WQP_ERR_INVALID_ARG, "%s: groups=%d must divide E=%d and be at most %d", nm, groups, E, kMaxGroups);
+  if (top_groups < 1 || top_groups > groups)
+    return fail(WQP_ERR_INVALID_ARG, "%s: top_groups=%d outside 1..%d", nm, top_groups, groups);
+  if (group_best != 1 && group_best != 2) return fail(WQP_ERR_INVALID_ARG, "%s: group_best=%d is not 1 or 2", nm, group_best);
+  if (top_k > E / groups * top_groups)
+    return fail(WQP_ERR_INVALID_ARG, "%s: top_k=%d of %d experts", nm, top_k, E / groups * top_groups);
+  if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return fail(WQP_ERR_INVALID_ARG, "%s: scale=%g must be finite", nm, scale);
+  if (T == 0) return WQP_OK;
+  if (!X) return fail(WQP_ERR_INVALID_ARG, "%s: NULL logits", nm);
+  if (!aligned(X, dtype == WQP_F32 ? 4 : 2)) return fail(WQP_ERR_INVALID_ARG, "%s: logits must be aligned to their type", nm);
+  if (ldl < E) return fail(WQP_ERR_INVALID_ARG, "%s: pitch %d of logits must be >= E=%d", nm, ldl, E);
+  if (bias && !aligned(bias, 4)) return fail(WQP_ERR_INVALID_ARG, "%s: bias must be 4-byte aligned", nm);
+  if ((st = check_words(nm, "ids", ids)) != WQP_OK || (st = check_words(nm, "weights", weights)) != WQP_OK) return st;
+  DeviceInfo* dev = nullptr;
+  if ((st = device_setup(&dev)) != WQP_OK) return st;
+  const RouteArgs a = {X, bias, ids, weights, dtype, T, E, ldl, top_k, scoring == WQP_SIGMOID, renormalise != 0,
+                       groups, top_groups, group_best, scale, dev->num_sms, g_pdl.load(std::memory_order_relaxed) != 0};
+  const cudaError_t e = launch_expert_route(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? WQP_OK : cuda_fail(e, nm);
+}
+
+int run_order(const int* ids, int* rows, int* offsets, int R, int E, void* stream) {
+  const char* nm = "expert_order";
+  if (R < 0 || R > (1 << 30)) return fail(WQP_ERR_INVALID_ARG, "%s: R=%d outside 0..2^30", nm, R);
+  if (E < 1 || E > kMaxExperts) return fail(WQP_ERR_INVALID_ARG, "%s: E=%d outside 1..%d", nm, E, kMaxExperts);
+  int st = check_words(nm, "offsets", offsets);
+  if (st == WQP_OK && R > 0) st = check_words(nm, "ids", ids);
+  if (st == WQP_OK && R > 0) st = check_words(nm, "rows", rows);
+  DeviceInfo* dev = nullptr;
+  if (st != WQP_OK || (st = device_setup(&dev)) != WQP_OK) return st;
+  const OrderArgs a = {ids, rows, offsets, R, E, g_pdl.load(std::memory_order_relaxed) != 0};
+  const cudaError_t e = launch_expert_order(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? WQP_OK : cuda_fail(e, nm);
+}
+
+int run_experts(const void* A, int lda, const void* W, const void* scales, const float* globals, const int* rows,
+                const int* offsets, void* C, int ldc, int T, int slots, int E, int N, int K, int gated, void* stream) {
+  const char* nm = "w4a16_experts";
+  int st = check_pairs(nm, T, slots, E);
+  if (st != WQP_OK) return st;
+  if (N < 1 || N > (1 << 24)) return fail(WQP_ERR_INVALID_ARG, "%s: N=%d outside 1..2^24", nm, N);
+  if (gated && N % 2 != 0) return fail(WQP_ERR_INVALID_ARG, "%s: N=%d must be even, gate and up", nm, N);
+  if (K < 128 || K > (1 << 20) || K % 128 != 0)
+    return fail(WQP_ERR_INVALID_ARG, "%s: K=%d must be a multiple of 128 in [128, 2^20]", nm, K);
+  if (T == 0) return WQP_OK;
+  if ((st = check_pitched(nm, "A", A, lda, K)) != WQP_OK) return st;
+  if (!W || !scales || !C) return fail(WQP_ERR_INVALID_ARG, "%s: NULL W, scales or C", nm);
+  if (!aligned(W, 16) || !aligned(scales, 16))
+    return fail(WQP_ERR_INVALID_ARG, "%s: W and scales must be 16-byte aligned", nm);
+  if (globals && !aligned(globals, 4)) return fail(WQP_ERR_INVALID_ARG, "%s: global_scales must be 4-byte aligned", nm);
+  if ((st = check_words(nm, "rows", rows)) != WQP_OK || (st = check_words(nm, "offsets", offsets)) != WQP_OK) return st;
+  const int outs = gated ? N / 2 : N;
+  if (!aligned(C, 2)) return fail(WQP_ERR_INVALID_ARG, "%s: C must be 2-byte aligned", nm);
+  if (ldc < outs) return fail(WQP_ERR_INVALID_ARG, "%s: ldc=%d must be >= %d", nm, ldc, outs);
+  DeviceInfo* dev = nullptr;
+  if ((st = device_setup(&dev)) != WQP_OK) return st;
+  const ExpertsArgs a = {A, static_cast<const uint8_t*>(W), static_cast<const uint8_t*>(scales), globals, rows, offsets, C,
+                         lda, ldc, T, slots, E, N, K, gated != 0, dev->err, dev->num_sms,
+                         g_pdl.load(std::memory_order_relaxed) != 0};
+  const cudaError_t e = launch_w4a16_experts(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? WQP_OK : cuda_fail(e, nm);
+}
+
+int run_combine(const void* Y, int ldy, const float* weights, const int* ids, int E, const void* R, int ldr, void* out,
+                int ldo, int dtype, int T, int slots, int H, void* stream) {
+  const char* nm = "expert_combine";
+  int st = check_pairs(nm, T, slots, E);
+  if (st != WQP_OK) return st;
+  if (dtype < WQP_BF16 || dtype > WQP_F32) return fail(WQP_ERR_INVALID_ARG, "%s: dtype=%d is not a wqp_dtype", nm, dtype);
+  if (H < 8 || H > (1 << 20) || H % 8 != 0)
+    return fail(WQP_ERR_INVALID_ARG, "%s: H=%d must be a multiple of 8 in [8, 2^20]", nm, H);
+  if (static_cast<long long>(T) * H > (1ll << 40)) return fail(WQP_ERR_INVALID_ARG, "%s: T=%d rows of %d are too many", nm, T, H);
+  if (T == 0) return WQP_OK;
+  st = check_pitched(nm, "Y", Y, ldy, H);
+  if (st == WQP_OK && R) st = check_pitched(nm, "residual", R, ldr, H);
+  if (st == WQP_OK) st = check_pitched(nm, "out", out, ldo, H);
+  if (st == WQP_OK) st = check_words(nm, "weights", weights);
+  if (st == WQP_OK) st = check_words(nm, "ids", ids);
+  DeviceInfo* dev = nullptr;
+  if (st != WQP_OK || (st = device_setup(&dev)) != WQP_OK) return st;
+  const CombineArgs a = {Y, weights, ids, R, out, ldy, ldr, ldo, dtype, T, slots, E, H,
+                         g_pdl.load(std::memory_order_relaxed) != 0};
+  const cudaError_t e = launch_expert_combine(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? WQP_OK : cuda_fail(e, nm);
+}
+
 }  // namespace
 
 namespace wqp {
@@ -450,6 +561,27 @@ int w4a4_gemm(const void* A, const void* a_scales, float a_global, const void* W
 int w8a8_gemm(const void* A, const float* a_scales, const void* W, const float* w_scales, void* C, int ldc, int M,
               int N, int K, void* stream) {
   return run_act_gemm(false, A, a_scales, 1.0f, W, w_scales, 1.0f, C, ldc, M, N, K, stream);
+}
+
+int expert_route(const void* logits, int ldl, int dtype, const float* bias, int* ids, float* weights, int T, int E,
+                 int top_k, int scoring, int groups, int top_groups, int group_best, int renormalise, float scale,
+                 void* stream) {
+  return run_route(logits, ldl, dtype, bias, ids, weights, T, E, top_k, scoring, groups, top_groups, group_best, renormalise,
+                   scale, stream);
+}
+
+int expert_order(const int* ids, int* rows, int* offsets, int R, int E, void* stream) {
+  return run_order(ids, rows, offsets, R, E, stream);
+}
+
+int w4a16_experts(const void* A, int lda, const void* W, const void* scales, const float* global_scales, const int* rows,
+                  const int* offsets, void* C, int ldc, int T, int slots, int E, int N, int K, int gated, void* stream) {
+  return run_experts(A, lda, W, scales, global_scales, rows, offsets, C, ldc, T, slots, E, N, K, gated, stream);
+}
+
+int expert_combine(const void* Y, int ldy, const float* weights, const int* ids, int E, const void* residual, int ldr,
+                   void* out, int ldo, int dtype, int T, int slots, int H, void* stream) {
+  return run_combine(Y, ldy, weights, ids, E, residual, ldr, out, ldo, dtype, T, slots, H, stream);
 }
 
 int q2_dequant(const void* W, float* out, int N, int K, void* stream) {

@@ -1,0 +1,549 @@
+// The steps around the experts' products: routing, ordering the pairs by
+// expert, and combining a token's rows.
+//
+// expert_route, per token, with logits l: s = softmax(l) or sigmoid(l),
+// choice c = s + bias (l itself without a bias: the same order). Of groups of
+// experts the ones with the largest sums of their best choices stay; of their
+// experts the top_k largest choices are taken, equal ones by the lower index.
+// weight = s, divided by the sum of those taken, times scale.
+#include <cuda_fp16.h>
+
+#include "decode.cuh"
+#include "tc.cuh"
+
+namespace wqp {
+namespace {
+
+using tc::cluster_rank;
+using tc::cluster_sync;
+using tc::mapa_shared;
+
+constexpr unsigned kAll = 0xFFFFFFFFu;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// ------------------------------------------------------------ routing
+struct RouteParams {
+  const void* X;
+  const float* bias;
+  int* ids;
+  float* weights;
+  int T, E, ldl, top_k;
+  int sigmoid, renormalise;
+  int groups, top_groups, group_best;
+  float scale;
+};
+
+// Keys that order as the numbers do; 0 is below every number's but -inf's and
+// NaN's, which are not candidates.
+__device__ __forceinline__ uint32_t key_of(float c) {
+  const uint32_t b = __float_as_uint(c + 0.0f);            // -0 is 0
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ unsigned long long key_of(double c) {
+  const unsigned long long b = __double_as_longlong(c + 0.0);
+  return b >> 63 ? ~b : b | 0x8000000000000000ull;
+}
+__device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
+__device__ __forceinline__ double value_of(unsigned long long k) {
+  return __longlong_as_double(k >> 63 ? k & 0x7FFFFFFFFFFFFFFFull : ~k);
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kAll, v); }
+__device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const unsigned long long u = __shfl_xor_sync(kAll, v, o);
+    v = u > v ? u : v;
+  }
+  return v;
+}
+template <class Real>
+__device__ __forceinline__ Real warp_add(Real v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+
+// One token in one warp; expert i is element i / 32 of lane i % 32. `part` is
+// the warp's [E] scratch. Returns false, with nothing written, where two
+// choices that matter lie closer than the arithmetic's error: the caller then
+// takes the token again in FP64, whose order is the answer. (One token in
+// some hundreds with a bias; never without one and without groups, where the
+// logits themselves are the keys.)
+template <class T, int NV, class Real, class Key>
+__device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lane, Real* part) {
+  constexpr bool kCheck = sizeof(Real) == 4;
+  const T* x = static_cast<const T*>(p.X) + static_cast<long long>(t) * p.ldl;
+  const float kNone = __int_as_float(0xFF800000);
+  float l[NV];
+  bool odd = false;                                        // NaN, or an infinite exponential
+  float top = kNone;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int i = lane + 32 * j;
+    l[j] = i < p.E ? to_f32(x[i]) : kNone;
+    odd |= l[j] != l[j] || (!p.sigmoid && l[j] == __int_as_float(0x7F800000));
+    top = fmaxf(top, l[j]);
+  }
+  odd = __any_sync(kAll, odd);
+  top = value_of(warp_max(key_of(top)));
+
+  // Scores where the order needs them.
+  const bool by_score = !odd && (p.bias || (p.groups > 1 && p.group_best == 2));
+  Real sum = 1;
+  if (!p.sigmoid && (by_score || !p.renormalise)) {
+    Real e = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) e += l[j] > kNone ? exp(static_cast<Real>(l[j]) - static_cast<Real>(top)) : Real(0);
+    sum = warp_add(e);
+  }
+  const auto score = [&](float v) -> Real {
+    if (p.sigmoid) return Real(1) / (Real(1) + exp(-static_cast<Real>(v)));
+    return exp(static_cast<Real>(v) - static_cast<Real>(top)) / sum;
+  };
+  Key key[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int i = lane + 32 * j;
+    Real c = l[j];
+    if (by_score && p.bias && i < p.E) c = score(l[j]) + static_cast<Real>(p.bias[i]);
+    key[j] = l[j] > kNone && c > static_cast<Real>(kNone) ? key_of(c) : Key(0);
+  }
+  // A bound on the error of a choice, in units of 2^-24 at 1: the exponential
+  // and its argument, the sum's and the quotient's roundings (up to 32 + 5
+  // additions on any path), each relative to a score of at most s_max.
+  const float s_max = p.sigmoid ? 0.125f : 1.0f / static_cast<float>(sum);
+  const auto close = [&](Real a, Real b, float terms) {
+    return kCheck && a - b <= Real(terms * 0x1p-23f) * (Real(64) * Real(s_max) + fabs(a) + Real(1));
+  };
+
+  if (p.groups > 1 && !odd) {
+    const int size = p.E / p.groups;
+    const bool from_choice = p.bias || p.group_best == 1;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = lane + 32 * j;
+      if (i < p.E) part[i] = !key[j] ? static_cast<Real>(kNone) : (from_choice ? value_of(key[j]) : score(l[j]));
+    }
+    __syncwarp();
+    // `lanes` lanes to a group find its two best.
+    int log = 0;
+    while ((1 << log) < p.groups) ++log;
+    const int lanes = 32 >> log, g = lane / lanes;
+    Real a = kNone, b = kNone;
+    if (g < p.groups)
+      for (int i = lane % lanes; i < size; i += lanes) {
+        const Real v = part[g * size + i];
+        b = v > a ? a : (v > b ? v : b);
+        a = v > a ? v : a;
+      }
+    for (int o = 1; o < lanes; o <<= 1) {
+      const Real a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
+      const Real lo = a < a2 ? a : a2, hi = b > b2 ? b : b2;
+      a = a > a2 ? a : a2;
+      b = lo > hi ? lo : hi;
+    }
+    const Real mine = p.group_best == 2 && b > static_cast<Real>(kNone) ? a + b : a;
+    // A group stays where fewer than top_groups are better.
+    int better = 0;
+    Real above = kNone;                                    // the best that goes
+    for (int h = 0; h < p.groups; ++h) {
+      const Real v = __shfl_sync(kAll, mine, h * lanes);
+      better += v > mine || (v == mine && h < g);
+    }
+    const bool stays = g < p.groups && better < p.top_groups;
+    const unsigned keep = __ballot_sync(kAll, stays);
+    if (kCheck && p.top_groups < p.groups && (p.bias || p.group_best == 2)) {
+      Real least = 0;
+      bool some = false;
+      for (int h = 0; h < p.groups; ++h) {
+        const Real v = __shfl_sync(kAll, mine, h * lanes);
+        if (keep >> (h * lanes) & 1) {
+          least = !some || v < least ? v : least;
+          some = true;
+        } else {
+          above = v > above ? v : above;
+        }
+      }
+      if (close(least, above, 2.0f * p.group_best)) return false;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = lane + 32 * j;
+      if (i < p.E && !(keep >> (i / size * lanes) & 1)) key[j] = 0;
+    }
+  }
+
+  // The best key of a lane's own, of equal ones the lowest index; then the
+  // best of the lanes', top_k times, and once more where it has to be known
+  // that the next is clearly less.
+  Key best = 0;
+  int at = 0;
+  const auto own_best = [&] {
+    best = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (key[j] > best) best = key[j], at = j;
+  };
+  own_best();
+  int id = -1;                                             // of slot `lane`
+  float lg = kNone;
+  Key prev = 0;
+  float prev_l = 0, prev_b = 0;
+  const bool check = kCheck && p.bias && !odd;
+  for (int s = 0; s < p.top_k + (check ? 1 : 0); ++s) {
+    const Key m = warp_max(best);
+    if (!m) break;
+    const int i = __reduce_min_sync(kAll, best == m ? at * 32 + lane : 0x7FFFFFFF);
+    float li = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (j == i >> 5) li = l[j];
+    li = __shfl_sync(kAll, li, i & 31);
+    if (check) {
+      const float bi = p.bias[i];
+      // Two experts of one logit and one bias tie in any arithmetic; behind the
+      // last one taken others could lie between.
+      if (s > 0 && !(s < p.top_k && li == prev_l && bi == prev_b) && close(value_of(prev), value_of(m), 2.0f)) return false;
+      prev = m, prev_l = li, prev_b = bi;
+    }
+    if (s < p.top_k && lane == s) id = i, lg = li;
+    if (lane == (i & 31)) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (j == i >> 5) key[j] = 0;
+      own_best();
+    }
+  }
+
+  float w = 0.0f;
+  const bool live = id >= 0;
+  if (p.renormalise) {
+    // Scores relative to the largest taken, so that they cannot all vanish: a
+    // sigmoid far below 0 is an exponential too.
+    const float most = value_of(warp_max(live ? key_of(lg) : 0u));
+    if (p.sigmoid && most > -80.0f) w = live ? 1.0f / (1.0f + expf(-lg)) : 0.0f;
+    else w = live ? expf(lg - most) : 0.0f;
+    const float total = warp_sum(w);
+    w = total > 0.0f ? w / total : 0.0f;
+  } else if (live) {
+    w = static_cast<float>(score(lg));
+  }
+  w *= p.scale;
+  if (odd) w = __int_as_float(0x7FFFFFFF);
+  if (lane < p.top_k) {
+    const long long o = static_cast<long long>(t) * p.top_k + lane;
+    p.ids[o] = id;
+    p.weights[o] = w;
+  }
+  return true;
+}
+
+constexpr int kRouteWarps = 4;
+
+template <class T, int NV>
+__device__ __noinline__ void route_token_f64(const RouteParams& p, int t, int lane, double* part) {
+  route_token<T, NV, double, unsigned long long>(p, t, lane, part);
+}
+
+// Bound by the latency of one token's steps (k + 1 reductions of some 50
+// clocks each, two exponentials an expert), which many warps overlap.
+template <class T, int NV>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p) {
+  extern __shared__ double route_part[];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * kRouteWarps + warp;
+  if (t >= p.T) return;
+  double* part = route_part + static_cast<size_t>(warp) * p.E;
+  if (!route_token<T, NV, float, uint32_t>(p, t, lane, reinterpret_cast<float*>(part)))
+    route_token_f64<T, NV>(p, t, lane, part);
+}
+
+template <class T>
+cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t s) {
+  const RouteParams p = {a.X, a.bias, a.ids, a.weights, a.T, a.E, a.ldl, a.top_k, a.sigmoid, a.renormalise,
+                         a.groups, a.top_groups, a.group_best, a.scale};
+  const dim3 grid((a.T + kRouteWarps - 1) / kRouteWarps), block(kRouteWarps * 32);
+  // Only groups use the scratch. 32 KB at most: no opt-in.
+  const size_t smem = a.groups > 1 ? sizeof(double) * kRouteWarps * a.E : 0;
+  if (a.E <= 64) return launch(route_kernel<T, 2>, grid, block, smem, s, a.pdl, p);
+  if (a.E <= 128) return launch(route_kernel<T, 4>, grid, block, smem, s, a.pdl, p);
+  if (a.E <= 256) return launch(route_kernel<T, 8>, grid, block, smem, s, a.pdl, p);
+  if (a.E <= 512) return launch(route_kernel<T, 16>, grid, block, smem, s, a.pdl, p);
+  return launch(route_kernel<T, 32>, grid, block, smem, s, a.pdl, p);
+}
+
+// ------------------------------------------------------------ ordering
+// A counting sort that keeps the pairs' order: every warp counts the ids of
+// its run of pairs, the counts of earlier warps (of earlier CTAs, through the
+// cluster's shared memory) give each warp its place in each expert's list, and
+// a second pass over the run puts the pairs there. One launch; no atomics, so
+// the result is the same every time.
+constexpr int kOrderWarps = 32;
+
+__global__ void __launch_bounds__(kOrderWarps * 32) order_kernel(const int* ids, int* rows, int* offsets, int R, int E, int run) {
+  extern __shared__ int order_sh[];
+  __shared__ int scan_sh[33];
+  int* const count = order_sh;                             // [warps][E]: counts, then places
+  int* const total = order_sh + kOrderWarps * E;           // [E]: this CTA's counts
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ranks = gridDim.x, rank = ranks > 1 ? static_cast<int>(cluster_rank()) : 0;
+  pdl_launch_dependents();
+  for (int i = threadIdx.x; i < kOrderWarps * E; i += blockDim.x) count[i] = 0;
+  __syncthreads();
+  pdl_wait();
+  const long long first = static_cast<long long>(rank * kOrderWarps + warp) * run;
+  const int begin = static_cast<int>(first < R ? first : R), end = static_cast<int>(first + run < R ? first + run : R);
+  int* const mine = count + warp * E;
+  const auto id_at = [&](int i) {
+    const int e = i < end ? ids[i] : -1;
+    return static_cast<unsigned>(e) < static_cast<unsigned>(E) ? e : -1;
+  };
+  // The first eight batches of a run stay in registers for the second pass.
+  constexpr int kKept = 8;
+  int kept[kKept];
+#pragma unroll
+  for (int b = 0; b < kKept; ++b) kept[b] = id_at(begin + 32 * b + lane);
+  const auto count_batch = [&](int e) {
+    const unsigned same = __match_any_sync(kAll, e);
+    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+    __syncwarp();
+  };
+#pragma unroll
+  for (int b = 0; b < kKept; ++b)
+    if (begin + 32 * b < end) count_batch(kept[b]);
+  for (int i = begin + 32 * kKept; i < end; i += 32) count_batch(id_at(i + lane));
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    int sum = 0;
+#pragma unroll 8
+    for (int w = 0; w < kOrderWarps; ++w) {
+      const int c = count[w * E + e];
+      count[w * E + e] = sum;
+      sum += c;
+    }
+    total[e] = sum;
+  }
+  if (ranks > 1) cluster_sync();
+  else __syncthreads();
+  // Thread e: expert e's counts of every CTA, and where its list starts.
+  const int e = threadIdx.x;
+  int all = 0, before = 0;
+  if (e < E) {
+    if (ranks > 1) {
+      const uint32_t at = smem_u32(total + e);
+      for (int r = 0; r < ranks; ++r) {
+        int c;
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(mapa_shared(at, r)) : "memory");
+        before += r < rank ? c : 0;
+        all += c;
+      }
+    } else {
+      all = total[e];
+    }
+  }
+  int incl = all;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(kAll, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) scan_sh[warp] = incl;
+  // No CTA reads another's shared memory after this, nor ends before it.
+  if (ranks > 1) cluster_sync();
+  else __syncthreads();
+  if (warp == 0) {
+    int v = scan_sh[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(kAll, v, o);
+      if (lane >= o) v += u;
+    }
+    scan_sh[lane] = v;
+  }
+  __syncthreads();
+  const int start = incl - all + (warp ? scan_sh[warp - 1] : 0);
+  const int live = scan_sh[31];
+  if (e < E) {
+    total[e] = start + before;
+    if (rank == 0) {
+      offsets[e] = start;
+      if (e == E - 1) offsets[E] = live;
+    }
+  }
+  __syncthreads();
+  const auto place_batch = [&](int i, int e) {
+    const unsigned same = __match_any_sync(kAll, e);
+    int at = 0;
+    if (e >= 0) at = mine[e];
+    __syncwarp();
+    if (e >= 0) {
+      rows[total[e] + at + __popc(same & ((1u << lane) - 1))] = i;
+      if (lane == __ffs(same) - 1) mine[e] = at + __popc(same);
+    }
+    __syncwarp();
+  };
+#pragma unroll
+  for (int b = 0; b < kKept; ++b)
+    if (begin + 32 * b < end) place_batch(begin + 32 * b + lane, kept[b]);
+  for (int i = begin + 32 * kKept; i < end; i += 32) place_batch(i + lane, id_at(i + lane));
+  for (long long i = live + static_cast<long long>(rank) * blockDim.x + threadIdx.x; i < R; i += static_cast<long long>(ranks) * blockDim.x)
+    rows[i] = -1;
+}
+
+// ------------------------------------------------------------ combining
+// Bound by memory: every row of Y is read once. A thread has 8 elements of a
+// token, the loads of eight slots in flight at a time, and adds in FP32 in the
+// slots' order, the residual last.
+template <class T>
+struct Eight {
+  uint4 r;
+  __device__ __forceinline__ void load(const T* p) { r = ld_act_v4(p); }
+  __device__ __forceinline__ void add(float (&v)[8], float w) const;
+};
+template <>
+__device__ __forceinline__ void Eight<__nv_bfloat16>::add(float (&v)[8], float w) const {
+  const uint32_t x[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] += w * bf16lo(x[i]);
+    v[2 * i + 1] += w * bf16hi(x[i]);
+  }
+}
+template <>
+__device__ __forceinline__ void Eight<__half>::add(float (&v)[8], float w) const {
+  const uint32_t x[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = f16x2_to_float2(x[i]);
+    v[2 * i] += w * f.x;
+    v[2 * i + 1] += w * f.y;
+  }
+}
+template <>
+struct Eight<float> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = ld_act_v4(p);
+    b = ld_act_v4(p + 4);
+  }
+  __device__ __forceinline__ void add(float (&v)[8], float w) const {
+    const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += w * __uint_as_float(x[i]);
+  }
+};
+__device__ __forceinline__ void store_eight(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store_eight(__half* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store_eight(float* p, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+constexpr int kCombineThreads = 128;
+
+template <class T>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineArgs a, int chunks) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long c = static_cast<long long>(blockIdx.x) * kCombineThreads + threadIdx.x;
+  const long long t = c / chunks;
+  if (t >= a.T) return;
+  const int col = static_cast<int>(c - t * chunks) * 8;
+  const T* y = static_cast<const T*>(a.Y) + t * a.slots * a.ldy + col;
+  const int* ids = a.ids + t * a.slots;
+  const float* weights = a.weights + t * a.slots;
+  Eight<T> r;
+  if (a.R) r.load(static_cast<const T*>(a.R) + t * a.ldr + col);
+  float v[8] = {};
+  constexpr int U = sizeof(T) == 2 ? 8 : 4;
+  for (int s0 = 0; s0 < a.slots; s0 += U) {
+    Eight<T> x[U];
+    float w[U];
+    bool on[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      on[u] = s0 + u < a.slots && static_cast<unsigned>(ids[s0 + u]) < static_cast<unsigned>(a.E);
+      if (on[u]) {
+        x[u].load(y + static_cast<long long>(s0 + u) * a.ldy);
+        w[u] = weights[s0 + u];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (on[u]) x[u].add(v, w[u]);
+  }
+  if (a.R) r.add(v, 1.0f);
+  store_eight(static_cast<T*>(a.out) + t * a.ldo + col, v);
+}
+
+template <class T>
+cudaError_t launch_combine_t(const CombineArgs& a, cudaStream_t s) {
+  const int chunks = a.H / 8;
+  const long long blocks = (static_cast<long long>(a.T) * chunks + kCombineThreads - 1) / kCombineThreads;
+  return launch(combine_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(kCombineThreads), 0, s, a.pdl, a, chunks);
+}
+
+}  // namespace
+
+cudaError_t launch_expert_route(const RouteArgs& a, cudaStream_t s) {
+  if (a.dtype == 0) return launch_route_t<__nv_bfloat16>(a, s);
+  if (a.dtype == 1) return launch_route_t<__half>(a, s);
+  return launch_route_t<float>(a, s);
+}
+
+// One CTA up to 2048 pairs, else a cluster of eight.
+cudaError_t launch_expert_order(const OrderArgs& a, cudaStream_t s) {
+  constexpr int kOne = 2048, kCluster = 8;
+  const int ranks = a.R <= kOne ? 1 : kCluster;
+  const long long warps = static_cast<long long>(ranks) * kOrderWarps;
+  const int run = static_cast<int>((a.R + warps * 32 - 1) / (warps * 32) * 32);
+  const size_t smem = sizeof(int) * (kOrderWarps + 1) * a.E;
+  static AttrLatch latch;
+  const cudaError_t e = set_smem_attrs(order_kernel, latch, static_cast<int>(sizeof(int)) * (kOrderWarps + 1) * kMaxExperts, false);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ranks);
+  cfg.blockDim = dim3(kOrderWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, order_kernel, a.ids, a.rows, a.offsets, a.R, a.E, run);
+}
+
+cudaError_t launch_expert_combine(const CombineArgs& a, cudaStream_t s) {
+  if (a.dtype == 0) return launch_combine_t<__nv_bfloat16>(a, s);
+  if (a.dtype == 1) return launch_combine_t<__half>(a, s);
+  return launch_combine_t<float>(a, s);
+}
+
+}  // namespace wqp

@@ -105,6 +105,67 @@ struct ActGemmArgs {
   bool pdl;
 };
 
+// Most experts, chosen experts of a token and groups of experts.
+constexpr int kMaxExperts = 1024, kMaxTopK = 32, kMaxGroups = 32;
+
+// Experts of T tokens from their logits [T, ldl]: ids and weights [T, top_k].
+struct RouteArgs {
+  const void* X;
+  const float* bias;    // [E] or NULL
+  int* ids;
+  float* weights;
+  int dtype, T, E, ldl, top_k;
+  bool sigmoid, renormalise;
+  int groups, top_groups, group_best;
+  float scale;
+  int num_sms;
+  bool pdl;
+};
+
+// The positions of R ids by expert.
+struct OrderArgs {
+  const int* ids;
+  int* rows;            // [R]
+  int* offsets;         // [E + 1]
+  int R, E;
+  bool pdl;
+};
+
+// Products of rows with their experts' packed W4A16 matrices. R = T * slots
+// pairs; pair p has row p / slots of A and row p of C.
+struct ExpertsArgs {
+  const void* A;        // bf16 [T, lda]
+  const uint8_t* W;     // [E, N, K / 2]
+  const uint8_t* scales;   // [E, N, K / 16]
+  const float* globals; // [E] or NULL
+  const int* rows;      // [R]
+  const int* offsets;   // [E + 1]
+  void* C;              // bf16 [R, ldc]
+  int lda, ldc;
+  int T, slots, E, N, K;
+  bool gated;
+  unsigned* err;
+  int num_sms;
+  bool pdl;
+};
+
+// out [T, ldo] = R + sum over the slots of weights * Y [T * slots, ldy].
+struct CombineArgs {
+  const void* Y;
+  const float* weights;
+  const int* ids;
+  const void* R;
+  void* out;
+  int ldy, ldr, ldo;
+  int dtype, T, slots, E, H;
+  bool pdl;
+};
+
+cudaError_t launch_expert_route(const RouteArgs& a, cudaStream_t s);
+cudaError_t launch_expert_order(const OrderArgs& a, cudaStream_t s);
+cudaError_t launch_w4a16_experts(const ExpertsArgs& a, cudaStream_t s);
+cudaError_t launch_expert_combine(const CombineArgs& a, cudaStream_t s);
+
 cudaError_t launch_w4_quantize(const QuantArgs& a, cudaStream_t s);
 cudaError_t launch_a8_quantize(const QuantArgs& a, cudaStream_t s);
 cudaError_t launch_rms_norm(const NormArgs& a, cudaStream_t s);
