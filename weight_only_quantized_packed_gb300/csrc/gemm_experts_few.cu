@@ -11,9 +11,9 @@
 //    one tile of pairs. Units are numbered through all experts, and each CTA
 //    takes an equal run of them: of 2048 units on 304 CTAs none takes more than
 //    7, where tiles of 64 rows would leave every sixth CTA idle.
-//  * A CTA takes up to four units of one tile at a time. Its eight warps split
+//  * A CTA takes up to eight units of one tile at a time. Its eight warps split
 //    K: a warp turns its part of the pairs' activations into MMA fragments once
-//    for the four units, and the warps' sums meet in shared memory.
+//    for them all, and the warps' sums meet in shared memory.
 //  * Weights arrive by 16-byte asynchronous copies, each lane's own into a
 //    ring of its warp, which runs on through the ends of units: a warp waits
 //    for its copies alone, and there is no barrier between CTAs or warps but
@@ -30,9 +30,9 @@ namespace {
 using namespace f16op;
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kUnits = 4;                      // units at a time
+constexpr int kUnits = 8;                      // units at a time
 constexpr int kStage = 16 * 64 + 16 * 8;       // codes and scales of 16 rows x 128 K
-constexpr int kStages = 6;                     // of a warp's ring
+constexpr int kStages = 7;                     // of a warp's ring
 constexpr int kRow = 16 * kUnits + 4;          // floats of a pair's sums (+ 4: free of bank conflicts)
 
 template <int kTiles>
@@ -90,38 +90,45 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(ExpertsArgs a) {
   const int blocks = a.K >> 7;                 // of 128 K; this warp's: [b0, b1)
   const int b0 = blocks * warp / kWarps, b1 = blocks * (warp + 1) / kWarps;
 
-  // Weight rows g and g + 8 of a unit; rows past the last read that one.
-  const auto row_of = [&](int unit, int r) {
-    if (kGated) return min(unit * 8 + (r & 7), outs - 1) + (r >> 3) * outs;
-    return min(unit * 16 + r, outs - 1);
-  };
   // The copies run kStages - 1 stages ahead of their use, in the same order:
-  // per run its blocks, per block its units.
+  // per run its blocks, per block its units. A lane copies its own 16 bytes of
+  // rows g and g + 8 of a unit (gated: gate row g and up row g), and lanes 0..15
+  // the scales of rows 0..15; rows past the last read that one.
+  const uint32_t wpitch = static_cast<uint32_t>(a.K) >> 1, spitch = static_cast<uint32_t>(a.K) >> 4;
+  const long long half = kGated ? static_cast<long long>(outs) : 0;
+  const int r_lo = g, r_hi = kGated ? g : g + 8, r_s = kGated ? lane & 7 : lane & 15;
+  const uint32_t ring_at = smem_u32(ring) + lane * 16, ring_sc = smem_u32(ring) + 1024 + lane * 8;
   Run ahead = {first, last, per, 0, 0, 0, 0};
+  const uint8_t *w_lo = nullptr, *w_hi = nullptr, *w_s = nullptr;   // of row 0 of the expert's halves, at block ab
   int ab = b1, au = 0, put = 0;
-  bool more = true;
+  bool more = b0 < b1;
   const auto copy_next = [&] {
     if (ab == b1) {
-      do more = more && ahead.next(table);
-      while (more && b0 == b1);
+      more = more && ahead.next(table);
       ab = b0;
-      au = 0;
+      au = ahead.unit;
+      if (more) {
+        const long long row = static_cast<long long>(ahead.expert) * a.N;
+        w_lo = a.W + row * wpitch + b0 * 64 + t4 * 16;
+        w_hi = w_lo + half * wpitch;
+        w_s = a.scales + (row + (kGated && lane >= 8 ? half : 0)) * spitch + b0 * 8;
+      }
     }
     if (more) {
-      const int unit = ahead.unit + au;
-      const long long base = static_cast<long long>(ahead.expert) * a.N;
-      const long long lo = (base + row_of(unit, g)) * blocks + ab, hi = (base + row_of(unit, g + 8)) * blocks + ab;
-      const uint32_t dst = smem_u32(ring + put * kStage);
-      copy16(dst + lane * 16, a.W + lo * 64 + t4 * 16);
-      copy16(dst + 512 + lane * 16, a.W + hi * 64 + t4 * 16);
-      if (lane < 16) copy8(dst + 1024 + lane * 8, a.scales + ((base + row_of(unit, lane)) * blocks + ab) * 8);
-      if (++au == ahead.units) {
-        au = 0;
+      const int o = au * kOuts, top = outs - 1;
+      copy16(ring_at + put, w_lo + static_cast<uint64_t>(static_cast<uint32_t>(min(o + r_lo, top))) * wpitch);
+      copy16(ring_at + put + 512, w_hi + static_cast<uint64_t>(static_cast<uint32_t>(min(o + r_hi, top))) * wpitch);
+      if (lane < 16) copy8(ring_sc + put, w_s + static_cast<uint64_t>(static_cast<uint32_t>(min(o + r_s, top))) * spitch);
+      if (++au == ahead.unit + ahead.units) {
+        au = ahead.unit;
         ++ab;
+        w_lo += 64;
+        w_hi += 64;
+        w_s += 8;
       }
     }
     copies_close();
-    if (++put == kStages) put = 0;
+    put = put == (kStages - 1) * kStage ? 0 : put + kStage;
   };
 #pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) copy_next();
@@ -138,8 +145,8 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(ExpertsArgs a) {
     const uint16_t* act[kTiles];
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
-      const int p = pair_at(8 * n + g);
-      act[n] = p >= 0 ? static_cast<const uint16_t*>(a.A) + static_cast<long long>(p / a.slots) * a.lda + 32 * t4 : nullptr;
+      const int p = pair_at(8 * n + g);        // without a pair: any row, the sums go nowhere
+      act[n] = static_cast<const uint16_t*>(a.A) + static_cast<long long>(max(p, 0) / a.slots) * a.lda + b0 * 128 + 32 * t4;
     }
     float tot[kUnits][kTiles][4];
 #pragma unroll
@@ -156,16 +163,12 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(ExpertsArgs a) {
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) {
         uint32_t r[16];
-        if (act[n]) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint4 v = *reinterpret_cast<const uint4*>(act[n] + b * 128 + 8 * q);
-            r[4 * q] = v.x, r[4 * q + 1] = v.y, r[4 * q + 2] = v.z, r[4 * q + 3] = v.w;
-          }
-        } else {
-#pragma unroll
-          for (int q = 0; q < 16; ++q) r[q] = 0;
+        for (int q = 0; q < 4; ++q) {
+          const uint4 v = *reinterpret_cast<const uint4*>(act[n] + 8 * q);
+          r[4 * q] = v.x, r[4 * q + 1] = v.y, r[4 * q + 2] = v.z, r[4 * q + 3] = v.w;
         }
+        act[n] += 128;
         float own;
         build_bfrag_regs(r, bf[n], own);
         inv[n][0] = __shfl_sync(0xFFFFFFFFu, own, 8 * t4);
@@ -178,8 +181,8 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(ExpertsArgs a) {
           copy_next();
           copies_wait<kStages - 1>();
           __syncwarp();
-          const uint8_t* st = ring + get * kStage;
-          if (++get == kStages) get = 0;
+          const uint8_t* st = ring + get;
+          get = get == (kStages - 1) * kStage ? 0 : get + kStage;
           const uint4 lo = lds128(st + lane * 16), hi = lds128(st + 512 + lane * 16);
           const uint32_t slo = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(st + 1024 + g * 8 + 2 * t4));
           const uint32_t shi = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(st + 1024 + (g + 8) * 8 + 2 * t4));
@@ -233,15 +236,18 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(ExpertsArgs a) {
         return v * gs;
       };
       if (kGated) {
-        const int o = run.unit * 8 + lane;
-        if (lane < run.units * 8 && o < outs) {
-          const int r = (lane >> 3) * 16 + (lane & 7);
-          const float gate = sum_at(r), up = sum_at(r + 8);
-          c[o] = f32_to_bf16_rn(gate / (1.0f + expf(-gate)) * up);
+#pragma unroll
+        for (int h = 0; h < kUnits / 4; ++h) {
+          const int i8 = 32 * h + lane, o = run.unit * 8 + i8;
+          if (i8 < run.units * 8 && o < outs) {
+            const int r = (i8 >> 3) * 16 + (i8 & 7);
+            const float gate = sum_at(r), up = sum_at(r + 8);
+            c[o] = f32_to_bf16_rn(gate / (1.0f + expf(-gate)) * up);
+          }
         }
       } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kUnits / 2; ++h) {
           const int r = 32 * h + lane, o = run.unit * 16 + r;
           if (r < run.units * 16 && o < outs) c[o] = f32_to_bf16_rn(sum_at(r));
         }
