@@ -390,6 +390,8 @@ int run_experts(const void* A, int lda, const void* W, const void* scales, const
   if (globals && !aligned(globals, 4)) return fail(WQP_ERR_INVALID_ARG, "%s: global_scales must be 4-byte aligned", nm);
   if ((st = check_words(nm, "rows", rows)) != WQP_OK || (st = check_words(nm, "offsets", offsets)) != WQP_OK) return st;
   const int outs = gated ? N / 2 : N;
+  if (static_cast<long long>(T) * slots * outs > (1ll << 38))
+    return fail(WQP_ERR_INVALID_ARG, "%s: %lld rows of %d outputs are too many", nm, static_cast<long long>(T) * slots, outs);
   if (!aligned(C, 2)) return fail(WQP_ERR_INVALID_ARG, "%s: C must be 2-byte aligned", nm);
   if (ldc < outs) return fail(WQP_ERR_INVALID_ARG, "%s: ldc=%d must be >= %d", nm, ldc, outs);
   DeviceInfo* dev = nullptr;

@@ -268,6 +268,7 @@ cudaError_t launch_few_t(const ExpertsArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_w4a16_experts(const ExpertsArgs& a, cudaStream_t s) {
+  if (static_cast<long long>(a.T) * a.slots > 4ll * a.E) return launch_w4a16_experts_many(a, s);
   return a.gated ? launch_few_t<1, true>(a, s) : launch_few_t<1, false>(a, s);
 }
 

@@ -1,0 +1,434 @@
+// Products of rows with their experts' packed W4A16 matrices on the 5th-
+// generation tensor core, for any number of rows an expert.
+//
+// The weights are the first operand: a tile is 256 weight rows by up to 256 of
+// an expert's pairs, on a pair of CTAs (act.cuh) that hold 128 weight rows and
+// half of the pairs' activations each. Decoding them is what has to be fed
+// (128 * 64 weights a CTA and stage), and it has the same cost however few
+// pairs there are: from about 100 pairs a tile the tensor core is the limit,
+// below that the decoding or the bytes.
+//
+//  * Decoding, two sets of four warps that take the 128-K chunks in turn: a
+//    thread owns a weight row (a lane of tensor memory). Its codes and scales
+//    come by asynchronous copies into a ring that only this thread uses, so no
+//    barrier is in between; e2m1 * e4m3 is exact in BF16, and goes straight to
+//    tensor memory, from where the MMAs take it.
+//  * Activations, four warps: rows of BF16 gathered by pair, 16 bytes a copy,
+//    into 128-byte-swizzled tiles of 64 K.
+//  * MMA, one warp of the even CTA: M = 256, N = the tile's pairs rounded up to
+//    32, so that a short expert costs no more than its rows.
+//  * Output, four warps: a lane has a weight row and, column by column, the
+//    pairs. Gated: gate and up rows take turns as lanes, and lanes exchange
+//    halves of their columns.
+#include "act.cuh"
+#include "experts.cuh"
+
+namespace wqp {
+namespace act {
+namespace {
+
+constexpr int kS = 8;                          // stages of 64 K
+constexpr int kStageB = 128 * 128;             // activations of a stage: 128 rows of 64 K
+constexpr int kSets = 2, kSlots = 4;           // decoding sets, and chunks of 128 K in a set's ring
+constexpr int kSlot = 128 * 72;                // codes and scales of 128 rows x 128 K
+constexpr int kRaw = kS * kStageB, kTableAt = kRaw + kSets * kSlots * kSlot;
+constexpr int kFeeders = 4, kDecoders = 4 * kSets, kEpi = 4;
+constexpr int kWarpDec = kFeeders, kWarpEpi = kWarpDec + kDecoders, kWarpMma = kWarpEpi + kEpi;
+constexpr int kThreads = (kWarpMma + 1) * 32;
+constexpr int kMaxN = 256;                     // pairs of a tile
+constexpr int kAhead = 4;                      // stages of copies of a feeder that may be on their way
+constexpr uint32_t kColA = 256;                // tensor memory: accumulator, then kS stages of 32 columns
+static_assert(kColA + kS * 32 <= 512, "tensor memory");
+
+constexpr int many_bytes(int E) { return 1024 + kTableAt + experts::Table::bytes(E); }
+static_assert(many_bytes(kMaxExperts) <= 226 * 1024, "shared memory");
+
+// D (+)= A * B^T, A from tensor memory, BF16, K = 16, by a pair.
+__device__ __forceinline__ void pair_mma_ts(uint32_t d, uint32_t a, uint64_t bd, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bd), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// A tile of the walk: token tiles of each expert in turn, all its weight tiles
+// one after the other.
+struct Tile {
+  int expert, nt, p0, pairs, n;                // pairs p0 .. p0 + pairs - 1 of the order; n: rounded up
+  __device__ __forceinline__ void at(const experts::Table& table, int id, int weight_tiles) {
+    const int t = id / weight_tiles;
+    nt = id - t * weight_tiles;
+    expert = table.expert_of(t);
+    const int begin = table.begin[expert], count = table.begin[expert + 1] - begin;
+    const int tiles = (count + kMaxN - 1) / kMaxN;
+    const int each = ((count + tiles - 1) / tiles + 31) & ~31;   // even shares: at most kMaxN, none empty
+    const int from = (t - table.tiles[expert]) * each;
+    p0 = begin + from;
+    pairs = min(count - from, each);
+    n = (pairs + 31) & ~31;
+  }
+};
+
+// Two E2M1 codes, as f16x2 and with their group's scale as f16x2, to BF16
+// pairs, exactly. The two forms use different pipes (conversions to FP32 and a
+// byte permutation; shifts and masks, with the scale times 2^112 in BF16, as
+// the FP16 bits moved by 3 are a BF16 number 2^-112 as large).
+__device__ __forceinline__ uint32_t decode_by_cvt(uint32_t h, uint32_t s_f16) { return f16x2_to_bf16x2_exact(mul_f16x2(h, s_f16)); }
+__device__ __forceinline__ uint32_t decode_by_mask(uint32_t h, uint32_t s_bf16) {
+  return mul_bf16x2(((h >> 3) & 0x0FFF0FFFu) | (h & 0x80008000u), s_bf16);
+}
+
+// 16 codes of a group (two words) to 8 BF16 pairs.
+template <int kMaskEvery>
+__device__ __forceinline__ void decode_group(uint32_t w0, uint32_t w1, uint32_t s_f16, uint32_t s_bf16, uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t h = e2m1x2_to_f16x2((i < 4 ? w0 : w1) >> (8 * (i & 3)));
+    r[i] = kMaskEvery && i % kMaskEvery == 0 ? decode_by_mask(h, s_bf16) : decode_by_cvt(h, s_f16);
+  }
+}
+
+template <bool kGated>
+__global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  // full and acc_free count both CTAs' work and are used in the even CTA; empty
+  // and acc_full are told to both.
+  __shared__ __align__(8) uint64_t full_sh[kS], empty_sh[kS], acc_full_sh, acc_free_sh, drained_sh;
+  __shared__ uint32_t tmem_sh;
+  __shared__ int abort_sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const uint32_t full = smem_u32(full_sh), empty = smem_u32(empty_sh);
+  const uint32_t acc_full = smem_u32(&acc_full_sh), acc_free = smem_u32(&acc_free_sh), drained = smem_u32(&drained_sh);
+  volatile int* abort_flag = &abort_sh;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kS; ++i) {
+      mbar_init(full + 8 * i, 2 * (kFeeders + 4));
+      mbar_init(empty + 8 * i, 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_free, 2 * kEpi);
+    mbar_init(drained, 1);
+    abort_sh = 0;
+    mbar_fence_init();
+  }
+  __syncwarp();
+  cluster_arrive_relaxed();
+  if (warp == kWarpMma) {
+    pair_tmem_alloc(smem_u32(&tmem_sh), 512);
+    tc_fence_before();
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  const int R = a.T * a.slots;
+  experts::Table table;                        // its barriers publish tmem_sh too
+  table.make(smem + kTableAt, a.offsets, a.E, R, [](int n) { return (n + kMaxN - 1) / kMaxN; });
+  tc_fence_after();
+  cluster_wait();
+  const uint32_t tmem = tmem_sh;
+
+  const int outs = kGated ? a.N / 2 : a.N;
+  constexpr int kOuts = kGated ? 128 : 256;    // outputs of a tile
+  const int weight_tiles = (outs + kOuts - 1) / kOuts, total = table.total() * weight_tiles;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int mine = first < total ? (total - first + step - 1) / step : 0;   // tiles of this pair
+  const int stages = a.K >> 6, chunks = a.K >> 7;                           // of a tile
+  const uint32_t full0 = mapa_shared(full, 0);
+
+  if (warp < kWarpDec) {
+    // Activations. Thread t copies 16-byte piece t % 8 of rows t / 8 + 16 i.
+    const int piece = threadIdx.x & 7, row0 = threadIdx.x >> 3;
+    const uint32_t dst0 = sb + row0 * 128 + ((piece ^ (row0 & 7)) << 4);
+    int s = 0, told = 0;                       // the stage to fill; the next to announce
+    uint32_t ph = 1;
+    long long issued = 0;
+    bool ok = true;
+    const auto announce = [&] {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) pair_arrive(full0 + 8 * told);
+      if (++told == kS) told = 0;
+    };
+    for (int i = 0; i < mine && ok; ++i) {
+      Tile tile;
+      tile.at(table, first + i * step, weight_tiles);
+      const int half = tile.n >> 1;
+      const uint8_t* src[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = row0 + 16 * j, c = rank * half + r;
+        const int p = r < half && c < tile.pairs ? a.rows[tile.p0 + c] : -1;
+        src[j] = static_cast<unsigned>(p) < static_cast<unsigned>(R)
+                     ? static_cast<const uint8_t*>(a.A) + static_cast<long long>(p / a.slots) * a.lda * 2 + piece * 16
+                     : nullptr;
+      }
+      for (int k = 0; k < stages; ++k) {
+        if (issued >= kS) ok = __all_sync(0xFFFFFFFFu, wait_or_abort(empty + 8 * s, ph, a.err, abort_flag));
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (src[j]) {
+            copy16(dst0 + s * kStageB + j * 16 * 128, src[j]);
+            src[j] += 128;
+          }
+        copies_close();
+        if (++s == kS) s = 0, ph ^= 1;
+        if (++issued > kAhead) {
+          copies_wait<kAhead>();
+          announce();
+        }
+      }
+    }
+    copies_wait<0>();
+    if (ok)
+      for (long long left = issued < kAhead ? issued : kAhead; left > 0; --left) announce();
+    // Every stage's MMAs are done, and told to both CTAs, before this one ends.
+    if (warp == 0) {
+      const int used = issued < kS ? static_cast<int>(issued) : kS;
+      for (int t = 0; t < used && ok; ++t) {
+        const int at = used < kS ? t : s;
+        ok = __all_sync(0xFFFFFFFFu, wait_or_abort(empty + 8 * at, used < kS ? 0u : ph, a.err, abort_flag));
+        if (used == kS && ++s == kS) s = 0, ph ^= 1;
+      }
+    }
+  } else if (warp < kWarpEpi) {
+    // Weights. Thread: lane `row` of tensor memory.
+    const int set = (warp - kWarpDec) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t raw = sb + kRaw + set * kSlots * kSlot;
+    const uint8_t* const raw_ptr = smem + kRaw + set * kSlots * kSlot;
+    const uint32_t at = tmem + kColA + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const long long wpitch = a.K >> 1, spitch = a.K >> 4;
+    // The next chunk of this set to copy: chunks of all tiles are numbered through.
+    int ai = 0, ac = set;                      // tile of the pair, chunk in it
+    while (ai < mine && ac >= chunks) ac -= chunks, ++ai;
+    int loaded = -1, put = 0;
+    const uint8_t *w = nullptr, *sc = nullptr;
+    const auto copy_next = [&] {
+      if (ai < mine) {
+        if (loaded != ai) {
+          loaded = ai;
+          const int id = first + ai * step, t = id / weight_tiles, nt = id - t * weight_tiles;
+          long long n = static_cast<long long>(table.expert_of(t)) * a.N;
+          if (kGated) n += min(nt * 128 + rank * 64 + (row >> 1), outs - 1) + (row & 1) * static_cast<long long>(outs);
+          else n += min(nt * 256 + rank * 128 + row, outs - 1);
+          w = a.W + n * wpitch;
+          sc = a.scales + n * spitch;
+        }
+        const uint32_t dst = raw + put * kSlot + row * 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) copy16(dst + j * 2048, w + ac * 64 + j * 16);
+        copy8(raw + put * kSlot + 8192 + row * 8, sc + ac * 8);
+        ac += kSets;
+        while (ai < mine && ac >= chunks) ac -= chunks, ++ai;
+      }
+      copies_close();
+      if (++put == kSlots) put = 0;
+    };
+#pragma unroll 1
+    for (int i = 0; i < kSlots - 1; ++i) copy_next();
+    const long long all = static_cast<long long>(mine) * chunks;
+    int get = 0, s = 2 * set;
+    uint32_t ph = 1;
+    bool ok = true;
+    for (long long c = set; c < all && ok; c += kSets) {
+      copy_next();
+      copies_wait<kSlots - 1>();
+      const uint8_t* q = raw_ptr + get * kSlot + row * 16;
+      const uint2 scales = *reinterpret_cast<const uint2*>(raw_ptr + get * kSlot + 8192 + row * 8);
+      if (++get == kSlots) get = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 w0 = *reinterpret_cast<const uint4*>(q + h * 4096), w1 = *reinterpret_cast<const uint4*>(q + h * 4096 + 2048);
+        const uint32_t s4 = h ? scales.y : scales.x;
+        const uint32_t f01 = e4m3x2_to_f16x2(s4 & 0xFFFFu), f23 = e4m3x2_to_f16x2(s4 >> 16);
+        const uint32_t ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        uint32_t r[32];
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr) {
+          const uint32_t f = gr < 2 ? f01 : f23;
+          const uint32_t sf = __byte_perm(f, f, gr & 1 ? 0x3232 : 0x1010);
+          const float sv = __half2float(__ushort_as_half(static_cast<unsigned short>(sf))) * 0x1p112f;
+          const uint32_t sbf = __byte_perm(__float_as_uint(sv), 0, 0x3232);
+          decode_group<2>(ww[2 * gr], ww[2 * gr + 1], sf, sbf, r + 8 * gr);
+        }
+        if (2 * c + h >= kS) ok = __all_sync(0xFFFFFFFFu, wait_or_abort(empty + 8 * s, ph, a.err, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        tmem_st32(at + s * 32, r);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) pair_arrive(full0 + 8 * s);
+        ++s;
+      }
+      s += 2 * (kSets - 1);
+      if (s >= kS) s -= kS, ph ^= 1;
+    }
+    copies_wait<0>();
+  } else if (warp < kWarpMma) {
+    // Output: this warp's 32 lanes, all columns.
+    const int q = warp & 3, row = q * 32 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const uint32_t acc_free0 = mapa_shared(acc_free, 0);
+    uint32_t ph = 0;
+    for (int i = 0; i < mine; ++i) {
+      Tile tile;
+      tile.at(table, first + i * step, weight_tiles);
+      const float gs = a.globals ? a.globals[tile.expert] : 1.0f;
+      const int o = kGated ? tile.nt * 128 + rank * 64 + (row >> 1) : tile.nt * 256 + rank * 128 + row;
+      uint16_t* const c = static_cast<uint16_t*>(a.C) + o;
+      wait_or_abort(acc_full, ph, a.err, abort_flag);
+      ph ^= 1;
+      __syncwarp();
+      if (__any_sync(0xFFFFFFFFu, *abort_flag)) break;
+      tc_fence_after();
+      for (int c0 = 0; c0 < tile.n; c0 += 32) {
+        const int pl = c0 + lane < tile.pairs ? a.rows[tile.p0 + c0 + lane] : -1;   // the pair of column c0 + lane
+        uint32_t v[32];
+        tmem_ld32_start(tl + c0, v);
+        tmem_ld_wait(v);
+        if (c0 + 32 >= tile.n) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0 && i + 1 < mine) pair_arrive(acc_free0);
+        }
+        if constexpr (kGated) {
+          // Even lanes have gates and take columns 0..15, odd ones ups and 16..31.
+          const bool odd = lane & 1;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float keep = __uint_as_float(odd ? v[16 + j] : v[j]), give = __uint_as_float(odd ? v[j] : v[16 + j]);
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+            const float gate = (odd ? got : keep) * gs, up = (odd ? keep : got) * gs;
+            const int p = __shfl_sync(0xFFFFFFFFu, pl, odd ? 16 + j : j);
+            if (static_cast<unsigned>(p) < static_cast<unsigned>(R) && o < outs)
+              c[static_cast<long long>(p) * a.ldc] = f32_to_bf16_rn(gate / (1.0f + expf(-gate)) * up);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int p = __shfl_sync(0xFFFFFFFFu, pl, j);
+            if (static_cast<unsigned>(p) < static_cast<unsigned>(R) && o < outs)
+              c[static_cast<long long>(p) * a.ldc] = f32_to_bf16_rn(__uint_as_float(v[j]) * gs);
+          }
+        }
+      }
+    }
+  } else if (rank == 0) {
+    // A wait that follows MMAs costs the tensor core a pause, so the next stage is
+    // looked up before this one's MMAs are issued.
+    const uint64_t bd0 = tile_desc(sb);
+    int s = 0;
+    uint32_t ph = 0, acc_ph = 0;
+    bool ok = true, loaded = false;
+    for (int i = 0; i < mine && ok; ++i) {
+      Tile tile;
+      tile.at(table, first + i * step, weight_tiles);
+      const uint32_t idesc = idesc_bf16(256, tile.n);
+      if (i > 0) {
+        ok = __all_sync(0xFFFFFFFFu, wait_or_abort(acc_free, acc_ph, a.err, abort_flag));
+        acc_ph ^= 1;
+      }
+      for (int k = 0; k < stages && ok; ++k) {
+        if (!loaded) ok = __all_sync(0xFFFFFFFFu, wait_or_abort(full + 8 * s, ph, a.err, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        const int s1 = s + 1 == kS ? 0 : s + 1;
+        const uint32_t ph1 = s1 ? ph : ph ^ 1;
+        const bool l1 = mbar_test(full + 8 * s1, ph1);
+        if (elect_one()) {
+          const uint64_t bd = bd0 + s * (kStageB >> 4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) pair_mma_ts(tmem, tmem + kColA + s * 32 + 8 * j, bd + 2 * j, idesc, (k | j) ? 1u : 0u);
+          pair_commit(empty + 8 * s);
+          if (k + 1 == stages) pair_commit(acc_full);
+        }
+        __syncwarp();
+        loaded = __all_sync(0xFFFFFFFFu, l1);
+        s = s1, ph = ph1;
+      }
+    }
+    if (elect_one()) pair_commit_own(drained);
+    __syncwarp();
+    mbar_wait(drained, 0, a.err);
+  }
+  // Nothing of the pair is on its way any more, and both are done with the
+  // pair's tensor memory.
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive_relaxed();
+  cluster_wait();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    pair_tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool kGated>
+cudaError_t launch_experts_many_t(const ExpertsArgs& a, cudaStream_t s) {
+  static AttrLatch latch;
+  const cudaError_t e = set_smem_attrs(experts_kernel<kGated>, latch, many_bytes(kMaxExperts), true);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.num_sms / 2 * 2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = many_bytes(a.E);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, experts_kernel<kGated>, a);
+}
+
+}  // namespace
+}  // namespace act
+
+cudaError_t launch_w4a16_experts_many(const ExpertsArgs& a, cudaStream_t s) {
+  return a.gated ? act::launch_experts_many_t<true>(a, s) : act::launch_experts_many_t<false>(a, s);
+}
+
+}  // namespace wqp

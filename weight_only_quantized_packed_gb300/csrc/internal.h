@@ -165,6 +165,8 @@ cudaError_t launch_expert_route(const RouteArgs& a, cudaStream_t s);
 cudaError_t launch_expert_order(const OrderArgs& a, cudaStream_t s);
 cudaError_t launch_w4a16_experts(const ExpertsArgs& a, cudaStream_t s);
 cudaError_t launch_expert_combine(const CombineArgs& a, cudaStream_t s);
+// The kernel on the 5th-generation tensor core (gemm_experts_many.cu).
+cudaError_t launch_w4a16_experts_many(const ExpertsArgs& a, cudaStream_t s);
 
 cudaError_t launch_w4_quantize(const QuantArgs& a, cudaStream_t s);
 cudaError_t launch_a8_quantize(const QuantArgs& a, cudaStream_t s);
