@@ -4,17 +4,17 @@
 // The weights are the first operand: a tile is 256 weight rows by up to 256 of
 // an expert's pairs, on a pair of CTAs (act.cuh) that hold 128 weight rows and
 // half of the pairs' activations each. Decoding them is what has to be fed
-// (128 * 64 weights a CTA and stage), and it has the same cost however few
+// (128 * 128 weights a CTA and stage), and it has the same cost however few
 // pairs there are: from about 100 pairs a tile the tensor core is the limit,
 // below that the decoding or the bytes.
 //
-//  * Decoding, two sets of four warps that take the 128-K chunks in turn: a
+//  * Decoding, two sets of four warps that take the stages in turn: a
 //    thread owns a weight row (a lane of tensor memory). Its codes and scales
 //    come by asynchronous copies into a ring that only this thread uses, so no
 //    barrier is in between; e2m1 * e4m3 is exact in BF16, and goes straight to
 //    tensor memory, from where the MMAs take it.
 //  * Activations, four warps: rows of BF16 gathered by pair, 16 bytes a copy,
-//    into 128-byte-swizzled tiles of 64 K.
+//    into 128-byte-swizzled tiles of 64 K, two a stage.
 //  * MMA, one warp of the even CTA: M = 256, N = the tile's pairs rounded up to
 //    32, so that a short expert costs no more than its rows.
 //  * Output, four warps: a lane has a weight row and, column by column, the
@@ -22,23 +22,25 @@
 //    halves of their columns.
 #include "act.cuh"
 #include "experts.cuh"
+#include "mma_f16.cuh"
 
 namespace wqp {
 namespace act {
 namespace {
 
-constexpr int kS = 8;                          // stages of 64 K
-constexpr int kStageB = 128 * 128;             // activations of a stage: 128 rows of 64 K
-constexpr int kSets = 2, kSlots = 4;           // decoding sets, and chunks of 128 K in a set's ring
+constexpr int kS = 4;                          // stages of 128 K
+constexpr int kHalfB = 128 * 128;              // activations of half a stage: 128 rows of 64 K
+constexpr int kStageB = 2 * kHalfB;
+constexpr int kSets = 2, kSlots = 4;           // decoding sets, and stages in a set's ring
 constexpr int kSlot = 128 * 72;                // codes and scales of 128 rows x 128 K
 constexpr int kRaw = kS * kStageB, kTableAt = kRaw + kSets * kSlots * kSlot;
 constexpr int kFeeders = 4, kDecoders = 4 * kSets, kEpi = 4;
-constexpr int kWarpDec = kFeeders, kWarpEpi = kWarpDec + kDecoders, kWarpMma = kWarpEpi + kEpi;
-constexpr int kThreads = (kWarpMma + 1) * 32;
+constexpr int kWarpDec = kFeeders, kWarpEpi = kWarpDec + kDecoders, kWarpMma = kWarpEpi + kEpi,
+              kWarpRelay = kWarpMma + 1;
+constexpr int kThreads = (kWarpRelay + 1) * 32;
 constexpr int kMaxN = 256;                     // pairs of a tile
-constexpr int kAhead = 4;                      // stages of copies of a feeder that may be on their way
-constexpr uint32_t kColA = 256;                // tensor memory: accumulator, then kS stages of 32 columns
-static_assert(kColA + kS * 32 <= 512, "tensor memory");
+constexpr uint32_t kColA = 256;                // tensor memory: accumulator, then kS stages of 64 columns
+static_assert(kColA + kS * 64 <= 512, "tensor memory");
 
 constexpr int many_bytes(int E) { return 1024 + kTableAt + experts::Table::bytes(E); }
 static_assert(many_bytes(kMaxExperts) <= 226 * 1024, "shared memory");
@@ -70,19 +72,19 @@ __device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// One arrival at the barrier when this thread's copies so far have landed.
+__device__ __forceinline__ void copies_land(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
+// An arrival that waits for nothing of this thread: what it announces is in
+// tensor memory, behind the store's own wait and fence. (A release would wait for
+// the copies of later chunks.)
+__device__ __forceinline__ void pair_arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // A tile of the walk: token tiles of each expert in turn, all its weight tiles
@@ -103,44 +105,36 @@ struct Tile {
   }
 };
 
-// Two E2M1 codes, as f16x2 and with their group's scale as f16x2, to BF16
-// pairs, exactly. The two forms use different pipes (conversions to FP32 and a
-// byte permutation; shifts and masks, with the scale times 2^112 in BF16, as
-// the FP16 bits moved by 3 are a BF16 number 2^-112 as large).
-__device__ __forceinline__ uint32_t decode_by_cvt(uint32_t h, uint32_t s_f16) { return f16x2_to_bf16x2_exact(mul_f16x2(h, s_f16)); }
-__device__ __forceinline__ uint32_t decode_by_mask(uint32_t h, uint32_t s_bf16) {
-  return mul_bf16x2(((h >> 3) & 0x0FFF0FFFu) | (h & 0x80008000u), s_bf16);
-}
-
-// 16 codes of a group (two words) to 8 BF16 pairs.
-template <int kMaskEvery>
-__device__ __forceinline__ void decode_group(uint32_t w0, uint32_t w1, uint32_t s_f16, uint32_t s_bf16, uint32_t* r) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t h = e2m1x2_to_f16x2((i < 4 ? w0 : w1) >> (8 * (i & 3)));
-    r[i] = kMaskEvery && i % kMaskEvery == 0 ? decode_by_mask(h, s_bf16) : decode_by_cvt(h, s_f16);
-  }
+// Eight E2M1 codes of a word to BF16 pairs with their group's scale (f16x2),
+// exactly: the product is exact in FP16, and widened to FP32 it has nothing in
+// its lower half.
+__device__ __forceinline__ void decode_word(uint32_t w, uint32_t s, uint32_t* r) {
+  r[0] = f16x2_to_bf16x2_exact(f16op::mul_f16x2(f16op::e2m1x2_byte<0>(w), s));
+  r[1] = f16x2_to_bf16x2_exact(f16op::mul_f16x2(f16op::e2m1x2_byte<1>(w), s));
+  r[2] = f16x2_to_bf16x2_exact(f16op::mul_f16x2(f16op::e2m1x2_byte<2>(w), s));
+  r[3] = f16x2_to_bf16x2_exact(f16op::mul_f16x2(f16op::e2m1x2_byte<3>(w), s));
 }
 
 template <bool kGated>
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
   extern __shared__ uint8_t smem_raw[];
   // full and acc_free count both CTAs' work and are used in the even CTA; empty
-  // and acc_full are told to both.
-  __shared__ __align__(8) uint64_t full_sh[kS], empty_sh[kS], acc_full_sh, acc_free_sh, drained_sh;
+  // and acc_full are told to both; landed is each CTA's own.
+  __shared__ __align__(8) uint64_t full_sh[kS], empty_sh[kS], landed_sh[kS], acc_full_sh, acc_free_sh, drained_sh;
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
-  const uint32_t full = smem_u32(full_sh), empty = smem_u32(empty_sh);
+  const uint32_t full = smem_u32(full_sh), empty = smem_u32(empty_sh), landed = smem_u32(landed_sh);
   const uint32_t acc_full = smem_u32(&acc_full_sh), acc_free = smem_u32(&acc_free_sh), drained = smem_u32(&drained_sh);
   volatile int* abort_flag = &abort_sh;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kS; ++i) {
-      mbar_init(full + 8 * i, 2 * (kFeeders + 4));
+      mbar_init(full + 8 * i, 2 * (1 + 4));
+      mbar_init(landed + 8 * i, kFeeders * 32);
       mbar_init(empty + 8 * i, 1);
     }
     mbar_init(acc_full, 1);
@@ -169,56 +163,47 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
   const int weight_tiles = (outs + kOuts - 1) / kOuts, total = table.total() * weight_tiles;
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   const int mine = first < total ? (total - first + step - 1) / step : 0;   // tiles of this pair
-  const int stages = a.K >> 6, chunks = a.K >> 7;                           // of a tile
+  const int stages = a.K >> 7;                                              // of a tile
   const uint32_t full0 = mapa_shared(full, 0);
 
   if (warp < kWarpDec) {
-    // Activations. Thread t copies 16-byte piece t % 8 of rows t / 8 + 16 i.
-    const int piece = threadIdx.x & 7, row0 = threadIdx.x >> 3;
-    const uint32_t dst0 = sb + row0 * 128 + ((piece ^ (row0 & 7)) << 4);
-    int s = 0, told = 0;                       // the stage to fill; the next to announce
+    // Activations. Thread t copies 16-byte piece t % 16 of rows t / 16 + 8 i.
+    const int piece = threadIdx.x & 15, row0 = threadIdx.x >> 4;
+    const uint32_t dst0 = sb + (piece >> 3) * kHalfB + row0 * 128 + (((piece & 7) ^ row0) << 4);
+    int s = 0;
     uint32_t ph = 1;
     long long issued = 0;
     bool ok = true;
-    const auto announce = [&] {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) pair_arrive(full0 + 8 * told);
-      if (++told == kS) told = 0;
-    };
     for (int i = 0; i < mine && ok; ++i) {
       Tile tile;
       tile.at(table, first + i * step, weight_tiles);
-      const int half = tile.n >> 1;
-      const uint8_t* src[8];
+      const int half = tile.n >> 1;            // of this CTA, a multiple of 16
+      const uint8_t* src[16];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int r = row0 + 16 * j, c = rank * half + r;
-        const int p = r < half && c < tile.pairs ? a.rows[tile.p0 + c] : -1;
-        src[j] = static_cast<unsigned>(p) < static_cast<unsigned>(R)
-                     ? static_cast<const uint8_t*>(a.A) + static_cast<long long>(p / a.slots) * a.lda * 2 + piece * 16
-                     : nullptr;
+      for (int j = 0; j < 16; ++j) {           // rows without a pair: any row, their columns go nowhere
+        const int r = row0 + 8 * j, c = rank * half + r;
+        const int p = r < half && c < tile.pairs ? a.rows[tile.p0 + c] : 0;
+        const int t = static_cast<unsigned>(p) < static_cast<unsigned>(R) ? p / a.slots : 0;
+        src[j] = static_cast<const uint8_t*>(a.A) + static_cast<long long>(t) * a.lda * 2 + piece * 16;
       }
       for (int k = 0; k < stages; ++k) {
         if (issued >= kS) ok = __all_sync(0xFFFFFFFFu, wait_or_abort(empty + 8 * s, ph, a.err, abort_flag));
         if (!ok) break;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (src[j]) {
-            copy16(dst0 + s * kStageB + j * 16 * 128, src[j]);
-            src[j] += 128;
-          }
-        copies_close();
-        if (++s == kS) s = 0, ph ^= 1;
-        if (++issued > kAhead) {
-          copies_wait<kAhead>();
-          announce();
+        for (int j = 0; j < 16; j += 2) {
+          if (8 * j >= half) break;
+          copy16(dst0 + s * kStageB + j * 1024, src[j]);
+          copy16(dst0 + s * kStageB + j * 1024 + 1024, src[j + 1]);
+          src[j] += 256;
+          src[j + 1] += 256;
         }
+        copies_land(landed + 8 * s);
+        ++issued;
+        if (++s == kS) s = 0, ph ^= 1;
       }
     }
+    copies_close();
     copies_wait<0>();
-    if (ok)
-      for (long long left = issued < kAhead ? issued : kAhead; left > 0; --left) announce();
     // Every stage's MMAs are done, and told to both CTAs, before this one ends.
     if (warp == 0) {
       const int used = issued < kS ? static_cast<int>(issued) : kS;
@@ -234,10 +219,10 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
     const uint32_t raw = sb + kRaw + set * kSlots * kSlot;
     const uint8_t* const raw_ptr = smem + kRaw + set * kSlots * kSlot;
     const uint32_t at = tmem + kColA + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const long long wpitch = a.K >> 1, spitch = a.K >> 4;
-    // The next chunk of this set to copy: chunks of all tiles are numbered through.
-    int ai = 0, ac = set;                      // tile of the pair, chunk in it
-    while (ai < mine && ac >= chunks) ac -= chunks, ++ai;
+    // The next stage of this set to copy: the stages of all tiles are numbered
+    // through, and the sets take them in turn.
+    int ai = 0, ac = set;                      // tile of the pair, stage in it
+    while (ai < mine && ac >= stages) ac -= stages, ++ai;
     int loaded = -1, put = 0;
     const uint8_t *w = nullptr, *sc = nullptr;
     const auto copy_next = [&] {
@@ -248,26 +233,27 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
           long long n = static_cast<long long>(table.expert_of(t)) * a.N;
           if (kGated) n += min(nt * 128 + rank * 64 + (row >> 1), outs - 1) + (row & 1) * static_cast<long long>(outs);
           else n += min(nt * 256 + rank * 128 + row, outs - 1);
-          w = a.W + n * wpitch;
-          sc = a.scales + n * spitch;
+          w = a.W + n * (a.K >> 1) + ac * 64;
+          sc = a.scales + n * (a.K >> 4) + ac * 8;
         }
         const uint32_t dst = raw + put * kSlot + row * 16;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) copy16(dst + j * 2048, w + ac * 64 + j * 16);
-        copy8(raw + put * kSlot + 8192 + row * 8, sc + ac * 8);
+        for (int j = 0; j < 4; ++j) copy16(dst + j * 2048, w + j * 16);
+        copy8(raw + put * kSlot + 8192 + row * 8, sc);
+        w += kSets * 64;
+        sc += kSets * 8;
         ac += kSets;
-        while (ai < mine && ac >= chunks) ac -= chunks, ++ai;
+        while (ai < mine && ac >= stages) ac -= stages, ++ai;
       }
       copies_close();
       if (++put == kSlots) put = 0;
     };
 #pragma unroll 1
     for (int i = 0; i < kSlots - 1; ++i) copy_next();
-    const long long all = static_cast<long long>(mine) * chunks;
-    int get = 0, s = 2 * set;
+    const long long all = static_cast<long long>(mine) * stages;
+    int get = 0, s = set;
     uint32_t ph = 1;
-    bool ok = true;
-    for (long long c = set; c < all && ok; c += kSets) {
+    for (long long c = set; c < all; c += kSets) {
       copy_next();
       copies_wait<kSlots - 1>();
       const uint8_t* q = raw_ptr + get * kSlot + row * 16;
@@ -284,23 +270,21 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
         for (int gr = 0; gr < 4; ++gr) {
           const uint32_t f = gr < 2 ? f01 : f23;
           const uint32_t sf = __byte_perm(f, f, gr & 1 ? 0x3232 : 0x1010);
-          const float sv = __half2float(__ushort_as_half(static_cast<unsigned short>(sf))) * 0x1p112f;
-          const uint32_t sbf = __byte_perm(__float_as_uint(sv), 0, 0x3232);
-          decode_group<2>(ww[2 * gr], ww[2 * gr + 1], sf, sbf, r + 8 * gr);
+          decode_word(ww[2 * gr], sf, r + 8 * gr);
+          decode_word(ww[2 * gr + 1], sf, r + 8 * gr + 4);
         }
-        if (2 * c + h >= kS) ok = __all_sync(0xFFFFFFFFu, wait_or_abort(empty + 8 * s, ph, a.err, abort_flag));
-        if (!ok) break;
-        tc_fence_after();
-        tmem_st32(at + s * 32, r);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) pair_arrive(full0 + 8 * s);
-        ++s;
+        if (h == 0 && c >= kS && !__all_sync(0xFFFFFFFFu, wait_or_abort(empty + 8 * s, ph, a.err, abort_flag))) goto decoded;
+        if (h == 0) tc_fence_after();
+        tmem_st32(at + s * 64 + h * 32, r);
       }
-      s += 2 * (kSets - 1);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) pair_arrive_relaxed(full0 + 8 * s);
+      s += kSets;
       if (s >= kS) s -= kS, ph ^= 1;
     }
+  decoded:
     copies_wait<0>();
   } else if (warp < kWarpMma) {
     // Output: this warp's 32 lanes, all columns.
@@ -351,6 +335,20 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
         }
       }
     }
+  } else if (warp == kWarpRelay) {
+    // Announces the stages whose activations have landed. The fence that makes
+    // them visible to the MMAs waits for all copies of the thread that makes it,
+    // so a feeder would wait for those of later stages.
+    const long long all = static_cast<long long>(mine) * stages;
+    int s = 0;
+    uint32_t ph = 0;
+    for (long long c = 0; c < all; ++c) {
+      if (!__all_sync(0xFFFFFFFFu, wait_or_abort(landed + 8 * s, ph, a.err, abort_flag))) break;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) pair_arrive(full0 + 8 * s);
+      if (++s == kS) s = 0, ph ^= 1;
+    }
   } else if (rank == 0) {
     // A wait that follows MMAs costs the tensor core a pause, so the next stage is
     // looked up before this one's MMAs are issued.
@@ -376,7 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
         if (elect_one()) {
           const uint64_t bd = bd0 + s * (kStageB >> 4);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) pair_mma_ts(tmem, tmem + kColA + s * 32 + 8 * j, bd + 2 * j, idesc, (k | j) ? 1u : 0u);
+          for (int j = 0; j < 8; ++j)
+            pair_mma_ts(tmem, tmem + kColA + s * 64 + 8 * j, bd + (j >> 2) * (kHalfB >> 4) + 2 * (j & 3), idesc, (k | j) ? 1u : 0u);
           pair_commit(empty + 8 * s);
           if (k + 1 == stages) pair_commit(acc_full);
         }
