@@ -10,7 +10,7 @@
 //
 //  * Decoding, two sets of four warps that take the stages in turn: a
 //    thread owns a weight row (a lane of tensor memory). Its codes and scales
-//    come by asynchronous copies into a ring that only this thread uses, so no
+//    come by asynchronous copies into a ring that only its warp uses, so no
 //    barrier is in between; e2m1 * e4m3 is exact in BF16, and goes straight to
 //    tensor memory, from where the MMAs take it.
 //  * Activations, four warps: rows of BF16 gathered by pair, 16 bytes a copy,
@@ -33,11 +33,16 @@ constexpr int kHalfB = 128 * 128;              // activations of half a stage: 1
 constexpr int kStageB = 2 * kHalfB;
 constexpr int kSets = 2, kSlots = 4;           // decoding sets, and stages in a set's ring
 constexpr int kSlot = 128 * 72;                // codes and scales of 128 rows x 128 K
-constexpr int kRaw = kS * kStageB, kTableAt = kRaw + kSets * kSlots * kSlot;
+constexpr int kRaw = kS * kStageB, kOutAt = kRaw + kSets * kSlots * kSlot;
+constexpr int kOut = 32 * 64;                  // 32 pairs by 32 outputs of an output warp
+constexpr int kTableAt = kOutAt + 4 * kOut;
 constexpr int kFeeders = 4, kDecoders = 4 * kSets, kEpi = 4;
 constexpr int kWarpDec = kFeeders, kWarpEpi = kWarpDec + kDecoders, kWarpMma = kWarpEpi + kEpi,
               kWarpRelay = kWarpMma + 1;
-constexpr int kThreads = (kWarpRelay + 1) * 32;
+constexpr int kThreads = (kWarpMma + 4) * 32;  // registers are shared out by four warps at a time
+// Registers: launched with 96 a thread, 480 to the five threads of one index.
+constexpr int kRegsLaunch = 96, kRegsFeed = 80, kRegsOut = 168, kRegsRest = 40;
+static_assert(kThreads == 640 && kRegsFeed + 2 * kRegsLaunch + kRegsOut + kRegsRest <= 5 * kRegsLaunch, "registers");
 constexpr int kMaxN = 256;                     // pairs of a tile
 constexpr uint32_t kColA = 256;                // tensor memory: accumulator, then kS stages of 64 columns
 static_assert(kColA + kS * 64 <= 512, "tensor memory");
@@ -115,6 +120,30 @@ __device__ __forceinline__ void decode_word(uint32_t w, uint32_t s, uint32_t* r)
   r[3] = f16x2_to_bf16x2_exact(f16op::mul_f16x2(f16op::e2m1x2_byte<3>(w), s));
 }
 
+// g * sigmoid(g), through e^-|g|, which cannot overflow: 4 roundings and two
+// approximations of 2 ulp.
+__device__ __forceinline__ float silu(float g) {
+  const float t = __expf(-fabsf(g));
+  return __fdividef(g * (g < 0.0f ? t : 1.0f), 1.0f + t);
+}
+
+// How C's rows are aligned, in bytes: 16 or 2.
+__device__ __forceinline__ int out_align(const ExpertsArgs& a) {
+  return (reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && a.ldc % 8 == 0) ? 16 : 2;
+}
+// Up to 8 outputs of a row, of which `left` are inside it.
+__device__ __forceinline__ void store_piece(uint16_t* c, const uint8_t* from, int left, int align) {
+  const uint4 v = *reinterpret_cast<const uint4*>(from);
+  if (align == 16 && left >= 8) {
+    *reinterpret_cast<uint4*>(c) = v;
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) c[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+  }
+}
+
 template <bool kGated>
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -167,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
   const uint32_t full0 = mapa_shared(full, 0);
 
   if (warp < kWarpDec) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFeed));
     // Activations. Thread t copies 16-byte piece t % 16 of rows t / 16 + 8 i.
     const int piece = threadIdx.x & 15, row0 = threadIdx.x >> 4;
     const uint32_t dst0 = sb + (piece >> 3) * kHalfB + row0 * 128 + (((piece & 7) ^ row0) << 4);
@@ -216,31 +246,41 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
   } else if (warp < kWarpEpi) {
     // Weights. Thread: lane `row` of tensor memory.
     const int set = (warp - kWarpDec) >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t raw = sb + kRaw + set * kSlots * kSlot;
-    const uint8_t* const raw_ptr = smem + kRaw + set * kSlots * kSlot;
+    // A warp's rows in a slot: 32 rows of 64 bytes, piece j of row r at j ^ (r / 2
+    // mod 4), then 32 of 8. A copy takes whole rows of 64 bytes (as 16 bytes of 32
+    // rows the copies took most of a stage's time).
+    const uint32_t raw = sb + kRaw + set * kSlots * kSlot + (warp & 3) * kSlot / 4;
+    const uint8_t* const raw_ptr = smem + kRaw + set * kSlots * kSlot + (warp & 3) * kSlot / 4;
+    const uint32_t dst_w = (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
     const uint32_t at = tmem + kColA + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     // The next stage of this set to copy: the stages of all tiles are numbered
     // through, and the sets take them in turn.
     int ai = 0, ac = set;                      // tile of the pair, stage in it
     while (ai < mine && ac >= stages) ac -= stages, ++ai;
     int loaded = -1, put = 0;
-    const uint8_t *w = nullptr, *sc = nullptr;
+    const uint8_t *w[4] = {}, *sc = nullptr;
     const auto copy_next = [&] {
       if (ai < mine) {
         if (loaded != ai) {
           loaded = ai;
           const int id = first + ai * step, t = id / weight_tiles, nt = id - t * weight_tiles;
-          long long n = static_cast<long long>(table.expert_of(t)) * a.N;
-          if (kGated) n += min(nt * 128 + rank * 64 + (row >> 1), outs - 1) + (row & 1) * static_cast<long long>(outs);
-          else n += min(nt * 256 + rank * 128 + row, outs - 1);
-          w = a.W + n * (a.K >> 1) + ac * 64;
-          sc = a.scales + n * (a.K >> 4) + ac * 8;
-        }
-        const uint32_t dst = raw + put * kSlot + row * 16;
+          const long long base = static_cast<long long>(table.expert_of(t)) * a.N;
+          const auto row_at = [&](int r) {     // the weight row of lane r of the tile; rows past the last read that one
+            return kGated ? base + min(nt * 128 + rank * 64 + (r >> 1), outs - 1) + (r & 1) * static_cast<long long>(outs)
+                          : base + min(nt * 256 + rank * 128 + r, outs - 1);
+          };
 #pragma unroll
-        for (int j = 0; j < 4; ++j) copy16(dst + j * 2048, w + j * 16);
-        copy8(raw + put * kSlot + 8192 + row * 8, sc);
-        w += kSets * 64;
+          for (int j = 0; j < 4; ++j)
+            w[j] = a.W + row_at((warp & 3) * 32 + 8 * j + (lane >> 2)) * (a.K >> 1) + ac * 64 + (lane & 3) * 16;
+          sc = a.scales + row_at(row) * (a.K >> 4) + ac * 8;
+        }
+        const uint32_t dst = raw + put * kSlot;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          copy16(dst + j * 512 + dst_w, w[j]);
+          w[j] += kSets * 64;
+        }
+        copy8(dst + 2048 + lane * 8, sc);
         sc += kSets * 8;
         ac += kSets;
         while (ai < mine && ac >= stages) ac -= stages, ++ai;
@@ -254,14 +294,19 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
     int get = 0, s = set;
     uint32_t ph = 1;
     for (long long c = set; c < all; c += kSets) {
+      __syncwarp();                            // the slot that the next copies fill has been read
       copy_next();
       copies_wait<kSlots - 1>();
-      const uint8_t* q = raw_ptr + get * kSlot + row * 16;
-      const uint2 scales = *reinterpret_cast<const uint2*>(raw_ptr + get * kSlot + 8192 + row * 8);
+      __syncwarp();
+      const uint8_t* q = raw_ptr + get * kSlot;
+      const uint2 scales = *reinterpret_cast<const uint2*>(q + 2048 + lane * 8);
+      q += lane * 64;
       if (++get == kSlots) get = 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint4 w0 = *reinterpret_cast<const uint4*>(q + h * 4096), w1 = *reinterpret_cast<const uint4*>(q + h * 4096 + 2048);
+        const int x = (lane >> 1) & 3;
+        const uint4 w0 = *reinterpret_cast<const uint4*>(q + ((2 * h ^ x) << 4));
+        const uint4 w1 = *reinterpret_cast<const uint4*>(q + (((2 * h + 1) ^ x) << 4));
         const uint32_t s4 = h ? scales.y : scales.x;
         const uint32_t f01 = e4m3x2_to_f16x2(s4 & 0xFFFFu), f23 = e4m3x2_to_f16x2(s4 >> 16);
         const uint32_t ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
@@ -287,55 +332,109 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
   decoded:
     copies_wait<0>();
   } else if (warp < kWarpMma) {
-    // Output: this warp's 32 lanes, all columns.
-    const int q = warp & 3, row = q * 32 + lane;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+    // Output: this warp's 32 lanes, all columns. First into registers as BF16, so
+    // that the accumulator is free for the next tile; then, while that is
+    // computed, 32 pairs at a time through shared memory to rows of C.
+    const int q = warp & 3;
     const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t acc_free0 = mapa_shared(acc_free, 0);
+    uint8_t* const out = smem + kOutAt + q * kOut;
+    const int align = out_align(a);
     uint32_t ph = 0;
     for (int i = 0; i < mine; ++i) {
       Tile tile;
       tile.at(table, first + i * step, weight_tiles);
       const float gs = a.globals ? a.globals[tile.expert] : 1.0f;
-      const int o = kGated ? tile.nt * 128 + rank * 64 + (row >> 1) : tile.nt * 256 + rank * 128 + row;
-      uint16_t* const c = static_cast<uint16_t*>(a.C) + o;
       wait_or_abort(acc_full, ph, a.err, abort_flag);
       ph ^= 1;
       __syncwarp();
       if (__any_sync(0xFFFFFFFFu, *abort_flag)) break;
       tc_fence_after();
-      for (int c0 = 0; c0 < tile.n; c0 += 32) {
-        const int pl = c0 + lane < tile.pairs ? a.rows[tile.p0 + c0 + lane] : -1;   // the pair of column c0 + lane
+      uint32_t packed[kMaxN / 32][kGated ? 8 : 16], next[32];
+      tmem_ld32_start(tl, next);
+#pragma unroll
+      for (int ch = 0; ch < kMaxN / 32; ++ch) {
+        if (32 * ch >= tile.n) break;
         uint32_t v[32];
-        tmem_ld32_start(tl + c0, v);
-        tmem_ld_wait(v);
-        if (c0 + 32 >= tile.n) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0 && i + 1 < mine) pair_arrive(acc_free0);
-        }
+        tmem_ld_wait(next);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = next[j];
+        if (kGated && ch + 1 < kMaxN / 32 && 32 * ch + 32 < tile.n) tmem_ld32_start(tl + 32 * ch + 32, next);
         if constexpr (kGated) {
           // Even lanes have gates and take columns 0..15, odd ones ups and 16..31.
           const bool odd = lane & 1;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float keep = __uint_as_float(odd ? v[16 + j] : v[j]), give = __uint_as_float(odd ? v[j] : v[16 + j]);
-            const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-            const float gate = (odd ? got : keep) * gs, up = (odd ? keep : got) * gs;
-            const int p = __shfl_sync(0xFFFFFFFFu, pl, odd ? 16 + j : j);
-            if (static_cast<unsigned>(p) < static_cast<unsigned>(R) && o < outs)
-              c[static_cast<long long>(p) * a.ldc] = f32_to_bf16_rn(gate / (1.0f + expf(-gate)) * up);
+          for (int j = 0; j < 8; ++j) {
+            float y[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int c = 2 * j + e;
+              const float keep = __uint_as_float(odd ? v[16 + c] : v[c]), give = __uint_as_float(odd ? v[c] : v[16 + c]);
+              const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+              y[e] = silu((odd ? got : keep) * gs) * ((odd ? keep : got) * gs);
+            }
+            packed[ch][j] = pack_bf16(y[0], y[1]);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int p = __shfl_sync(0xFFFFFFFFu, pl, j);
-            if (static_cast<unsigned>(p) < static_cast<unsigned>(R) && o < outs)
-              c[static_cast<long long>(p) * a.ldc] = f32_to_bf16_rn(__uint_as_float(v[j]) * gs);
+          for (int j = 0; j < 16; ++j) packed[ch][j] = pack_bf16(__uint_as_float(v[2 * j]) * gs, __uint_as_float(v[2 * j + 1]) * gs);
+          if (ch + 1 < kMaxN / 32 && 32 * ch + 32 < tile.n) tmem_ld32_start(tl + 32 * ch + 32, next);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && i + 1 < mine) pair_arrive(acc_free0);
+
+      // Outputs o0 .. of this warp: 32, or (gated) 16.
+      const int o0 = kGated ? tile.nt * 128 + rank * 64 + q * 16 : tile.nt * 256 + rank * 128 + q * 32;
+      const int left = outs - o0;
+#pragma unroll
+      for (int ch = 0; ch < kMaxN / 32; ++ch) {
+        if (32 * ch >= tile.n) break;
+        const int pl = 32 * ch + lane < tile.pairs ? a.rows[tile.p0 + 32 * ch + lane] : -1;   // the pair of column 32 ch + lane
+        __syncwarp();
+        if constexpr (kGated) {                // 32 pairs of 32 bytes, piece h of pair c at h ^ (c / 4 mod 2)
+          const int n = lane >> 1;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int c = 2 * j + (lane & 1) * 16;
+            *reinterpret_cast<uint16_t*>(out + c * 32 + (((n >> 3) ^ ((c >> 2) & 1)) << 4) + (n & 7) * 2) = static_cast<uint16_t>(packed[ch][j]);
+            *reinterpret_cast<uint16_t*>(out + (c + 1) * 32 + (((n >> 3) ^ ((c >> 2) & 1)) << 4) + (n & 7) * 2) =
+                static_cast<uint16_t>(packed[ch][j] >> 16);
+          }
+          __syncwarp();
+          const int p = pl;
+          if (static_cast<unsigned>(p) < static_cast<unsigned>(R)) {
+            uint16_t* const c = static_cast<uint16_t*>(a.C) + static_cast<long long>(p) * a.ldc + o0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              store_piece(c + 8 * h, out + lane * 32 + ((h ^ ((lane >> 2) & 1)) << 4), left - 8 * h, align);
+          }
+        } else {                               // 32 pairs of 64 bytes, piece h of pair c at h ^ (c / 2 mod 4)
+          const int n = lane;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            uint8_t* const d = out + 2 * j * 64 + (((n >> 3) ^ (j & 3)) << 4) + (n & 7) * 2;
+            *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(packed[ch][j]);
+            *reinterpret_cast<uint16_t*>(d + 64) = static_cast<uint16_t>(packed[ch][j] >> 16);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int c = 8 * k + (lane >> 2), h = lane & 3;
+            const int p = __shfl_sync(0xFFFFFFFFu, pl, c);
+            if (static_cast<unsigned>(p) < static_cast<unsigned>(R))
+              store_piece(static_cast<uint16_t*>(a.C) + static_cast<long long>(p) * a.ldc + o0 + 8 * h,
+                          out + c * 64 + ((h ^ ((c >> 1) & 3)) << 4), left - 8 * h, align);
           }
         }
       }
     }
-  } else if (warp == kWarpRelay) {
+  } else if (warp < kWarpMma + 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+  }
+  if (warp == kWarpRelay) {
     // Announces the stages whose activations have landed. The fence that makes
     // them visible to the MMAs waits for all copies of the thread that makes it,
     // so a feeder would wait for those of later stages.
@@ -349,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
       if (lane == 0) pair_arrive(full0 + 8 * s);
       if (++s == kS) s = 0, ph ^= 1;
     }
-  } else if (rank == 0) {
+  } else if (warp == kWarpMma && rank == 0) {
     // A wait that follows MMAs costs the tensor core a pause, so the next stage is
     // looked up before this one's MMAs are issued.
     const uint64_t bd0 = tile_desc(sb);
