@@ -41,6 +41,8 @@
 #ifndef WQP_H
 #define WQP_H
 
+#include <stddef.h>
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -349,7 +351,14 @@ int expert_order(const int* ids, int* rows, int* offsets, int R, int E, void* st
  * others, but which kernel runs (and with it the order of the sums) on T * slots
  * and E. */
 int w4a16_experts(const void* A, int lda, const void* W, const void* scales, const float* global_scales, const int* rows,
-                  const int* offsets, void* C, int ldc, int T, int slots, int E, int N, int K, int gated, void* stream);
+                  const int* offsets, void* C, int ldc, int T, int slots, int E, int N, int K, int gated, void* workspace,
+                  void* stream);
+
+/* Bytes of workspace (device memory, 16-byte aligned, the call's own until it
+ * has run) that w4a16_experts can use for these sizes, 0 where it has no use for
+ * any (or refuses them). Without it (NULL) the call computes the same
+ * products by a slower kernel. Host only: no CUDA call. */
+size_t w4a16_experts_workspace(int T, int slots, int E, int K);
 
 /* out[t] = residual[t] + sum_s weights[t, s] * Y[t * slots + s], over the slots
  * whose id is in 0..E-1 (other rows of Y are not read), in FP32 and in the

@@ -28,8 +28,8 @@ def L():
 #        logits ldl dtype bias ids weights T E k scoring groups top_groups best renorm scale
 ROUTE = [P[0], 64, 2, P[1], P[2], P[3], 5, 64, 6, 1, 8, 3, 2, 1, 1.0, NUL]
 ORDER = [P[0], P[1], P[2], 40, 16, NUL]
-#          A lda W scales globals rows offsets C ldc T slots E N K gated
-EXPERTS = [P[0], 256, P[1], P[2], P[3], P[4], P[5], P[6], 40, 3, 2, 8, 40, 256, 0, NUL]
+#          A lda W scales globals rows offsets C ldc T slots E N K gated workspace
+EXPERTS = [P[0], 256, P[1], P[2], P[3], P[4], P[5], P[6], 40, 3, 2, 8, 40, 256, 0, P[7], NUL]
 #          Y ldy weights ids E residual ldr out ldo dtype T slots H
 COMBINE = [P[0], 256, P[1], P[2], 8, P[3], 256, P[4], 256, 0, 3, 2, 256, NUL]
 
@@ -47,7 +47,7 @@ CASES = (
         (0, NUL, "NULL A"), (0, OFF8, "16-byte"), (1, 248, "pitch"), (1, 260, "pitch"), (2, NUL, "NULL"), (2, OFF8, "16-byte"), (3, NUL, "NULL"),
         (3, OFF8, "16-byte"), (4, OFF2, "global_scales"), (5, NUL, "rows"), (5, OFF2, "rows"), (6, NUL, "offsets"), (6, OFF1, "offsets"),
         (7, NUL, "NULL"), (7, OFF1, "2-byte"), (8, 39, "ldc"), (9, -1, "T="), (9, 1 << 30, "pairs"), (10, 0, "slots"), (10, 33, "slots"),
-        (11, 0, "E="), (11, 1025, "E="), (12, 0, "N="), (12, (1 << 24) + 1, "N="), (13, 0, "K="), (13, 192, "K="), (13, (1 << 20) + 128, "K=")]]
+        (11, 0, "E="), (11, 1025, "E="), (12, 0, "N="), (12, (1 << 24) + 1, "N="), (13, 0, "K="), (13, 192, "K="), (13, (1 << 20) + 128, "K="), (15, OFF8, "workspace")]]
     + [("expert_combine", COMBINE, *c) for c in [
         (0, NUL, "NULL Y"), (0, OFF8, "16-byte"), (1, 248, "pitch"), (1, 260, "pitch"), (2, NUL, "weights"), (2, OFF2, "weights"), (3, NUL, "ids"),
         (3, OFF2, "ids"), (4, 0, "E="), (4, 1025, "E="), (5, OFF8, "residual"), (6, 128, "residual"), (7, NUL, "out"), (7, OFF8, "out"),

@@ -62,7 +62,8 @@ EXPORTS = {
     "w8a8_gemm": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P],
     "expert_route": [_P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P],
     "expert_order": [_P, _P, _P, _I, _I, _P],
-    "w4a16_experts": [_P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P],
+    "w4a16_experts": [_P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P],
+    "w4a16_experts_workspace": [_I, _I, _I, _I],
     "expert_combine": [_P, _I, _P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _P],
     "q2_dequant": [_P, _P, _I, _I, _P],
     "w4a16_dequant": [_P, _P, _F, _P, _I, _I, _P],
@@ -104,6 +105,7 @@ def lib() -> ctypes.CDLL:
                 fn.restype = _I
             L.wqp_status_string.restype = ctypes.c_char_p
             L.wqp_last_error.restype = ctypes.c_char_p
+            L.w4a16_experts_workspace.restype = ctypes.c_size_t
             _lib = L
     return _lib
 
@@ -575,8 +577,11 @@ def w4a16_experts(A, W, scales, rows, offsets, N: int, K: int, global_scales=Non
     if gated and N % 2:
         raise ValueError(f"N={N} must be even, gate and up")
     C, ldc = _gemm_out(A, R, N // 2 if gated else N, out, stream)
-    status = (_lib or lib()).w4a16_experts(A.data_ptr(), lda, pw, ps, pg, pr, po, C.data_ptr(), ldc, T, slots, E, N, K,
-                                           1 if gated else 0, _stream(stream))
+    L = _lib or lib()
+    need = L.w4a16_experts_workspace(T, slots, E, K)
+    work = _empty((need,), torch.uint8, A.device, stream) if need else None
+    status = L.w4a16_experts(A.data_ptr(), lda, pw, ps, pg, pr, po, C.data_ptr(), ldc, T, slots, E, N, K, 1 if gated else 0,
+                             _ptr(work), _stream(stream))
     if status:
         _check(status, "w4a16_experts")
     return C

@@ -374,7 +374,8 @@ int run_order(const int* ids, int* rows, int* offsets, int R, int E, void* strea
 }
 
 int run_experts(const void* A, int lda, const void* W, const void* scales, const float* globals, const int* rows,
-                const int* offsets, void* C, int ldc, int T, int slots, int E, int N, int K, int gated, void* stream) {
+                const int* offsets, void* C, int ldc, int T, int slots, int E, int N, int K, int gated, void* workspace,
+                void* stream) {
   const char* nm = "w4a16_experts";
   int st = check_pairs(nm, T, slots, E);
   if (st != WQP_OK) return st;
@@ -390,6 +391,7 @@ int run_experts(const void* A, int lda, const void* W, const void* scales, const
   if (globals && !aligned(globals, 4)) return fail(WQP_ERR_INVALID_ARG, "%s: global_scales must be 4-byte aligned", nm);
   if ((st = check_words(nm, "rows", rows)) != WQP_OK || (st = check_words(nm, "offsets", offsets)) != WQP_OK) return st;
   const int outs = gated ? N / 2 : N;
+  if (workspace && !aligned(workspace, 16)) return fail(WQP_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", nm);
   if (static_cast<long long>(T) * slots * outs > (1ll << 38))
     return fail(WQP_ERR_INVALID_ARG, "%s: %lld rows of %d outputs are too many", nm, static_cast<long long>(T) * slots, outs);
   if (!aligned(C, 2)) return fail(WQP_ERR_INVALID_ARG, "%s: C must be 2-byte aligned", nm);
@@ -397,7 +399,7 @@ int run_experts(const void* A, int lda, const void* W, const void* scales, const
   DeviceInfo* dev = nullptr;
   if ((st = device_setup(&dev)) != WQP_OK) return st;
   const ExpertsArgs a = {A, static_cast<const uint8_t*>(W), static_cast<const uint8_t*>(scales), globals, rows, offsets, C,
-                         lda, ldc, T, slots, E, N, K, gated != 0, dev->err, dev->num_sms,
+                         lda, ldc, T, slots, E, N, K, gated != 0, workspace, nullptr, dev->err, dev->num_sms,
                          g_pdl.load(std::memory_order_relaxed) != 0};
   const cudaError_t e = launch_w4a16_experts(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? WQP_OK : cuda_fail(e, nm);
@@ -577,8 +579,14 @@ int expert_order(const int* ids, int* rows, int* offsets, int R, int E, void* st
 }
 
 int w4a16_experts(const void* A, int lda, const void* W, const void* scales, const float* global_scales, const int* rows,
-                  const int* offsets, void* C, int ldc, int T, int slots, int E, int N, int K, int gated, void* stream) {
-  return run_experts(A, lda, W, scales, global_scales, rows, offsets, C, ldc, T, slots, E, N, K, gated, stream);
+                  const int* offsets, void* C, int ldc, int T, int slots, int E, int N, int K, int gated, void* workspace,
+                  void* stream) {
+  return run_experts(A, lda, W, scales, global_scales, rows, offsets, C, ldc, T, slots, E, N, K, gated, workspace, stream);
+}
+
+size_t w4a16_experts_workspace(int T, int slots, int E, int K) {
+  if (check_pairs("w4a16_experts_workspace", T, slots, E) != WQP_OK) return 0;
+  return K < 128 || K > (1 << 20) || K % 128 != 0 ? 0 : experts_workspace(T, slots, E, K);
 }
 
 int expert_combine(const void* Y, int ldy, const float* weights, const int* ids, int E, const void* residual, int ldr,

@@ -28,29 +28,44 @@ namespace wqp {
 namespace act {
 namespace {
 
-constexpr int kS = 4;                          // stages of 128 K
-constexpr int kHalfB = 128 * 128;              // activations of half a stage: 128 rows of 64 K
-constexpr int kStageB = 2 * kHalfB;
-constexpr int kSets = 2, kSlots = 4;           // decoding sets, and stages in a set's ring
-constexpr int kSlot = 128 * 72;                // codes and scales of 128 rows x 128 K
-constexpr int kRaw = kS * kStageB, kOutAt = kRaw + kSets * kSlots * kSlot;
+constexpr int kFeeders = 4, kEpi = 4;          // warps
+constexpr int kCodes = 128 * 64, kScales = 128 * 8;   // bytes of 128 weight rows x 128 K
 constexpr int kOut = 32 * 64;                  // 32 pairs by 32 outputs of an output warp
-constexpr int kTableAt = kOutAt + 4 * kOut;
-constexpr int kFeeders = 4, kDecoders = 4 * kSets, kEpi = 4;
-constexpr int kWarpDec = kFeeders, kWarpEpi = kWarpDec + kDecoders, kWarpMma = kWarpEpi + kEpi,
-              kWarpRelay = kWarpMma + 1;
-constexpr int kThreads = (kWarpMma + 4) * 32;  // registers are shared out by four warps at a time
-// Registers: launched with 96 a thread, 480 to the five threads of one index.
-constexpr int kRegsLaunch = 96, kRegsFeed = 80, kRegsOut = 168, kRegsRest = 40;
-static_assert(kThreads == 640 && kRegsFeed + 2 * kRegsLaunch + kRegsOut + kRegsRest <= 5 * kRegsLaunch, "registers");
-constexpr int kMaxN = 256;                     // pairs of a tile
-constexpr uint32_t kColA = 256;                // tensor memory: accumulator, then kS stages of 64 columns
-static_assert(kColA + kS * 64 <= 512, "tensor memory");
 
-constexpr int many_bytes(int E) { return 1024 + kTableAt + experts::Table::bytes(E); }
-static_assert(many_bytes(kMaxExperts) <= 226 * 1024, "shared memory");
+// kHalf: FP16 operands, made from rows that half_rows_kernel has scaled, and
+// tiles of fewer pairs with more stages, for experts with few rows each.
+template <bool kHalf>
+struct Many {
+  static constexpr int kMaxN = kHalf ? 64 : 256;       // pairs of a tile
+  // Stages of 128 K: of activations in shared memory, of weights in tensor
+  // memory. From a copy's start to the MMAs that free its place it takes some
+  // 3000 clocks, many stages of a narrow tile.
+  static constexpr int kS = kHalf ? 12 : 4, kSA = kHalf ? 6 : 4;
+  static constexpr int kAcc = kHalf ? 2 : 1;           // accumulators
+  static constexpr int kHalfB = kMaxN * 64;            // activations of half a stage: kMaxN / 2 rows of 64 K
+  static constexpr int kStageB = 2 * kHalfB;
+  static constexpr int kSets = kHalf ? 3 : 2;          // decoding sets
+  static constexpr int kRing = kHalf ? 12 : 8;         // stages of packed weights
+  static constexpr int kCodesAt = kS * kStageB, kScalesAt = kCodesAt + kRing * kCodes, kOutAt = kScalesAt + kRing * kScales;
+  static constexpr int kTableAt = kOutAt + kEpi * kOut;
+  static constexpr int kWarpDec = kFeeders, kWarpEpi = kWarpDec + 4 * kSets, kWarpMma = kWarpEpi + kEpi, kWarpRelay = kWarpMma + 1,
+                       kWarpCodes = kWarpMma + 2, kWarpScales = kWarpMma + 3;
+  static constexpr int kThreads = (kWarpMma + 4) * 32; // registers are shared out by four warps at a time
+  // Registers a thread: at launch, and of each role.
+  static constexpr int kRegsLaunch = kHalf ? 80 : 96, kRegsFeed = kHalf ? 72 : 80, kRegsOut = kHalf ? 128 : 168, kRegsRest = 40;
+  static_assert(kRegsFeed + kSets * kRegsLaunch + kRegsOut + kRegsRest <= kThreads / 128 * kRegsLaunch, "registers");
+  // Tensor memory: the accumulators, then kSA stages of 64 columns.
+  static constexpr uint32_t kColA = kAcc * kMaxN;
+  static_assert(kColA + kSA * 64 <= 512 && kSA <= kS && kSA % kSets == 0 && kRing % kSets == 0, "stages");
+  static constexpr int bytes(int E) { return 1024 + kTableAt + experts::Table::bytes(E); }
+  static_assert(kTableAt + 2 * (kMaxExperts + 1) * 4 + 1024 <= 226 * 1024, "shared memory");
+};
 
-// D (+)= A * B^T, A from tensor memory, BF16, K = 16, by a pair.
+// idesc_bf16 with FP16 operands.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// D (+)= A * B^T, A from tensor memory, 16-bit operands, K = 16, by a pair.
 __device__ __forceinline__ void pair_mma_ts(uint32_t d, uint32_t a, uint64_t bd, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -92,8 +107,36 @@ __device__ __forceinline__ void pair_arrive_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// wait_or_abort with a long time limit of the wait itself: the polls of the warps
+// that wait take issue slots from those that decode.
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, unsigned* err, volatile int* abort_flag) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (int i = 0;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000)
+        : "memory");
+    if (ok) return true;
+    if ((i & 15) == 15) {
+      if (*abort_flag) return false;
+      const uint64_t t = global_ns();
+      if (!t0) t0 = t;
+      else if (t - t0 > kWaitLimitNs) break;
+    }
+  }
+  set_error(err, WQP_DEV_ERR_TIMEOUT);
+  *abort_flag = 1;
+  return false;
+}
+
 // A tile of the walk: token tiles of each expert in turn, all its weight tiles
 // one after the other.
+template <int kMaxN>
 struct Tile {
   int expert, nt, p0, pairs, n;                // pairs p0 .. p0 + pairs - 1 of the order; n: rounded up
   __device__ __forceinline__ void at(const experts::Table& table, int id, int weight_tiles) {
@@ -110,14 +153,20 @@ struct Tile {
   }
 };
 
-// Eight E2M1 codes of a word to BF16 pairs with their group's scale (f16x2),
-// exactly: the product is exact in FP16, and widened to FP32 it has nothing in
-// its lower half.
+// Eight E2M1 codes of a word with their group's scale (f16x2), exactly: the
+// product is exact in FP16, and widened to FP32 it has nothing in its lower
+// half, so that its upper is BF16.
+template <bool kHalf>
+__device__ __forceinline__ uint32_t operand(uint32_t e2m1, uint32_t s) {
+  const uint32_t h = f16op::mul_f16x2(e2m1, s);
+  return kHalf ? h : f16x2_to_bf16x2_exact(h);
+}
+template <bool kHalf>
 __device__ __forceinline__ void decode_word(uint32_t w, uint32_t s, uint32_t* r) {
-  r[0] = f16x2_to_bf16x2_exact(f16op::mul_f16x2(f16op::e2m1x2_byte<0>(w), s));
-  r[1] = f16x2_to_bf16x2_exact(f16op::mul_f16x2(f16op::e2m1x2_byte<1>(w), s));
-  r[2] = f16x2_to_bf16x2_exact(f16op::mul_f16x2(f16op::e2m1x2_byte<2>(w), s));
-  r[3] = f16x2_to_bf16x2_exact(f16op::mul_f16x2(f16op::e2m1x2_byte<3>(w), s));
+  r[0] = operand<kHalf>(f16op::e2m1x2_byte<0>(w), s);
+  r[1] = operand<kHalf>(f16op::e2m1x2_byte<1>(w), s);
+  r[2] = operand<kHalf>(f16op::e2m1x2_byte<2>(w), s);
+  r[3] = operand<kHalf>(f16op::e2m1x2_byte<3>(w), s);
 }
 
 // g * sigmoid(g), through e^-|g|, which cannot overflow: 4 roundings and two
@@ -144,37 +193,65 @@ __device__ __forceinline__ void store_piece(uint16_t* c, const uint8_t* from, in
   }
 }
 
+// The row of a stage's packed weights that lane `row` of tensor memory takes.
+// Gated: a warp's lanes 0..15 have gates (rows 0..63), 16..31 the ups of the same
+// outputs (rows 64..127).
 template <bool kGated>
-__global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
+__device__ __forceinline__ int smem_row(int row) {
+  return kGated ? (row & 16) * 4 + (row >> 5) * 16 + (row & 15) : row;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+template <bool kGated, bool kHalf>
+__global__ void __launch_bounds__(Many<kHalf>::kThreads, 1) experts_kernel(const __grid_constant__ CUtensorMap tmW, ExpertsArgs a) {
+  using L = Many<kHalf>;
+  constexpr int kS = L::kS, kSA = L::kSA, kAcc = L::kAcc, kSets = L::kSets, kRing = L::kRing, kMaxN = L::kMaxN;
   extern __shared__ uint8_t smem_raw[];
-  // full and acc_free count both CTAs' work and are used in the even CTA; empty
-  // and acc_full are told to both; landed is each CTA's own.
-  __shared__ __align__(8) uint64_t full_sh[kS], empty_sh[kS], landed_sh[kS], acc_full_sh, acc_free_sh, drained_sh;
+  // full (activations), decoded (weights) and acc_free count both CTAs' work and
+  // are used in the even CTA; done (a stage's MMAs) and acc_full are told to both;
+  // the others are each CTA's own.
+  __shared__ __align__(8) uint64_t full_sh[kS], done_sh[kS], landed_sh[kS], decoded_sh[kSA], raw_full_sh[kRing], raw_empty_sh[kRing],
+      acc_full_sh[kAcc], acc_free_sh[kAcc], drained_sh;
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
-  const uint32_t full = smem_u32(full_sh), empty = smem_u32(empty_sh), landed = smem_u32(landed_sh);
-  const uint32_t acc_full = smem_u32(&acc_full_sh), acc_free = smem_u32(&acc_free_sh), drained = smem_u32(&drained_sh);
+  const uint32_t full = smem_u32(full_sh), done = smem_u32(done_sh), landed = smem_u32(landed_sh), decoded = smem_u32(decoded_sh);
+  const uint32_t raw_full = smem_u32(raw_full_sh), raw_empty = smem_u32(raw_empty_sh);
+  const uint32_t acc_full = smem_u32(acc_full_sh), acc_free = smem_u32(acc_free_sh), drained = smem_u32(&drained_sh);
   volatile int* abort_flag = &abort_sh;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kS; ++i) {
-      mbar_init(full + 8 * i, 2 * (1 + 4));
-      mbar_init(landed + 8 * i, kFeeders * 32);
-      mbar_init(empty + 8 * i, 1);
+      mbar_init(full + 8 * i, 2);
+      mbar_init(landed + 8 * i, (kHalf ? 1 : kFeeders) * 32);
+      mbar_init(done + 8 * i, 1);
     }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_free, 2 * kEpi);
+    for (int i = 0; i < kSA; ++i) mbar_init(decoded + 8 * i, 2 * 4);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(raw_full + 8 * i, 1 + 32);
+      mbar_init(raw_empty + 8 * i, 4);
+    }
+    for (int i = 0; i < kAcc; ++i) {
+      mbar_init(acc_full + 8 * i, 1);
+      mbar_init(acc_free + 8 * i, 2 * kEpi);
+    }
     mbar_init(drained, 1);
     abort_sh = 0;
     mbar_fence_init();
   }
   __syncwarp();
   cluster_arrive_relaxed();
-  if (warp == kWarpMma) {
+  if (warp == L::kWarpMma) {
     pair_tmem_alloc(smem_u32(&tmem_sh), 512);
     tc_fence_before();
   }
@@ -182,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
   pdl_wait();
   const int R = a.T * a.slots;
   experts::Table table;                        // its barriers publish tmem_sh too
-  table.make(smem + kTableAt, a.offsets, a.E, R, [](int n) { return (n + kMaxN - 1) / kMaxN; });
+  table.make(smem + L::kTableAt, a.offsets, a.E, R, [](int n) { return (n + kMaxN - 1) / kMaxN; });
   tc_fence_after();
   cluster_wait();
   const uint32_t tmem = tmem_sh;
@@ -193,120 +270,86 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   const int mine = first < total ? (total - first + step - 1) / step : 0;   // tiles of this pair
   const int stages = a.K >> 7;                                              // of a tile
-  const uint32_t full0 = mapa_shared(full, 0);
+  const uint32_t full0 = mapa_shared(full, 0), decoded0 = mapa_shared(decoded, 0);
 
-  if (warp < kWarpDec) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFeed));
-    // Activations. Thread t copies 16-byte piece t % 16 of rows t / 16 + 8 i.
-    const int piece = threadIdx.x & 15, row0 = threadIdx.x >> 4;
-    const uint32_t dst0 = sb + (piece >> 3) * kHalfB + row0 * 128 + (((piece & 7) ^ row0) << 4);
-    int s = 0;
+  if (warp < L::kWarpDec) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRegsFeed));
+    // Activations, 16-byte pieces of rows. Wide tiles: a stage takes all four
+    // warps; narrow ones: one warp each, in turn.
+    constexpr int kTeam = kHalf ? 1 : kFeeders, kLeap = kFeeders / kTeam, kStep = 2 * kTeam;   // kStep rows a copy
+    const int member = kHalf ? lane : static_cast<int>(threadIdx.x), turn = kHalf ? warp : 0;
+    const int piece = member & 15, row0 = member >> 4;
+    const uint32_t dst0 = sb + (piece >> 3) * L::kHalfB + row0 * 128;
+    int s = turn, k = turn;                    // place and stage of the tile
     uint32_t ph = 1;
-    long long issued = 0;
+    long long issued = 0;                      // stages of this warp
     bool ok = true;
-    for (int i = 0; i < mine && ok; ++i) {
-      Tile tile;
+    for (int i = 0; i < mine && ok; ++i, k -= stages) {
+      if (k >= stages) continue;
+      Tile<L::kMaxN> tile;
       tile.at(table, first + i * step, weight_tiles);
       const int half = tile.n >> 1;            // of this CTA, a multiple of 16
-      const uint8_t* src[16];
+      constexpr int kSteps = kMaxN / 2 / kStep;
+      const uint8_t* src[kSteps];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {           // rows without a pair: any row, their columns go nowhere
-        const int r = row0 + 8 * j, c = rank * half + r;
+      for (int j = 0; j < kSteps; ++j) {       // rows without a pair: any row, their columns go nowhere
+        const int r = row0 + kStep * j, c = rank * half + r;
         const int p = r < half && c < tile.pairs ? a.rows[tile.p0 + c] : 0;
         const int t = static_cast<unsigned>(p) < static_cast<unsigned>(R) ? p / a.slots : 0;
-        src[j] = static_cast<const uint8_t*>(a.A) + static_cast<long long>(t) * a.lda * 2 + piece * 16;
+        src[j] = static_cast<const uint8_t*>(a.A) + static_cast<long long>(t) * a.lda * 2 + k * 256 + piece * 16;
       }
-      for (int k = 0; k < stages; ++k) {
-        if (issued >= kS) ok = __all_sync(0xFFFFFFFFu, wait_or_abort(empty + 8 * s, ph, a.err, abort_flag));
+      for (; k < stages; k += kLeap) {
+        if (issued >= kS / kLeap) ok = __all_sync(0xFFFFFFFFu, wait_long(done + 8 * s, ph, a.err, abort_flag));
         if (!ok) break;
+        const uint32_t dst = dst0 + s * L::kStageB;
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          if (8 * j >= half) break;
-          copy16(dst0 + s * kStageB + j * 1024, src[j]);
-          copy16(dst0 + s * kStageB + j * 1024 + 1024, src[j + 1]);
-          src[j] += 256;
-          src[j + 1] += 256;
+        for (int j = 0; j < kSteps; ++j) {
+          if (j % 4 == 0 && kStep * j >= half) break;
+          copy16(dst + j * kStep * 128 + (((piece & 7) ^ ((row0 + kStep * j) & 7)) << 4), src[j]);
+          src[j] += kLeap * 256;
         }
         copies_land(landed + 8 * s);
         ++issued;
-        if (++s == kS) s = 0, ph ^= 1;
+        s += kLeap;
+        if (s >= kS) s -= kS, ph ^= 1;
       }
     }
     copies_close();
     copies_wait<0>();
     // Every stage's MMAs are done, and told to both CTAs, before this one ends.
-    if (warp == 0) {
-      const int used = issued < kS ? static_cast<int>(issued) : kS;
-      for (int t = 0; t < used && ok; ++t) {
-        const int at = used < kS ? t : s;
-        ok = __all_sync(0xFFFFFFFFu, wait_or_abort(empty + 8 * at, used < kS ? 0u : ph, a.err, abort_flag));
-        if (used == kS && ++s == kS) s = 0, ph ^= 1;
-      }
+    for (int t = 0; t < kS / kLeap && ok; ++t) {
+      if (issued >= kS / kLeap - t) ok = __all_sync(0xFFFFFFFFu, wait_long(done + 8 * s, ph, a.err, abort_flag));
+      s += kLeap;
+      if (s >= kS) s -= kS, ph ^= 1;
     }
-  } else if (warp < kWarpEpi) {
-    // Weights. Thread: lane `row` of tensor memory.
-    const int set = (warp - kWarpDec) >> 2, row = (warp & 3) * 32 + lane;
-    // A warp's rows in a slot: 32 rows of 64 bytes, piece j of row r at j ^ (r / 2
-    // mod 4), then 32 of 8. A copy takes whole rows of 64 bytes (as 16 bytes of 32
-    // rows the copies took most of a stage's time).
-    const uint32_t raw = sb + kRaw + set * kSlots * kSlot + (warp & 3) * kSlot / 4;
-    const uint8_t* const raw_ptr = smem + kRaw + set * kSlots * kSlot + (warp & 3) * kSlot / 4;
-    const uint32_t dst_w = (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
-    const uint32_t at = tmem + kColA + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    // The next stage of this set to copy: the stages of all tiles are numbered
-    // through, and the sets take them in turn.
-    int ai = 0, ac = set;                      // tile of the pair, stage in it
-    while (ai < mine && ac >= stages) ac -= stages, ++ai;
-    int loaded = -1, put = 0;
-    const uint8_t *w[4] = {}, *sc = nullptr;
-    const auto copy_next = [&] {
-      if (ai < mine) {
-        if (loaded != ai) {
-          loaded = ai;
-          const int id = first + ai * step, t = id / weight_tiles, nt = id - t * weight_tiles;
-          const long long base = static_cast<long long>(table.expert_of(t)) * a.N;
-          const auto row_at = [&](int r) {     // the weight row of lane r of the tile; rows past the last read that one
-            return kGated ? base + min(nt * 128 + rank * 64 + (r >> 1), outs - 1) + (r & 1) * static_cast<long long>(outs)
-                          : base + min(nt * 256 + rank * 128 + r, outs - 1);
-          };
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            w[j] = a.W + row_at((warp & 3) * 32 + 8 * j + (lane >> 2)) * (a.K >> 1) + ac * 64 + (lane & 3) * 16;
-          sc = a.scales + row_at(row) * (a.K >> 4) + ac * 8;
-        }
-        const uint32_t dst = raw + put * kSlot;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          copy16(dst + j * 512 + dst_w, w[j]);
-          w[j] += kSets * 64;
-        }
-        copy8(dst + 2048 + lane * 8, sc);
-        sc += kSets * 8;
-        ac += kSets;
-        while (ai < mine && ac >= stages) ac -= stages, ++ai;
-      }
-      copies_close();
-      if (++put == kSlots) put = 0;
-    };
-#pragma unroll 1
-    for (int i = 0; i < kSlots - 1; ++i) copy_next();
+  } else if (warp < L::kWarpEpi) {
+    // Weights. A thread has a lane of tensor memory; a set of four warps takes every
+    // kSets-th stage.
+    const int set = (warp - L::kWarpDec) >> 2, row = (warp & 3) * 32 + lane;
+    // Rows of 64 bytes in the 64-byte swizzle: piece j of row r at j ^ (r / 2 mod 4).
+    const int from = smem_row<kGated>(row);
+    const uint8_t* const codes = smem + L::kCodesAt + from * 64;
+    const uint8_t* const scales_at = smem + L::kScalesAt + from * 8;
+    const uint32_t at = tmem + L::kColA + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const long long all = static_cast<long long>(mine) * stages;
-    int get = 0, s = set;
-    uint32_t ph = 1;
+    // Stage c is in slot `get` of the packed ring and goes to place sa, which the
+    // MMAs of stage c - kSA leave; theirs is barrier sd of done.
+    int get = set, sa = set, sd = set;
+    uint32_t raw_ph = 0, ph = 0;
     for (long long c = set; c < all; c += kSets) {
-      __syncwarp();                            // the slot that the next copies fill has been read
-      copy_next();
-      copies_wait<kSlots - 1>();
+      if (!__all_sync(0xFFFFFFFFu, wait_long(raw_full + 8 * get, raw_ph, a.err, abort_flag))) break;
+      const int x = (from >> 1) & 3;
+      uint4 packed[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) packed[j] = *reinterpret_cast<const uint4*>(codes + get * kCodes + ((j ^ x) << 4));
+      const uint2 scales = *reinterpret_cast<const uint2*>(scales_at + get * kScales);
       __syncwarp();
-      const uint8_t* q = raw_ptr + get * kSlot;
-      const uint2 scales = *reinterpret_cast<const uint2*>(q + 2048 + lane * 8);
-      q += lane * 64;
-      if (++get == kSlots) get = 0;
+      if (lane == 0) mbar_arrive(raw_empty + 8 * get);
+      get += kSets;
+      if (get >= kRing) get -= kRing, raw_ph ^= 1;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int x = (lane >> 1) & 3;
-        const uint4 w0 = *reinterpret_cast<const uint4*>(q + ((2 * h ^ x) << 4));
-        const uint4 w1 = *reinterpret_cast<const uint4*>(q + (((2 * h + 1) ^ x) << 4));
+        const uint4 w0 = packed[2 * h], w1 = packed[2 * h + 1];
         const uint32_t s4 = h ? scales.y : scales.x;
         const uint32_t f01 = e4m3x2_to_f16x2(s4 & 0xFFFFu), f23 = e4m3x2_to_f16x2(s4 >> 16);
         const uint32_t ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
@@ -315,44 +358,56 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
         for (int gr = 0; gr < 4; ++gr) {
           const uint32_t f = gr < 2 ? f01 : f23;
           const uint32_t sf = __byte_perm(f, f, gr & 1 ? 0x3232 : 0x1010);
-          decode_word(ww[2 * gr], sf, r + 8 * gr);
-          decode_word(ww[2 * gr + 1], sf, r + 8 * gr + 4);
+          decode_word<kHalf>(ww[2 * gr], sf, r + 8 * gr);
+          decode_word<kHalf>(ww[2 * gr + 1], sf, r + 8 * gr + 4);
         }
-        if (h == 0 && c >= kS && !__all_sync(0xFFFFFFFFu, wait_or_abort(empty + 8 * s, ph, a.err, abort_flag))) goto decoded;
+        if (h == 0 && c >= kSA && !__all_sync(0xFFFFFFFFu, wait_long(done + 8 * sd, ph, a.err, abort_flag))) goto decoding_over;
         if (h == 0) tc_fence_after();
-        tmem_st32(at + s * 64 + h * 32, r);
+        tmem_st32(at + sa * 64 + h * 32, r);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) pair_arrive_relaxed(full0 + 8 * s);
-      s += kSets;
-      if (s >= kS) s -= kS, ph ^= 1;
+      if (lane == 0) pair_arrive_relaxed(decoded0 + 8 * sa);
+      sa += kSets;
+      if (sa >= kSA) sa -= kSA;
+      if (c >= kSA) {
+        sd += kSets;
+        if (sd >= kS) sd -= kS, ph ^= 1;
+      }
     }
-  decoded:
-    copies_wait<0>();
-  } else if (warp < kWarpMma) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+  decoding_over:;
+  } else if (warp < L::kWarpMma) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kRegsOut));
     // Output: this warp's 32 lanes, all columns. First into registers as BF16, so
     // that the accumulator is free for the next tile; then, while that is
     // computed, 32 pairs at a time through shared memory to rows of C.
     const int q = warp & 3;
     const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t acc_free0 = mapa_shared(acc_free, 0);
-    uint8_t* const out = smem + kOutAt + q * kOut;
+    int slot = 0;
+    uint8_t* const out = smem + L::kOutAt + q * kOut;
     const int align = out_align(a);
     uint32_t ph = 0;
     for (int i = 0; i < mine; ++i) {
-      Tile tile;
+      Tile<L::kMaxN> tile;
       tile.at(table, first + i * step, weight_tiles);
       const float gs = a.globals ? a.globals[tile.expert] : 1.0f;
-      wait_or_abort(acc_full, ph, a.err, abort_flag);
-      ph ^= 1;
+      int pl[kMaxN / 32];                      // the pair of column 32 ch + lane, and
+      float fl[kMaxN / 32];                    // its factor
+#pragma unroll
+      for (int ch = 0; ch < kMaxN / 32; ++ch) {
+        const int c = 32 * ch + lane, p = c < tile.pairs ? a.rows[tile.p0 + c] : -1;
+        pl[ch] = static_cast<unsigned>(p) < static_cast<unsigned>(R) ? p : -1;
+        fl[ch] = kHalf && pl[ch] >= 0 ? a.row_scales[pl[ch] / a.slots] * gs : gs;
+      }
+      wait_long(acc_full + 8 * slot, ph, a.err, abort_flag);
       __syncwarp();
       if (__any_sync(0xFFFFFFFFu, *abort_flag)) break;
       tc_fence_after();
       uint32_t packed[kMaxN / 32][kGated ? 8 : 16], next[32];
-      tmem_ld32_start(tl, next);
+      const uint32_t from = tl + slot * kMaxN;
+      tmem_ld32_start(from, next);
 #pragma unroll
       for (int ch = 0; ch < kMaxN / 32; ++ch) {
         if (32 * ch >= tile.n) break;
@@ -360,10 +415,11 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
         tmem_ld_wait(next);
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = next[j];
-        if (kGated && ch + 1 < kMaxN / 32 && 32 * ch + 32 < tile.n) tmem_ld32_start(tl + 32 * ch + 32, next);
+        if (kGated && ch + 1 < kMaxN / 32 && 32 * ch + 32 < tile.n) tmem_ld32_start(from + 32 * ch + 32, next);
         if constexpr (kGated) {
-          // Even lanes have gates and take columns 0..15, odd ones ups and 16..31.
-          const bool odd = lane & 1;
+          // Lanes 0..15 have gates and take columns 0..15, the others the same outputs'
+          // ups and columns 16..31.
+          const bool odd = lane & 16;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             float y[2];
@@ -371,20 +427,26 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
             for (int e = 0; e < 2; ++e) {
               const int c = 2 * j + e;
               const float keep = __uint_as_float(odd ? v[16 + c] : v[c]), give = __uint_as_float(odd ? v[c] : v[16 + c]);
-              const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-              y[e] = silu((odd ? got : keep) * gs) * ((odd ? keep : got) * gs);
+              const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 16);
+              const float f = kHalf ? __shfl_sync(0xFFFFFFFFu, fl[ch], odd ? 16 + c : c) : gs;
+              y[e] = silu((odd ? got : keep) * f) * ((odd ? keep : got) * f);
             }
             packed[ch][j] = pack_bf16(y[0], y[1]);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) packed[ch][j] = pack_bf16(__uint_as_float(v[2 * j]) * gs, __uint_as_float(v[2 * j + 1]) * gs);
-          if (ch + 1 < kMaxN / 32 && 32 * ch + 32 < tile.n) tmem_ld32_start(tl + 32 * ch + 32, next);
+          for (int j = 0; j < 16; ++j) {
+            const float f0 = kHalf ? __shfl_sync(0xFFFFFFFFu, fl[ch], 2 * j) : gs;
+            const float f1 = kHalf ? __shfl_sync(0xFFFFFFFFu, fl[ch], 2 * j + 1) : gs;
+            packed[ch][j] = pack_bf16(__uint_as_float(v[2 * j]) * f0, __uint_as_float(v[2 * j + 1]) * f1);
+          }
+          if (ch + 1 < kMaxN / 32 && 32 * ch + 32 < tile.n) tmem_ld32_start(from + 32 * ch + 32, next);
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0 && i + 1 < mine) pair_arrive(acc_free0);
+      if (lane == 0 && i + kAcc < mine) pair_arrive(acc_free0 + 8 * slot);
+      if (++slot == kAcc) slot = 0, ph ^= 1;
 
       // Outputs o0 .. of this warp: 32, or (gated) 16.
       const int o0 = kGated ? tile.nt * 128 + rank * 64 + q * 16 : tile.nt * 256 + rank * 128 + q * 32;
@@ -392,20 +454,19 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
 #pragma unroll
       for (int ch = 0; ch < kMaxN / 32; ++ch) {
         if (32 * ch >= tile.n) break;
-        const int pl = 32 * ch + lane < tile.pairs ? a.rows[tile.p0 + 32 * ch + lane] : -1;   // the pair of column 32 ch + lane
         __syncwarp();
         if constexpr (kGated) {                // 32 pairs of 32 bytes, piece h of pair c at h ^ (c / 4 mod 2)
-          const int n = lane >> 1;
+          const int n = lane & 15;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const int c = 2 * j + (lane & 1) * 16;
+            const int c = 2 * j + (lane & 16);
             *reinterpret_cast<uint16_t*>(out + c * 32 + (((n >> 3) ^ ((c >> 2) & 1)) << 4) + (n & 7) * 2) = static_cast<uint16_t>(packed[ch][j]);
             *reinterpret_cast<uint16_t*>(out + (c + 1) * 32 + (((n >> 3) ^ ((c >> 2) & 1)) << 4) + (n & 7) * 2) =
                 static_cast<uint16_t>(packed[ch][j] >> 16);
           }
           __syncwarp();
-          const int p = pl;
-          if (static_cast<unsigned>(p) < static_cast<unsigned>(R)) {
+          const int p = pl[ch];
+          if (p >= 0) {
             uint16_t* const c = static_cast<uint16_t*>(a.C) + static_cast<long long>(p) * a.ldc + o0;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -423,18 +484,18 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int c = 8 * k + (lane >> 2), h = lane & 3;
-            const int p = __shfl_sync(0xFFFFFFFFu, pl, c);
-            if (static_cast<unsigned>(p) < static_cast<unsigned>(R))
+            const int p = __shfl_sync(0xFFFFFFFFu, pl[ch], c);
+            if (p >= 0)
               store_piece(static_cast<uint16_t*>(a.C) + static_cast<long long>(p) * a.ldc + o0 + 8 * h,
                           out + c * 64 + ((h ^ ((c >> 1) & 3)) << 4), left - 8 * h, align);
           }
         }
       }
     }
-  } else if (warp < kWarpMma + 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+  } else if (warp < L::kWarpMma + 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRegsRest));
   }
-  if (warp == kWarpRelay) {
+  if (warp == L::kWarpRelay) {
     // Announces the stages whose activations have landed. The fence that makes
     // them visible to the MMAs waits for all copies of the thread that makes it,
     // so a feeder would wait for those of later stages.
@@ -442,46 +503,103 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
     int s = 0;
     uint32_t ph = 0;
     for (long long c = 0; c < all; ++c) {
-      if (!__all_sync(0xFFFFFFFFu, wait_or_abort(landed + 8 * s, ph, a.err, abort_flag))) break;
+      if (!__all_sync(0xFFFFFFFFu, wait_long(landed + 8 * s, ph, a.err, abort_flag))) break;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) pair_arrive(full0 + 8 * s);
       if (++s == kS) s = 0, ph ^= 1;
     }
-  } else if (warp == kWarpMma && rank == 0) {
+  } else if (warp == L::kWarpCodes && elect_one()) {
+    // Packed weights: 128 rows of a tile, 64 bytes each (gated: 64 gate rows, then
+    // the 64 up rows of the same outputs).
+    int s = 0;
+    uint32_t ph = 1;
+    long long c = 0;
+    bool ok = true;
+    for (int i = 0; i < mine && ok; ++i) {
+      const int id = first + i * step, t = id / weight_tiles, nt = id - t * weight_tiles, e = table.expert_of(t);
+      const int n0 = kGated ? nt * 128 + rank * 64 : nt * 256 + rank * 128;
+      for (int k = 0; k < stages; ++k, ++c) {
+        if (c >= kRing && !(ok = wait_long(raw_empty + 8 * s, ph, a.err, abort_flag))) break;
+        mbar_arrive_expect_tx(raw_full + 8 * s, kCodes);
+        const uint32_t dst = sb + L::kCodesAt + s * kCodes;
+        tma_load_3d(dst, &tmW, k * 64, n0, e, raw_full + 8 * s);
+        if (kGated) tma_load_3d(dst + kCodes / 2, &tmW, k * 64, outs + n0, e, raw_full + 8 * s);
+        if (++s == kRing) s = 0, ph ^= 1;
+      }
+    }
+    // Every copy has been used, or (after an abort) has at least arrived.
+    for (int t = 0; t < kRing; ++t) {
+      if (c >= kRing - t && !wait_long(raw_empty + 8 * s, ph, a.err, abort_flag)) mbar_wait(raw_full + 8 * s, ph, a.err);
+      if (++s == kRing) s = 0, ph ^= 1;
+    }
+  } else if (warp == L::kWarpScales) {
+    // Their scales: 8 bytes of a row, four rows a lane; rows past the last read that one.
+    int s = 0;
+    uint32_t ph = 1;
+    long long c = 0;
+    bool ok = true;
+    const uint32_t dst = sb + L::kScalesAt + lane * 8;
+    for (int i = 0; i < mine && ok; ++i) {
+      const int id = first + i * step, t = id / weight_tiles, nt = id - t * weight_tiles;
+      const long long base = static_cast<long long>(table.expert_of(t)) * a.N;
+      const uint8_t* src[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 32 * j + lane;
+        const long long n = kGated ? min(nt * 128 + rank * 64 + (r & 63), outs - 1) + (r >> 6) * static_cast<long long>(outs)
+                                   : min(nt * 256 + rank * 128 + r, outs - 1);
+        src[j] = a.scales + (base + n) * (a.K >> 4);
+      }
+      for (int k = 0; k < stages; ++k, ++c) {
+        if (c >= kRing && !(ok = __all_sync(0xFFFFFFFFu, wait_long(raw_empty + 8 * s, ph, a.err, abort_flag)))) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          copy8(dst + s * kScales + j * 256, src[j]);
+          src[j] += 8;
+        }
+        copies_land(raw_full + 8 * s);
+        if (++s == kRing) s = 0, ph ^= 1;
+      }
+    }
+    copies_close();
+    copies_wait<0>();
+  } else if (warp == L::kWarpMma && rank == 0) {
     // A wait that follows MMAs costs the tensor core a pause, so the next stage is
     // looked up before this one's MMAs are issued.
     const uint64_t bd0 = tile_desc(sb);
-    int s = 0;
-    uint32_t ph = 0, acc_ph = 0;
+    int s = 0, sa = 0, slot = 0;
+    uint32_t ph = 0, pha = 0, acc_ph = 1;
     bool ok = true, loaded = false;
     for (int i = 0; i < mine && ok; ++i) {
-      Tile tile;
+      Tile<L::kMaxN> tile;
       tile.at(table, first + i * step, weight_tiles);
-      const uint32_t idesc = idesc_bf16(256, tile.n);
-      if (i > 0) {
-        ok = __all_sync(0xFFFFFFFFu, wait_or_abort(acc_free, acc_ph, a.err, abort_flag));
-        acc_ph ^= 1;
-      }
+      const uint32_t idesc = kHalf ? idesc_f16(256, tile.n) : idesc_bf16(256, tile.n);
+      if (i >= kAcc) ok = __all_sync(0xFFFFFFFFu, wait_long(acc_free + 8 * slot, acc_ph, a.err, abort_flag));
       for (int k = 0; k < stages && ok; ++k) {
-        if (!loaded) ok = __all_sync(0xFFFFFFFFu, wait_or_abort(full + 8 * s, ph, a.err, abort_flag));
+        if (!loaded) {
+          ok = wait_long(full + 8 * s, ph, a.err, abort_flag) && wait_long(decoded + 8 * sa, pha, a.err, abort_flag);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+        }
         if (!ok) break;
         tc_fence_after();
-        const int s1 = s + 1 == kS ? 0 : s + 1;
-        const uint32_t ph1 = s1 ? ph : ph ^ 1;
-        const bool l1 = mbar_test(full + 8 * s1, ph1);
+        const int s1 = s + 1 == kS ? 0 : s + 1, sa1 = sa + 1 == kSA ? 0 : sa + 1;
+        const uint32_t ph1 = s1 ? ph : ph ^ 1, pha1 = sa1 ? pha : pha ^ 1;
+        const bool l1 = mbar_test(full + 8 * s1, ph1) && mbar_test(decoded + 8 * sa1, pha1);
         if (elect_one()) {
-          const uint64_t bd = bd0 + s * (kStageB >> 4);
+          const uint64_t bd = bd0 + s * (L::kStageB >> 4);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            pair_mma_ts(tmem, tmem + kColA + s * 64 + 8 * j, bd + (j >> 2) * (kHalfB >> 4) + 2 * (j & 3), idesc, (k | j) ? 1u : 0u);
-          pair_commit(empty + 8 * s);
-          if (k + 1 == stages) pair_commit(acc_full);
+            pair_mma_ts(tmem + slot * kMaxN, tmem + L::kColA + sa * 64 + 8 * j, bd + (j >> 2) * (L::kHalfB >> 4) + 2 * (j & 3), idesc,
+                        (k | j) ? 1u : 0u);
+          pair_commit(done + 8 * s);
+          if (k + 1 == stages) pair_commit(acc_full + 8 * slot);
         }
         __syncwarp();
         loaded = __all_sync(0xFFFFFFFFu, l1);
-        s = s1, ph = ph1;
+        s = s1, ph = ph1, sa = sa1, pha = pha1;
       }
+      if (++slot == kAcc) slot = 0, acc_ph ^= 1;
     }
     if (elect_one()) pair_commit_own(drained);
     __syncwarp();
@@ -494,21 +612,74 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(ExpertsArgs a) {
   __syncthreads();
   cluster_arrive_relaxed();
   cluster_wait();
-  if (warp == kWarpMma) {
+  if (warp == L::kWarpMma) {
     tc_fence_after();
     pair_tmem_dealloc(tmem, 512);
   }
 }
 
-template <bool kGated>
-cudaError_t launch_experts_many_t(const ExpertsArgs& a, cudaStream_t s) {
+// Rows of BF16 [M, ldx] to FP16 [M, K], each times the power of two that puts
+// its largest magnitude in [2^14, 2^15): exact for what is at least 2^-29 of
+// that; what is smaller is off by 2^-40 of it at most. inv [M] receives the
+// inverse powers.
+constexpr int kHalfThreads = 128, kHalfHeld = 8;   // chunks of 8 elements a thread keeps between the passes
+__global__ void __launch_bounds__(kHalfThreads) half_rows_kernel(const uint16_t* X, uint16_t* Y, float* inv, int K, int ldx) {
+  __shared__ uint32_t most_sh[kHalfThreads / 32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const uint16_t* x = X + static_cast<long long>(blockIdx.x) * ldx;
+  uint16_t* y = Y + static_cast<long long>(blockIdx.x) * K;
+  const int chunks = K >> 3;
+  uint4 held[kHalfHeld];
+  uint32_t mx = 0;
+  const auto most = [&](const uint4& v) {          // BF16 magnitudes order like their bits
+    mx = __vmaxu2(__vmaxu2(mx, v.x & 0x7FFF7FFFu), __vmaxu2(v.y & 0x7FFF7FFFu, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+  };
+#pragma unroll
+  for (int i = 0; i < kHalfHeld; ++i) {
+    const int c = threadIdx.x + i * kHalfThreads;
+    held[i] = c < chunks ? *reinterpret_cast<const uint4*>(x + 8 * c) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < kHalfHeld; ++i) most(held[i]);
+  for (int c = threadIdx.x + kHalfHeld * kHalfThreads; c < chunks; c += kHalfThreads) most(*reinterpret_cast<const uint4*>(x + 8 * c));
+  mx = __reduce_max_sync(0xFFFFFFFFu, max(mx & 0xFFFFu, mx >> 16));
+  if ((threadIdx.x & 31) == 0) most_sh[threadIdx.x >> 5] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kHalfThreads / 32; ++i) mx = max(mx, most_sh[i]);
+  const int sh = min(100, max(-113, 141 - static_cast<int>(mx >> 7)));   // 2^(exponent + sh) = 2^14
+  const float scale = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+  if (threadIdx.x == 0) inv[blockIdx.x] = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+  const auto put = [&](int c, const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = f16op::f32x2_to_f16x2(bf16hi(w[i]) * scale, bf16lo(w[i]) * scale);
+    *reinterpret_cast<uint4*>(y + 8 * c) = make_uint4(h[0], h[1], h[2], h[3]);
+  };
+#pragma unroll
+  for (int i = 0; i < kHalfHeld; ++i) {
+    const int c = threadIdx.x + i * kHalfThreads;
+    if (c < chunks) put(c, held[i]);
+  }
+  for (int c = threadIdx.x + kHalfHeld * kHalfThreads; c < chunks; c += kHalfThreads) put(c, *reinterpret_cast<const uint4*>(x + 8 * c));
+}
+
+template <bool kGated, bool kHalf>
+cudaError_t launch_experts_many_t(const ExpertsArgs& a, bool pdl, cudaStream_t s) {
   static AttrLatch latch;
-  const cudaError_t e = set_smem_attrs(experts_kernel<kGated>, latch, many_bytes(kMaxExperts), true);
+  cudaError_t e = set_smem_attrs(experts_kernel<kGated, kHalf>, latch, Many<kHalf>::bytes(kMaxExperts), true);
+  CUtensorMap mw = {};
+  const uint64_t row = static_cast<uint64_t>(a.K) / 2, N = static_cast<uint64_t>(a.N);
+  if (e == cudaSuccess)
+    e = cached_map_3d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.W, {row, N, static_cast<uint64_t>(a.E)}, {row, row * N},
+                      {64, kGated ? 64 : 128, 1}, CU_TENSOR_MAP_SWIZZLE_64B);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.num_sms / 2 * 2);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = many_bytes(a.E);
+  cfg.blockDim = dim3(Many<kHalf>::kThreads);
+  cfg.dynamicSmemBytes = Many<kHalf>::bytes(a.E);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -518,15 +689,31 @@ cudaError_t launch_experts_many_t(const ExpertsArgs& a, cudaStream_t s) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = a.pdl ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, experts_kernel<kGated>, a);
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, experts_kernel<kGated, kHalf>, mw, a);
 }
 
 }  // namespace
 }  // namespace act
 
 cudaError_t launch_w4a16_experts_many(const ExpertsArgs& a, cudaStream_t s) {
-  return a.gated ? act::launch_experts_many_t<true>(a, s) : act::launch_experts_many_t<false>(a, s);
+  return a.gated ? act::launch_experts_many_t<true, false>(a, a.pdl, s) : act::launch_experts_many_t<false, false>(a, a.pdl, s);
+}
+
+// The same on rows made FP16 first, in the workspace: decoding to FP16 takes
+// under half the time. The second launch may always overlap the first, for which
+// it waits before it reads anything.
+cudaError_t launch_w4a16_experts_half(const ExpertsArgs& a, cudaStream_t s) {
+  ExpertsArgs h = a;
+  uint16_t* rows = static_cast<uint16_t*>(a.workspace);
+  float* inv = reinterpret_cast<float*>(rows + static_cast<size_t>(a.T) * a.K);
+  const cudaError_t e = launch(act::half_rows_kernel, dim3(a.T), dim3(act::kHalfThreads), 0, s, a.pdl,
+                               static_cast<const uint16_t*>(a.A), rows, inv, a.K, a.lda);
+  if (e != cudaSuccess) return e;
+  h.A = rows;
+  h.lda = a.K;
+  h.row_scales = inv;
+  return a.gated ? act::launch_experts_many_t<true, true>(h, true, s) : act::launch_experts_many_t<false, true>(h, true, s);
 }
 
 }  // namespace wqp

@@ -144,6 +144,8 @@ struct ExpertsArgs {
   int lda, ldc;
   int T, slots, E, N, K;
   bool gated;
+  void* workspace;      // experts_workspace() bytes, or NULL
+  const float* row_scales;   // of the workspace's rows
   unsigned* err;
   int num_sms;
   bool pdl;
@@ -167,6 +169,9 @@ cudaError_t launch_w4a16_experts(const ExpertsArgs& a, cudaStream_t s);
 cudaError_t launch_expert_combine(const CombineArgs& a, cudaStream_t s);
 // The kernel on the 5th-generation tensor core (gemm_experts_many.cu).
 cudaError_t launch_w4a16_experts_many(const ExpertsArgs& a, cudaStream_t s);
+cudaError_t launch_w4a16_experts_half(const ExpertsArgs& a, cudaStream_t s);
+// Bytes of workspace with which launch_w4a16_experts is fastest.
+size_t experts_workspace(int T, int slots, int E, int K);
 
 cudaError_t launch_w4_quantize(const QuantArgs& a, cudaStream_t s);
 cudaError_t launch_a8_quantize(const QuantArgs& a, cudaStream_t s);
