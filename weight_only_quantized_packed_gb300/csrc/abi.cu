@@ -391,6 +391,7 @@ int run_experts(const void* A, int lda, const void* W, const void* scales, const
   if (globals && !aligned(globals, 4)) return fail(WQP_ERR_INVALID_ARG, "%s: global_scales must be 4-byte aligned", nm);
   if ((st = check_words(nm, "rows", rows)) != WQP_OK || (st = check_words(nm, "offsets", offsets)) != WQP_OK) return st;
   const int outs = gated ? N / 2 : N;
+  if (!workspace && experts_workspace(T, slots, E, K)) return fail(WQP_ERR_INVALID_ARG, "%s: NULL workspace", nm);
   if (workspace && !aligned(workspace, 16)) return fail(WQP_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", nm);
   if (static_cast<long long>(T) * slots * outs > (1ll << 38))
     return fail(WQP_ERR_INVALID_ARG, "%s: %lld rows of %d outputs are too many", nm, static_cast<long long>(T) * slots, outs);

@@ -269,16 +269,16 @@ cudaError_t launch_few_t(const ExpertsArgs& a, cudaStream_t s) {
 
 #ifndef RF
 #define RF 4
-#define RH 100
+#define RH 64
 #endif
 size_t experts_workspace(int T, int slots, int E, int K) {
   const long long pairs = static_cast<long long>(T) * slots;
-  return pairs > RF * E && pairs <= RH * E ? static_cast<size_t>(T) * (static_cast<size_t>(K) * 2 + 4) : 0;
+  return pairs > RF * E ? static_cast<size_t>(T) * (static_cast<size_t>(K) * 2 + 4) : 0;
 }
 
 cudaError_t launch_w4a16_experts(const ExpertsArgs& a, cudaStream_t s) {
-  if (static_cast<long long>(a.T) * a.slots > RF * a.E)
-    return a.workspace && experts_workspace(a.T, a.slots, a.E, a.K) ? launch_w4a16_experts_half(a, s) : launch_w4a16_experts_many(a, s);
+  const long long pairs = static_cast<long long>(a.T) * a.slots;
+  if (pairs > RF * a.E) return launch_w4a16_experts_many(a, pairs > RH * a.E, s);
   return a.gated ? launch_few_t<1, true>(a, s) : launch_few_t<1, false>(a, s);
 }
 

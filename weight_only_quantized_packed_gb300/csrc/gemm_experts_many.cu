@@ -32,31 +32,31 @@ constexpr int kFeeders = 4, kEpi = 4;          // warps
 constexpr int kCodes = 128 * 64, kScales = 128 * 8;   // bytes of 128 weight rows x 128 K
 constexpr int kOut = 32 * 64;                  // 32 pairs by 32 outputs of an output warp
 
-// kHalf: FP16 operands, made from rows that half_rows_kernel has scaled, and
-// tiles of fewer pairs with more stages, for experts with few rows each.
-template <bool kHalf>
+// Wide tiles (up to 192 pairs) for many rows an expert, narrow ones (up to 64) with
+// deeper rings and two accumulators for few.
+template <bool kWide>
 struct Many {
-  static constexpr int kMaxN = kHalf ? 64 : 256;       // pairs of a tile
+  static constexpr int kMaxN = kWide ? 192 : 64;       // pairs of a tile
   // Stages of 128 K: of activations in shared memory, of weights in tensor
   // memory. From a copy's start to the MMAs that free its place it takes some
   // 3000 clocks, many stages of a narrow tile.
-  static constexpr int kS = kHalf ? 12 : 4, kSA = kHalf ? 6 : 4;
-  static constexpr int kAcc = kHalf ? 2 : 1;           // accumulators
+  static constexpr int kS = kWide ? 5 : 12, kSA = kWide ? 5 : 6;
+  static constexpr int kAcc = kWide ? 1 : 2;           // accumulators
   static constexpr int kHalfB = kMaxN * 64;            // activations of half a stage: kMaxN / 2 rows of 64 K
   static constexpr int kStageB = 2 * kHalfB;
-  static constexpr int kSets = kHalf ? 3 : 2;          // decoding sets
-  static constexpr int kRing = kHalf ? 12 : 8;         // stages of packed weights
+  static constexpr int kSets = 3;                      // decoding sets
+  static constexpr int kRing = kWide ? 8 : 12;         // stages of packed weights
   static constexpr int kCodesAt = kS * kStageB, kScalesAt = kCodesAt + kRing * kCodes, kOutAt = kScalesAt + kRing * kScales;
   static constexpr int kTableAt = kOutAt + kEpi * kOut;
   static constexpr int kWarpDec = kFeeders, kWarpEpi = kWarpDec + 4 * kSets, kWarpMma = kWarpEpi + kEpi, kWarpRelay = kWarpMma + 1,
                        kWarpCodes = kWarpMma + 2, kWarpScales = kWarpMma + 3;
   static constexpr int kThreads = (kWarpMma + 4) * 32; // registers are shared out by four warps at a time
   // Registers a thread: at launch, and of each role.
-  static constexpr int kRegsLaunch = kHalf ? 80 : 96, kRegsFeed = kHalf ? 72 : 80, kRegsOut = kHalf ? 128 : 168, kRegsRest = 40;
+  static constexpr int kRegsLaunch = 80, kRegsFeed = 64, kRegsOut = 136, kRegsRest = 40;
   static_assert(kRegsFeed + kSets * kRegsLaunch + kRegsOut + kRegsRest <= kThreads / 128 * kRegsLaunch, "registers");
   // Tensor memory: the accumulators, then kSA stages of 64 columns.
   static constexpr uint32_t kColA = kAcc * kMaxN;
-  static_assert(kColA + kSA * 64 <= 512 && kSA <= kS && kSA % kSets == 0 && kRing % kSets == 0, "stages");
+  static_assert(kColA + kSA * 64 <= 512 && kSA <= kS && kSets <= kSA && kSets <= kRing, "stages");
   static constexpr int bytes(int E) { return 1024 + kTableAt + experts::Table::bytes(E); }
   static_assert(kTableAt + 2 * (kMaxExperts + 1) * 4 + 1024 <= 226 * 1024, "shared memory");
 };
@@ -153,20 +153,12 @@ struct Tile {
   }
 };
 
-// Eight E2M1 codes of a word with their group's scale (f16x2), exactly: the
-// product is exact in FP16, and widened to FP32 it has nothing in its lower
-// half, so that its upper is BF16.
-template <bool kHalf>
-__device__ __forceinline__ uint32_t operand(uint32_t e2m1, uint32_t s) {
-  const uint32_t h = f16op::mul_f16x2(e2m1, s);
-  return kHalf ? h : f16x2_to_bf16x2_exact(h);
-}
-template <bool kHalf>
+// Eight E2M1 codes of a word with their group's scale (f16x2), exactly.
 __device__ __forceinline__ void decode_word(uint32_t w, uint32_t s, uint32_t* r) {
-  r[0] = operand<kHalf>(f16op::e2m1x2_byte<0>(w), s);
-  r[1] = operand<kHalf>(f16op::e2m1x2_byte<1>(w), s);
-  r[2] = operand<kHalf>(f16op::e2m1x2_byte<2>(w), s);
-  r[3] = operand<kHalf>(f16op::e2m1x2_byte<3>(w), s);
+  r[0] = f16op::mul_f16x2(f16op::e2m1x2_byte<0>(w), s);
+  r[1] = f16op::mul_f16x2(f16op::e2m1x2_byte<1>(w), s);
+  r[2] = f16op::mul_f16x2(f16op::e2m1x2_byte<2>(w), s);
+  r[3] = f16op::mul_f16x2(f16op::e2m1x2_byte<3>(w), s);
 }
 
 // g * sigmoid(g), through e^-|g|, which cannot overflow: 4 roundings and two
@@ -209,9 +201,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-template <bool kGated, bool kHalf>
-__global__ void __launch_bounds__(Many<kHalf>::kThreads, 1) experts_kernel(const __grid_constant__ CUtensorMap tmW, ExpertsArgs a) {
-  using L = Many<kHalf>;
+template <bool kGated, bool kWide>
+__global__ void __launch_bounds__(Many<kWide>::kThreads, 1) experts_kernel(const __grid_constant__ CUtensorMap tmW, ExpertsArgs a) {
+  using L = Many<kWide>;
   constexpr int kS = L::kS, kSA = L::kSA, kAcc = L::kAcc, kSets = L::kSets, kRing = L::kRing, kMaxN = L::kMaxN;
   extern __shared__ uint8_t smem_raw[];
   // full (activations), decoded (weights) and acc_free count both CTAs' work and
@@ -233,7 +225,7 @@ __global__ void __launch_bounds__(Many<kHalf>::kThreads, 1) experts_kernel(const
   if (threadIdx.x == 0) {
     for (int i = 0; i < kS; ++i) {
       mbar_init(full + 8 * i, 2);
-      mbar_init(landed + 8 * i, (kHalf ? 1 : kFeeders) * 32);
+      mbar_init(landed + 8 * i, (kWide ? kFeeders : 1) * 32);
       mbar_init(done + 8 * i, 1);
     }
     for (int i = 0; i < kSA; ++i) mbar_init(decoded + 8 * i, 2 * 4);
@@ -276,8 +268,8 @@ __global__ void __launch_bounds__(Many<kHalf>::kThreads, 1) experts_kernel(const
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRegsFeed));
     // Activations, 16-byte pieces of rows. Wide tiles: a stage takes all four
     // warps; narrow ones: one warp each, in turn.
-    constexpr int kTeam = kHalf ? 1 : kFeeders, kLeap = kFeeders / kTeam, kStep = 2 * kTeam;   // kStep rows a copy
-    const int member = kHalf ? lane : static_cast<int>(threadIdx.x), turn = kHalf ? warp : 0;
+    constexpr int kTeam = kWide ? kFeeders : 1, kLeap = kFeeders / kTeam, kStep = 2 * kTeam;   // kStep rows a copy
+    const int member = kWide ? static_cast<int>(threadIdx.x) : lane, turn = kWide ? 0 : warp;
     const int piece = member & 15, row0 = member >> 4;
     const uint32_t dst0 = sb + (piece >> 3) * L::kHalfB + row0 * 128;
     int s = turn, k = turn;                    // place and stage of the tile
@@ -335,6 +327,8 @@ __global__ void __launch_bounds__(Many<kHalf>::kThreads, 1) experts_kernel(const
     // Stage c is in slot `get` of the packed ring and goes to place sa, which the
     // MMAs of stage c - kSA leave; theirs is barrier sd of done.
     int get = set, sa = set, sd = set;
+    while (sd < kSA) sd += kSets;
+    sd -= kSA;
     uint32_t raw_ph = 0, ph = 0;
     for (long long c = set; c < all; c += kSets) {
       if (!__all_sync(0xFFFFFFFFu, wait_long(raw_full + 8 * get, raw_ph, a.err, abort_flag))) break;
@@ -358,8 +352,8 @@ __global__ void __launch_bounds__(Many<kHalf>::kThreads, 1) experts_kernel(const
         for (int gr = 0; gr < 4; ++gr) {
           const uint32_t f = gr < 2 ? f01 : f23;
           const uint32_t sf = __byte_perm(f, f, gr & 1 ? 0x3232 : 0x1010);
-          decode_word<kHalf>(ww[2 * gr], sf, r + 8 * gr);
-          decode_word<kHalf>(ww[2 * gr + 1], sf, r + 8 * gr + 4);
+          decode_word(ww[2 * gr], sf, r + 8 * gr);
+          decode_word(ww[2 * gr + 1], sf, r + 8 * gr + 4);
         }
         if (h == 0 && c >= kSA && !__all_sync(0xFFFFFFFFu, wait_long(done + 8 * sd, ph, a.err, abort_flag))) goto decoding_over;
         if (h == 0) tc_fence_after();
@@ -399,7 +393,7 @@ __global__ void __launch_bounds__(Many<kHalf>::kThreads, 1) experts_kernel(const
       for (int ch = 0; ch < kMaxN / 32; ++ch) {
         const int c = 32 * ch + lane, p = c < tile.pairs ? a.rows[tile.p0 + c] : -1;
         pl[ch] = static_cast<unsigned>(p) < static_cast<unsigned>(R) ? p : -1;
-        fl[ch] = kHalf && pl[ch] >= 0 ? a.row_scales[pl[ch] / a.slots] * gs : gs;
+        fl[ch] = pl[ch] >= 0 ? a.row_scales[pl[ch] / a.slots] * gs : gs;
       }
       wait_long(acc_full + 8 * slot, ph, a.err, abort_flag);
       __syncwarp();
@@ -428,7 +422,7 @@ __global__ void __launch_bounds__(Many<kHalf>::kThreads, 1) experts_kernel(const
               const int c = 2 * j + e;
               const float keep = __uint_as_float(odd ? v[16 + c] : v[c]), give = __uint_as_float(odd ? v[c] : v[16 + c]);
               const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 16);
-              const float f = kHalf ? __shfl_sync(0xFFFFFFFFu, fl[ch], odd ? 16 + c : c) : gs;
+              const float f = __shfl_sync(0xFFFFFFFFu, fl[ch], odd ? 16 + c : c);
               y[e] = silu((odd ? got : keep) * f) * ((odd ? keep : got) * f);
             }
             packed[ch][j] = pack_bf16(y[0], y[1]);
@@ -436,8 +430,8 @@ __global__ void __launch_bounds__(Many<kHalf>::kThreads, 1) experts_kernel(const
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float f0 = kHalf ? __shfl_sync(0xFFFFFFFFu, fl[ch], 2 * j) : gs;
-            const float f1 = kHalf ? __shfl_sync(0xFFFFFFFFu, fl[ch], 2 * j + 1) : gs;
+            const float f0 = __shfl_sync(0xFFFFFFFFu, fl[ch], 2 * j);
+            const float f1 = __shfl_sync(0xFFFFFFFFu, fl[ch], 2 * j + 1);
             packed[ch][j] = pack_bf16(__uint_as_float(v[2 * j]) * f0, __uint_as_float(v[2 * j + 1]) * f1);
           }
           if (ch + 1 < kMaxN / 32 && 32 * ch + 32 < tile.n) tmem_ld32_start(from + 32 * ch + 32, next);
@@ -566,44 +560,39 @@ __global__ void __launch_bounds__(Many<kHalf>::kThreads, 1) experts_kernel(const
     copies_wait<0>();
   } else if (warp == L::kWarpMma && rank == 0) {
     // A wait that follows MMAs costs the tensor core a pause, so the next stage is
-    // looked up before this one's MMAs are issued.
-    const uint64_t bd0 = tile_desc(sb);
-    int s = 0, sa = 0, slot = 0;
-    uint32_t ph = 0, pha = 0, acc_ph = 1;
-    bool ok = true, loaded = false;
-    for (int i = 0; i < mine && ok; ++i) {
-      Tile<L::kMaxN> tile;
-      tile.at(table, first + i * step, weight_tiles);
-      const uint32_t idesc = kHalf ? idesc_f16(256, tile.n) : idesc_bf16(256, tile.n);
-      if (i >= kAcc) ok = __all_sync(0xFFFFFFFFu, wait_long(acc_free + 8 * slot, acc_ph, a.err, abort_flag));
-      for (int k = 0; k < stages && ok; ++k) {
-        if (!loaded) {
-          ok = wait_long(full + 8 * s, ph, a.err, abort_flag) && wait_long(decoded + 8 * sa, pha, a.err, abort_flag);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-        }
-        if (!ok) break;
-        tc_fence_after();
-        const int s1 = s + 1 == kS ? 0 : s + 1, sa1 = sa + 1 == kSA ? 0 : sa + 1;
-        const uint32_t ph1 = s1 ? ph : ph ^ 1, pha1 = sa1 ? pha : pha ^ 1;
-        const bool l1 = mbar_test(full + 8 * s1, ph1) && mbar_test(decoded + 8 * sa1, pha1);
-        if (elect_one()) {
+    // looked up before this one's MMAs are issued. All by one thread: the warp's
+    // own steps between stages took longer than a narrow stage's MMAs.
+    if (elect_one()) {
+      const uint64_t bd0 = tile_desc(sb);
+      int s = 0, sa = 0, slot = 0;
+      uint32_t ph = 0, pha = 0, acc_ph = 1;
+      bool ok = true, loaded = false;
+      for (int i = 0; i < mine && ok; ++i) {
+        Tile<L::kMaxN> tile;
+        tile.at(table, first + i * step, weight_tiles);
+        const uint32_t idesc = idesc_f16(256, tile.n), acc = tmem + slot * kMaxN;
+        if (i >= kAcc) ok = wait_long(acc_free + 8 * slot, acc_ph, a.err, abort_flag);
+        for (int k = 0; k < stages && ok; ++k) {
+          if (!loaded) ok = wait_long(full + 8 * s, ph, a.err, abort_flag) && wait_long(decoded + 8 * sa, pha, a.err, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const int s1 = s + 1 == kS ? 0 : s + 1, sa1 = sa + 1 == kSA ? 0 : sa + 1;
+          const uint32_t ph1 = s1 ? ph : ph ^ 1, pha1 = sa1 ? pha : pha ^ 1;
+          loaded = mbar_test(full + 8 * s1, ph1) && mbar_test(decoded + 8 * sa1, pha1);
           const uint64_t bd = bd0 + s * (L::kStageB >> 4);
+          const uint32_t at = tmem + L::kColA + sa * 64;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            pair_mma_ts(tmem + slot * kMaxN, tmem + L::kColA + sa * 64 + 8 * j, bd + (j >> 2) * (L::kHalfB >> 4) + 2 * (j & 3), idesc,
-                        (k | j) ? 1u : 0u);
+            pair_mma_ts(acc, at + 8 * j, bd + (j >> 2) * (L::kHalfB >> 4) + 2 * (j & 3), idesc, (k | j) ? 1u : 0u);
           pair_commit(done + 8 * s);
           if (k + 1 == stages) pair_commit(acc_full + 8 * slot);
+          s = s1, ph = ph1, sa = sa1, pha = pha1;
         }
-        __syncwarp();
-        loaded = __all_sync(0xFFFFFFFFu, l1);
-        s = s1, ph = ph1, sa = sa1, pha = pha1;
+        if (++slot == kAcc) slot = 0, acc_ph ^= 1;
       }
-      if (++slot == kAcc) slot = 0, acc_ph ^= 1;
+      pair_commit_own(drained);
+      mbar_wait(drained, 0, a.err);
     }
-    if (elect_one()) pair_commit_own(drained);
-    __syncwarp();
-    mbar_wait(drained, 0, a.err);
   }
   // Nothing of the pair is on its way any more, and both are done with the
   // pair's tensor memory.
@@ -666,10 +655,10 @@ __global__ void __launch_bounds__(kHalfThreads) half_rows_kernel(const uint16_t*
   for (int c = threadIdx.x + kHalfHeld * kHalfThreads; c < chunks; c += kHalfThreads) put(c, *reinterpret_cast<const uint4*>(x + 8 * c));
 }
 
-template <bool kGated, bool kHalf>
+template <bool kGated, bool kWide>
 cudaError_t launch_experts_many_t(const ExpertsArgs& a, bool pdl, cudaStream_t s) {
   static AttrLatch latch;
-  cudaError_t e = set_smem_attrs(experts_kernel<kGated, kHalf>, latch, Many<kHalf>::bytes(kMaxExperts), true);
+  cudaError_t e = set_smem_attrs(experts_kernel<kGated, kWide>, latch, Many<kWide>::bytes(kMaxExperts), true);
   CUtensorMap mw = {};
   const uint64_t row = static_cast<uint64_t>(a.K) / 2, N = static_cast<uint64_t>(a.N);
   if (e == cudaSuccess)
@@ -678,8 +667,8 @@ cudaError_t launch_experts_many_t(const ExpertsArgs& a, bool pdl, cudaStream_t s
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.num_sms / 2 * 2);
-  cfg.blockDim = dim3(Many<kHalf>::kThreads);
-  cfg.dynamicSmemBytes = Many<kHalf>::bytes(a.E);
+  cfg.blockDim = dim3(Many<kWide>::kThreads);
+  cfg.dynamicSmemBytes = Many<kWide>::bytes(a.E);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -690,20 +679,17 @@ cudaError_t launch_experts_many_t(const ExpertsArgs& a, bool pdl, cudaStream_t s
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, experts_kernel<kGated, kHalf>, mw, a);
+  return cudaLaunchKernelEx(&cfg, experts_kernel<kGated, kWide>, mw, a);
 }
 
 }  // namespace
 }  // namespace act
 
-cudaError_t launch_w4a16_experts_many(const ExpertsArgs& a, cudaStream_t s) {
-  return a.gated ? act::launch_experts_many_t<true, false>(a, a.pdl, s) : act::launch_experts_many_t<false, false>(a, a.pdl, s);
-}
-
-// The same on rows made FP16 first, in the workspace: decoding to FP16 takes
-// under half the time. The second launch may always overlap the first, for which
-// it waits before it reads anything.
-cudaError_t launch_w4a16_experts_half(const ExpertsArgs& a, cudaStream_t s) {
+// Two launches: the rows to FP16, in the workspace (decoding to BF16 took more
+// than twice the time), and the products. The second may always overlap the first,
+// for which it waits before it reads anything.
+template <bool kWide>
+cudaError_t launch_many(const ExpertsArgs& a, cudaStream_t s) {
   ExpertsArgs h = a;
   uint16_t* rows = static_cast<uint16_t*>(a.workspace);
   float* inv = reinterpret_cast<float*>(rows + static_cast<size_t>(a.T) * a.K);
@@ -713,7 +699,11 @@ cudaError_t launch_w4a16_experts_half(const ExpertsArgs& a, cudaStream_t s) {
   h.A = rows;
   h.lda = a.K;
   h.row_scales = inv;
-  return a.gated ? act::launch_experts_many_t<true, true>(h, true, s) : act::launch_experts_many_t<false, true>(h, true, s);
+  return a.gated ? act::launch_experts_many_t<true, kWide>(h, true, s) : act::launch_experts_many_t<false, kWide>(h, true, s);
+}
+
+cudaError_t launch_w4a16_experts_many(const ExpertsArgs& a, bool wide, cudaStream_t s) {
+  return wide ? launch_many<true>(a, s) : launch_many<false>(a, s);
 }
 
 }  // namespace wqp

@@ -144,7 +144,7 @@ struct ExpertsArgs {
   int lda, ldc;
   int T, slots, E, N, K;
   bool gated;
-  void* workspace;      // experts_workspace() bytes, or NULL
+  void* workspace;      // experts_workspace() bytes
   const float* row_scales;   // of the workspace's rows
   unsigned* err;
   int num_sms;
@@ -168,9 +168,8 @@ cudaError_t launch_expert_order(const OrderArgs& a, cudaStream_t s);
 cudaError_t launch_w4a16_experts(const ExpertsArgs& a, cudaStream_t s);
 cudaError_t launch_expert_combine(const CombineArgs& a, cudaStream_t s);
 // The kernel on the 5th-generation tensor core (gemm_experts_many.cu).
-cudaError_t launch_w4a16_experts_many(const ExpertsArgs& a, cudaStream_t s);
-cudaError_t launch_w4a16_experts_half(const ExpertsArgs& a, cudaStream_t s);
-// Bytes of workspace with which launch_w4a16_experts is fastest.
+cudaError_t launch_w4a16_experts_many(const ExpertsArgs& a, bool wide, cudaStream_t s);
+// Bytes of workspace that launch_w4a16_experts needs.
 size_t experts_workspace(int T, int slots, int E, int K);
 
 cudaError_t launch_w4_quantize(const QuantArgs& a, cudaStream_t s);
