@@ -273,7 +273,7 @@ cudaError_t launch_few_t(const ExpertsArgs& a, cudaStream_t s) {
 #endif
 size_t experts_workspace(int T, int slots, int E, int K) {
   const long long pairs = static_cast<long long>(T) * slots;
-  return pairs > RF * E ? static_cast<size_t>(T) * (static_cast<size_t>(K) * 2 + 4) : 0;
+  return pairs > RF * E ? static_cast<size_t>(pairs) * (static_cast<size_t>(K) * 2 + 4) : 0;
 }
 
 cudaError_t launch_w4a16_experts(const ExpertsArgs& a, cudaStream_t s) {

@@ -28,35 +28,33 @@ namespace wqp {
 namespace act {
 namespace {
 
-constexpr int kFeeders = 4, kEpi = 4;          // warps
+constexpr int kEpi = 4;                        // output warps
 constexpr int kCodes = 128 * 64, kScales = 128 * 8;   // bytes of 128 weight rows x 128 K
 constexpr int kOut = 32 * 64;                  // 32 pairs by 32 outputs of an output warp
 
 // Wide tiles (up to 192 pairs) for many rows an expert, narrow ones (up to 64) with
-// deeper rings and two accumulators for few.
+// two accumulators for few.
 template <bool kWide>
 struct Many {
   static constexpr int kMaxN = kWide ? 192 : 64;       // pairs of a tile
-  // Stages of 128 K: of activations in shared memory, of weights in tensor
-  // memory. From a copy's start to the MMAs that free its place it takes some
-  // 3000 clocks, many stages of a narrow tile.
-  static constexpr int kS = kWide ? 5 : 12, kSA = kWide ? 5 : 6;
+  static constexpr int kBox = kWide ? 32 : 16;         // rows of activations a copy
+  static constexpr int kS = kWide ? 5 : 6;             // stages of 128 K
   static constexpr int kAcc = kWide ? 1 : 2;           // accumulators
   static constexpr int kHalfB = kMaxN * 64;            // activations of half a stage: kMaxN / 2 rows of 64 K
   static constexpr int kStageB = 2 * kHalfB;
   static constexpr int kSets = 3;                      // decoding sets
-  static constexpr int kRing = kWide ? 8 : 12;         // stages of packed weights
+  static constexpr int kRing = kWide ? 8 : 15;         // stages of packed weights
   static constexpr int kCodesAt = kS * kStageB, kScalesAt = kCodesAt + kRing * kCodes, kOutAt = kScalesAt + kRing * kScales;
   static constexpr int kTableAt = kOutAt + kEpi * kOut;
-  static constexpr int kWarpDec = kFeeders, kWarpEpi = kWarpDec + 4 * kSets, kWarpMma = kWarpEpi + kEpi, kWarpRelay = kWarpMma + 1,
-                       kWarpCodes = kWarpMma + 2, kWarpScales = kWarpMma + 3;
+  static constexpr int kWarpEpi = 4 * kSets, kWarpMma = kWarpEpi + kEpi, kWarpRows = kWarpMma + 1, kWarpCodes = kWarpMma + 2,
+                       kWarpScales = kWarpMma + 3;
   static constexpr int kThreads = (kWarpMma + 4) * 32; // registers are shared out by four warps at a time
-  // Registers a thread: at launch, and of each role.
-  static constexpr int kRegsLaunch = 80, kRegsFeed = 64, kRegsOut = 136, kRegsRest = 40;
-  static_assert(kRegsFeed + kSets * kRegsLaunch + kRegsOut + kRegsRest <= kThreads / 128 * kRegsLaunch, "registers");
-  // Tensor memory: the accumulators, then kSA stages of 64 columns.
+  // Registers a thread: at launch (and decoding), of the output's and of the rest.
+  static constexpr int kRegsLaunch = 96, kRegsOut = 152, kRegsRest = 40;
+  static_assert(kSets * kRegsLaunch + kRegsOut + kRegsRest <= kThreads / 128 * kRegsLaunch, "registers");
+  // Tensor memory: the accumulators, then kS stages of 64 columns.
   static constexpr uint32_t kColA = kAcc * kMaxN;
-  static_assert(kColA + kSA * 64 <= 512 && kSA <= kS && kSets <= kSA && kSets <= kRing, "stages");
+  static_assert(kColA + kS * 64 <= 512 && kSets <= kS && kSets <= kRing, "stages");
   static constexpr int bytes(int E) { return 1024 + kTableAt + experts::Table::bytes(E); }
   static_assert(kTableAt + 2 * (kMaxExperts + 1) * 4 + 1024 <= 226 * 1024, "shared memory");
 };
@@ -84,9 +82,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
       "r"(r[31])
       : "memory");
-}
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
@@ -202,33 +197,31 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 }
 
 template <bool kGated, bool kWide>
-__global__ void __launch_bounds__(Many<kWide>::kThreads, 1) experts_kernel(const __grid_constant__ CUtensorMap tmW, ExpertsArgs a) {
+__global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
+    experts_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW, ExpertsArgs a) {
   using L = Many<kWide>;
-  constexpr int kS = L::kS, kSA = L::kSA, kAcc = L::kAcc, kSets = L::kSets, kRing = L::kRing, kMaxN = L::kMaxN;
+  constexpr int kS = L::kS, kAcc = L::kAcc, kSets = L::kSets, kRing = L::kRing, kMaxN = L::kMaxN;
   extern __shared__ uint8_t smem_raw[];
-  // full (activations), decoded (weights) and acc_free count both CTAs' work and
-  // are used in the even CTA; done (a stage's MMAs) and acc_full are told to both;
-  // the others are each CTA's own.
-  __shared__ __align__(8) uint64_t full_sh[kS], done_sh[kS], landed_sh[kS], decoded_sh[kSA], raw_full_sh[kRing], raw_empty_sh[kRing],
-      acc_full_sh[kAcc], acc_free_sh[kAcc], drained_sh;
+  // full (a stage's activations and decoded weights) and acc_free count both CTAs'
+  // work and are used in the even CTA; done (a stage's MMAs) and acc_full are told
+  // to both; raw_full and raw_empty are each CTA's own.
+  __shared__ __align__(8) uint64_t full_sh[kS], done_sh[kS], raw_full_sh[kRing], raw_empty_sh[kRing], acc_full_sh[kAcc], acc_free_sh[kAcc],
+      drained_sh;
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
-  const uint32_t full = smem_u32(full_sh), done = smem_u32(done_sh), landed = smem_u32(landed_sh), decoded = smem_u32(decoded_sh);
-  const uint32_t raw_full = smem_u32(raw_full_sh), raw_empty = smem_u32(raw_empty_sh);
+  const uint32_t full = smem_u32(full_sh), done = smem_u32(done_sh), raw_full = smem_u32(raw_full_sh), raw_empty = smem_u32(raw_empty_sh);
   const uint32_t acc_full = smem_u32(acc_full_sh), acc_free = smem_u32(acc_free_sh), drained = smem_u32(&drained_sh);
   volatile int* abort_flag = &abort_sh;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kS; ++i) {
-      mbar_init(full + 8 * i, 2);
-      mbar_init(landed + 8 * i, (kWide ? kFeeders : 1) * 32);
+      mbar_init(full + 8 * i, 2 * (1 + 4));
       mbar_init(done + 8 * i, 1);
     }
-    for (int i = 0; i < kSA; ++i) mbar_init(decoded + 8 * i, 2 * 4);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(raw_full + 8 * i, 1 + 32);
       mbar_init(raw_empty + 8 * i, 4);
@@ -262,74 +255,21 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1) experts_kernel(const
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   const int mine = first < total ? (total - first + step - 1) / step : 0;   // tiles of this pair
   const int stages = a.K >> 7;                                              // of a tile
-  const uint32_t full0 = mapa_shared(full, 0), decoded0 = mapa_shared(decoded, 0);
+  const uint32_t full0 = mapa_shared(full, 0);
 
-  if (warp < L::kWarpDec) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRegsFeed));
-    // Activations, 16-byte pieces of rows. Wide tiles: a stage takes all four
-    // warps; narrow ones: one warp each, in turn.
-    constexpr int kTeam = kWide ? kFeeders : 1, kLeap = kFeeders / kTeam, kStep = 2 * kTeam;   // kStep rows a copy
-    const int member = kWide ? static_cast<int>(threadIdx.x) : lane, turn = kWide ? 0 : warp;
-    const int piece = member & 15, row0 = member >> 4;
-    const uint32_t dst0 = sb + (piece >> 3) * L::kHalfB + row0 * 128;
-    int s = turn, k = turn;                    // place and stage of the tile
-    uint32_t ph = 1;
-    long long issued = 0;                      // stages of this warp
-    bool ok = true;
-    for (int i = 0; i < mine && ok; ++i, k -= stages) {
-      if (k >= stages) continue;
-      Tile<L::kMaxN> tile;
-      tile.at(table, first + i * step, weight_tiles);
-      const int half = tile.n >> 1;            // of this CTA, a multiple of 16
-      constexpr int kSteps = kMaxN / 2 / kStep;
-      const uint8_t* src[kSteps];
-#pragma unroll
-      for (int j = 0; j < kSteps; ++j) {       // rows without a pair: any row, their columns go nowhere
-        const int r = row0 + kStep * j, c = rank * half + r;
-        const int p = r < half && c < tile.pairs ? a.rows[tile.p0 + c] : 0;
-        const int t = static_cast<unsigned>(p) < static_cast<unsigned>(R) ? p / a.slots : 0;
-        src[j] = static_cast<const uint8_t*>(a.A) + static_cast<long long>(t) * a.lda * 2 + k * 256 + piece * 16;
-      }
-      for (; k < stages; k += kLeap) {
-        if (issued >= kS / kLeap) ok = __all_sync(0xFFFFFFFFu, wait_long(done + 8 * s, ph, a.err, abort_flag));
-        if (!ok) break;
-        const uint32_t dst = dst0 + s * L::kStageB;
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
-          if (j % 4 == 0 && kStep * j >= half) break;
-          copy16(dst + j * kStep * 128 + (((piece & 7) ^ ((row0 + kStep * j) & 7)) << 4), src[j]);
-          src[j] += kLeap * 256;
-        }
-        copies_land(landed + 8 * s);
-        ++issued;
-        s += kLeap;
-        if (s >= kS) s -= kS, ph ^= 1;
-      }
-    }
-    copies_close();
-    copies_wait<0>();
-    // Every stage's MMAs are done, and told to both CTAs, before this one ends.
-    for (int t = 0; t < kS / kLeap && ok; ++t) {
-      if (issued >= kS / kLeap - t) ok = __all_sync(0xFFFFFFFFu, wait_long(done + 8 * s, ph, a.err, abort_flag));
-      s += kLeap;
-      if (s >= kS) s -= kS, ph ^= 1;
-    }
-  } else if (warp < L::kWarpEpi) {
+  if (warp < L::kWarpEpi) {
     // Weights. A thread has a lane of tensor memory; a set of four warps takes every
     // kSets-th stage.
-    const int set = (warp - L::kWarpDec) >> 2, row = (warp & 3) * 32 + lane;
+    const int set = warp >> 2, row = (warp & 3) * 32 + lane;
     // Rows of 64 bytes in the 64-byte swizzle: piece j of row r at j ^ (r / 2 mod 4).
     const int from = smem_row<kGated>(row);
     const uint8_t* const codes = smem + L::kCodesAt + from * 64;
     const uint8_t* const scales_at = smem + L::kScalesAt + from * 8;
     const uint32_t at = tmem + L::kColA + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const long long all = static_cast<long long>(mine) * stages;
-    // Stage c is in slot `get` of the packed ring and goes to place sa, which the
-    // MMAs of stage c - kSA leave; theirs is barrier sd of done.
-    int get = set, sa = set, sd = set;
-    while (sd < kSA) sd += kSets;
-    sd -= kSA;
-    uint32_t raw_ph = 0, ph = 0;
+    // Stage c is in slot `get` of the packed ring and goes to place s.
+    int get = set, s = set;
+    uint32_t raw_ph = 0, ph = 1;
     for (long long c = set; c < all; c += kSets) {
       if (!__all_sync(0xFFFFFFFFu, wait_long(raw_full + 8 * get, raw_ph, a.err, abort_flag))) break;
       const int x = (from >> 1) & 3;
@@ -355,20 +295,16 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1) experts_kernel(const
           decode_word(ww[2 * gr], sf, r + 8 * gr);
           decode_word(ww[2 * gr + 1], sf, r + 8 * gr + 4);
         }
-        if (h == 0 && c >= kSA && !__all_sync(0xFFFFFFFFu, wait_long(done + 8 * sd, ph, a.err, abort_flag))) goto decoding_over;
+        if (h == 0 && c >= kS && !__all_sync(0xFFFFFFFFu, wait_long(done + 8 * s, ph, a.err, abort_flag))) goto decoding_over;
         if (h == 0) tc_fence_after();
-        tmem_st32(at + sa * 64 + h * 32, r);
+        tmem_st32(at + s * 64 + h * 32, r);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) pair_arrive_relaxed(decoded0 + 8 * sa);
-      sa += kSets;
-      if (sa >= kSA) sa -= kSA;
-      if (c >= kSA) {
-        sd += kSets;
-        if (sd >= kS) sd -= kS, ph ^= 1;
-      }
+      if (lane == 0) pair_arrive_relaxed(full0 + 8 * s);
+      s += kSets;
+      if (s >= kS) s -= kS, ph ^= 1;
     }
   decoding_over:;
   } else if (warp < L::kWarpMma) {
@@ -393,7 +329,7 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1) experts_kernel(const
       for (int ch = 0; ch < kMaxN / 32; ++ch) {
         const int c = 32 * ch + lane, p = c < tile.pairs ? a.rows[tile.p0 + c] : -1;
         pl[ch] = static_cast<unsigned>(p) < static_cast<unsigned>(R) ? p : -1;
-        fl[ch] = pl[ch] >= 0 ? a.row_scales[pl[ch] / a.slots] * gs : gs;
+        fl[ch] = pl[ch] >= 0 ? a.row_scales[tile.p0 + c] * gs : gs;
       }
       wait_long(acc_full + 8 * slot, ph, a.err, abort_flag);
       __syncwarp();
@@ -489,18 +425,33 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1) experts_kernel(const
   } else if (warp < L::kWarpMma + 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRegsRest));
   }
-  if (warp == L::kWarpRelay) {
-    // Announces the stages whose activations have landed. The fence that makes
-    // them visible to the MMAs waits for all copies of the thread that makes it,
-    // so a feeder would wait for those of later stages.
-    const long long all = static_cast<long long>(mine) * stages;
+  if (warp == L::kWarpRows && elect_one()) {
+    // Activations: this CTA's half of the tile's rows, kBox at a time (more of them
+    // than the tile has: their columns go nowhere), in two tiles of 64 K.
     int s = 0;
-    uint32_t ph = 0;
-    for (long long c = 0; c < all; ++c) {
-      if (!__all_sync(0xFFFFFFFFu, wait_long(landed + 8 * s, ph, a.err, abort_flag))) break;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) pair_arrive(full0 + 8 * s);
+    uint32_t ph = 1;
+    long long c = 0;
+    bool ok = true;
+    for (int i = 0; i < mine && ok; ++i) {
+      Tile<L::kMaxN> tile;
+      tile.at(table, first + i * step, weight_tiles);
+      const int half = tile.n >> 1, row0 = tile.p0 + rank * half, boxes = (half + L::kBox - 1) / L::kBox;
+      for (int k = 0; k < stages; ++k, ++c) {
+        if (c >= kS && !(ok = wait_long(done + 8 * s, ph, a.err, abort_flag))) break;
+        // The even CTA's barrier takes both CTAs' bytes; each announces its own.
+        pair_arrive_expect_tx(full0 + 8 * s, boxes * L::kBox * 256);
+        const uint32_t dst = sb + s * L::kStageB;
+        for (int b = 0; b < boxes; ++b) {
+          pair_tma_load_2d(dst + b * L::kBox * 128, &tmA, k * 128, row0 + b * L::kBox, full0 + 8 * s);
+          pair_tma_load_2d(dst + L::kHalfB + b * L::kBox * 128, &tmA, k * 128 + 64, row0 + b * L::kBox, full0 + 8 * s);
+        }
+        if (++s == kS) s = 0, ph ^= 1;
+      }
+    }
+    // Every stage's MMAs are done, and told to both CTAs, before this one ends; or
+    // (after an abort) its copies have at least arrived.
+    for (int t = 0; t < kS; ++t) {
+      if (c >= kS - t && !wait_long(done + 8 * s, ph, a.err, abort_flag) && rank == 0) mbar_wait(full + 8 * s, ph, a.err);
       if (++s == kS) s = 0, ph ^= 1;
     }
   } else if (warp == L::kWarpCodes && elect_one()) {
@@ -564,8 +515,8 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1) experts_kernel(const
     // own steps between stages took longer than a narrow stage's MMAs.
     if (elect_one()) {
       const uint64_t bd0 = tile_desc(sb);
-      int s = 0, sa = 0, slot = 0;
-      uint32_t ph = 0, pha = 0, acc_ph = 1;
+      int s = 0, slot = 0;
+      uint32_t ph = 0, acc_ph = 1;
       bool ok = true, loaded = false;
       for (int i = 0; i < mine && ok; ++i) {
         Tile<L::kMaxN> tile;
@@ -573,20 +524,20 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1) experts_kernel(const
         const uint32_t idesc = idesc_f16(256, tile.n), acc = tmem + slot * kMaxN;
         if (i >= kAcc) ok = wait_long(acc_free + 8 * slot, acc_ph, a.err, abort_flag);
         for (int k = 0; k < stages && ok; ++k) {
-          if (!loaded) ok = wait_long(full + 8 * s, ph, a.err, abort_flag) && wait_long(decoded + 8 * sa, pha, a.err, abort_flag);
+          if (!loaded) ok = wait_long(full + 8 * s, ph, a.err, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          const int s1 = s + 1 == kS ? 0 : s + 1, sa1 = sa + 1 == kSA ? 0 : sa + 1;
-          const uint32_t ph1 = s1 ? ph : ph ^ 1, pha1 = sa1 ? pha : pha ^ 1;
-          loaded = mbar_test(full + 8 * s1, ph1) && mbar_test(decoded + 8 * sa1, pha1);
+          const int s1 = s + 1 == kS ? 0 : s + 1;
+          const uint32_t ph1 = s1 ? ph : ph ^ 1;
+          loaded = mbar_test(full + 8 * s1, ph1);
           const uint64_t bd = bd0 + s * (L::kStageB >> 4);
-          const uint32_t at = tmem + L::kColA + sa * 64;
+          const uint32_t at = tmem + L::kColA + s * 64;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             pair_mma_ts(acc, at + 8 * j, bd + (j >> 2) * (L::kHalfB >> 4) + 2 * (j & 3), idesc, (k | j) ? 1u : 0u);
           pair_commit(done + 8 * s);
           if (k + 1 == stages) pair_commit(acc_full + 8 * slot);
-          s = s1, ph = ph1, sa = sa1, pha = pha1;
+          s = s1, ph = ph1;
         }
         if (++slot == kAcc) slot = 0, acc_ph ^= 1;
       }
@@ -607,16 +558,21 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1) experts_kernel(const
   }
 }
 
-// Rows of BF16 [M, ldx] to FP16 [M, K], each times the power of two that puts
-// its largest magnitude in [2^14, 2^15): exact for what is at least 2^-29 of
-// that; what is smaller is off by 2^-40 of it at most. inv [M] receives the
-// inverse powers.
+// The rows of X (BF16) in the order of the pairs, as FP16 [R, K], each times the
+// power of two that puts its largest magnitude in [2^14, 2^15): exact for what is
+// at least 2^-29 of that; what is smaller is off by 2^-40 of it at most. inv [R]
+// receives the inverse powers. In that order a tile's rows are consecutive, and
+// few threads copy them (gathered by the kernel itself, through asynchronous
+// copies, they took four warps, and their latency every third stage).
 constexpr int kHalfThreads = 128, kHalfHeld = 8;   // chunks of 8 elements a thread keeps between the passes
-__global__ void __launch_bounds__(kHalfThreads) half_rows_kernel(const uint16_t* X, uint16_t* Y, float* inv, int K, int ldx) {
+__global__ void __launch_bounds__(kHalfThreads)
+    half_rows_kernel(const uint16_t* X, const int* rows, uint16_t* Y, float* inv, int R, int slots, int K, int ldx) {
   __shared__ uint32_t most_sh[kHalfThreads / 32];
   pdl_launch_dependents();
   pdl_wait();
-  const uint16_t* x = X + static_cast<long long>(blockIdx.x) * ldx;
+  const int p = rows[blockIdx.x];
+  if (static_cast<unsigned>(p) >= static_cast<unsigned>(R)) return;
+  const uint16_t* x = X + static_cast<long long>(p / slots) * ldx;
   uint16_t* y = Y + static_cast<long long>(blockIdx.x) * K;
   const int chunks = K >> 3;
   uint4 held[kHalfHeld];
@@ -659,8 +615,11 @@ template <bool kGated, bool kWide>
 cudaError_t launch_experts_many_t(const ExpertsArgs& a, bool pdl, cudaStream_t s) {
   static AttrLatch latch;
   cudaError_t e = set_smem_attrs(experts_kernel<kGated, kWide>, latch, Many<kWide>::bytes(kMaxExperts), true);
-  CUtensorMap mw = {};
+  CUtensorMap ma = {}, mw = {};
   const uint64_t row = static_cast<uint64_t>(a.K) / 2, N = static_cast<uint64_t>(a.N);
+  if (e == cudaSuccess)
+    e = make_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.A, a.K, static_cast<uint64_t>(a.T) * a.slots, static_cast<uint64_t>(a.K) * 2, 64,
+                    Many<kWide>::kBox, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e == cudaSuccess)
     e = cached_map_3d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.W, {row, N, static_cast<uint64_t>(a.E)}, {row, row * N},
                       {64, kGated ? 64 : 128, 1}, CU_TENSOR_MAP_SWIZZLE_64B);
@@ -679,7 +638,7 @@ cudaError_t launch_experts_many_t(const ExpertsArgs& a, bool pdl, cudaStream_t s
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, experts_kernel<kGated, kWide>, mw, a);
+  return cudaLaunchKernelEx(&cfg, experts_kernel<kGated, kWide>, ma, mw, a);
 }
 
 }  // namespace
@@ -691,13 +650,13 @@ cudaError_t launch_experts_many_t(const ExpertsArgs& a, bool pdl, cudaStream_t s
 template <bool kWide>
 cudaError_t launch_many(const ExpertsArgs& a, cudaStream_t s) {
   ExpertsArgs h = a;
+  const int R = a.T * a.slots;
   uint16_t* rows = static_cast<uint16_t*>(a.workspace);
-  float* inv = reinterpret_cast<float*>(rows + static_cast<size_t>(a.T) * a.K);
-  const cudaError_t e = launch(act::half_rows_kernel, dim3(a.T), dim3(act::kHalfThreads), 0, s, a.pdl,
-                               static_cast<const uint16_t*>(a.A), rows, inv, a.K, a.lda);
+  float* inv = reinterpret_cast<float*>(rows + static_cast<size_t>(R) * a.K);
+  const cudaError_t e = launch(act::half_rows_kernel, dim3(R), dim3(act::kHalfThreads), 0, s, a.pdl, static_cast<const uint16_t*>(a.A),
+                               a.rows, rows, inv, R, a.slots, a.K, a.lda);
   if (e != cudaSuccess) return e;
   h.A = rows;
-  h.lda = a.K;
   h.row_scales = inv;
   return a.gated ? act::launch_experts_many_t<true, kWide>(h, true, s) : act::launch_experts_many_t<false, kWide>(h, true, s);
 }
