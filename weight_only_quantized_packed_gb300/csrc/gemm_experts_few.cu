@@ -269,7 +269,6 @@ cudaError_t launch_few_t(const ExpertsArgs& a, cudaStream_t s) {
 
 #ifndef RF
 #define RF 4
-#define RH 64
 #endif
 size_t experts_workspace(int T, int slots, int E, int K) {
   const long long pairs = static_cast<long long>(T) * slots;
@@ -278,7 +277,7 @@ size_t experts_workspace(int T, int slots, int E, int K) {
 
 cudaError_t launch_w4a16_experts(const ExpertsArgs& a, cudaStream_t s) {
   const long long pairs = static_cast<long long>(a.T) * a.slots;
-  if (pairs > RF * a.E) return launch_w4a16_experts_many(a, pairs > RH * a.E, s);
+  if (pairs > RF * a.E) return launch_w4a16_experts_many(a, s);
   return a.gated ? launch_few_t<1, true>(a, s) : launch_few_t<1, false>(a, s);
 }
 

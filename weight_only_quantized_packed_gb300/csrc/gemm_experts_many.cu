@@ -28,36 +28,29 @@ namespace wqp {
 namespace act {
 namespace {
 
-constexpr int kEpi = 4;                        // output warps
-constexpr int kCodes = 128 * 64, kScales = 128 * 8;   // bytes of 128 weight rows x 128 K
+constexpr int kMaxN = 192;                     // pairs of a tile
+constexpr int kBox = 32;                       // rows of activations a copy
+constexpr int kS = 5;                          // stages of 128 K
+constexpr int kHalfB = kMaxN * 64;             // activations of half a stage: kMaxN / 2 rows of 64 K
+constexpr int kStageB = 2 * kHalfB;
+constexpr int kSets = 3;                       // decoding sets
+constexpr int kRing = 4;                       // double stages of packed weights: 128 rows x 256 K
+constexpr int kCodes = 128 * 128, kScales = 128 * 16;   // bytes of one
+constexpr int kEpi = 8;                        // output warps
 constexpr int kOut = 32 * 64;                  // 32 pairs by 32 outputs of an output warp
+constexpr int kCodesAt = kS * kStageB, kScalesAt = kCodesAt + kRing * kCodes, kOutAt = kScalesAt + kRing * kScales;
+constexpr int kTableAt = kOutAt + kEpi * kOut;
+constexpr int kWarpEpi = 4 * kSets, kWarpMma = kWarpEpi + kEpi, kWarpRows = kWarpMma + 1, kWarpCodes = kWarpMma + 2, kWarpScales = kWarpMma + 3;
+constexpr int kThreads = (kWarpMma + 4) * 32;  // registers are shared out by four warps at a time
+// Registers a thread: at launch (and decoding), of the output's and of the rest.
+constexpr int kRegsLaunch = 80, kRegsOut = 96, kRegsRest = 40;
+static_assert(kSets * kRegsLaunch + kEpi / 4 * kRegsOut + kRegsRest <= kThreads / 128 * kRegsLaunch, "registers");
+// Tensor memory: the accumulator, then kS stages of 64 columns.
+constexpr uint32_t kColA = kMaxN;
+static_assert(kColA + kS * 64 <= 512 && kSets <= kRing, "stages");
 
-// Wide tiles (up to 192 pairs) for many rows an expert, narrow ones (up to 64) with
-// two accumulators for few.
-template <bool kWide>
-struct Many {
-  static constexpr int kMaxN = kWide ? 192 : 64;       // pairs of a tile
-  static constexpr int kBox = kWide ? 32 : 16;         // rows of activations a copy
-  static constexpr int kS = kWide ? 5 : 6;             // stages of 128 K
-  static constexpr int kAcc = kWide ? 1 : 2;           // accumulators
-  static constexpr int kHalfB = kMaxN * 64;            // activations of half a stage: kMaxN / 2 rows of 64 K
-  static constexpr int kStageB = 2 * kHalfB;
-  static constexpr int kSets = 3;                      // decoding sets
-  static constexpr int kRing = kWide ? 8 : 15;         // stages of packed weights
-  static constexpr int kCodesAt = kS * kStageB, kScalesAt = kCodesAt + kRing * kCodes, kOutAt = kScalesAt + kRing * kScales;
-  static constexpr int kTableAt = kOutAt + kEpi * kOut;
-  static constexpr int kWarpEpi = 4 * kSets, kWarpMma = kWarpEpi + kEpi, kWarpRows = kWarpMma + 1, kWarpCodes = kWarpMma + 2,
-                       kWarpScales = kWarpMma + 3;
-  static constexpr int kThreads = (kWarpMma + 4) * 32; // registers are shared out by four warps at a time
-  // Registers a thread: at launch (and decoding), of the output's and of the rest.
-  static constexpr int kRegsLaunch = 96, kRegsOut = 152, kRegsRest = 40;
-  static_assert(kSets * kRegsLaunch + kRegsOut + kRegsRest <= kThreads / 128 * kRegsLaunch, "registers");
-  // Tensor memory: the accumulators, then kS stages of 64 columns.
-  static constexpr uint32_t kColA = kAcc * kMaxN;
-  static_assert(kColA + kS * 64 <= 512 && kSets <= kS && kSets <= kRing, "stages");
-  static constexpr int bytes(int E) { return 1024 + kTableAt + experts::Table::bytes(E); }
-  static_assert(kTableAt + 2 * (kMaxExperts + 1) * 4 + 1024 <= 226 * 1024, "shared memory");
-};
+constexpr int many_bytes(int E) { return 1024 + kTableAt + experts::Table::bytes(E); }
+static_assert(many_bytes(kMaxExperts) <= 226 * 1024, "shared memory");
 
 // idesc_bf16 with FP16 operands.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
@@ -82,6 +75,9 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
       "r"(r[31])
       : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
@@ -131,7 +127,6 @@ __device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, unsigne
 
 // A tile of the walk: token tiles of each expert in turn, all its weight tiles
 // one after the other.
-template <int kMaxN>
 struct Tile {
   int expert, nt, p0, pairs, n;                // pairs p0 .. p0 + pairs - 1 of the order; n: rounded up
   __device__ __forceinline__ void at(const experts::Table& table, int id, int weight_tiles) {
@@ -140,10 +135,12 @@ struct Tile {
     expert = table.expert_of(t);
     const int begin = table.begin[expert], count = table.begin[expert + 1] - begin;
     const int tiles = (count + kMaxN - 1) / kMaxN;
-    const int each = ((count + tiles - 1) / tiles + 31) & ~31;   // even shares: at most kMaxN, none empty
-    const int from = (t - table.tiles[expert]) * each;
+    // Even shares of whole 32s, at most kMaxN, none empty.
+    const int whole = (count + 31) >> 5, share = t - table.tiles[expert];
+    const int from = static_cast<int>(static_cast<long long>(whole) * share / tiles) * 32;
+    const int to = static_cast<int>(static_cast<long long>(whole) * (share + 1) / tiles) * 32;
     p0 = begin + from;
-    pairs = min(count - from, each);
+    pairs = min(count, to) - from;
     n = (pairs + 31) & ~31;
   }
 };
@@ -196,17 +193,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-template <bool kGated, bool kWide>
-__global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
+template <bool kGated>
+__global__ void __launch_bounds__(kThreads, 1)
     experts_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW, ExpertsArgs a) {
-  using L = Many<kWide>;
-  constexpr int kS = L::kS, kAcc = L::kAcc, kSets = L::kSets, kRing = L::kRing, kMaxN = L::kMaxN;
   extern __shared__ uint8_t smem_raw[];
   // full (a stage's activations and decoded weights) and acc_free count both CTAs'
   // work and are used in the even CTA; done (a stage's MMAs) and acc_full are told
   // to both; raw_full and raw_empty are each CTA's own.
-  __shared__ __align__(8) uint64_t full_sh[kS], done_sh[kS], raw_full_sh[kRing], raw_empty_sh[kRing], acc_full_sh[kAcc], acc_free_sh[kAcc],
-      drained_sh;
+  __shared__ __align__(8) uint64_t full_sh[kS], done_sh[kS], raw_full_sh[kRing], raw_empty_sh[kRing], acc_full_sh, acc_free_sh, drained_sh;
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -214,7 +208,7 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
   const uint32_t full = smem_u32(full_sh), done = smem_u32(done_sh), raw_full = smem_u32(raw_full_sh), raw_empty = smem_u32(raw_empty_sh);
-  const uint32_t acc_full = smem_u32(acc_full_sh), acc_free = smem_u32(acc_free_sh), drained = smem_u32(&drained_sh);
+  const uint32_t acc_full = smem_u32(&acc_full_sh), acc_free = smem_u32(&acc_free_sh), drained = smem_u32(&drained_sh);
   volatile int* abort_flag = &abort_sh;
 
   if (threadIdx.x == 0) {
@@ -226,17 +220,15 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
       mbar_init(raw_full + 8 * i, 1 + 32);
       mbar_init(raw_empty + 8 * i, 4);
     }
-    for (int i = 0; i < kAcc; ++i) {
-      mbar_init(acc_full + 8 * i, 1);
-      mbar_init(acc_free + 8 * i, 2 * kEpi);
-    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_free, 2 * kEpi);
     mbar_init(drained, 1);
     abort_sh = 0;
     mbar_fence_init();
   }
   __syncwarp();
   cluster_arrive_relaxed();
-  if (warp == L::kWarpMma) {
+  if (warp == kWarpMma) {
     pair_tmem_alloc(smem_u32(&tmem_sh), 512);
     tc_fence_before();
   }
@@ -244,7 +236,7 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
   pdl_wait();
   const int R = a.T * a.slots;
   experts::Table table;                        // its barriers publish tmem_sh too
-  table.make(smem + L::kTableAt, a.offsets, a.E, R, [](int n) { return (n + kMaxN - 1) / kMaxN; });
+  table.make(smem + kTableAt, a.offsets, a.E, R, [](int n) { return (n + kMaxN - 1) / kMaxN; });
   tc_fence_after();
   cluster_wait();
   const uint32_t tmem = tmem_sh;
@@ -257,95 +249,109 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
   const int stages = a.K >> 7;                                              // of a tile
   const uint32_t full0 = mapa_shared(full, 0);
 
-  if (warp < L::kWarpEpi) {
+  if (warp < kWarpEpi) {
     // Weights. A thread has a lane of tensor memory; a set of four warps takes every
     // kSets-th stage.
     const int set = warp >> 2, row = (warp & 3) * 32 + lane;
-    // Rows of 64 bytes in the 64-byte swizzle: piece j of row r at j ^ (r / 2 mod 4).
+    // Rows of 128 bytes in the 128-byte swizzle: piece j of row r at j ^ (r mod 8).
     const int from = smem_row<kGated>(row);
-    const uint8_t* const codes = smem + L::kCodesAt + from * 64;
-    const uint8_t* const scales_at = smem + L::kScalesAt + from * 8;
-    const uint32_t at = tmem + L::kColA + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const long long all = static_cast<long long>(mine) * stages;
-    // Stage c is in slot `get` of the packed ring and goes to place s.
-    int get = set, s = set;
+    const uint8_t* const codes = smem + kCodesAt + from * 128;
+    const uint8_t* const scales_at = smem + kScalesAt + from * 16;
+    const uint32_t at = tmem + kColA + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    // Double stage u of tile i, number `get` of all, is for this set; its stages go
+    // to places s and s + 1.
+    const int doubles = (stages + 1) >> 1;
+    int i = 0, u = 0, get = 0, s = 0;
     uint32_t raw_ph = 0, ph = 1;
-    for (long long c = set; c < all; c += kSets) {
-      if (!__all_sync(0xFFFFFFFFu, wait_long(raw_full + 8 * get, raw_ph, a.err, abort_flag))) break;
-      const int x = (from >> 1) & 3;
-      uint4 packed[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) packed[j] = *reinterpret_cast<const uint4*>(codes + get * kCodes + ((j ^ x) << 4));
-      const uint2 scales = *reinterpret_cast<const uint2*>(scales_at + get * kScales);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(raw_empty + 8 * get);
-      get += kSets;
-      if (get >= kRing) get -= kRing, raw_ph ^= 1;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4 w0 = packed[2 * h], w1 = packed[2 * h + 1];
-        const uint32_t s4 = h ? scales.y : scales.x;
-        const uint32_t f01 = e4m3x2_to_f16x2(s4 & 0xFFFFu), f23 = e4m3x2_to_f16x2(s4 >> 16);
-        const uint32_t ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-        uint32_t r[32];
-#pragma unroll
-        for (int gr = 0; gr < 4; ++gr) {
-          const uint32_t f = gr < 2 ? f01 : f23;
-          const uint32_t sf = __byte_perm(f, f, gr & 1 ? 0x3232 : 0x1010);
-          decode_word(ww[2 * gr], sf, r + 8 * gr);
-          decode_word(ww[2 * gr + 1], sf, r + 8 * gr + 4);
-        }
-        if (h == 0 && c >= kS && !__all_sync(0xFFFFFFFFu, wait_long(done + 8 * s, ph, a.err, abort_flag))) goto decoding_over;
-        if (h == 0) tc_fence_after();
-        tmem_st32(at + s * 64 + h * 32, r);
+    const auto skip = [&](int n) {             // the next n double stages
+      for (; n > 0 && i < mine; --n) {
+        s += 2 * u + 1 < stages ? 2 : 1;
+        if (s >= kS) s -= kS, ph ^= 1;
+        if (++get == kRing) get = 0, raw_ph ^= 1;
+        if (++u == doubles) u = 0, ++i;
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) pair_arrive_relaxed(full0 + 8 * s);
-      s += kSets;
-      if (s >= kS) s -= kS, ph ^= 1;
+    };
+    skip(set);
+    while (i < mine) {
+      if (!__all_sync(0xFFFFFFFFu, wait_long(raw_full + 8 * get, raw_ph, a.err, abort_flag))) break;
+      const int x = from & 7;
+      int place = s;
+      uint32_t place_ph = ph;
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        if (2 * u + d >= stages) break;
+        uint4 packed[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) packed[j] = *reinterpret_cast<const uint4*>(codes + get * kCodes + (((4 * d + j) ^ x) << 4));
+        const uint2 scales = *reinterpret_cast<const uint2*>(scales_at + get * kScales + 8 * d);
+        if (d == 1 || 2 * u + 1 >= stages) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(raw_empty + 8 * get);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 w0 = packed[2 * h], w1 = packed[2 * h + 1];
+          const uint32_t s4 = h ? scales.y : scales.x;
+          const uint32_t f01 = e4m3x2_to_f16x2(s4 & 0xFFFFu), f23 = e4m3x2_to_f16x2(s4 >> 16);
+          const uint32_t ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+          uint32_t r[32];
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr) {
+            const uint32_t f = gr < 2 ? f01 : f23;
+            const uint32_t sf = __byte_perm(f, f, gr & 1 ? 0x3232 : 0x1010);
+            decode_word(ww[2 * gr], sf, r + 8 * gr);
+            decode_word(ww[2 * gr + 1], sf, r + 8 * gr + 4);
+          }
+          // Parity 1 of a barrier that has completed no phase counts as complete.
+          if (h == 0 && !__all_sync(0xFFFFFFFFu, wait_long(done + 8 * place, place_ph, a.err, abort_flag))) goto decoding_over;
+          if (h == 0) tc_fence_after();
+          tmem_st32(at + place * 64 + h * 32, r);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) pair_arrive_relaxed(full0 + 8 * place);
+        if (++place == kS) place = 0, place_ph ^= 1;
+      }
+      skip(kSets);
     }
   decoding_over:;
-  } else if (warp < L::kWarpMma) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kRegsOut));
+  } else if (warp < kWarpMma) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsOut));
     // Output: this warp's 32 lanes, all columns. First into registers as BF16, so
     // that the accumulator is free for the next tile; then, while that is
     // computed, 32 pairs at a time through shared memory to rows of C.
-    const int q = warp & 3;
+    const int q = warp & 3, ew = warp - kWarpEpi, h = ew >> 2;   // every second 32 columns
     const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t acc_free0 = mapa_shared(acc_free, 0);
-    int slot = 0;
-    uint8_t* const out = smem + L::kOutAt + q * kOut;
+    uint8_t* const out = smem + kOutAt + ew * kOut;
     const int align = out_align(a);
     uint32_t ph = 0;
+    constexpr int kChunks = kMaxN / 32 / 2;
     for (int i = 0; i < mine; ++i) {
-      Tile<L::kMaxN> tile;
+      Tile tile;
       tile.at(table, first + i * step, weight_tiles);
       const float gs = a.globals ? a.globals[tile.expert] : 1.0f;
-      int pl[kMaxN / 32];                      // the pair of column 32 ch + lane, and
-      float fl[kMaxN / 32];                    // its factor
+      int pl[kChunks];                         // the pair of column 32 (2 ch + h) + lane, and
+      float fl[kChunks];                       // its factor
 #pragma unroll
-      for (int ch = 0; ch < kMaxN / 32; ++ch) {
-        const int c = 32 * ch + lane, p = c < tile.pairs ? a.rows[tile.p0 + c] : -1;
+      for (int ch = 0; ch < kChunks; ++ch) {
+        const int c = 32 * (2 * ch + h) + lane, p = c < tile.pairs ? a.rows[tile.p0 + c] : -1;
         pl[ch] = static_cast<unsigned>(p) < static_cast<unsigned>(R) ? p : -1;
         fl[ch] = pl[ch] >= 0 ? a.row_scales[tile.p0 + c] * gs : gs;
       }
-      wait_long(acc_full + 8 * slot, ph, a.err, abort_flag);
+      wait_long(acc_full, ph, a.err, abort_flag);
+      ph ^= 1;
       __syncwarp();
       if (__any_sync(0xFFFFFFFFu, *abort_flag)) break;
       tc_fence_after();
-      uint32_t packed[kMaxN / 32][kGated ? 8 : 16], next[32];
-      const uint32_t from = tl + slot * kMaxN;
-      tmem_ld32_start(from, next);
+      uint32_t packed[kChunks][kGated ? 8 : 16];
 #pragma unroll
-      for (int ch = 0; ch < kMaxN / 32; ++ch) {
-        if (32 * ch >= tile.n) break;
+      for (int ch = 0; ch < kChunks; ++ch) {
+        if (32 * (2 * ch + h) >= tile.n) break;
         uint32_t v[32];
-        tmem_ld_wait(next);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = next[j];
-        if (kGated && ch + 1 < kMaxN / 32 && 32 * ch + 32 < tile.n) tmem_ld32_start(from + 32 * ch + 32, next);
+        tmem_ld32_start(tl + 32 * (2 * ch + h), v);
+        tmem_ld_wait(v);
         if constexpr (kGated) {
           // Lanes 0..15 have gates and take columns 0..15, the others the same outputs'
           // ups and columns 16..31.
@@ -366,24 +372,21 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float f0 = __shfl_sync(0xFFFFFFFFu, fl[ch], 2 * j);
-            const float f1 = __shfl_sync(0xFFFFFFFFu, fl[ch], 2 * j + 1);
+            const float f0 = __shfl_sync(0xFFFFFFFFu, fl[ch], 2 * j), f1 = __shfl_sync(0xFFFFFFFFu, fl[ch], 2 * j + 1);
             packed[ch][j] = pack_bf16(__uint_as_float(v[2 * j]) * f0, __uint_as_float(v[2 * j + 1]) * f1);
           }
-          if (ch + 1 < kMaxN / 32 && 32 * ch + 32 < tile.n) tmem_ld32_start(from + 32 * ch + 32, next);
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0 && i + kAcc < mine) pair_arrive(acc_free0 + 8 * slot);
-      if (++slot == kAcc) slot = 0, ph ^= 1;
+      if (lane == 0 && i + 1 < mine) pair_arrive(acc_free0);
 
       // Outputs o0 .. of this warp: 32, or (gated) 16.
       const int o0 = kGated ? tile.nt * 128 + rank * 64 + q * 16 : tile.nt * 256 + rank * 128 + q * 32;
       const int left = outs - o0;
 #pragma unroll
-      for (int ch = 0; ch < kMaxN / 32; ++ch) {
-        if (32 * ch >= tile.n) break;
+      for (int ch = 0; ch < kChunks; ++ch) {
+        if (32 * (2 * ch + h) >= tile.n) break;
         __syncwarp();
         if constexpr (kGated) {                // 32 pairs of 32 bytes, piece h of pair c at h ^ (c / 4 mod 2)
           const int n = lane & 15;
@@ -399,8 +402,8 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
           if (p >= 0) {
             uint16_t* const c = static_cast<uint16_t*>(a.C) + static_cast<long long>(p) * a.ldc + o0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              store_piece(c + 8 * h, out + lane * 32 + ((h ^ ((lane >> 2) & 1)) << 4), left - 8 * h, align);
+            for (int e = 0; e < 2; ++e)
+              store_piece(c + 8 * e, out + lane * 32 + ((e ^ ((lane >> 2) & 1)) << 4), left - 8 * e, align);
           }
         } else {                               // 32 pairs of 64 bytes, piece h of pair c at h ^ (c / 2 mod 4)
           const int n = lane;
@@ -413,19 +416,19 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int c = 8 * k + (lane >> 2), h = lane & 3;
+            const int c = 8 * k + (lane >> 2), e = lane & 3;
             const int p = __shfl_sync(0xFFFFFFFFu, pl[ch], c);
             if (p >= 0)
-              store_piece(static_cast<uint16_t*>(a.C) + static_cast<long long>(p) * a.ldc + o0 + 8 * h,
-                          out + c * 64 + ((h ^ ((c >> 1) & 3)) << 4), left - 8 * h, align);
+              store_piece(static_cast<uint16_t*>(a.C) + static_cast<long long>(p) * a.ldc + o0 + 8 * e,
+                          out + c * 64 + ((e ^ ((c >> 1) & 3)) << 4), left - 8 * e, align);
           }
         }
       }
     }
-  } else if (warp < L::kWarpMma + 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRegsRest));
+  } else if (warp < kWarpMma + 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
   }
-  if (warp == L::kWarpRows && elect_one()) {
+  if (warp == kWarpRows && elect_one()) {
     // Activations: this CTA's half of the tile's rows, kBox at a time (more of them
     // than the tile has: their columns go nowhere), in two tiles of 64 K.
     int s = 0;
@@ -433,17 +436,17 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
     long long c = 0;
     bool ok = true;
     for (int i = 0; i < mine && ok; ++i) {
-      Tile<L::kMaxN> tile;
+      Tile tile;
       tile.at(table, first + i * step, weight_tiles);
-      const int half = tile.n >> 1, row0 = tile.p0 + rank * half, boxes = (half + L::kBox - 1) / L::kBox;
+      const int half = tile.n >> 1, row0 = tile.p0 + rank * half, boxes = (half + kBox - 1) / kBox;
       for (int k = 0; k < stages; ++k, ++c) {
         if (c >= kS && !(ok = wait_long(done + 8 * s, ph, a.err, abort_flag))) break;
         // The even CTA's barrier takes both CTAs' bytes; each announces its own.
-        pair_arrive_expect_tx(full0 + 8 * s, boxes * L::kBox * 256);
-        const uint32_t dst = sb + s * L::kStageB;
+        pair_arrive_expect_tx(full0 + 8 * s, boxes * kBox * 256);
+        const uint32_t dst = sb + s * kStageB;
         for (int b = 0; b < boxes; ++b) {
-          pair_tma_load_2d(dst + b * L::kBox * 128, &tmA, k * 128, row0 + b * L::kBox, full0 + 8 * s);
-          pair_tma_load_2d(dst + L::kHalfB + b * L::kBox * 128, &tmA, k * 128 + 64, row0 + b * L::kBox, full0 + 8 * s);
+          pair_tma_load_2d(dst + b * kBox * 128, &tmA, k * 128, row0 + b * kBox, full0 + 8 * s);
+          pair_tma_load_2d(dst + kHalfB + b * kBox * 128, &tmA, k * 128 + 64, row0 + b * kBox, full0 + 8 * s);
         }
         if (++s == kS) s = 0, ph ^= 1;
       }
@@ -454,9 +457,9 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
       if (c >= kS - t && !wait_long(done + 8 * s, ph, a.err, abort_flag) && rank == 0) mbar_wait(full + 8 * s, ph, a.err);
       if (++s == kS) s = 0, ph ^= 1;
     }
-  } else if (warp == L::kWarpCodes && elect_one()) {
-    // Packed weights: 128 rows of a tile, 64 bytes each (gated: 64 gate rows, then
-    // the 64 up rows of the same outputs).
+  } else if (warp == kWarpCodes && elect_one()) {
+    // Packed weights: 128 rows of a tile, 128 bytes each (gated: 64 gate rows, then
+    // the 64 up rows of the same outputs; behind the end of a row: zeros).
     int s = 0;
     uint32_t ph = 1;
     long long c = 0;
@@ -464,10 +467,10 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
     for (int i = 0; i < mine && ok; ++i) {
       const int id = first + i * step, t = id / weight_tiles, nt = id - t * weight_tiles, e = table.expert_of(t);
       const int n0 = kGated ? nt * 128 + rank * 64 : nt * 256 + rank * 128;
-      for (int k = 0; k < stages; ++k, ++c) {
+      for (int k = 0; k < stages; k += 2, ++c) {
         if (c >= kRing && !(ok = wait_long(raw_empty + 8 * s, ph, a.err, abort_flag))) break;
         mbar_arrive_expect_tx(raw_full + 8 * s, kCodes);
-        const uint32_t dst = sb + L::kCodesAt + s * kCodes;
+        const uint32_t dst = sb + kCodesAt + s * kCodes;
         tma_load_3d(dst, &tmW, k * 64, n0, e, raw_full + 8 * s);
         if (kGated) tma_load_3d(dst + kCodes / 2, &tmW, k * 64, outs + n0, e, raw_full + 8 * s);
         if (++s == kRing) s = 0, ph ^= 1;
@@ -478,13 +481,15 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
       if (c >= kRing - t && !wait_long(raw_empty + 8 * s, ph, a.err, abort_flag)) mbar_wait(raw_full + 8 * s, ph, a.err);
       if (++s == kRing) s = 0, ph ^= 1;
     }
-  } else if (warp == L::kWarpScales) {
-    // Their scales: 8 bytes of a row, four rows a lane; rows past the last read that one.
+  } else if (warp == kWarpScales) {
+    // Their scales: 16 bytes of a row (8 behind an odd stage), four rows a lane; rows
+    // past the last read that one.
     int s = 0;
     uint32_t ph = 1;
     long long c = 0;
     bool ok = true;
-    const uint32_t dst = sb + L::kScalesAt + lane * 8;
+    const bool odd = stages & 1;               // rows are not multiples of 16 bytes
+    const uint32_t dst = sb + kScalesAt + lane * 16;
     for (int i = 0; i < mine && ok; ++i) {
       const int id = first + i * step, t = id / weight_tiles, nt = id - t * weight_tiles;
       const long long base = static_cast<long long>(table.expert_of(t)) * a.N;
@@ -496,12 +501,18 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
                                    : min(nt * 256 + rank * 128 + r, outs - 1);
         src[j] = a.scales + (base + n) * (a.K >> 4);
       }
-      for (int k = 0; k < stages; ++k, ++c) {
+      for (int k = 0; k < stages; k += 2, ++c) {
         if (c >= kRing && !(ok = __all_sync(0xFFFFFFFFu, wait_long(raw_empty + 8 * s, ph, a.err, abort_flag)))) break;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          copy8(dst + s * kScales + j * 256, src[j]);
-          src[j] += 8;
+          const uint32_t d = dst + s * kScales + j * 512;
+          if (!odd) {
+            copy16(d, src[j]);
+          } else {
+            copy8(d, src[j]);
+            if (k + 1 < stages) copy8(d + 8, src[j] + 8);
+          }
+          src[j] += 16;
         }
         copies_land(raw_full + 8 * s);
         if (++s == kRing) s = 0, ph ^= 1;
@@ -509,20 +520,21 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
     }
     copies_close();
     copies_wait<0>();
-  } else if (warp == L::kWarpMma && rank == 0) {
+  } else if (warp == kWarpMma && rank == 0) {
     // A wait that follows MMAs costs the tensor core a pause, so the next stage is
     // looked up before this one's MMAs are issued. All by one thread: the warp's
     // own steps between stages took longer than a narrow stage's MMAs.
     if (elect_one()) {
       const uint64_t bd0 = tile_desc(sb);
-      int s = 0, slot = 0;
+      int s = 0;
       uint32_t ph = 0, acc_ph = 1;
       bool ok = true, loaded = false;
       for (int i = 0; i < mine && ok; ++i) {
-        Tile<L::kMaxN> tile;
+        Tile tile;
         tile.at(table, first + i * step, weight_tiles);
-        const uint32_t idesc = idesc_f16(256, tile.n), acc = tmem + slot * kMaxN;
-        if (i >= kAcc) ok = wait_long(acc_free + 8 * slot, acc_ph, a.err, abort_flag);
+        const uint32_t idesc = idesc_f16(256, tile.n);
+        if (i > 0) ok = wait_long(acc_free, acc_ph, a.err, abort_flag);
+        acc_ph ^= 1;
         for (int k = 0; k < stages && ok; ++k) {
           if (!loaded) ok = wait_long(full + 8 * s, ph, a.err, abort_flag);
           if (!ok) break;
@@ -530,16 +542,15 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
           const int s1 = s + 1 == kS ? 0 : s + 1;
           const uint32_t ph1 = s1 ? ph : ph ^ 1;
           loaded = mbar_test(full + 8 * s1, ph1);
-          const uint64_t bd = bd0 + s * (L::kStageB >> 4);
-          const uint32_t at = tmem + L::kColA + s * 64;
+          const uint64_t bd = bd0 + s * (kStageB >> 4);
+          const uint32_t at = tmem + kColA + s * 64;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            pair_mma_ts(acc, at + 8 * j, bd + (j >> 2) * (L::kHalfB >> 4) + 2 * (j & 3), idesc, (k | j) ? 1u : 0u);
+            pair_mma_ts(tmem, at + 8 * j, bd + (j >> 2) * (kHalfB >> 4) + 2 * (j & 3), idesc, (k | j) ? 1u : 0u);
           pair_commit(done + 8 * s);
-          if (k + 1 == stages) pair_commit(acc_full + 8 * slot);
+          if (k + 1 == stages) pair_commit(acc_full);
           s = s1, ph = ph1;
         }
-        if (++slot == kAcc) slot = 0, acc_ph ^= 1;
       }
       pair_commit_own(drained);
       mbar_wait(drained, 0, a.err);
@@ -552,7 +563,7 @@ __global__ void __launch_bounds__(Many<kWide>::kThreads, 1)
   __syncthreads();
   cluster_arrive_relaxed();
   cluster_wait();
-  if (warp == L::kWarpMma) {
+  if (warp == kWarpMma) {
     tc_fence_after();
     pair_tmem_dealloc(tmem, 512);
   }
@@ -611,23 +622,23 @@ __global__ void __launch_bounds__(kHalfThreads)
   for (int c = threadIdx.x + kHalfHeld * kHalfThreads; c < chunks; c += kHalfThreads) put(c, *reinterpret_cast<const uint4*>(x + 8 * c));
 }
 
-template <bool kGated, bool kWide>
+template <bool kGated>
 cudaError_t launch_experts_many_t(const ExpertsArgs& a, bool pdl, cudaStream_t s) {
   static AttrLatch latch;
-  cudaError_t e = set_smem_attrs(experts_kernel<kGated, kWide>, latch, Many<kWide>::bytes(kMaxExperts), true);
+  cudaError_t e = set_smem_attrs(experts_kernel<kGated>, latch, many_bytes(kMaxExperts), true);
   CUtensorMap ma = {}, mw = {};
   const uint64_t row = static_cast<uint64_t>(a.K) / 2, N = static_cast<uint64_t>(a.N);
   if (e == cudaSuccess)
     e = make_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.A, a.K, static_cast<uint64_t>(a.T) * a.slots, static_cast<uint64_t>(a.K) * 2, 64,
-                    Many<kWide>::kBox, CU_TENSOR_MAP_SWIZZLE_128B);
+                    kBox, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e == cudaSuccess)
     e = cached_map_3d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.W, {row, N, static_cast<uint64_t>(a.E)}, {row, row * N},
-                      {64, kGated ? 64 : 128, 1}, CU_TENSOR_MAP_SWIZZLE_64B);
+                      {128, kGated ? 64 : 128, 1}, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.num_sms / 2 * 2);
-  cfg.blockDim = dim3(Many<kWide>::kThreads);
-  cfg.dynamicSmemBytes = Many<kWide>::bytes(a.E);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = many_bytes(a.E);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -638,7 +649,7 @@ cudaError_t launch_experts_many_t(const ExpertsArgs& a, bool pdl, cudaStream_t s
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, experts_kernel<kGated, kWide>, ma, mw, a);
+  return cudaLaunchKernelEx(&cfg, experts_kernel<kGated>, ma, mw, a);
 }
 
 }  // namespace
@@ -647,8 +658,7 @@ cudaError_t launch_experts_many_t(const ExpertsArgs& a, bool pdl, cudaStream_t s
 // Two launches: the rows to FP16, in the workspace (decoding to BF16 took more
 // than twice the time), and the products. The second may always overlap the first,
 // for which it waits before it reads anything.
-template <bool kWide>
-cudaError_t launch_many(const ExpertsArgs& a, cudaStream_t s) {
+cudaError_t launch_w4a16_experts_many(const ExpertsArgs& a, cudaStream_t s) {
   ExpertsArgs h = a;
   const int R = a.T * a.slots;
   uint16_t* rows = static_cast<uint16_t*>(a.workspace);
@@ -658,11 +668,7 @@ cudaError_t launch_many(const ExpertsArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   h.A = rows;
   h.row_scales = inv;
-  return a.gated ? act::launch_experts_many_t<true, kWide>(h, true, s) : act::launch_experts_many_t<false, kWide>(h, true, s);
-}
-
-cudaError_t launch_w4a16_experts_many(const ExpertsArgs& a, bool wide, cudaStream_t s) {
-  return wide ? launch_many<true>(a, s) : launch_many<false>(a, s);
+  return a.gated ? act::launch_experts_many_t<true>(h, true, s) : act::launch_experts_many_t<false>(h, true, s);
 }
 
 }  // namespace wqp

@@ -168,7 +168,7 @@ cudaError_t launch_expert_order(const OrderArgs& a, cudaStream_t s);
 cudaError_t launch_w4a16_experts(const ExpertsArgs& a, cudaStream_t s);
 cudaError_t launch_expert_combine(const CombineArgs& a, cudaStream_t s);
 // The kernel on the 5th-generation tensor core (gemm_experts_many.cu).
-cudaError_t launch_w4a16_experts_many(const ExpertsArgs& a, bool wide, cudaStream_t s);
+cudaError_t launch_w4a16_experts_many(const ExpertsArgs& a, cudaStream_t s);
 // Bytes of workspace that launch_w4a16_experts needs.
 size_t experts_workspace(int T, int slots, int E, int K);
 
