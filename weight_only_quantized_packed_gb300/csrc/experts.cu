@@ -66,6 +66,13 @@ __device__ __forceinline__ Real warp_add(Real v) {
   return v;
 }
 
+// e^x and 1 / x for the order of the experts: approximate in FP32, where the
+// bounds of route_token allow for them.
+__device__ __forceinline__ float order_exp(float x) { return __expf(x); }
+__device__ __forceinline__ double order_exp(double x) { return exp(x); }
+__device__ __forceinline__ float order_rcp(float x) { return __fdividef(1.0f, x); }
+__device__ __forceinline__ double order_rcp(double x) { return 1.0 / x; }
+
 // One token in one warp; expert i is element i / 32 of lane i % 32. `part` is
 // the warp's [E] scratch. Returns false, with nothing written, where two
 // choices that matter lie closer than the arithmetic's error: the caller then
@@ -92,16 +99,16 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
 
   // Scores where the order needs them.
   const bool by_score = !odd && (p.bias || (p.groups > 1 && p.group_best == 2));
-  Real sum = 1;
-  if (!p.sigmoid && (by_score || !p.renormalise)) {
+  Real inv = 1;                                            // of the exponentials' sum
+  if (!p.sigmoid && by_score) {
     Real e = 0;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) e += l[j] > kNone ? exp(static_cast<Real>(l[j]) - static_cast<Real>(top)) : Real(0);
-    sum = warp_add(e);
+    for (int j = 0; j < NV; ++j) e += order_exp(static_cast<Real>(l[j]) - static_cast<Real>(top));   // -inf gives 0
+    inv = Real(1) / warp_add(e);
   }
   const auto score = [&](float v) -> Real {
-    if (p.sigmoid) return Real(1) / (Real(1) + exp(-static_cast<Real>(v)));
-    return exp(static_cast<Real>(v) - static_cast<Real>(top)) / sum;
+    if (p.sigmoid) return order_rcp(Real(1) + order_exp(-static_cast<Real>(v)));
+    return order_exp(static_cast<Real>(v) - static_cast<Real>(top)) * inv;
   };
   Key key[NV];
 #pragma unroll
@@ -111,12 +118,14 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
     if (by_score && p.bias && i < p.E) c = score(l[j]) + static_cast<Real>(p.bias[i]);
     key[j] = l[j] > kNone && c > static_cast<Real>(kNone) ? key_of(c) : Key(0);
   }
-  // A bound on the error of a choice, in units of 2^-24 at 1: the exponential
-  // and its argument, the sum's and the quotient's roundings (up to 32 + 5
-  // additions on any path), each relative to a score of at most s_max.
-  const float s_max = p.sigmoid ? 0.125f : 1.0f / static_cast<float>(sum);
-  const auto close = [&](Real a, Real b, float terms) {
-    return kCheck && a - b <= Real(terms * 0x1p-23f) * (Real(64) * Real(s_max) + fabs(a) + Real(1));
+  // The error of a choice c is at most 2^-24 (64 s_max + |c|): of a sigmoid s,
+  // whose exponential is off by 4 + 3 |l| of these units, s (1 - s) times that and
+  // 3 s more, under 8; of a softmax, whose sum has up to 37 roundings on any path,
+  // at most 64 of its largest score. Two that are closer than twice that may
+  // have changed places.
+  const float s_max = p.sigmoid ? 0.125f : static_cast<float>(inv);
+  const auto close = [&](Real a, Real b, float terms, Real most) {
+    return kCheck && a - b <= Real(0x1p-23f) * (Real(64.0f * terms) * Real(s_max) + most);
   };
 
   if (p.groups > 1 && !odd) {
@@ -132,13 +141,14 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
     // `lanes` lanes to a group find its two best.
     int log = 0;
     while ((1 << log) < p.groups) ++log;
-    const int lanes = 32 >> log, g = lane / lanes;
+    const int lanes = 32 >> log, g = lane >> (5 - log);
     Real a = kNone, b = kNone;
     if (g < p.groups)
-      for (int i = lane % lanes; i < size; i += lanes) {
+      for (int i = lane & (lanes - 1); i < size; i += lanes) {
         const Real v = part[g * size + i];
-        b = v > a ? a : (v > b ? v : b);
-        a = v > a ? v : a;
+        const Real lo = v < a ? v : a;
+        a = v < a ? a : v;
+        b = b < lo ? lo : b;
       }
     for (int o = 1; o < lanes; o <<= 1) {
       const Real a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
@@ -146,81 +156,75 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
       a = a > a2 ? a : a2;
       b = lo > hi ? lo : hi;
     }
-    const Real mine = p.group_best == 2 && b > static_cast<Real>(kNone) ? a + b : a;
+    const bool pair = p.group_best == 2 && b > static_cast<Real>(kNone);
+    const Real mine = pair ? a + b : a;
     // A group stays where fewer than top_groups are better.
     int better = 0;
-    Real above = kNone;                                    // the best that goes
     for (int h = 0; h < p.groups; ++h) {
-      const Real v = __shfl_sync(kAll, mine, h * lanes);
+      const Real v = __shfl_sync(kAll, mine, h << (5 - log));
       better += v > mine || (v == mine && h < g);
     }
     const bool stays = g < p.groups && better < p.top_groups;
     const unsigned keep = __ballot_sync(kAll, stays);
-    if (kCheck && p.top_groups < p.groups && (p.bias || p.group_best == 2)) {
-      Real least = 0;
-      bool some = false;
-      for (int h = 0; h < p.groups; ++h) {
-        const Real v = __shfl_sync(kAll, mine, h * lanes);
-        if (keep >> (h * lanes) & 1) {
-          least = !some || v < least ? v : least;
-          some = true;
-        } else {
-          above = v > above ? v : above;
-        }
-      }
-      if (close(least, above, 2.0f * p.group_best)) return false;
+    if (kCheck && p.top_groups < p.groups && by_score) {
+      const auto magnitude = [](Real v) { return v > Real(-3e38f) && v < Real(3e38f) ? fabs(v) : Real(0); };
+      const Key least = ~warp_max(static_cast<Key>(stays ? ~key_of(mine) : Key(0)));
+      const Key above = warp_max(!stays && g < p.groups ? key_of(mine) : Key(0));
+      const Real most = value_of(warp_max(key_of(magnitude(a) + (pair ? magnitude(b) : Real(0)))));
+      if (above && close(value_of(least), value_of(above), 2.0f, 2 * most)) return false;
     }
+    const float per = 1.0f / static_cast<float>(size);     // i / size, for i < 1024, from (i + 1/2) / size
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int i = lane + 32 * j;
-      if (i < p.E && !(keep >> (i / size * lanes) & 1)) key[j] = 0;
+      const int i = lane + 32 * j, of = static_cast<int>((static_cast<float>(i) + 0.5f) * per);
+      if (!(keep >> (of << (5 - log) & 31) & 1)) key[j] = 0;
     }
   }
 
   // The best key of a lane's own, of equal ones the lowest index; then the
   // best of the lanes', top_k times, and once more where it has to be known
   // that the next is clearly less.
-  Key best = 0;
-  int at = 0;
+  Key best;
+  int at;                                                  // its index
   const auto own_best = [&] {
-    best = 0;
+    best = key[0];
+    at = lane;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (key[j] > best) best = key[j], at = j;
+    for (int j = 1; j < NV; ++j)
+      if (key[j] > best) best = key[j], at = 32 * j + lane;
   };
   own_best();
   int id = -1;                                             // of slot `lane`
-  float lg = kNone;
   Key prev = 0;
-  float prev_l = 0, prev_b = 0;
+  int prev_i = 0;
   const bool check = kCheck && p.bias && !odd;
-  for (int s = 0; s < p.top_k + (check ? 1 : 0); ++s) {
+  const int rounds = p.top_k + (check ? 1 : 0);
+  for (int s = 0; s < rounds; ++s) {
     const Key m = warp_max(best);
     if (!m) break;
-    const int i = __reduce_min_sync(kAll, best == m ? at * 32 + lane : 0x7FFFFFFF);
-    float li = 0;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (j == i >> 5) li = l[j];
-    li = __shfl_sync(kAll, li, i & 31);
-    if (check) {
-      const float bi = p.bias[i];
-      // Two experts of one logit and one bias tie in any arithmetic; behind the
-      // last one taken others could lie between.
-      if (s > 0 && !(s < p.top_k && li == prev_l && bi == prev_b) && close(value_of(prev), value_of(m), 2.0f)) return false;
-      prev = m, prev_l = li, prev_b = bi;
+    const int i = __reduce_min_sync(kAll, best == m ? at : 0x7FFFFFFF);
+    if (check && s > 0) {
+      const Real a = value_of(prev), b = value_of(m);
+      if (close(a, b, 1.0f, fabs(a))) {
+        // Two experts of one logit and one bias tie in any arithmetic; behind the
+        // last one taken others could lie between.
+        const bool tie = s < p.top_k && to_f32(x[i]) == to_f32(x[prev_i]) && p.bias[i] == p.bias[prev_i];
+        if (!tie) return false;
+      }
     }
-    if (s < p.top_k && lane == s) id = i, lg = li;
-    if (lane == (i & 31)) {
+    prev = m, prev_i = i;
+    if (s < p.top_k && lane == s) id = i;
+    if (at == i) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (j == i >> 5) key[j] = 0;
+        if (i == 32 * j + lane) key[j] = 0;
       own_best();
     }
   }
 
-  float w = 0.0f;
   const bool live = id >= 0;
+  const float lg = live ? to_f32(x[id]) : kNone;
+  float w = 0.0f;
   if (p.renormalise) {
     // Scores relative to the largest taken, so that they cannot all vanish: a
     // sigmoid far below 0 is an exponential too.
@@ -229,8 +233,14 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
     else w = live ? expf(lg - most) : 0.0f;
     const float total = warp_sum(w);
     w = total > 0.0f ? w / total : 0.0f;
-  } else if (live) {
-    w = static_cast<float>(score(lg));
+  } else if (p.sigmoid) {
+    w = live ? 1.0f / (1.0f + expf(-lg)) : 0.0f;
+  } else {
+    float e = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) e += l[j] > kNone ? expf(l[j] - top) : 0.0f;
+    e = warp_sum(e);
+    if (live) w = expf(lg - top) / e;
   }
   w *= p.scale;
   if (odd) w = __int_as_float(0x7FFFFFFF);
@@ -282,8 +292,8 @@ cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t s) {
 // A counting sort that keeps the pairs' order: every warp counts the ids of
 // its run of pairs, the counts of earlier warps (of earlier CTAs, through the
 // cluster's shared memory) give each warp its place in each expert's list, and
-// a second pass over the run puts the pairs there. One launch; no atomics, so
-// the result is the same every time.
+// a second pass over the run puts the pairs there. One launch; the order of the
+// counts' atomics does not show, so the result is the same every time.
 constexpr int kOrderWarps = 32;
 
 __global__ void __launch_bounds__(kOrderWarps * 32) order_kernel(const int* ids, int* rows, int* offsets, int R, int E, int run) {
@@ -294,8 +304,6 @@ __global__ void __launch_bounds__(kOrderWarps * 32) order_kernel(const int* ids,
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ranks = gridDim.x, rank = ranks > 1 ? static_cast<int>(cluster_rank()) : 0;
   pdl_launch_dependents();
-  for (int i = threadIdx.x; i < kOrderWarps * E; i += blockDim.x) count[i] = 0;
-  __syncthreads();
   pdl_wait();
   const long long first = static_cast<long long>(rank * kOrderWarps + warp) * run;
   const int begin = static_cast<int>(first < R ? first : R), end = static_cast<int>(first + run < R ? first + run : R);
@@ -309,15 +317,15 @@ __global__ void __launch_bounds__(kOrderWarps * 32) order_kernel(const int* ids,
   int kept[kKept];
 #pragma unroll
   for (int b = 0; b < kKept; ++b) kept[b] = id_at(begin + 32 * b + lane);
-  const auto count_batch = [&](int e) {
-    const unsigned same = __match_any_sync(kAll, e);
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
-  };
+  for (int i = lane; i < E; i += 32) mine[i] = 0;
+  __syncwarp();
 #pragma unroll
   for (int b = 0; b < kKept; ++b)
-    if (begin + 32 * b < end) count_batch(kept[b]);
-  for (int i = begin + 32 * kKept; i < end; i += 32) count_batch(id_at(i + lane));
+    if (kept[b] >= 0) atomicAdd(mine + kept[b], 1);
+  for (int i = begin + 32 * kKept; i < end; i += 32) {
+    const int e = id_at(i + lane);
+    if (e >= 0) atomicAdd(mine + e, 1);
+  }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     int sum = 0;
@@ -377,8 +385,16 @@ __global__ void __launch_bounds__(kOrderWarps * 32) order_kernel(const int* ids,
     }
   }
   __syncthreads();
+  // Lanes of one id from a vote on each of its bits (a match of whole values
+  // took 32 of the kernel's first 39 thousand clocks at 65536 pairs of 256).
+  const int bits = 32 - __clz(E);
   const auto place_batch = [&](int i, int e) {
-    const unsigned same = __match_any_sync(kAll, e);
+    unsigned same = kAll;
+    for (int b = 0; b < bits; ++b) {
+      const bool on = (e + 1) >> b & 1;
+      const unsigned vote = __ballot_sync(kAll, on);
+      same &= on ? vote : ~vote;
+    }
     int at = 0;
     if (e >= 0) at = mine[e];
     __syncwarp();
