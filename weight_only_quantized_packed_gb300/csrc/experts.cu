@@ -75,10 +75,12 @@ __device__ __forceinline__ double order_rcp(double x) { return 1.0 / x; }
 
 // One token in one warp; expert i is element i / 32 of lane i % 32. `part` is
 // the warp's [E] scratch. Returns false, with nothing written, where two
-// choices that matter lie closer than the arithmetic's error: the caller then
-// takes the token again in FP64, whose order is the answer. (One token in
-// some hundreds with a bias; never without one and without groups, where the
-// logits themselves are the keys.)
+// choices that matter lie closer than the arithmetic's error and it takes more
+// than the experts found to tell: the caller then takes the token again in FP64,
+// whose order is the answer. (One token in thousands with sigmoids and a bias;
+// never without a bias and without groups, where the logits themselves are the
+// keys. All FP64, one token in some hundreds, the kernel took 31 us for 8191x256
+// with groups, a third of that with a few warps left.)
 template <class T, int NV, class Real, class Key>
 __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lane, Real* part) {
   constexpr bool kCheck = sizeof(Real) == 4;
@@ -131,37 +133,55 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
   if (p.groups > 1 && !odd) {
     const int size = p.E / p.groups;
     const bool from_choice = p.bias || p.group_best == 1;
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = lane + 32 * j;
-      if (i < p.E) part[i] = !key[j] ? static_cast<Real>(kNone) : (from_choice ? value_of(key[j]) : score(l[j]));
-    }
-    __syncwarp();
-    // `lanes` lanes to a group find its two best.
-    int log = 0;
-    while ((1 << log) < p.groups) ++log;
-    const int lanes = 32 >> log, g = lane >> (5 - log);
+    // Group g's two best, in the lanes from g << shift on.
+    int shift = 0;
     Real a = kNone, b = kNone;
-    if (g < p.groups)
-      for (int i = lane & (lanes - 1); i < size; i += lanes) {
-        const Real v = part[g * size + i];
-        const Real lo = v < a ? v : a;
-        a = v < a ? a : v;
-        b = b < lo ? lo : b;
+    if (size == 32) {                                      // group j is element j of every lane
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (j < p.groups) {
+          const Key k = from_choice || !key[j] ? key[j] : key_of(score(l[j]));
+          const Key k1 = warp_max(k);
+          const int owner = __ffs(__ballot_sync(kAll, k == k1)) - 1;
+          const Key k2 = warp_max(lane == owner ? Key(0) : k);
+          if (lane == j) {
+            if (k1) a = value_of(k1);
+            if (k2) b = value_of(k2);
+          }
+        }
+    } else {
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int i = lane + 32 * j;
+        if (i < p.E) part[i] = !key[j] ? static_cast<Real>(kNone) : (from_choice ? value_of(key[j]) : score(l[j]));
       }
-    for (int o = 1; o < lanes; o <<= 1) {
-      const Real a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
-      const Real lo = a < a2 ? a : a2, hi = b > b2 ? b : b2;
-      a = a > a2 ? a : a2;
-      b = lo > hi ? lo : hi;
+      __syncwarp();
+      int log = 0;
+      while ((1 << log) < p.groups) ++log;
+      shift = 5 - log;
+      const int lanes = 32 >> log, own = lane >> shift;
+      if (own < p.groups)
+        for (int i = lane & (lanes - 1); i < size; i += lanes) {
+          const Real v = part[own * size + i];
+          const Real lo = v < a ? v : a;
+          a = v < a ? a : v;
+          b = b < lo ? lo : b;
+        }
+      for (int o = 1; o < lanes; o <<= 1) {
+        const Real a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
+        const Real lo = a < a2 ? a : a2, hi = b > b2 ? b : b2;
+        a = a > a2 ? a : a2;
+        b = lo > hi ? lo : hi;
+      }
     }
+    const int g = lane >> shift;
     const bool pair = p.group_best == 2 && b > static_cast<Real>(kNone);
     const Real mine = pair ? a + b : a;
     // A group stays where fewer than top_groups are better.
     int better = 0;
     for (int h = 0; h < p.groups; ++h) {
-      const Real v = __shfl_sync(kAll, mine, h << (5 - log));
+      const Real v = __shfl_sync(kAll, mine, h << shift);
       better += v > mine || (v == mine && h < g);
     }
     const bool stays = g < p.groups && better < p.top_groups;
@@ -173,17 +193,21 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
       const Real most = value_of(warp_max(key_of(magnitude(a) + (pair ? magnitude(b) : Real(0)))));
       if (above && close(value_of(least), value_of(above), 2.0f, 2 * most)) return false;
     }
-    const float per = 1.0f / static_cast<float>(size);     // i / size, for i < 1024, from (i + 1/2) / size
+    if (size == 32) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = lane + 32 * j, of = static_cast<int>((static_cast<float>(i) + 0.5f) * per);
-      if (!(keep >> (of << (5 - log) & 31) & 1)) key[j] = 0;
+      for (int j = 0; j < NV; ++j)
+        if (!(keep >> j & 1)) key[j] = 0;
+    } else {
+      const float per = 1.0f / static_cast<float>(size);   // i / size, for i < 1024, from (i + 1/2) / size
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int i = lane + 32 * j, of = static_cast<int>((static_cast<float>(i) + 0.5f) * per);
+        if (!(keep >> (of << shift & 31) & 1)) key[j] = 0;
+      }
     }
   }
 
-  // The best key of a lane's own, of equal ones the lowest index; then the
-  // best of the lanes', top_k times, and once more where it has to be known
-  // that the next is clearly less.
+  // The best key of a lane's own, of equal ones the lowest index.
   Key best;
   int at;                                                  // its index
   const auto own_best = [&] {
@@ -195,25 +219,81 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
   };
   own_best();
   int id = -1;                                             // of slot `lane`
-  Key prev = 0;
-  int prev_i = 0;
   const bool check = kCheck && p.bias && !odd;
-  const int rounds = p.top_k + (check ? 1 : 0);
-  for (int s = 0; s < rounds; ++s) {
-    const Key m = warp_max(best);
-    if (!m) break;
-    const int i = __reduce_min_sync(kAll, best == m ? at : 0x7FFFFFFF);
-    if (check && s > 0) {
-      const Real a = value_of(prev), b = value_of(m);
-      if (close(a, b, 1.0f, fabs(a))) {
-        // Two experts of one logit and one bias tie in any arithmetic; behind the
-        // last one taken others could lie between.
-        const bool tie = s < p.top_k && to_f32(x[i]) == to_f32(x[prev_i]) && p.bias[i] == p.bias[prev_i];
-        if (!tie) return false;
+  bool sorted = false;
+  if constexpr (kCheck) if (p.top_k < 32) {
+    // Only keys of at least the (top_k + 1)-th largest of the lanes' best can be
+    // among the top_k + 1: a few more than that, mostly. They are collected and
+    // ranked, a lane each.
+    Key v = best;
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+      for (int o = size >> 1; o > 0; o >>= 1) {
+        const Key u = __shfl_xor_sync(kAll, v, o);
+        const bool up = ((lane & o) == 0) == ((lane & size) == 0 || size == 32);
+        v = up == (u > v) ? u : v;
       }
+    const Key least = max(__shfl_sync(kAll, v, p.top_k), Key(1));
+    uint32_t* const cand = reinterpret_cast<uint32_t*>(part);   // keys, indexes, and again in order
+    int n = 0;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in = key[j] >= least;
+      const unsigned who = __ballot_sync(kAll, in);
+      const int to = n + __popc(who & ((1u << lane) - 1));
+      if (in && to < 32) {
+        cand[to] = static_cast<uint32_t>(key[j]);
+        cand[32 + to] = 32 * j + lane;
+      }
+      n += __popc(who);
     }
-    prev = m, prev_i = i;
-    if (s < p.top_k && lane == s) id = i;
+    __syncwarp();
+    if (n <= 32) {
+      const uint32_t k = lane < n ? cand[lane] : 0;
+      int place = 0;                                       // in rising order of the index
+      for (int j = 0; j < n; ++j) {
+        const uint32_t u = __shfl_sync(kAll, k, j);
+        place += u > k || (u == k && j < lane);
+      }
+      if (lane < n) {
+        cand[64 + place] = k;
+        cand[96 + place] = cand[32 + lane];
+      }
+      __syncwarp();
+      const int last = min(n, p.top_k);
+      bool near = false;
+      if (check && lane < last && lane + 1 < n) {
+        const Real a = value_of(static_cast<Key>(cand[64 + lane])), b = value_of(static_cast<Key>(cand[64 + lane + 1]));
+        near = close(a, b, 1.0f, fabs(a));
+      }
+      sorted = !__any_sync(kAll, near);
+      if (sorted && lane < last) id = cand[96 + lane];
+    }
+  }
+  // One after the other, where there are too many of equal keys, or some too
+  // close to each other: the best of the lanes', top_k times; with choices that
+  // FP32 rounds, on to the first that is clearly less.
+  Key prev = 0;
+  int found = 0;
+  bool unsure = false;
+  for (; !sorted; ++found) {
+    const Key m = warp_max(best);
+    if (!m || (!check && found == p.top_k)) break;
+    if (check && found > 0) {
+      const Real a = value_of(prev), b = value_of(m);
+      const bool near = close(a, b, 1.0f, fabs(a));
+      if (!near && found >= p.top_k) break;
+      unsure |= near;
+    }
+    if (found == 32) {
+      if (unsure) return false;
+      break;
+    }
+    const int i = __reduce_min_sync(kAll, best == m ? at : 0x7FFFFFFF);
+    prev = m;
+    if (lane == found) id = i;
     if (at == i) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
@@ -221,6 +301,25 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
       own_best();
     }
   }
+  if (unsure) {
+    // The experts found so far hold the top_k for sure: their order by FP64
+    // choices, a lane each (of a softmax those need the whole sum).
+    if (!p.sigmoid) return false;
+    double c = id >= 0 ? 1.0 / (1.0 + exp(-static_cast<double>(to_f32(x[id])))) + p.bias[id] : 0.0;
+    int place = 0;
+    for (int j = 0; j < found; ++j) {
+      const double u = __shfl_sync(kAll, c, j);
+      const int v = __shfl_sync(kAll, id, j);
+      place += u > c || (u == c && v < id);
+    }
+    int at_place = -1;
+    for (int j = 0; j < found; ++j) {
+      const int u = __shfl_sync(kAll, place, j), v = __shfl_sync(kAll, id, j);
+      if (u == lane) at_place = v;
+    }
+    id = at_place;
+  }
+  if (lane >= p.top_k) id = -1;
 
   const bool live = id >= 0;
   const float lg = live ? to_f32(x[id]) : kNone;
@@ -253,6 +352,8 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
 }
 
 constexpr int kRouteWarps = 4;
+// Doubles of a warp's scratch: the choices, or four times 32 words.
+__host__ __device__ constexpr int route_scratch(int E) { return E > 64 ? E : 64; }
 
 template <class T, int NV>
 __device__ __noinline__ void route_token_f64(const RouteParams& p, int t, int lane, double* part) {
@@ -269,7 +370,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * kRouteWarps + warp;
   if (t >= p.T) return;
-  double* part = route_part + static_cast<size_t>(warp) * p.E;
+  double* part = route_part + static_cast<size_t>(warp) * route_scratch(p.E);
   if (!route_token<T, NV, float, uint32_t>(p, t, lane, reinterpret_cast<float*>(part)))
     route_token_f64<T, NV>(p, t, lane, part);
 }
@@ -279,8 +380,7 @@ cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t s) {
   const RouteParams p = {a.X, a.bias, a.ids, a.weights, a.T, a.E, a.ldl, a.top_k, a.sigmoid, a.renormalise,
                          a.groups, a.top_groups, a.group_best, a.scale};
   const dim3 grid((a.T + kRouteWarps - 1) / kRouteWarps), block(kRouteWarps * 32);
-  // Only groups use the scratch. 32 KB at most: no opt-in.
-  const size_t smem = a.groups > 1 ? sizeof(double) * kRouteWarps * a.E : 0;
+  const size_t smem = sizeof(double) * kRouteWarps * route_scratch(a.E);   // 32 KB at most: no opt-in
   if (a.E <= 64) return launch(route_kernel<T, 2>, grid, block, smem, s, a.pdl, p);
   if (a.E <= 128) return launch(route_kernel<T, 4>, grid, block, smem, s, a.pdl, p);
   if (a.E <= 256) return launch(route_kernel<T, 8>, grid, block, smem, s, a.pdl, p);
