@@ -587,24 +587,39 @@ def w4a16_experts(A, W, scales, rows, offsets, N: int, K: int, global_scales=Non
     return C
 
 
+def _rows_of(name, t, shape, y):
+    """The pitch of rows of a given shape with the type of y."""
+    if not t.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
+    stride = t.stride()
+    if t.dtype is not y.dtype or t.shape != shape or (stride[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be {list(shape)} of y's type, with unit column stride")
+    ld = stride[0] if shape[0] > 1 else shape[1]
+    if ld > _INT_MAX:
+        _too_far(name, ld)
+    return ld
+
+
 def expert_combine(y, weights, ids, E: int, residual=None, out=None, stream=None):
     """[T, H]: residual + the sum over the slots of weights[t, s] * y[t * slots + s], in y's type (bfloat16, float16 or
     float32); y [T * slots, H], float32 weights and int32 ids [T, slots]. Rows whose id is outside 0..E-1 are not read.
     out may be the residual."""
     torch = _torch or _load_torch()
     ldy, dt, R, H = _typed_rows("y", y)
-    if weights.dim() != 2 or weights.shape[0] * weights.shape[1] != R:
+    of = weights.shape
+    if len(of) != 2 or of[0] * of[1] != R:
         raise ValueError(f"weights must be [T, slots] with T * slots = {R}")
-    T, slots = weights.shape
+    T, slots = of
     pw, pi = _packed("weights", weights, (T, slots), torch.float32), _packed("ids", ids, (T, slots), torch.int32)
-    like = y[:T]
-    ldr = _rows_like("residual", residual, like) if residual is not None else 0
+    shape, pr, ldr = (T, H), None, 0
+    if residual is not None:
+        pr, ldr = residual.data_ptr(), _rows_of("residual", residual, shape, y)
     if out is None:
-        out, ldo = _empty((T, H), y.dtype, y.device, stream), H
+        out, ldo = _empty(shape, y.dtype, y.device, stream), H
     else:
-        ldo = _rows_like("out", out, like)
-    status = (_lib or lib()).expert_combine(y.data_ptr(), ldy, pw, pi, E, None if residual is None else residual.data_ptr(),
-                                            ldr, out.data_ptr(), ldo, dt, T, slots, H, _stream(stream))
+        ldo = ldr if out is residual else _rows_of("out", out, shape, y)
+    status = (_lib or lib()).expert_combine(y.data_ptr(), ldy, pw, pi, E, pr, ldr, out.data_ptr(), ldo, dt, T, slots, H,
+                                            _stream(stream))
     if status:
         _check(status, "expert_combine")
     return out
