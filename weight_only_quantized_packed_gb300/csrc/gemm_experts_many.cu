@@ -521,27 +521,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     copies_close();
     copies_wait<0>();
   } else if (warp == kWarpMma && rank == 0) {
-    // A wait that follows MMAs costs the tensor core a pause, so the next stage is
-    // looked up before this one's MMAs are issued. All by one thread: the warp's
-    // own steps between stages took longer than a narrow stage's MMAs.
+    // All by one thread: the warp's own steps between stages took longer than a
+    // narrow stage's MMAs. A look at a barrier costs it some 120 clocks, as much as
+    // those MMAs, so it looks at two at a time.
     if (elect_one()) {
       const uint64_t bd0 = tile_desc(sb);
       int s = 0;
       uint32_t ph = 0, acc_ph = 1;
-      bool ok = true, loaded = false;
+      bool ok = true;
       for (int i = 0; i < mine && ok; ++i) {
         Tile tile;
         tile.at(table, first + i * step, weight_tiles);
         const uint32_t idesc = idesc_f16(256, tile.n);
         if (i > 0) ok = wait_long(acc_free, acc_ph, a.err, abort_flag);
         acc_ph ^= 1;
+        int ready = 0;                         // stages from this one on that are known to be full
         for (int k = 0; k < stages && ok; ++k) {
-          if (!loaded) ok = wait_long(full + 8 * s, ph, a.err, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const int s1 = s + 1 == kS ? 0 : s + 1;
-          const uint32_t ph1 = s1 ? ph : ph ^ 1;
-          loaded = mbar_test(full + 8 * s1, ph1);
+          if (!ready) {
+            const int s1 = s + 1 == kS ? 0 : s + 1;
+            const bool l0 = mbar_test(full + 8 * s, ph), l1 = mbar_test(full + 8 * s1, s1 ? ph : ph ^ 1);
+            ready = l0 && l1 ? 2 : 1;
+            if (!l0) ok = wait_long(full + 8 * s, ph, a.err, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          --ready;
           const uint64_t bd = bd0 + s * (kStageB >> 4);
           const uint32_t at = tmem + kColA + s * 64;
 #pragma unroll
@@ -549,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             pair_mma_ts(tmem, at + 8 * j, bd + (j >> 2) * (kHalfB >> 4) + 2 * (j & 3), idesc, (k | j) ? 1u : 0u);
           pair_commit(done + 8 * s);
           if (k + 1 == stages) pair_commit(acc_full);
-          s = s1, ph = ph1;
+          if (++s == kS) s = 0, ph ^= 1;
         }
       }
       pair_commit_own(drained);
@@ -576,15 +580,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 // few threads copy them (gathered by the kernel itself, through asynchronous
 // copies, they took four warps, and their latency every third stage).
 constexpr int kHalfThreads = 128, kHalfHeld = 8;   // chunks of 8 elements a thread keeps between the passes
+// kWarps warps a row: one for rows that its registers hold (a block's latency per
+// row of 4 KB took 58 us at 32768x2048).
+template <int kWarps>
 __global__ void __launch_bounds__(kHalfThreads)
     half_rows_kernel(const uint16_t* X, const int* rows, uint16_t* Y, float* inv, int R, int slots, int K, int ldx) {
+  constexpr int kThreads = kWarps * 32, kRows = kHalfThreads / kThreads;
   __shared__ uint32_t most_sh[kHalfThreads / 32];
   pdl_launch_dependents();
   pdl_wait();
-  const int p = rows[blockIdx.x];
-  if (static_cast<unsigned>(p) >= static_cast<unsigned>(R)) return;
+  const int at = static_cast<int>(threadIdx.x) % kThreads, r = blockIdx.x * kRows + static_cast<int>(threadIdx.x) / kThreads;
+  const int p = r < R ? rows[r] : -1;
+  if (static_cast<unsigned>(p) >= static_cast<unsigned>(R)) return;   // all threads of the row
   const uint16_t* x = X + static_cast<long long>(p / slots) * ldx;
-  uint16_t* y = Y + static_cast<long long>(blockIdx.x) * K;
+  uint16_t* y = Y + static_cast<long long>(r) * K;
   const int chunks = K >> 3;
   uint4 held[kHalfHeld];
   uint32_t mx = 0;
@@ -593,20 +602,22 @@ __global__ void __launch_bounds__(kHalfThreads)
   };
 #pragma unroll
   for (int i = 0; i < kHalfHeld; ++i) {
-    const int c = threadIdx.x + i * kHalfThreads;
+    const int c = at + i * kThreads;
     held[i] = c < chunks ? *reinterpret_cast<const uint4*>(x + 8 * c) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int i = 0; i < kHalfHeld; ++i) most(held[i]);
-  for (int c = threadIdx.x + kHalfHeld * kHalfThreads; c < chunks; c += kHalfThreads) most(*reinterpret_cast<const uint4*>(x + 8 * c));
+  for (int c = at + kHalfHeld * kThreads; c < chunks; c += kThreads) most(*reinterpret_cast<const uint4*>(x + 8 * c));
   mx = __reduce_max_sync(0xFFFFFFFFu, max(mx & 0xFFFFu, mx >> 16));
-  if ((threadIdx.x & 31) == 0) most_sh[threadIdx.x >> 5] = mx;
-  __syncthreads();
+  if (kWarps > 1) {
+    if ((threadIdx.x & 31) == 0) most_sh[threadIdx.x >> 5] = mx;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kHalfThreads / 32; ++i) mx = max(mx, most_sh[i]);
+    for (int i = 0; i < kHalfThreads / 32; ++i) mx = max(mx, most_sh[i]);
+  }
   const int sh = min(100, max(-113, 141 - static_cast<int>(mx >> 7)));   // 2^(exponent + sh) = 2^14
   const float scale = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-  if (threadIdx.x == 0) inv[blockIdx.x] = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+  if (at == 0) inv[r] = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
   const auto put = [&](int c, const uint4& v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t h[4];
@@ -616,10 +627,18 @@ __global__ void __launch_bounds__(kHalfThreads)
   };
 #pragma unroll
   for (int i = 0; i < kHalfHeld; ++i) {
-    const int c = threadIdx.x + i * kHalfThreads;
+    const int c = at + i * kThreads;
     if (c < chunks) put(c, held[i]);
   }
-  for (int c = threadIdx.x + kHalfHeld * kHalfThreads; c < chunks; c += kHalfThreads) put(c, *reinterpret_cast<const uint4*>(x + 8 * c));
+  for (int c = at + kHalfHeld * kThreads; c < chunks; c += kThreads) put(c, *reinterpret_cast<const uint4*>(x + 8 * c));
+}
+
+cudaError_t launch_half_rows(const ExpertsArgs& a, uint16_t* rows, float* inv, cudaStream_t s) {
+  const int R = a.T * a.slots;
+  const auto* X = static_cast<const uint16_t*>(a.A);
+  if (a.K <= 32 * 8 * kHalfHeld)
+    return launch(half_rows_kernel<1>, dim3((R + 3) / 4), dim3(kHalfThreads), 0, s, a.pdl, X, a.rows, rows, inv, R, a.slots, a.K, a.lda);
+  return launch(half_rows_kernel<4>, dim3(R), dim3(kHalfThreads), 0, s, a.pdl, X, a.rows, rows, inv, R, a.slots, a.K, a.lda);
 }
 
 template <bool kGated>
@@ -663,8 +682,7 @@ cudaError_t launch_w4a16_experts_many(const ExpertsArgs& a, cudaStream_t s) {
   const int R = a.T * a.slots;
   uint16_t* rows = static_cast<uint16_t*>(a.workspace);
   float* inv = reinterpret_cast<float*>(rows + static_cast<size_t>(R) * a.K);
-  const cudaError_t e = launch(act::half_rows_kernel, dim3(R), dim3(act::kHalfThreads), 0, s, a.pdl, static_cast<const uint16_t*>(a.A),
-                               a.rows, rows, inv, R, a.slots, a.K, a.lda);
+  const cudaError_t e = act::launch_half_rows(a, rows, inv, s);
   if (e != cudaSuccess) return e;
   h.A = rows;
   h.row_scales = inv;
