@@ -347,11 +347,11 @@ int expert_order(const int* ids, int* rows, int* offsets, int R, int E, void* st
  * expert_order's. C is BF16 [T * slots, ldc]; rows of pairs without an expert are
  * left as they were. Alignment, K, N, lda and ldc as for w4a16_gemv.
  * Numerics: FP16 operands and FP32 sums. The weights' are exact. The activations
- * are scaled by a power of two per row and rounded: exact where they are at least
- * 2^-29 of their row's largest magnitude, otherwise off by at most 2^-40 of it
- * (up to few pairs an expert: per row and 128 K, as for w4a16_gemm_mma). A row does
- * not depend on the others, but which kernel runs (and with it the order of the
- * sums) on T * slots and E. workspace: w4a16_experts_workspace() bytes. */
+ * are scaled by a power of two, per row or (few pairs an expert) per row and 256 K,
+ * and rounded: exact where they are at least 2^-29 of the row's largest magnitude,
+ * otherwise off by at most 2^-40 of it. The exponential of silu is off by 2^-22. A
+ * row does not depend on the others, but which kernel runs (and with it the order of
+ * the sums) on T * slots, E, N and K. workspace: w4a16_experts_workspace() bytes. */
 int w4a16_experts(const void* A, int lda, const void* W, const void* scales, const float* global_scales, const int* rows,
                   const int* offsets, void* C, int ldc, int T, int slots, int E, int N, int K, int gated, void* workspace,
                   void* stream);
@@ -359,7 +359,7 @@ int w4a16_experts(const void* A, int lda, const void* W, const void* scales, con
 /* Bytes of workspace (device memory, 16-byte aligned, the call's own until it
  * has run) that w4a16_experts needs for these sizes; 0 where it needs none, and
  * may get NULL, and for sizes that it refuses. Host only: no CUDA call. */
-size_t w4a16_experts_workspace(int T, int slots, int E, int K);
+size_t w4a16_experts_workspace(int T, int slots, int E, int N, int K);
 
 /* out[t] = residual[t] + sum_s weights[t, s] * Y[t * slots + s], over the slots
  * whose id is in 0..E-1 (other rows of Y are not read), in FP32 and in the

@@ -63,7 +63,7 @@ EXPORTS = {
     "expert_route": [_P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P],
     "expert_order": [_P, _P, _P, _I, _I, _P],
     "w4a16_experts": [_P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P],
-    "w4a16_experts_workspace": [_I, _I, _I, _I],
+    "w4a16_experts_workspace": [_I, _I, _I, _I, _I],
     "expert_combine": [_P, _I, _P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _P],
     "q2_dequant": [_P, _P, _I, _I, _P],
     "w4a16_dequant": [_P, _P, _F, _P, _I, _I, _P],
@@ -578,7 +578,7 @@ def w4a16_experts(A, W, scales, rows, offsets, N: int, K: int, global_scales=Non
         raise ValueError(f"N={N} must be even, gate and up")
     C, ldc = _gemm_out(A, R, N // 2 if gated else N, out, stream)
     L = _lib or lib()
-    need = L.w4a16_experts_workspace(T, slots, E, K)
+    need = L.w4a16_experts_workspace(T, slots, E, N, K)
     work = _empty((need,), torch.uint8, A.device, stream) if need else None
     status = L.w4a16_experts(A.data_ptr(), lda, pw, ps, pg, pr, po, C.data_ptr(), ldc, T, slots, E, N, K, 1 if gated else 0,
                              _ptr(work), _stream(stream))

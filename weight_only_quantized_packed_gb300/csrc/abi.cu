@@ -391,7 +391,7 @@ int run_experts(const void* A, int lda, const void* W, const void* scales, const
   if (globals && !aligned(globals, 4)) return fail(WQP_ERR_INVALID_ARG, "%s: global_scales must be 4-byte aligned", nm);
   if ((st = check_words(nm, "rows", rows)) != WQP_OK || (st = check_words(nm, "offsets", offsets)) != WQP_OK) return st;
   const int outs = gated ? N / 2 : N;
-  if (!workspace && experts_workspace(T, slots, E, K)) return fail(WQP_ERR_INVALID_ARG, "%s: NULL workspace", nm);
+  if (!workspace && experts_workspace(T, slots, E, N, K)) return fail(WQP_ERR_INVALID_ARG, "%s: NULL workspace", nm);
   if (workspace && !aligned(workspace, 16)) return fail(WQP_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", nm);
   if (static_cast<long long>(T) * slots * outs > (1ll << 38))
     return fail(WQP_ERR_INVALID_ARG, "%s: %lld rows of %d outputs are too many", nm, static_cast<long long>(T) * slots, outs);
@@ -585,9 +585,10 @@ int w4a16_experts(const void* A, int lda, const void* W, const void* scales, con
   return run_experts(A, lda, W, scales, global_scales, rows, offsets, C, ldc, T, slots, E, N, K, gated, workspace, stream);
 }
 
-size_t w4a16_experts_workspace(int T, int slots, int E, int K) {
+size_t w4a16_experts_workspace(int T, int slots, int E, int N, int K) {
   if (check_pairs("w4a16_experts_workspace", T, slots, E) != WQP_OK) return 0;
-  return K < 128 || K > (1 << 20) || K % 128 != 0 ? 0 : experts_workspace(T, slots, E, K);
+  if (N < 1 || N > (1 << 24) || K < 128 || K > (1 << 20) || K % 128 != 0) return 0;
+  return experts_workspace(T, slots, E, N, K);
 }
 
 int expert_combine(const void* Y, int ldy, const float* weights, const int* ids, int E, const void* residual, int ldr,

@@ -170,7 +170,7 @@ cudaError_t launch_expert_combine(const CombineArgs& a, cudaStream_t s);
 // The kernel on the 5th-generation tensor core (gemm_experts_many.cu).
 cudaError_t launch_w4a16_experts_many(const ExpertsArgs& a, cudaStream_t s);
 // Bytes of workspace that launch_w4a16_experts needs.
-size_t experts_workspace(int T, int slots, int E, int K);
+size_t experts_workspace(int T, int slots, int E, int N, int K);
 
 cudaError_t launch_w4_quantize(const QuantArgs& a, cudaStream_t s);
 cudaError_t launch_a8_quantize(const QuantArgs& a, cudaStream_t s);
