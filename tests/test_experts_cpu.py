@@ -7,6 +7,8 @@ import ctypes
 import pytest
 import torch
 
+from tests.test_binding_cpu import CURRENT, SIDE, Stream, Tensor, world  # noqa: F401 (world is a fixture)
+
 P = [ctypes.c_void_p(0x10000 * (i + 1)) for i in range(8)]
 OFF8, OFF2, OFF1 = ctypes.c_void_p(0x10008), ctypes.c_void_p(0x10002), ctypes.c_void_p(0x10001)
 NUL = ctypes.c_void_p(0)
@@ -89,3 +91,141 @@ def test_binding_refuses_host_tensors(L):
                  lambda: wqp.w4a16_experts(x, w, s, rows, offsets, 8, 256), lambda: wqp.expert_combine(x, weights, ids, 4)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+# ---------------------------------------------------------------- the binding, with stand-ins
+class Here(Tensor):
+    """A stand-in of the device `place`."""
+
+    place = 0
+
+    def get_device(self):
+        return self.place
+
+
+def t(dtype, *shape, strides=None, place=0):
+    x = Here(shape, dtype, strides)
+    x.place = place
+    return x
+
+
+def bf16(*shape, **k):
+    return t(torch.bfloat16, *shape, **k)
+
+
+def f32(*shape, **k):
+    return t(torch.float32, *shape, **k)
+
+
+def i32(*shape, **k):
+    return t(torch.int32, *shape, **k)
+
+
+def u8(*shape, **k):
+    return t(torch.uint8, *shape, **k)
+
+
+@pytest.fixture
+def experts(world, monkeypatch):  # noqa: F811
+    from weight_only_quantized_packed_gb300 import binding
+
+    binding._torch.int32 = torch.int32
+    monkeypatch.setattr(binding, "_current_device", lambda: 0)
+    made, empty = world.made, binding._torch.empty
+
+    def here(*shape, dtype, device):
+        out = empty(*shape, dtype=dtype, device=device)
+        out.get_device = lambda: 0
+        return out
+
+    binding._torch.empty = here
+    world.need = 0
+    binding._lib.w4a16_experts_workspace = lambda *a: world.need
+    return world
+
+
+T, k, E, N, K, H = 6, 2, 4, 48, 256, 128
+
+
+def call(name, **kw):
+    from weight_only_quantized_packed_gb300 import binding as b
+
+    return {
+        "expert_route": lambda: b.expert_route(kw.pop("x", f32(T, E)), k, **kw),
+        "expert_order": lambda: b.expert_order(kw.pop("x", i32(T, k)), E, **kw),
+        "w4a16_experts": lambda: b.w4a16_experts(kw.pop("x", bf16(T, K)), kw.pop("w", u8(E, N, K // 2)), u8(E, N, K // 16), kw.pop("rows", i32(T * k)),
+                                                 i32(E + 1), N, K, **kw),
+        "expert_combine": lambda: b.expert_combine(kw.pop("x", bf16(T * k, H)), f32(T, k), kw.pop("ids", i32(T, k)), E, **kw),
+    }[name]()
+
+
+MAKES = {"expert_route": 2, "expert_order": 2, "w4a16_experts": 1, "expert_combine": 1}
+
+
+@pytest.mark.parametrize("name", sorted(MAKES))
+@pytest.mark.parametrize("need", [0, 4096])
+def test_outputs_and_workspace_come_from_the_stream_that_is_passed(experts, name, need):
+    experts.need = need
+    call(name, stream=Stream(SIDE))
+    count = MAKES[name] + (1 if need and name == "w4a16_experts" else 0)
+    assert [m.pool for m in experts.made] == [SIDE] * count and [m.recorded for m in experts.made] == [[CURRENT]] * count
+    assert experts.calls[-1][0] == name and experts.calls[-1][1][-1] == SIDE
+    experts.made.clear()
+    call(name)
+    assert [(m.pool, m.recorded) for m in experts.made] == [(CURRENT, [])] * count
+
+
+@pytest.mark.parametrize("name", sorted(MAKES))
+def test_another_device_is_refused(experts, name):
+    x = {"expert_route": f32(T, E, place=1), "expert_order": i32(T, k, place=1), "w4a16_experts": bf16(T, K, place=1),
+         "expert_combine": bf16(T * k, H, place=1)}[name]
+    with pytest.raises(ValueError, match="current device"):
+        call(name, x=x)
+    assert not experts.calls
+
+
+def test_binding_refuses_what_does_not_fit(experts):
+    for name, kw, kind, word in [
+            ("expert_route", {"scoring": "relu"}, ValueError, "scoring"), ("expert_route", {"bias": f32(E + 1)}, ValueError, "bias"),
+            ("expert_route", {"bias": bf16(E)}, TypeError, "bias"), ("expert_route", {"x": i32(T, E)}, TypeError, "logits"),
+            ("expert_route", {"out": (i32(T, k + 1), f32(T, k))}, ValueError, "ids"), ("expert_route", {"out": (i32(T, k), bf16(T, k))}, TypeError, "weights"),
+            ("expert_order", {"x": t(torch.int64, T, k)}, TypeError, "ids"), ("expert_order", {"x": i32(T, k, strides=(1, T))}, ValueError, "ids"),
+            ("expert_order", {"out": (i32(T * k), i32(E))}, ValueError, "offsets"),
+            ("w4a16_experts", {"x": bf16(5, K)}, ValueError, "pairs"), ("w4a16_experts", {"x": f32(T, K)}, TypeError, "A"),
+            ("w4a16_experts", {"w": u8(E, N, K)}, ValueError, "W"), ("w4a16_experts", {"global_scales": f32(E - 1)}, ValueError, "global_scales"),
+            ("w4a16_experts", {"gated": True, "out": bf16(T * k, N)}, ValueError, "out"), ("w4a16_experts", {"rows": bf16(T * k)}, TypeError, "rows"),
+            ("expert_combine", {"x": bf16(T * k + 1, H)}, ValueError, "weights"), ("expert_combine", {"ids": i32(T * k)}, ValueError, "ids"),
+            ("expert_combine", {"residual": f32(T, H)}, ValueError, "residual"), ("expert_combine", {"out": bf16(T * k, H)}, ValueError, "out"),
+            ("w4a16_experts", {"x": bf16(T, K, strides=(2 ** 31, 1))}, ValueError, "pitch"),
+            ("w4a16_experts", {"out": bf16(T * k, N, strides=(2 ** 31, 1))}, ValueError, "pitch"),
+            ("expert_combine", {"x": bf16(T * k, H, strides=(2 ** 31, 1))}, ValueError, "pitch"),
+            ("expert_combine", {"out": bf16(T, H, strides=(2 ** 31, 1))}, ValueError, "pitch"),
+            ("expert_route", {"x": f32(T, E, strides=(2 ** 31, 1))}, ValueError, "pitch")]:
+        with pytest.raises(kind, match=word):
+            call(name, **kw)
+    assert not experts.calls
+
+
+def test_arguments_arrive(experts):
+    call("w4a16_experts", x=bf16(T * k, K, strides=(K + 8, 1)), gated=True)       # a row of its own for each pair
+    assert experts.calls[-1][1][1] == K + 8 and experts.calls[-1][1][8:15] == (N // 2, T * k, 1, E, N, K, 1)
+    call("w4a16_experts")
+    assert experts.calls[-1][1][8:15] == (N, T, k, E, N, K, 0) and experts.calls[-1][1][15] is None
+    res = bf16(T, H, strides=(H + 8, 1))
+    call("expert_combine", residual=res, out=res)
+    assert experts.calls[-1][1][1] == H and experts.calls[-1][1][6] == experts.calls[-1][1][8] == H + 8
+    call("expert_route", x=f32(T, E, strides=(E + 3, 1)), scoring="sigmoid", renormalise=False, scale=2.5)
+    assert experts.calls[-1][1][1:3] == (E + 3, 2) and experts.calls[-1][1][6:15] == (T, E, k, 1, 1, 1, 2, 0, 2.5)
+
+
+def test_workspace_sizes(L):
+    """Small calls need none; where it is needed, a row of K halves and a factor for each pair."""
+    size = L.w4a16_experts_workspace
+    assert size(1, 8, 128, 4096, 5120) == 0 and size(0, 1, 8, 64, 256) == 0
+    assert size(4096, 8, 128, 4096, 5120) == 32768 * (5120 * 2 + 4)
+    assert size(1 << 20, 8, 8, 64, 4096) == (8 << 20) * (4096 * 2 + 4)            # beyond 32 bits
+    for bad in [(-1, 8, 8, 64, 256), (4, 33, 8, 64, 256), (4, 2, 0, 64, 256), (4, 2, 8, 0, 256), (4, 2, 8, 64, 200)]:
+        assert size(*bad) == 0
+    args = list(EXPERTS)
+    args[9], args[10], args[15] = 100, 8, NUL
+    assert size(100, 8, 8, 40, 256) and L.w4a16_experts(*args) == INVALID and "workspace" in L.wqp_last_error().decode()

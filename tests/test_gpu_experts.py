@@ -311,8 +311,51 @@ def test_experts_one_expert_has_all_and_none():
 
 
 @pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("counts", [[700, 0, 3, 193, 0, 1], [192, 384, 385, 0], [1, 1, 1, 1], [0, 0, 0, 4000]])
+def test_experts_of_all_sizes_in_one_call(counts, gated):
+    """Tiles of pairs of every width, several to an expert, empty experts between, and an odd number of 128 K."""
+    ids = torch.cat([torch.full((n,), e, dtype=torch.int32) for e, n in enumerate(counts)])
+    ids = ids[torch.randperm(len(ids), generator=torch.Generator().manual_seed(1))].to(DEV).view(-1, 1)
+    check_experts(len(ids), 1, len(counts), 300, 640, gated, seed=3, ids=ids)
+
+
+@pytest.mark.parametrize("T,K", [(3, 256), (200, 384)])
+def test_experts_same_expert_twice(T, K):
+    """Two slots of a token may name one expert: two pairs with equal rows."""
+    ids = torch.randint(0, 3, (T, 1), generator=gen(T), device=DEV, dtype=torch.int32).repeat(1, 2)
+    w, s, gs = make_experts(3, 50, K, 6)
+    a = torch.randn((T, K), generator=gen(7), device=DEV).bfloat16()
+    got = wqp.w4a16_experts(a, w, s, *wqp.expert_order(ids, 3), 50, K, gs).view(T, 2, 50)
+    assert torch.equal(got[:, 0], got[:, 1])
+
+
+@pytest.mark.parametrize("T", [5, 400])
+def test_experts_other_rows_and_offsets(T):
+    """Positions that name no pair are passed over, offsets that go back or out of range are taken as far as they go:
+    nothing outside the tensors is read or written."""
+    E, k, N, K = 6, 2, 40, 256
+    w, s, gs = make_experts(E, N, K, 8)
+    a = torch.randn((T, K), generator=gen(9), device=DEV).bfloat16()
+    ids = torch.randint(0, E, (T, k), generator=gen(10), device=DEV, dtype=torch.int32)
+    rows, offsets = wqp.expert_order(ids, E)
+    clean = wqp.w4a16_experts(a, w, s, rows, offsets, N, K, gs)
+    bad = rows.clone()
+    bad[::3] = torch.tensor([-1, -2 ** 31, 2 ** 31 - 1, T * k], device=DEV, dtype=torch.int32).repeat(T)[:len(bad[::3])]
+    out = torch.full_like(clean, -5.0)
+    wqp.w4a16_experts(a, w, s, bad, offsets, N, K, gs, out=out)
+    hit = torch.zeros(T * k, dtype=torch.bool, device=DEV)
+    hit[rows[::3].long()] = True
+    assert (out[hit] == -5).all() and torch.equal(out[~hit], clean[~hit])
+    for values in ([0, 4, 2, 8, 3, 9, 10], [-7, 2 ** 31 - 1, 0, -2 ** 31, 5, 5, 1], [2 ** 31 - 1] * 7, [-1] * 7):
+        out.fill_(-5.0)
+        wqp.w4a16_experts(a, w, s, rows, torch.tensor(values, device=DEV, dtype=torch.int32), N, K, gs, out=out)
+        assert out.isfinite().all()
+
+
+@pytest.mark.parametrize("gated", [False, True])
 def test_experts_long_k(gated):
     check_experts(3, 2, 2, 20, 65536, gated, seed=9)
+    check_experts(40, 2, 2, 20, 32768 + 128, gated, seed=9)
 
 
 @pytest.mark.parametrize("T", [2, 200])
@@ -465,6 +508,37 @@ def test_block_in_a_graph(T, pdl):
                 r.copy_(i[1])
                 graph.replay()
                 assert all(torch.equal(p, q) for p, q in zip(got, w))
+    finally:
+        wqp.set_pdl(old)
+
+
+@pytest.mark.parametrize("T", [1, 300])
+def test_block_under_programmatic_dependent_launch(T):
+    """Call after call into the same buffers with other tokens each time: a value left from before would show."""
+    b = Block(512, 256, 16, 4)
+    g = gen(150 + T)
+    inputs = [[torch.randn((T, b.H), generator=g, device=DEV).bfloat16() for _ in range(2)] for _ in range(4)]
+    logits = [i[0].float() @ b.router for i in inputs]
+    order = (torch.empty(T * 4, dtype=torch.int32, device=DEV), torch.empty(17, dtype=torch.int32, device=DEV))
+    routed = (torch.empty((T, 4), dtype=torch.int32, device=DEV), torch.empty((T, 4), device=DEV))
+    u, y, out = (torch.empty((n, m), dtype=torch.bfloat16, device=DEV) for n, m in ((T * 4, 256), (T * 4, 512), (T, 512)))
+
+    def chain(i):
+        wqp.expert_route(logits[i], 4, "sigmoid", b.bias, 4, 2, out=routed)
+        wqp.expert_order(routed[0], 16, out=order)
+        wqp.w4a16_experts(inputs[i][0], b.up[0], b.up[1], *order, 512, 512, b.up[2], gated=True, out=u)
+        wqp.w4a16_experts(u, b.down[0], b.down[1], *order, 512, 256, b.down[2], out=y)
+        wqp.expert_combine(y, routed[1], routed[0], 16, residual=inputs[i][1], out=out)
+        return [*routed, *order, u, y, out]
+
+    want = [[t.clone() for t in chain(i)] for i in range(4)]
+    torch.cuda.synchronize()
+    old = wqp.set_pdl(True)
+    try:
+        for _ in range(4):
+            for i in range(4):
+                got = [t.clone() for t in chain(i)]
+                assert all(torch.equal(p, q) for p, q in zip(got, want[i]))
     finally:
         wqp.set_pdl(old)
 

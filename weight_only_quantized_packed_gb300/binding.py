@@ -509,6 +509,21 @@ def w8a8_gemm(A, a_scales, W, w_scales, N: int, K: int, out=None, stream=None):
 
 
 _SCORING = {"softmax": 0, "sigmoid": 1}
+_current_device = None   # () -> index of this thread's current device, set on first use
+
+
+def _here(*ts):
+    """The experts' entries take tensors of the current device: the library launches there."""
+    global _current_device
+    if _current_device is None:
+        _load_torch()
+        _current_device = getattr(_torch._C, "_cuda_getDevice", None) or _torch.cuda.current_device
+    for t in ts:
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
+            if t.get_device() != _current_device():
+                raise ValueError("all tensors must be on the current device")
 
 
 def expert_route(logits, top_k: int, scoring: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
@@ -518,6 +533,7 @@ def expert_route(logits, top_k: int, scoring: str = "softmax", bias=None, groups
     float32 weights [T, top_k], the scores, renormalised to sum to 1 and times scale. Id -1: no expert was left (logits
     of -inf). out: (ids, weights) to write to."""
     torch = _torch or _load_torch()
+    _here(logits, bias)
     ldl, dt, T, E = _typed_rows("logits", logits)
     if scoring not in _SCORING:
         raise ValueError("scoring must be 'softmax' or 'sigmoid'")
@@ -527,6 +543,7 @@ def expert_route(logits, top_k: int, scoring: str = "softmax", bias=None, groups
                         _empty((T, top_k), torch.float32, logits.device, stream))
     else:
         ids, weights = out
+        _here(ids, weights)
         _packed("ids", ids, (T, top_k), torch.int32)
         _packed("weights", weights, (T, top_k), torch.float32)
     status = (_lib or lib()).expert_route(logits.data_ptr(), ldl, dt, pb, ids.data_ptr(), weights.data_ptr(), T, E, top_k,
@@ -541,12 +558,14 @@ def expert_order(ids, E: int, out=None, stream=None):
     """(rows, offsets): the pairs (elements of the int32 ids [T, top_k]) by expert, int32 [T * top_k] with -1 behind the
     last, and where each expert's begin, int32 [E + 1]. Ids outside 0..E-1 have no expert. out: (rows, offsets) to write to."""
     torch = _torch or _load_torch()
+    _here(ids)
     R = ids.numel()
     pi = _weights("ids", ids, R, torch.int32)
     if out is None:
         rows, offsets = (_empty((R,), torch.int32, ids.device, stream), _empty((E + 1,), torch.int32, ids.device, stream))
     else:
         rows, offsets = out
+        _here(rows, offsets)
         _packed("rows", rows, (R,), torch.int32)
         _packed("offsets", offsets, (E + 1,), torch.int32)
     status = (_lib or lib()).expert_order(pi, rows.data_ptr(), offsets.data_ptr(), R, E, _stream(stream))
@@ -562,9 +581,8 @@ def w4a16_experts(A, W, scales, rows, offsets, N: int, K: int, global_scales=Non
     [N, K], global_scales their float32 scales [E]; rows and offsets are expert_order's. Rows of pairs without an expert
     are not written: a new out holds anything there."""
     torch = _torch or _load_torch()
+    _here(A, W, scales, rows, offsets, global_scales, out)
     T, lda = _rows(A, K)
-    if not A.is_cuda:
-        raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
     E, R = offsets.numel() - 1, rows.numel()
     if E < 1:
         raise ValueError("offsets must hold E + 1 values")
@@ -605,6 +623,7 @@ def expert_combine(y, weights, ids, E: int, residual=None, out=None, stream=None
     float32); y [T * slots, H], float32 weights and int32 ids [T, slots]. Rows whose id is outside 0..E-1 are not read.
     out may be the residual."""
     torch = _torch or _load_torch()
+    _here(y, weights, ids, residual, out)
     ldy, dt, R, H = _typed_rows("y", y)
     of = weights.shape
     if len(of) != 2 or of[0] * of[1] != R:
