@@ -518,12 +518,16 @@ def _here(*ts):
     if _current_device is None:
         _load_torch()
         _current_device = getattr(_torch._C, "_cuda_getDevice", None) or _torch.cuda.current_device
+    device = -1
     for t in ts:
-        if t is not None:
-            if not t.is_cuda:
-                raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
-            if t.get_device() != _current_device():
-                raise ValueError("all tensors must be on the current device")
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("all tensors must be CUDA tensors (no CPU fallback)")
+        if device < 0:
+            device = _current_device()
+        if t.get_device() != device:
+            raise ValueError("all tensors must be on the current device")
 
 
 def expert_route(logits, top_k: int, scoring: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
