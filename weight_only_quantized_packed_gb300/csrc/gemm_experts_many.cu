@@ -47,7 +47,7 @@ constexpr int kRegsLaunch = 80, kRegsOut = 96, kRegsRest = 40;
 static_assert(kSets * kRegsLaunch + kEpi / 4 * kRegsOut + kRegsRest <= kThreads / 128 * kRegsLaunch, "registers");
 // Tensor memory: the accumulator, then kS stages of 64 columns.
 constexpr uint32_t kColA = kMaxN;
-static_assert(kColA + kS * 64 <= 512 && kSets <= kRing, "stages");
+static_assert(kColA + kS * 64 <= 512 && kSets <= kRing && kS > 2 * (kSets - 1), "stages");
 
 constexpr int many_bytes(int E) { return 1024 + kTableAt + experts::Table::bytes(E); }
 static_assert(many_bytes(kMaxExperts) <= 226 * 1024, "shared memory");
@@ -273,7 +273,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     skip(set);
     while (i < mine) {
-      if (!__all_sync(0xFFFFFFFFu, wait_long(raw_full + 8 * get, raw_ph, a.err, abort_flag))) break;
+      // A set sees only every kSets-th use of the ring, and a barrier tells its phases
+      // apart by parity alone: that the place's last contents have been used shows that
+      // the phase waited for is the next one.
+      if (!__all_sync(0xFFFFFFFFu, wait_long(raw_empty + 8 * get, raw_ph ^ 1, a.err, abort_flag) &&
+                                       wait_long(raw_full + 8 * get, raw_ph, a.err, abort_flag)))
+        break;
       const int x = from & 7;
       int place = s;
       uint32_t place_ph = ph;
@@ -302,7 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             decode_word(ww[2 * gr], sf, r + 8 * gr);
             decode_word(ww[2 * gr + 1], sf, r + 8 * gr + 4);
           }
-          // Parity 1 of a barrier that has completed no phase counts as complete.
+          // Parity 1 of a barrier that has completed no phase counts as complete. The set's
+          // stage before was kS stages back or later, so it has seen the phase before.
           if (h == 0 && !__all_sync(0xFFFFFFFFu, wait_long(done + 8 * place, place_ph, a.err, abort_flag))) goto decoding_over;
           if (h == 0) tc_fence_after();
           tmem_st32(at + place * 64 + h * 32, r);
