@@ -354,7 +354,7 @@ int run_route(const void* X, int ldl, int dtype, const float* bias, int* ids, fl
   DeviceInfo* dev = nullptr;
   if ((st = device_setup(&dev)) != WQP_OK) return st;
   const RouteArgs a = {X, bias, ids, weights, dtype, T, E, ldl, top_k, scoring == WQP_SIGMOID, renormalise != 0,
-                       groups, top_groups, group_best, scale, dev->num_sms, g_pdl.load(std::memory_order_relaxed) != 0};
+                       groups, top_groups, group_best, scale, g_pdl.load(std::memory_order_relaxed) != 0};
   const cudaError_t e = launch_expert_route(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? WQP_OK : cuda_fail(e, nm);
 }

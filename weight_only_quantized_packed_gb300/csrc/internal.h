@@ -118,7 +118,6 @@ struct RouteArgs {
   bool sigmoid, renormalise;
   int groups, top_groups, group_best;
   float scale;
-  int num_sms;
   bool pdl;
 };
 
