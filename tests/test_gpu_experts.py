@@ -400,6 +400,30 @@ def test_experts_rows_do_not_touch_each_other(T):
         assert torch.equal(wqp.w4a16_experts(a * 2.0 ** e, w, s, *order, N, K, gs).float() * 2.0 ** -e, clean.float())
 
 
+@pytest.mark.parametrize("T", [2, 60])
+@pytest.mark.parametrize("gated", [False, True])
+def test_experts_small_rows_with_small_global_scales(T, gated):
+    """Outputs in BF16's range from rows and global scales whose powers of two alone FP32 does not hold; none from no weights."""
+    E, k, N, K = 2, 2, 48, 512
+    g = gen(14)
+    w = torch.randint(0, 256, (E, N, K // 2), generator=g, device=DEV, dtype=torch.uint8)
+    s = torch.full((E, N, K // 16), 0x7E, dtype=torch.uint8, device=DEV)
+    a = torch.randn((T, K), generator=g, device=DEV)
+    ids = torch.randint(0, E, (T, k), generator=g, device=DEV, dtype=torch.int32)
+    order = wqp.expert_order(ids, E)
+    for rows, globals_ in ((2.0 ** -86, 2.0 ** -48), (2.0 ** -16, 2.0 ** -120)):
+        small = (a * rows).bfloat16()
+        gs = torch.tensor([1.37, 0.71], device=DEV) * globals_
+        if gated:
+            gs = gs * 2.0 ** (58 if rows < 2.0 ** -80 else 60)
+        got = wqp.w4a16_experts(small, w, s, *order, N, K, gs, gated).double().cpu()
+        want, tol, _ = experts64(small, w, s, gs, ids, gated, k)
+        assert ((got - want).abs() <= tol).all()
+    large = (a * 2.0 ** 100).bfloat16()
+    got = wqp.w4a16_experts(large, torch.zeros_like(w), s, *order, N, K, torch.full((E,), 2.0 ** 50, device=DEV), gated)
+    assert (got == 0).all()
+
+
 def test_experts_pairs_across_the_end_of_a_large_buffer():
     """Weights and outputs beyond 2^31 elements from their base."""
     E, N, K = 220, 4096, 5120

@@ -339,18 +339,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile.at(table, first + i * step, weight_tiles);
       const float gs = a.globals ? a.globals[tile.expert] : 1.0f;
       int pl[kChunks];                         // the pair of column 32 (2 ch + h) + lane, and
-      float fl[kChunks];                       // its factor
+      float fl[kChunks];                       // the inverse of its row's scaling
 #pragma unroll
       for (int ch = 0; ch < kChunks; ++ch) {
         const int c = 32 * (2 * ch + h) + lane, p = c < tile.pairs ? a.rows[tile.p0 + c] : -1;
         pl[ch] = static_cast<unsigned>(p) < static_cast<unsigned>(R) ? p : -1;
-        fl[ch] = pl[ch] >= 0 ? a.row_scales[tile.p0 + c] * gs : gs;
+        fl[ch] = pl[ch] >= 0 ? a.row_scales[tile.p0 + c] : 1.0f;
       }
       wait_long(acc_full, ph, a.err, abort_flag);
       ph ^= 1;
       __syncwarp();
       if (__any_sync(0xFFFFFFFFu, *abort_flag)) break;
       tc_fence_after();
+      // The inverse power of two first: FP32 may not hold its product with gs where it
+      // holds the output.
       uint32_t packed[kChunks][kGated ? 8 : 16];
 #pragma unroll
       for (int ch = 0; ch < kChunks; ++ch) {
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float keep = __uint_as_float(odd ? v[16 + c] : v[c]), give = __uint_as_float(odd ? v[c] : v[16 + c]);
               const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 16);
               const float f = __shfl_sync(0xFFFFFFFFu, fl[ch], odd ? 16 + c : c);
-              y[e] = silu((odd ? got : keep) * f) * ((odd ? keep : got) * f);
+              y[e] = silu((odd ? got : keep) * f * gs) * ((odd ? keep : got) * f * gs);
             }
             packed[ch][j] = pack_bf16(y[0], y[1]);
           }
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float f0 = __shfl_sync(0xFFFFFFFFu, fl[ch], 2 * j), f1 = __shfl_sync(0xFFFFFFFFu, fl[ch], 2 * j + 1);
-            packed[ch][j] = pack_bf16(__uint_as_float(v[2 * j]) * f0, __uint_as_float(v[2 * j + 1]) * f1);
+            packed[ch][j] = pack_bf16(__uint_as_float(v[2 * j]) * f0 * gs, __uint_as_float(v[2 * j + 1]) * f1 * gs);
           }
         }
       }
@@ -657,7 +659,7 @@ cudaError_t launch_experts_many_t(const ExpertsArgs& a, bool pdl, cudaStream_t s
     e = make_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.A, a.K, static_cast<uint64_t>(a.T) * a.slots, static_cast<uint64_t>(a.K) * 2, 64,
                     kBox, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e == cudaSuccess)
-    e = cached_map_3d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.W, {row, N, static_cast<uint64_t>(a.E)}, {row, row * N},
+    e = make_map_3d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.W, {row, N, static_cast<uint64_t>(a.E)}, {row, row * N},
                       {128, kGated ? 64 : 128, 1}, CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
