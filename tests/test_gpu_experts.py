@@ -472,6 +472,27 @@ def test_combine(dtype, T, k, H, pad, with_residual):
             assert torch.equal(same, out)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,k,H", [(1, 3, 16), (23, 9, 160), (300, 2, 2080)])
+def test_combine_same_bits_whatever_the_alignment(dtype, T, k, H):
+    """Bases and pitches of 32 bytes, and of 16: each in turn, and all."""
+    g, E, step = gen(T + k), 5, 128 // torch.finfo(dtype).bits
+    ids = torch.randint(-1, E, (T, k), generator=g, device=DEV, dtype=torch.int32)
+    weights = torch.rand((T, k), generator=g, device=DEV)
+    y, res = torch.randn((T * k, H), generator=g, device=DEV).to(dtype), torch.randn((T, H), generator=g, device=DEV).to(dtype)
+
+    def place(x, base, pitch):
+        buf = torch.full((x.shape[0] + 1, H + 16), 7.0, dtype=dtype, device=DEV).view(-1)
+        return buf.as_strided(x.shape, (H + pitch * 8, 1), base * step).copy_(x)
+
+    want = wqp.expert_combine(y, weights, ids, E, residual=res)
+    for how in ((0, 0, 0, 0, 0, 0), (1, 0, 0, 0, 0, 0), (0, 1, 0, 0, 0, 0), (0, 0, 1, 0, 0, 0), (0, 0, 0, 1, 0, 0), (0, 0, 0, 0, 1, 0),
+                (0, 0, 0, 0, 0, 1), (1, 1, 1, 1, 1, 1), (0, 2, 0, 2, 0, 2)):
+        out = place(torch.zeros_like(res), *how[4:])
+        got = wqp.expert_combine(place(y, *how[:2]), weights, ids, E, residual=place(res, *how[2:4]), out=out)
+        assert torch.equal(got, want)
+
+
 # ---------------------------------------------------------------- together
 class Block:
     """A feed-forward part of E experts."""

@@ -414,7 +414,7 @@ int run_combine(const void* Y, int ldy, const float* weights, const int* ids, in
   if (dtype < WQP_BF16 || dtype > WQP_F32) return fail(WQP_ERR_INVALID_ARG, "%s: dtype=%d is not a wqp_dtype", nm, dtype);
   if (H < 8 || H > (1 << 20) || H % 8 != 0)
     return fail(WQP_ERR_INVALID_ARG, "%s: H=%d must be a multiple of 8 in [8, 2^20]", nm, H);
-  if (static_cast<long long>(T) * H > (1ll << 40)) return fail(WQP_ERR_INVALID_ARG, "%s: T=%d rows of %d are too many", nm, T, H);
+  if (static_cast<long long>(T) * H > (1ll << 38)) return fail(WQP_ERR_INVALID_ARG, "%s: T=%d rows of %d are too many", nm, T, H);
   if (T == 0) return WQP_OK;
   st = check_pitched(nm, "Y", Y, ldy, H);
   if (st == WQP_OK && R) st = check_pitched(nm, "residual", R, ldr, H);
