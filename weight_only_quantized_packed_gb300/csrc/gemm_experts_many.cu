@@ -1,25 +1,40 @@
 // Products of rows with their experts' packed W4A16 matrices on the 5th-
 // generation tensor core, for any number of rows an expert.
 //
-// The weights are the first operand: a tile is 256 weight rows by up to 256 of
-// an expert's pairs, on a pair of CTAs (act.cuh) that hold 128 weight rows and
-// half of the pairs' activations each. Decoding them is what has to be fed
-// (128 * 128 weights a CTA and stage), and it has the same cost however few
-// pairs there are: from about 100 pairs a tile the tensor core is the limit,
-// below that the decoding or the bytes.
+// The weights are the first operand: a tile is 256 weight rows by up to 192 of
+// an expert's pairs (its pairs are split evenly, in whole 32s), on a pair of CTAs
+// (act.cuh) that hold 128 weight rows and half of the pairs' activations each. One
+// CTA an SM, which takes every 76th tile of the walk; a tile's steps are stages of
+// 128 K, five of them in tensor memory and shared memory at a time.
 //
-//  * Decoding, two sets of four warps that take the stages in turn: a
-//    thread owns a weight row (a lane of tensor memory). Its codes and scales
-//    come by asynchronous copies into a ring that only its warp uses, so no
-//    barrier is in between; e2m1 * e4m3 is exact in BF16, and goes straight to
-//    tensor memory, from where the MMAs take it.
-//  * Activations, four warps: rows of BF16 gathered by pair, 16 bytes a copy,
-//    into 128-byte-swizzled tiles of 64 K, two a stage.
-//  * MMA, one warp of the even CTA: M = 256, N = the tile's pairs rounded up to
+//  * Rows first go to FP16 in the order of the pairs (half_rows_kernel below), so
+//    that both operands are FP16: the hardware converts E2M1 to FP16 at 2.5 clocks
+//    a pair and scheduler with its product, to BF16 at 6 to 8, and a tile's rows are
+//    consecutive. e2m1 * e4m3 is exact in FP16.
+//  * Packed weights, one warp for the codes (tensor copies) and one for the scales
+//    (asynchronous copies): a ring of four double stages of 128 rows.
+//  * Decoding, three sets of four warps that take the double stages in turn: a
+//    thread owns a weight row (a lane of tensor memory), and its FP16 weights go
+//    straight to tensor memory, from where the MMAs take them.
+//  * Activations, one thread: tensor copies of kBox rows.
+//  * MMA, one thread of the even CTA: M = 256, N = the tile's pairs rounded up to
 //    32, so that a short expert costs no more than its rows.
-//  * Output, four warps: a lane has a weight row and, column by column, the
+//  * Output, eight warps: a lane has a weight row and, column by column, the
 //    pairs. Gated: gate and up rows take turns as lanes, and lanes exchange
 //    halves of their columns.
+//
+// Measured (128 experts, rows' conversion included): 333x8, gated 4096x5120 345 to
+// 350 us, 4.4 TB/s of packed weights; 4096x8, gated 4096x5120 935 to 960 us, 1.4 to
+// 1.5 PFLOP/s; 4096x8, 5120x2048 515 to 580 us (it varies with the power limit). No
+// unit is full: at 333x8 DRAM is 56 % busy, issue slots and the ALU 58 %, the tensor
+// core 21 %. What a stage costs is its hand-overs: copies and barriers alone, without
+// decoding, stores to tensor memory and seven of eight MMAs, take 290, 700 and 403
+// us; one MMA of eight instead of all saves 7 of 350 and 125 of 960. At a tile's end
+// the MMAs wait some 3300 clocks for the accumulator. Did not help: 256 pairs a tile
+// and four stages (410, 966, 522 us), as many activations as fit (362, 975, 573), a
+// longer ring of weights for narrow tiles (363), two accumulators in turn (362, 924,
+// 546), looks at barriers by another warp (356, 946, 515), 256 K a stage (348, 1051,
+// 625).
 #include "act.cuh"
 #include "experts.cuh"
 #include "mma_f16.cuh"
