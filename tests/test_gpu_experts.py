@@ -133,6 +133,28 @@ def test_route_choices_that_fp32_cannot_tell_apart(E, groups, top_groups, scorin
         check_route(x + shift, 8, scoring, bias, groups, top_groups, 1)
 
 
+@pytest.mark.parametrize("E,groups,top_groups", [(64, 4, 2), (256, 8, 4), (96, 32, 7), (120, 5, 3)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_best", [1, 2])
+def test_route_groups_that_fp32_cannot_tell_apart(E, groups, top_groups, scoring, group_best):
+    """Every group has two experts that stand out and lie within FP32's last bits of the other groups'; biases of +-infinity."""
+    g = gen(E + groups)
+    x = torch.randn((40, E), generator=g, device=DEV)
+    s = (torch.sigmoid(x.double()) if scoring == "sigmoid" else torch.softmax(x.double(), 1)).cpu()
+    bias = torch.full((E,), -3.0)
+    first = torch.arange(groups) * (E // groups)
+    for at in (first, first + 1):
+        bias[at] = (1.0 - s[0, at]).float()
+    for shift in (0.0, 2.0 ** -22):
+        check_route(x + shift, 3, scoring, bias.to(DEV), groups, top_groups, group_best)
+    if group_best == 2:
+        check_route(x[:1].expand(3, E).contiguous(), 2, scoring, None, groups, top_groups)
+    bias[2::E // groups] = bias[2].item()                    # a third, far below
+    bias[0] = bias[1] = bias[E - 1] = INF
+    bias[3] = -INF
+    check_route(x, 3, scoring, bias.to(DEV), groups, top_groups, group_best)
+
+
 def test_route_far_logits():
     """Scores that vanish in FP32, and their quotients."""
     x = torch.zeros(4, 16, device=DEV)

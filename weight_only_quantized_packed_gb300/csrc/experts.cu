@@ -59,35 +59,119 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
   }
   return v;
 }
-template <class Real>
-__device__ __forceinline__ Real warp_add(Real v) {
+__device__ __forceinline__ double warp_add(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
 }
 
-// e^x and 1 / x for the order of the experts: approximate in FP32, where the
-// bounds of route_token allow for them.
-__device__ __forceinline__ float order_exp(float x) { return __expf(x); }
-__device__ __forceinline__ double order_exp(double x) { return exp(x); }
-__device__ __forceinline__ float order_rcp(float x) { return __fdividef(1.0f, x); }
-__device__ __forceinline__ double order_rcp(double x) { return 1.0 / x; }
+// Whether the experts' order needs scores, and their groups' the choices.
+__device__ __forceinline__ bool by_scores(const RouteParams& p) { return p.bias || (p.groups > 1 && p.group_best == 2); }
+__device__ __forceinline__ bool group_by_choice(const RouteParams& p) { return p.bias || p.group_best == 1; }
 
-// One token in one warp; expert i is element i / 32 of lane i % 32. `part` is
-// the warp's [E] scratch. Returns false, with nothing written, where two
-// choices that matter lie closer than the arithmetic's error and it takes more
-// than the experts found to tell: the caller then takes the token again in FP64,
-// whose order is the answer. (One token in thousands with sigmoids and a bias;
-// never without a bias and without groups, where the logits themselves are the
-// keys. All FP64, one token in some hundreds, the kernel took 31 us for 8191x256
-// with groups, a third of that with a few warps left.)
-template <class T, int NV, class Real, class Key>
-__device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lane, Real* part) {
-  constexpr bool kCheck = sizeof(Real) == 4;
-  const T* x = static_cast<const T*>(p.X) + static_cast<long long>(t) * p.ldl;
-  const float kNone = __int_as_float(0xFF800000);
-  float l[NV];
-  bool odd = false;                                        // NaN, or an infinite exponential
+// One token in one warp, in FP64: its experts, slot `lane`'s in the result, or -1.
+// For tokens without NaN whose order needs scores and is too close for FP32; loops
+// over shared memory (key [E]).
+template <class T>
+__device__ __noinline__ int route_exact(const RouteParams& p, const T* x, int lane, unsigned long long* key) {
+  const double none = __longlong_as_double(0xFFF0000000000000ll);
+  double top = none, inv = 1.0;
+  if (!p.sigmoid) {
+#pragma unroll 1
+    for (int i = lane; i < p.E; i += 32) top = fmax(top, static_cast<double>(to_f32(x[i])));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(kAll, top, o));
+  }
+  const auto power = [&](int i) {              // of a sigmoid e^-l, of a softmax e^(l - top): -inf gives inf and 0
+    const double l = to_f32(x[i]);
+    return exp(p.sigmoid ? -l : l - top);
+  };
+  const auto score = [&](int i) {
+    const double e = power(i);
+    return p.sigmoid ? 1.0 / (1.0 + e) : e * inv;
+  };
+  if (!p.sigmoid) {
+    double sum = 0.0;
+#pragma unroll 1
+    for (int i = lane; i < p.E; i += 32) sum += power(i);
+    inv = 1.0 / warp_add(sum);
+  }
+  __syncwarp();
+  const int size = p.E / p.groups;
+  const bool from_choice = group_by_choice(p);
+#pragma unroll 4
+  for (int i = lane; i < p.E; i += 32) {
+    const double l = to_f32(x[i]), s = score(i), c = p.bias ? s + p.bias[i] : l;
+    key[i] = l > none && c > none ? key_of(from_choice ? c : s) : 0;
+  }
+  __syncwarp();
+  unsigned long long mine = 0;                 // of group `lane`: its score's key
+#pragma unroll 1
+  for (int g = 0; g < p.groups; ++g) {
+    unsigned long long k1 = 0, k2 = 0;
+#pragma unroll 1
+    for (int j = lane; j < size; j += 32) {
+      const unsigned long long k = key[g * size + j];
+      k2 = max(k2, min(k, k1));
+      k1 = max(k1, k);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const unsigned long long u1 = __shfl_xor_sync(kAll, k1, o), u2 = __shfl_xor_sync(kAll, k2, o);
+      k2 = max(max(k2, u2), min(k1, u1));
+      k1 = max(k1, u1);
+    }
+    if (lane == g) mine = k2 && p.group_best == 2 ? key_of(value_of(k1) + value_of(k2)) : k1;
+  }
+  int better = 0;
+#pragma unroll 1
+  for (int h = 0; h < p.groups; ++h) {
+    const unsigned long long k = __shfl_sync(kAll, mine, h);
+    better += k > mine || (k == mine && h < lane);
+  }
+  const unsigned keep = __ballot_sync(kAll, better < p.top_groups);
+  if (!from_choice)                            // the choices are the logits
+#pragma unroll 1
+    for (int i = lane; i < p.E; i += 32)
+      if (key[i]) key[i] = key_of(static_cast<double>(to_f32(x[i])));
+  __syncwarp();
+  int id = -1;
+#pragma unroll 1
+  for (int k = 0; k < p.top_k; ++k) {
+    unsigned long long best = 0;
+    int at = 0x7FFFFFFF;
+#pragma unroll 1
+    for (int i = lane; i < p.E; i += 32)
+      if (key[i] > best && (keep >> (i / size) & 1)) best = key[i], at = i;
+    const unsigned long long m = warp_max(best);
+    if (!m) break;
+    const int i = __reduce_min_sync(kAll, best == m ? at : 0x7FFFFFFF);
+    if (lane == k) id = i;
+    if (at == i) key[i] = 0;
+    __syncwarp();
+  }
+  return id;
+}
+
+constexpr float kNone = -INFINITY;
+
+// A token's logits; expert i is element i / 32 of lane i % 32.
+template <int NV>
+struct Logits {
+  float l[NV];                                             // -inf behind the last
+  float top;
+  bool odd;                                                // NaN, or an infinite exponential
+};
+
+// One token in one warp, in FP32; `part` is the warp's [E] scratch. Returns
+// false where two choices that matter lie closer than the arithmetic's error and
+// it takes more than the experts found to tell: route_exact's is then the answer. (One
+// token in thousands with sigmoids and a bias; never without a bias and without
+// groups, where the logits themselves are the keys.) id: as route_exact's.
+template <class T, int NV>
+__device__ __forceinline__ bool route_token(const RouteParams& p, const T* x, int lane, float* part, Logits<NV>& logits, int& id) {
+  float (&l)[NV] = logits.l;
+  bool odd = false;
   float top = kNone;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -96,54 +180,54 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
     odd |= l[j] != l[j] || (!p.sigmoid && l[j] == __int_as_float(0x7F800000));
     top = fmaxf(top, l[j]);
   }
-  odd = __any_sync(kAll, odd);
-  top = value_of(warp_max(key_of(top)));
+  logits.odd = odd = __any_sync(kAll, odd);
+  logits.top = top = value_of(warp_max(key_of(top)));
 
   // Scores where the order needs them.
-  const bool by_score = !odd && (p.bias || (p.groups > 1 && p.group_best == 2));
-  Real inv = 1;                                            // of the exponentials' sum
+  const bool by_score = !odd && by_scores(p);
+  float inv = 1.0f;                                           // of the exponentials' sum
   if (!p.sigmoid && by_score) {
-    Real e = 0;
+    float e = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) e += order_exp(static_cast<Real>(l[j]) - static_cast<Real>(top));   // -inf gives 0
-    inv = Real(1) / warp_add(e);
+    for (int j = 0; j < NV; ++j) e += __expf(l[j] - top);   // -inf gives 0
+    inv = 1.0f / warp_sum(e);
   }
-  const auto score = [&](float v) -> Real {
-    if (p.sigmoid) return order_rcp(Real(1) + order_exp(-static_cast<Real>(v)));
-    return order_exp(static_cast<Real>(v) - static_cast<Real>(top)) * inv;
+  const auto score = [&](float v) {
+    if (p.sigmoid) return __fdividef(1.0f, 1.0f + __expf(-v));
+    return __expf(v - top) * inv;
   };
-  Key key[NV];
+  uint32_t key[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int i = lane + 32 * j;
-    Real c = l[j];
-    if (by_score && p.bias && i < p.E) c = score(l[j]) + static_cast<Real>(p.bias[i]);
-    key[j] = l[j] > kNone && c > static_cast<Real>(kNone) ? key_of(c) : Key(0);
+    float c = l[j];
+    if (by_score && p.bias && i < p.E) c = score(l[j]) + p.bias[i];
+    key[j] = l[j] > kNone && c > kNone ? key_of(c) : 0u;
   }
   // The error of a choice c is at most 2^-24 (64 s_max + |c|): of a sigmoid s,
   // whose exponential is off by 4 + 3 |l| of these units, s (1 - s) times that and
   // 3 s more, under 8; of a softmax, whose sum has up to 37 roundings on any path,
   // at most 64 of its largest score. Two that are closer than twice that may
   // have changed places.
-  const float s_max = p.sigmoid ? 0.125f : static_cast<float>(inv);
-  const auto close = [&](Real a, Real b, float terms, Real most) {
-    return kCheck && a - b <= Real(0x1p-23f) * (Real(64.0f * terms) * Real(s_max) + most);
+  const float s_max = p.sigmoid ? 0.125f : inv;
+  const auto close = [&](float a, float b, float terms, float most) {
+    return a - b <= 0x1p-23f * (64.0f * terms * s_max + most);
   };
 
   if (p.groups > 1 && !odd) {
     const int size = p.E / p.groups;
-    const bool from_choice = p.bias || p.group_best == 1;
+    const bool from_choice = group_by_choice(p);
     // Group g's two best, in the lanes from g << shift on.
     int shift = 0;
-    Real a = kNone, b = kNone;
+    float a = kNone, b = kNone;
     if (size == 32) {                                      // group j is element j of every lane
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (j < p.groups) {
-          const Key k = from_choice || !key[j] ? key[j] : key_of(score(l[j]));
-          const Key k1 = warp_max(k);
+          const uint32_t k = from_choice || !key[j] ? key[j] : key_of(score(l[j]));
+          const uint32_t k1 = warp_max(k);
           const int owner = __ffs(__ballot_sync(kAll, k == k1)) - 1;
-          const Key k2 = warp_max(lane == owner ? Key(0) : k);
+          const uint32_t k2 = warp_max(lane == owner ? 0u : k);
           if (lane == j) {
             if (k1) a = value_of(k1);
             if (k2) b = value_of(k2);
@@ -154,7 +238,7 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int i = lane + 32 * j;
-        if (i < p.E) part[i] = !key[j] ? static_cast<Real>(kNone) : (from_choice ? value_of(key[j]) : score(l[j]));
+        if (i < p.E) part[i] = !key[j] ? kNone : (from_choice ? value_of(key[j]) : score(l[j]));
       }
       __syncwarp();
       int log = 0;
@@ -163,35 +247,79 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
       const int lanes = 32 >> log, own = lane >> shift;
       if (own < p.groups)
         for (int i = lane & (lanes - 1); i < size; i += lanes) {
-          const Real v = part[own * size + i];
-          const Real lo = v < a ? v : a;
+          const float v = part[own * size + i];
+          const float lo = v < a ? v : a;
           a = v < a ? a : v;
           b = b < lo ? lo : b;
         }
       for (int o = 1; o < lanes; o <<= 1) {
-        const Real a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
-        const Real lo = a < a2 ? a : a2, hi = b > b2 ? b : b2;
+        const float a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
+        const float lo = a < a2 ? a : a2, hi = b > b2 ? b : b2;
         a = a > a2 ? a : a2;
         b = lo > hi ? lo : hi;
       }
     }
     const int g = lane >> shift;
-    const bool pair = p.group_best == 2 && b > static_cast<Real>(kNone);
-    const Real mine = pair ? a + b : a;
+    const bool pair = p.group_best == 2 && b > kNone;
+    const float mine = pair ? a + b : a;
     // A group stays where fewer than top_groups are better.
     int better = 0;
     for (int h = 0; h < p.groups; ++h) {
-      const Real v = __shfl_sync(kAll, mine, h << shift);
+      const float v = __shfl_sync(kAll, mine, h << shift);
       better += v > mine || (v == mine && h < g);
     }
     const bool stays = g < p.groups && better < p.top_groups;
-    const unsigned keep = __ballot_sync(kAll, stays);
-    if (kCheck && p.top_groups < p.groups && by_score) {
-      const auto magnitude = [](Real v) { return v > Real(-3e38f) && v < Real(3e38f) ? fabs(v) : Real(0); };
-      const Key least = ~warp_max(static_cast<Key>(stays ? ~key_of(mine) : Key(0)));
-      const Key above = warp_max(!stays && g < p.groups ? key_of(mine) : Key(0));
-      const Real most = value_of(warp_max(key_of(magnitude(a) + (pair ? magnitude(b) : Real(0)))));
-      if (above && close(value_of(least), value_of(above), 2.0f, 2 * most)) return false;
+    unsigned keep = __ballot_sync(kAll, stays);
+    if (p.top_groups < p.groups && by_score) {
+      const auto magnitude = [](float v) { return v > -3e38f && v < 3e38f ? fabs(v) : 0.0f; };
+      const uint32_t least = ~warp_max(static_cast<uint32_t>(stays ? ~key_of(mine) : 0u));
+      const uint32_t above = warp_max(!stays && g < p.groups ? key_of(mine) : 0u);
+      const float most = value_of(warp_max(key_of(magnitude(a) + (pair ? magnitude(b) : 0.0f))));
+      if (above && close(value_of(least), value_of(above), 2.0f, 2 * most)) {
+        // Sigmoids: the groups again in FP64, from the experts that can be among a
+        // group's best, a lane each (of a softmax that needs the whole sum).
+        if (!p.sigmoid) return false;
+        const float last = pair ? b : a, low = fabsf(last) < INFINITY ? last - 0x1p-23f * (64.0f * s_max + fabsf(last)) : last;
+        int* const cand = reinterpret_cast<int*>(part);
+        int n = 0;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int i = lane + 32 * j, of = min(i, p.E - 1) / size;
+          const float least_in = __shfl_sync(kAll, low, of << shift);
+          const bool in = key[j] && (from_choice ? value_of(key[j]) : score(l[j])) >= least_in;
+          const unsigned who = __ballot_sync(kAll, in);
+          const int to = n + __popc(who & ((1u << lane) - 1));
+          if (in && to < 32) cand[to] = i;
+          n += __popc(who);
+        }
+        __syncwarp();
+        if (n > 32) return false;
+        unsigned long long mine64 = 0;
+        int of = -1;
+        if (lane < n) {
+          const int i = cand[lane];
+          const double v = 1.0 / (1.0 + exp(-static_cast<double>(to_f32(x[i])))) + (from_choice ? p.bias[i] : 0.0f);
+          mine64 = key_of(v);
+          of = i / size;
+        }
+        __syncwarp();
+        unsigned long long k1 = 0, k2 = 0;     // the two best of group `lane`
+        for (int j = 0; j < n; ++j) {
+          const unsigned long long k = __shfl_sync(kAll, mine64, j);
+          if (__shfl_sync(kAll, of, j) != lane) continue;
+          k2 = max(k2, min(k, k1));
+          k1 = max(k1, k);
+        }
+        if (k2 && p.group_best == 2) k1 = key_of(value_of(k1) + value_of(k2));
+        int above64 = 0;
+        for (int h = 0; h < p.groups; ++h) {
+          const unsigned long long k = __shfl_sync(kAll, k1, h);
+          above64 += k > k1 || (k == k1 && h < lane);
+        }
+        const unsigned stay64 = __ballot_sync(kAll, lane < p.groups && above64 < p.top_groups);
+        keep = __ballot_sync(kAll, stay64 >> g & 1);
+      }
     }
     if (size == 32) {
 #pragma unroll
@@ -208,7 +336,7 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
   }
 
   // The best key of a lane's own, of equal ones the lowest index.
-  Key best;
+  uint32_t best;
   int at;                                                  // its index
   const auto own_best = [&] {
     best = key[0];
@@ -218,23 +346,23 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
       if (key[j] > best) best = key[j], at = 32 * j + lane;
   };
   own_best();
-  int id = -1;                                             // of slot `lane`
-  const bool check = kCheck && p.bias && !odd;
+  id = -1;                                                 // of slot `lane`
+  const bool check = p.bias && !odd;
   bool sorted = false;
-  if constexpr (kCheck) if (p.top_k < 32) {
+  if (p.top_k < 32) {
     // Only keys of at least the (top_k + 1)-th largest of the lanes' best can be
     // among the top_k + 1: a few more than that, mostly. They are collected and
     // ranked, a lane each.
-    Key v = best;
+    uint32_t v = best;
 #pragma unroll
     for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
       for (int o = size >> 1; o > 0; o >>= 1) {
-        const Key u = __shfl_xor_sync(kAll, v, o);
+        const uint32_t u = __shfl_xor_sync(kAll, v, o);
         const bool up = ((lane & o) == 0) == ((lane & size) == 0 || size == 32);
         v = up == (u > v) ? u : v;
       }
-    const Key least = max(__shfl_sync(kAll, v, p.top_k), Key(1));
+    const uint32_t least = max(__shfl_sync(kAll, v, p.top_k), 1u);
     uint32_t* const cand = reinterpret_cast<uint32_t*>(part);   // keys, indexes, and again in order
     int n = 0;
     __syncwarp();
@@ -265,7 +393,7 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
       const int last = min(n, p.top_k);
       bool near = false;
       if (check && lane < last && lane + 1 < n) {
-        const Real a = value_of(static_cast<Key>(cand[64 + lane])), b = value_of(static_cast<Key>(cand[64 + lane + 1]));
+        const float a = value_of(static_cast<uint32_t>(cand[64 + lane])), b = value_of(static_cast<uint32_t>(cand[64 + lane + 1]));
         near = close(a, b, 1.0f, fabs(a));
       }
       sorted = !__any_sync(kAll, near);
@@ -275,14 +403,14 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
   // One after the other, where there are too many of equal keys, or some too
   // close to each other: the best of the lanes', top_k times; with choices that
   // FP32 rounds, on to the first that is clearly less.
-  Key prev = 0;
+  uint32_t prev = 0;
   int found = 0;
   bool unsure = false;
   for (; !sorted; ++found) {
-    const Key m = warp_max(best);
+    const uint32_t m = warp_max(best);
     if (!m || (!check && found == p.top_k)) break;
     if (check && found > 0) {
-      const Real a = value_of(prev), b = value_of(m);
+      const float a = value_of(prev), b = value_of(m);
       const bool near = close(a, b, 1.0f, fabs(a));
       if (!near && found >= p.top_k) break;
       unsure |= near;
@@ -320,7 +448,12 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
     id = at_place;
   }
   if (lane >= p.top_k) id = -1;
+  return true;
+}
 
+// The weights of a token's experts, and both to memory.
+template <class T, int NV>
+__device__ __forceinline__ void route_write(const RouteParams& p, const T* x, int t, int lane, const Logits<NV>& logits, int id) {
   const bool live = id >= 0;
   const float lg = live ? to_f32(x[id]) : kNone;
   float w = 0.0f;
@@ -337,31 +470,27 @@ __device__ __forceinline__ bool route_token(const RouteParams& p, int t, int lan
   } else {
     float e = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) e += l[j] > kNone ? expf(l[j] - top) : 0.0f;
+    for (int j = 0; j < NV; ++j) e += logits.l[j] > kNone ? expf(logits.l[j] - logits.top) : 0.0f;
     e = warp_sum(e);
-    if (live) w = expf(lg - top) / e;
+    if (live) w = expf(lg - logits.top) / e;
   }
   w *= p.scale;
-  if (odd) w = __int_as_float(0x7FFFFFFF);
+  if (logits.odd) w = __int_as_float(0x7FFFFFFF);
   if (lane < p.top_k) {
     const long long o = static_cast<long long>(t) * p.top_k + lane;
     p.ids[o] = id;
     p.weights[o] = w;
   }
-  return true;
 }
 
 constexpr int kRouteWarps = 4;
 // Doubles of a warp's scratch: the choices, or four times 32 words.
 __host__ __device__ constexpr int route_scratch(int E) { return E > 64 ? E : 64; }
 
-template <class T, int NV>
-__device__ __noinline__ void route_token_f64(const RouteParams& p, int t, int lane, double* part) {
-  route_token<T, NV, double, unsigned long long>(p, t, lane, part);
-}
-
 // Bound by the latency of one token's steps (k + 1 reductions of some 50
 // clocks each, two exponentials an expert), which many warps overlap.
+// 8191x256, 8 groups: 16.4 us; 25 us where close groups send the whole token to
+// route_exact, 8 of them for the last such token's FP64 steps. 8192x128, softmax: 7.5 us.
 template <class T, int NV>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p) {
   extern __shared__ double route_part[];
@@ -371,8 +500,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
   const int t = blockIdx.x * kRouteWarps + warp;
   if (t >= p.T) return;
   double* part = route_part + static_cast<size_t>(warp) * route_scratch(p.E);
-  if (!route_token<T, NV, float, uint32_t>(p, t, lane, reinterpret_cast<float*>(part)))
-    route_token_f64<T, NV>(p, t, lane, part);
+  const T* x = static_cast<const T*>(p.X) + static_cast<long long>(t) * p.ldl;
+  Logits<NV> logits;
+  int id;
+  if (!route_token<T, NV>(p, x, lane, reinterpret_cast<float*>(part), logits, id))
+    id = route_exact(p, x, lane, reinterpret_cast<unsigned long long*>(part));
+  route_write(p, x, t, lane, logits, id);
 }
 
 template <class T>
