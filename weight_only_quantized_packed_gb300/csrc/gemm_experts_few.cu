@@ -23,11 +23,12 @@
 //    scaled by a power of two per pair.
 //
 // 16x8 of 128, 5120x2048: 112 us, 4.3 TB/s of the experts' weights; 1x8, gated
-// 4096x5120: 25 us. The instructions around the MMAs set the pace, not the bytes:
-// in steps of 128 K 120 us (191 instructions a unit and 128 K, 72 of them MMAs,
-// conversions and products), with four units at a time 139 us; 24 warps of 80
-// registers instead of 16 148 us; sums in shared memory, so that the loop over the
-// units need not be unrolled, 123 us.
+// 4096x5120: 25.0 us (25.5 with the output rows and global scales loaded after the
+// sums). The instructions around the MMAs set the pace, not the bytes: in steps of
+// 128 K 120 us (191 instructions a unit and 128 K, 72 of them MMAs, conversions and
+// products), with four units at a time 139 us; 24 warps of 80 registers instead of
+// 16 148 us; sums in shared memory, so that the loop over the units need not be
+// unrolled, 123 us; the next run's pairs loaded during this one 127 us.
 #include "experts.cuh"
 #include "mma_f16.cuh"
 #include "decode.cuh"
@@ -161,6 +162,8 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(ExpertsArgs a) {
     };
     // Without a pair: any row, the sums go nowhere.
     const uint16_t* act = static_cast<const uint16_t*>(a.A) + static_cast<long long>(max(pair_at(g), 0) / a.slots) * a.lda + b0 * 128;
+    const int p = pair_at(warp);               // the sums' part: a warp to a pair
+    const float gs = a.globals ? a.globals[run.expert] : 1.0f;
     float tot[kUnits][4];
 #pragma unroll
     for (int u = 0; u < kUnits; ++u)
@@ -253,8 +256,6 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(ExpertsArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) mine[(2 * t4 + (i & 1)) * kRow + 16 * u + g + 8 * (i >> 1)] = tot[u][i];
     __syncthreads();
-    const float gs = a.globals ? a.globals[run.expert] : 1.0f;
-    const int p = pair_at(warp);               // a warp to a pair
     if (p < 0) continue;
     uint16_t* const c = static_cast<uint16_t*>(a.C) + static_cast<long long>(p) * a.ldc;
     const float* s = sums + warp * kRow;
