@@ -23,9 +23,9 @@
 //    pairs. Gated: gate and up rows take turns as lanes, and lanes exchange
 //    halves of their columns.
 //
-// Measured (128 experts, rows' conversion included): 333x8, gated 4096x5120 345 to
-// 350 us, 4.4 TB/s of packed weights; 4096x8, gated 4096x5120 935 to 960 us, 1.4 to
-// 1.5 PFLOP/s; 4096x8, 5120x2048 515 to 580 us (it varies with the power limit). No
+// Measured (128 experts, rows' conversion included): 333x8, gated 4096x5120 347
+// us, 4.4 TB/s of packed weights; 4096x8, gated 4096x5120 920 to 940 us, 1.5
+// PFLOP/s; 4096x8, 5120x2048 529 us (to 600, process by process). No
 // unit is full: at 333x8 DRAM is 56 % busy, issue slots and the ALU 58 %, the tensor
 // core 21 %. What a stage costs is its hand-overs: copies and barriers alone, without
 // decoding, stores to tensor memory and seven of eight MMAs, take 290, 700 and 403
@@ -54,12 +54,20 @@ constexpr int kCodes = 128 * 128, kScales = 128 * 16;   // bytes of one
 constexpr int kEpi = 8;                        // output warps
 constexpr int kOut = 32 * 64;                  // 32 pairs by 32 outputs of an output warp
 constexpr int kCodesAt = kS * kStageB, kScalesAt = kCodesAt + kRing * kCodes, kOutAt = kScalesAt + kRing * kScales;
-constexpr int kTableAt = kOutAt + kEpi * kOut;
+constexpr int kFactorsAt = kOutAt + kEpi * kOut, kFactors = kMaxN / 2 * 4;   // an output warp's pairs' factors
+constexpr int kTableAt = kFactorsAt + kEpi * kFactors;
 constexpr int kWarpEpi = 4 * kSets, kWarpMma = kWarpEpi + kEpi, kWarpRows = kWarpMma + 1, kWarpCodes = kWarpMma + 2, kWarpScales = kWarpMma + 3;
 constexpr int kThreads = (kWarpMma + 4) * 32;  // registers are shared out by four warps at a time
 // Registers a thread: at launch (and decoding), of the output's and of the rest.
-constexpr int kRegsLaunch = 80, kRegsOut = 96, kRegsRest = 40;
-static_assert(kSets * kRegsLaunch + kEpi / 4 * kRegsOut + kRegsRest <= kThreads / 128 * kRegsLaunch, "registers");
+// A plain output holds more at a time; 104 and 32 for both took 929 us instead of 921
+// at 4096x8, gated 4096x5120, 96 and 40 for both 537 instead of 529 at 5120x2048.
+constexpr int kRegsLaunch = 80;
+__host__ __device__ constexpr int regs_out(bool gated) { return gated ? 96 : 104; }
+__host__ __device__ constexpr int regs_rest(bool gated) { return gated ? 40 : 32; }
+constexpr bool regs_fit(bool gated) {
+  return kSets * kRegsLaunch + kEpi / 4 * regs_out(gated) + regs_rest(gated) <= kThreads / 128 * kRegsLaunch;
+}
+static_assert(regs_fit(true) && regs_fit(false), "registers");
 // Tensor memory: the accumulator, then kS stages of 64 columns.
 constexpr uint32_t kColA = kMaxN;
 static_assert(kColA + kS * 64 <= 512 && kSets <= kRing && kS > 2 * (kSets - 1), "stages");
@@ -338,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   decoding_over:;
   } else if (warp < kWarpMma) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsOut));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(regs_out(kGated)));
     // Output: this warp's 32 lanes, all columns. First into registers as BF16, so
     // that the accumulator is free for the next tile; then, while that is
     // computed, 32 pairs at a time through shared memory to rows of C.
@@ -346,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t acc_free0 = mapa_shared(acc_free, 0);
     uint8_t* const out = smem + kOutAt + ew * kOut;
+    float* const factors = reinterpret_cast<float*>(smem + kFactorsAt + ew * kFactors);   // the inverses of their rows' scaling
     const int align = out_align(a);
     uint32_t ph = 0;
     constexpr int kChunks = kMaxN / 32 / 2;
@@ -354,12 +363,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile.at(table, first + i * step, weight_tiles);
       const float gs = a.globals ? a.globals[tile.expert] : 1.0f;
       int pl[kChunks];                         // the pair of column 32 (2 ch + h) + lane, and
-      float fl[kChunks];                       // the inverse of its row's scaling
+      __syncwarp();
 #pragma unroll
       for (int ch = 0; ch < kChunks; ++ch) {
         const int c = 32 * (2 * ch + h) + lane, p = c < tile.pairs ? a.rows[tile.p0 + c] : -1;
         pl[ch] = static_cast<unsigned>(p) < static_cast<unsigned>(R) ? p : -1;
-        fl[ch] = pl[ch] >= 0 ? a.row_scales[tile.p0 + c] : 1.0f;
+        factors[32 * ch + lane] = pl[ch] >= 0 ? a.row_scales[tile.p0 + c] : 1.0f;
       }
       wait_long(acc_full, ph, a.err, abort_flag);
       ph ^= 1;
@@ -381,13 +390,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool odd = lane & 16;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
+            const float2 f2 = *reinterpret_cast<const float2*>(factors + 32 * ch + (lane & 16) + 2 * j);
             float y[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int c = 2 * j + e;
               const float keep = __uint_as_float(odd ? v[16 + c] : v[c]), give = __uint_as_float(odd ? v[c] : v[16 + c]);
               const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 16);
-              const float f = __shfl_sync(0xFFFFFFFFu, fl[ch], odd ? 16 + c : c);
+              const float f = e ? f2.y : f2.x;
               y[e] = silu((odd ? got : keep) * f * gs) * ((odd ? keep : got) * f * gs);
             }
             packed[ch][j] = pack_bf16(y[0], y[1]);
@@ -395,8 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float f0 = __shfl_sync(0xFFFFFFFFu, fl[ch], 2 * j), f1 = __shfl_sync(0xFFFFFFFFu, fl[ch], 2 * j + 1);
-            packed[ch][j] = pack_bf16(__uint_as_float(v[2 * j]) * f0 * gs, __uint_as_float(v[2 * j + 1]) * f1 * gs);
+            const float2 f = *reinterpret_cast<const float2*>(factors + 32 * ch + 2 * j);
+            packed[ch][j] = pack_bf16(__uint_as_float(v[2 * j]) * f.x * gs, __uint_as_float(v[2 * j + 1]) * f.y * gs);
           }
         }
       }
@@ -449,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < kWarpMma + 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(regs_rest(kGated)));
   }
   if (warp == kWarpRows && elect_one()) {
     // Activations: this CTA's half of the tile's rows, kBox at a time (more of them
