@@ -170,8 +170,9 @@ int w4a16_gemm_tc_ex(const void* A, int lda, const void* W, const void* scales,
  * two launches). The choice depends on N and K only, never on M. The weight
  * operand is e2m1 * e4m3(scale), exact in
  * FP16. Each activation row is scaled per 128-K block by the power of two
- * 2^e that puts its largest magnitude in [2^14, 2^15) and rounded to FP16
- * (exact for every value of at least 2^-31 times that maximum); each block's
+ * 2^e, e <= 109, that puts its largest magnitude in [2^14, 2^15) and rounded
+ * to FP16 (exact for every value of at least 2^-31 times that maximum, and
+ * for all where it is below 2^-95); each block's
  * FP32 sum is multiplied by 2^-e once, and the global scale multiplies each
  * FP32 result at the store.
  * Arguments and layouts are those of w4a16_gemv / w4a16_gemv_ex, with one
@@ -348,8 +349,8 @@ int expert_order(const int* ids, int* rows, int* offsets, int R, int E, void* st
  * left as they were. Alignment, K, N, lda and ldc as for w4a16_gemv.
  * Numerics: FP16 operands and FP32 sums. The weights' are exact. The activations
  * are scaled by a power of two, per row or (few pairs an expert) per row and 256 K,
- * and rounded: exact where they are at least 2^-29 of the row's largest magnitude,
- * otherwise off by at most 2^-40 of it. The exponential of silu is off by 2^-22. A
+ * and rounded: exact where they are at least 2^-31 of the largest magnitude there or it
+ * is below 2^-95, otherwise off by at most 2^-39 of it. The exponential of silu is off by 2^-22. A
  * row does not depend on the others, but which kernel runs (and with it the order of
  * the sums) on T * slots, E, N and K. workspace: w4a16_experts_workspace() bytes. */
 int w4a16_experts(const void* A, int lda, const void* W, const void* scales, const float* global_scales, const int* rows,

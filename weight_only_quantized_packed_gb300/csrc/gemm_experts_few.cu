@@ -201,9 +201,8 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(ExpertsArgs a) {
         mx = max(mx & 0xFFFFu, mx >> 16);
         mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
         mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-        const int sh = min(100, max(-113, 141 - static_cast<int>(mx >> 7)));   // 2^(exponent + sh) = 2^14
-        const float scale = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-        const float own = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+        const int sh = f16_shift(mx);
+        const float scale = pow2(sh), own = pow2(-sh);
 #pragma unroll
         for (int i = 0; i < 32; ++i) bf[i] = f32x2_to_f16x2(bf16hi(bf[i]) * scale, bf16lo(bf[i]) * scale);
         inv0 = __shfl_sync(0xFFFFFFFFu, own, 8 * t4);

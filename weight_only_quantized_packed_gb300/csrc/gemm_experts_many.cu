@@ -606,10 +606,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The rows of X (BF16) in the order of the pairs, as FP16 [R, K], each times the
-// power of two that puts its largest magnitude in [2^14, 2^15): exact for what is
-// at least 2^-29 of that; what is smaller is off by 2^-40 of it at most. inv [R]
-// receives the inverse powers. In that order a tile's rows are consecutive, and
+// The rows of X (BF16) in the order of the pairs, as FP16 [R, K], each times a
+// power of two (f16_shift): exact for what is at least 2^-31 of its largest
+// magnitude; what is smaller is off by 2^-39 of that at most. inv [R] receives
+// the inverse powers. In that order a tile's rows are consecutive, and
 // few threads copy them (gathered by the kernel itself, through asynchronous
 // copies, they took four warps, and their latency every third stage).
 constexpr int kHalfThreads = 128, kHalfHeld = 8;   // chunks of 8 elements a thread keeps between the passes
@@ -648,9 +648,9 @@ __global__ void __launch_bounds__(kHalfThreads)
 #pragma unroll
     for (int i = 0; i < kHalfThreads / 32; ++i) mx = max(mx, most_sh[i]);
   }
-  const int sh = min(100, max(-113, 141 - static_cast<int>(mx >> 7)));   // 2^(exponent + sh) = 2^14
-  const float scale = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-  if (at == 0) inv[r] = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+  const int sh = f16op::f16_shift(mx);
+  const float scale = f16op::pow2(sh);
+  if (at == 0) inv[r] = f16op::pow2(-sh);
   const auto put = [&](int c, const uint4& v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t h[4];

@@ -17,9 +17,9 @@
 // an E4M3 scale (at most 6 significant bits, within [2^-10, 2688]), is an
 // FP16 value, so the weight operand is exact. The activations are scaled per
 // (activation row, 128-K block) by a power of two 2^e that puts the block
-// row's largest magnitude in [2^14, 2^15), then rounded to FP16: every BF16
-// value of at least 2^-31 times that maximum is exact, and a smaller one is
-// off by at most 2^-25 in the scaled units (2^-39 of the block's largest
+// row's largest magnitude in [2^14, 2^15) (f16_shift), then rounded to FP16:
+// every BF16 value of at least 2^-31 times that maximum is exact, and a smaller
+// one is off by at most 2^-25 in the scaled units (2^-39 of the block's largest
 // activation). The MMA multiplies FP16 by FP16 exactly into FP32; the block's
 // FP32 sum is multiplied by 2^-e (and, for FP8, by the block scale) once and
 // added to the FP32 accumulator. Only the order of the FP32 additions differs
@@ -316,20 +316,23 @@ __global__ void __launch_bounds__(kThreads, kOcc)
       if (live) {
         const uint8_t* stage = smem + s * F::kStageBytes;
         const uint8_t* box = stage + b * F::kBoxBytes;
-        // Fold factors of this block: 2^-e per activation row (and the FP8
-        // block scale of the tile's 128-row group).
-        float f[MT][2];
+        // Fold factors of this block: 2^-e per activation row, and the FP8 block
+        // scale of the tile's 128-row group. FP32 may not hold the product of the
+        // two where 2^-e is small, so a small 2^-e multiplies the sum by itself
+        // (exactly, f16_shift) before the scale does.
+        float f[MT][2], fs[F::kW4 ? 1 : MT][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          if constexpr (F::kW4) {
-            f[mt][0] = fox[mt][0];
-            f[mt][1] = fox[mt][1];
-          } else {
-            const float sb = reinterpret_cast<const float*>(stage + F::kScaleOff)[b];
-            f[mt][0] = sb * fox[mt][0];
-            f[mt][1] = sb * fox[mt][1];
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if constexpr (F::kW4) {
+              f[mt][i] = fox[mt][i];
+            } else {
+              const float sb = reinterpret_cast<const float*>(stage + F::kScaleOff)[b];
+              fs[mt][i] = fminf(fox[mt][i], 1.0f);
+              f[mt][i] = fox[mt][i] < 1.0f ? sb : sb * fox[mt][i];
+            }
           }
-        }
 #pragma unroll
         for (int r0 = 0; r0 < kTiles; r0 += 2) {  // two row tiles' chains interleaved
           float c[2][MT][4];
@@ -402,10 +405,12 @@ __global__ void __launch_bounds__(kThreads, kOcc)
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
               float* t = tot[r0 + i][mt];
-              t[0] = fmaf(f[mt][0], c[i][mt][0], t[0]);
-              t[1] = fmaf(f[mt][1], c[i][mt][1], t[1]);
-              t[2] = fmaf(f[mt][0], c[i][mt][2], t[2]);
-              t[3] = fmaf(f[mt][1], c[i][mt][3], t[3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float v = c[i][mt][e];
+                if constexpr (!F::kW4) v *= fs[mt][e & 1];
+                t[e] = fmaf(f[mt][e & 1], v, t[e]);
+              }
             }
         }
       }

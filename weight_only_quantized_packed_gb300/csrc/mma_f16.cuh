@@ -65,10 +65,20 @@ __device__ __forceinline__ uint32_t e4m3x2_half(uint32_t x) {
 }
 __device__ __forceinline__ uint4 lds128(const void* p) { return *reinterpret_cast<const uint4*>(p); }
 
+// The exponent e of the power of two that activations are scaled by before they
+// become FP16, from the bits of their largest BF16 magnitude: 2^e puts it in
+// [2^14, 2^15). Values of at least 2^-31 of it are exact then; smaller ones are off by
+// at most 2^-25, 2^-39 of it. e is at most 109: there every BF16 number (a multiple of
+// 2^-133) is a multiple of FP16's least, 2^-24, so that smaller rows are exact as a
+// whole. Their sums with E2M1 * E4M3 or E4M3 weights are multiples of 2^-34, and times
+// 2^-109 still numbers that FP32 holds exactly. Infinities and NaN take -113.
+__device__ __forceinline__ int f16_shift(uint32_t most) { return min(109, max(-113, 141 - static_cast<int>(most >> 7))); }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
 // B fragments of one block for one column tile from this thread's 32
 // activations r (BF16 pairs in k order): scaled by 2^e and rounded to FP16,
-// and 2^-e, where 2^e puts the block row's largest magnitude (over the 4
-// lanes of the row, lanes 4g .. 4g + 3) in [2^14, 2^15).
+// and 2^-e, with e for the block row's largest magnitude (over the 4 lanes of
+// the row, lanes 4g .. 4g + 3).
 __device__ __forceinline__ void build_bfrag_regs(const uint32_t (&r)[16], uint32_t (&bf)[16], float& inv) {
   // Largest magnitude of the block row: BF16 magnitudes order like their bits.
   uint32_t mx = 0;
@@ -77,10 +87,9 @@ __device__ __forceinline__ void build_bfrag_regs(const uint32_t (&r)[16], uint32
   mx = max(mx & 0xFFFFu, mx >> 16);
   mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
   mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));   // the 4 lanes of row g hold its 128 activations
-  const int E = static_cast<int>(mx >> 7);              // BF16 exponent field of the maximum
-  const int sh = min(100, max(-113, 141 - E));           // 2^(E - 127 + sh) = 2^14
-  const float scale = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-  inv = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+  const int sh = f16_shift(mx);
+  const float scale = pow2(sh);
+  inv = pow2(-sh);
 #pragma unroll
   for (int i = 0; i < 16; ++i) bf[i] = f32x2_to_f16x2(bf16hi(r[i]) * scale, bf16lo(r[i]) * scale);
 }
