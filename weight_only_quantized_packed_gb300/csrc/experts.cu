@@ -457,16 +457,15 @@ __device__ __forceinline__ void route_write(const RouteParams& p, const T* x, in
   const bool live = id >= 0;
   const float lg = live ? to_f32(x[id]) : kNone;
   float w = 0.0f;
-  if (p.renormalise) {
-    // Scores relative to the largest taken, so that they cannot all vanish: a
-    // sigmoid far below 0 is an exponential too.
-    const float most = value_of(warp_max(live ? key_of(lg) : 0u));
-    if (p.sigmoid && most > -80.0f) w = live ? 1.0f / (1.0f + expf(-lg)) : 0.0f;
-    else w = live ? expf(lg - most) : 0.0f;
-    const float total = warp_sum(w);
-    w = total > 0.0f ? w / total : 0.0f;
-  } else if (p.sigmoid) {
-    w = live ? 1.0f / (1.0f + expf(-lg)) : 0.0f;
+  if (p.renormalise || p.sigmoid) {
+    // Renormalised: scores relative to the largest taken, so that they cannot all
+    // vanish. A sigmoid is e^min(l, 0) / (1 + e^-|l|), where nothing overflows.
+    const float most = p.renormalise ? value_of(warp_max(live ? key_of(lg) : 0u)) : 0.0f;
+    if (live) w = p.sigmoid ? expf(fminf(lg, 0.0f) - fminf(most, 0.0f)) / (1.0f + expf(-fabsf(lg))) : expf(lg - most);
+    if (p.renormalise) {
+      const float total = warp_sum(w);
+      w = total > 0.0f ? w / total : 0.0f;
+    }
   } else {
     float e = 0.0f;
 #pragma unroll
