@@ -350,7 +350,8 @@ int expert_order(const int* ids, int* rows, int* offsets, int R, int E, void* st
  * Numerics: FP16 operands and FP32 sums. The weights' are exact. The activations
  * are scaled by a power of two, per row or (few pairs an expert) per row and 256 K,
  * and rounded: exact where they are at least 2^-31 of the largest magnitude there or it
- * is below 2^-95, otherwise off by at most 2^-39 of it. The exponential of silu is off by 2^-22. A
+ * is below 2^-95, otherwise off by at most 2^-39 of it. silu is off by 13 * 2^-24 of
+ * itself, and by 2^-148 |gate| where e^gate is below FP32's normal numbers. A
  * row does not depend on the others, but which kernel runs (and with it the order of
  * the sums) on T * slots, E, N and K. workspace: w4a16_experts_workspace() bytes. */
 int w4a16_experts(const void* A, int lda, const void* W, const void* scales, const float* global_scales, const int* rows,

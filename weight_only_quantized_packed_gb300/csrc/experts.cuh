@@ -6,6 +6,15 @@
 namespace wqp {
 namespace experts {
 
+// g * sigmoid(g), through e^-|g|, which cannot overflow. expf is 2 ulp off at any
+// argument, where __expf's error grows with it (25 ulp at 20); it costs 1 % at
+// 4096x8, gated 4096x5120 (955 -> 965 us). The quotient is 2 ulp off: an IEEE
+// division took 1060 us there.
+__device__ __forceinline__ float silu(float g) {
+  const float t = expf(-fabsf(g));
+  return __fdividef(g < 0.0f ? g * t : g, 1.0f + t);
+}
+
 // Per expert its first position and, summed up, how many tiles of pairs it and
 // the experts before it have. Offsets are taken as expert_order writes them;
 // whatever else they hold, no position outside 0..R is used.

@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(ExpertsArgs a) {
         if (i8 < run.units * 8 && o < outs) {
           const int r = (i8 >> 3) * 16 + (i8 & 7);
           const float gate = sum_at(r), up = sum_at(r + 8);
-          c[o] = f32_to_bf16_rn(gate / (1.0f + expf(-gate)) * up);
+          c[o] = f32_to_bf16_rn(experts::silu(gate) * up);
         }
       }
     } else {

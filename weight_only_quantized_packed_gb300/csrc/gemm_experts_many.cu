@@ -176,13 +176,6 @@ __device__ __forceinline__ void decode_word(uint32_t w, uint32_t s, uint32_t* r)
   r[3] = f16op::mul_f16x2(f16op::e2m1x2_byte<3>(w), s);
 }
 
-// g * sigmoid(g), through e^-|g|, which cannot overflow: 4 roundings and two
-// approximations of 2 ulp.
-__device__ __forceinline__ float silu(float g) {
-  const float t = __expf(-fabsf(g));
-  return __fdividef(g * (g < 0.0f ? t : 1.0f), 1.0f + t);
-}
-
 // How C's rows are aligned, in bytes: 16 or 2.
 __device__ __forceinline__ int out_align(const ExpertsArgs& a) {
   return (reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && a.ldc % 8 == 0) ? 16 : 2;
@@ -398,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float keep = __uint_as_float(odd ? v[16 + c] : v[c]), give = __uint_as_float(odd ? v[c] : v[16 + c]);
               const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 16);
               const float f = e ? f2.y : f2.x;
-              y[e] = silu((odd ? got : keep) * f * gs) * ((odd ? keep : got) * f * gs);
+              y[e] = experts::silu((odd ? got : keep) * f * gs) * ((odd ? keep : got) * f * gs);
             }
             packed[ch][j] = pack_bf16(y[0], y[1]);
           }
