@@ -229,3 +229,30 @@ def test_workspace_sizes(L):
     args = list(EXPERTS)
     args[9], args[10], args[15] = 100, 8, NUL
     assert size(100, 8, 8, 40, 256) and L.w4a16_experts(*args) == INVALID and "workspace" in L.wqp_last_error().decode()
+
+
+BIG = [2 ** 31, 2 ** 32 + 2, -2 ** 32 + 2]
+
+
+@pytest.mark.parametrize("big", BIG)
+def test_sizes_beyond_an_int_are_refused(experts, big):
+    """The C ABI takes sizes as ints: a larger one would arrive as another size, and the call succeed for that one."""
+    from weight_only_quantized_packed_gb300 import binding as b
+
+    if big > 0:
+        for what, run in [
+                ("T=", lambda: b.expert_route(f32(big, 2), 1)), ("R=", lambda: b.expert_order(i32(big, 1), E)),
+                ("slots=", lambda: b.w4a16_experts(bf16(1, K), u8(E, N, K // 2), u8(E, N, K // 16), i32(big), i32(E + 1), N, K)),
+                ("E=", lambda: b.w4a16_experts(bf16(T, K), u8(big, N, K // 2), u8(big, N, K // 16), i32(T * k), i32(big + 1), N, K)),
+                ("T=", lambda: b.expert_combine(bf16(big, 8), f32(big, 1), i32(big, 1), E)),
+                ("slots=", lambda: b.expert_combine(bf16(big, 8), f32(1, big), i32(1, big), E))]:
+            with pytest.raises(ValueError, match=what):
+                run()
+    for name, kw in [("expert_route", {"groups": big}), ("expert_route", {"top_groups": big}), ("expert_route", {"group_best": big})]:
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            call(name, **kw)
+    for what, run in [("top_k=", lambda: b.expert_route(f32(T, E), big)), ("E=", lambda: b.expert_order(i32(T, k), big)),
+                      ("E=", lambda: b.expert_combine(bf16(T * k, H), f32(T, k), i32(T, k), big))]:
+        with pytest.raises(ValueError, match=what):
+            run()
+    assert not experts.calls and not experts.made

@@ -530,6 +530,13 @@ def _here(*ts):
             raise ValueError("all tensors must be on the current device")
 
 
+def _ints(names, *values):
+    """Sizes and counts go to the C ABI as ints: ctypes would cut others without a word."""
+    if max(values) > _INT_MAX or min(values) < -_INT_MAX:
+        bad = [f"{n}={v}" for n, v in zip(names.split(), values) if abs(v) > _INT_MAX]
+        raise ValueError(f"{', '.join(bad)}: beyond 2^31 - 1")
+
+
 def expert_route(logits, top_k: int, scoring: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
                  group_best: int = 2, renormalise: bool = True, scale: float = 1.0, out=None, stream=None):
     """(ids, weights): each token's top_k experts from its logits [T, E] (bfloat16, float16 or float32) by score
@@ -539,6 +546,7 @@ def expert_route(logits, top_k: int, scoring: str = "softmax", bias=None, groups
     torch = _torch or _load_torch()
     _here(logits, bias)
     ldl, dt, T, E = _typed_rows("logits", logits)
+    _ints("T E top_k groups top_groups group_best", T, E, top_k, groups, top_groups, group_best)
     if scoring not in _SCORING:
         raise ValueError("scoring must be 'softmax' or 'sigmoid'")
     pb = None if bias is None else _packed("bias", bias, (E,), torch.float32)
@@ -564,6 +572,7 @@ def expert_order(ids, E: int, out=None, stream=None):
     torch = _torch or _load_torch()
     _here(ids)
     R = ids.numel()
+    _ints("R E", R, E)
     pi = _weights("ids", ids, R, torch.int32)
     if out is None:
         rows, offsets = (_empty((R,), torch.int32, ids.device, stream), _empty((E + 1,), torch.int32, ids.device, stream))
@@ -593,6 +602,7 @@ def w4a16_experts(A, W, scales, rows, offsets, N: int, K: int, global_scales=Non
     slots = R // T if T else 1
     if R != T * slots or slots < 1 and T:
         raise ValueError(f"{R} pairs are not a multiple of the {T} rows of A")
+    _ints("T slots E N K", T, slots, E, N, K)
     pr, po = _packed("rows", rows, (R,), torch.int32), _packed("offsets", offsets, (E + 1,), torch.int32)
     pw, ps = _weights("W", W, E * N * (K // 2), torch.uint8), _weights("scales", scales, E * N * (K // 16), torch.uint8)
     pg = None if global_scales is None else _packed("global_scales", global_scales, (E,), torch.float32)
@@ -633,6 +643,7 @@ def expert_combine(y, weights, ids, E: int, residual=None, out=None, stream=None
     if len(of) != 2 or of[0] * of[1] != R:
         raise ValueError(f"weights must be [T, slots] with T * slots = {R}")
     T, slots = of
+    _ints("T slots E H", T, slots, E, H)
     pw, pi = _packed("weights", weights, (T, slots), torch.float32), _packed("ids", ids, (T, slots), torch.int32)
     shape, pr, ldr = (T, H), None, 0
     if residual is not None:
