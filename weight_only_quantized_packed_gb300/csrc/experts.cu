@@ -486,8 +486,11 @@ constexpr int kRouteWarps = 4;
 // Doubles of a warp's scratch: the choices, or four times 32 words.
 __host__ __device__ constexpr int route_scratch(int E) { return E > 64 ? E : 64; }
 
-// Bound by the latency of one token's steps (k + 1 reductions of some 50
-// clocks each, two exponentials an expert), which many warps overlap.
+// Bound by the latency of one token's chain of steps, which warps overlap: its
+// logits' loads, their maximum, an exponential an expert where the order needs
+// scores, the groups' maxima and ranks, a sort of the lanes' best and the ranking of
+// the candidates above it, the weights (issue slots 58 %, ALU 50 % at 8191x256). One
+// expert after the other only where choices are equal or close, or top_k is 32.
 // 8191x256, 8 groups: 16.4 us; 25 us where close groups send the whole token to
 // route_exact, 8 of them for the last such token's FP64 steps. 8192x128, softmax: 7.5 us.
 template <class T, int NV>

@@ -1,5 +1,5 @@
-// What the kernels of the experts' products share: the table of tiles that
-// each CTA makes from the experts' offsets.
+// What the kernels of the experts' products share: silu, and the table of tiles
+// that each CTA makes from the experts' offsets.
 #pragma once
 #include "common.cuh"
 

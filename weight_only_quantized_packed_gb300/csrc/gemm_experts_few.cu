@@ -293,7 +293,9 @@ cudaError_t launch_few_t(const ExpertsArgs& a, cudaStream_t s) {
   return launch(few_kernel<kGated>, dim3(2 * a.num_sms), dim3(kThreads), few_bytes(a.E), s, a.pdl, a);
 }
 
-// Whether the kernel above is the faster one. The other takes some 8 us for its two
+// Whether the kernel above is taken, from the sizes alone: pairs without an expert
+// count as well. Mostly it is the faster one then; small products of more pairs it
+// would have sooner too (the other's two launches). The other takes some 8 us for its two
 // launches and has the weights' bytes through in the same time for any number of
 // rows; this one takes longer per expert the longer its rows are, and again for
 // every 8 pairs. Measured, this | the other, us: 128 experts of 4096x5120 (gated),

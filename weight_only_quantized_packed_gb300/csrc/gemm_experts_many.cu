@@ -24,8 +24,10 @@
 //    halves of their columns.
 //
 // Measured (128 experts, rows' conversion included): 333x8, gated 4096x5120 347
-// us, 4.4 TB/s of packed weights; 4096x8, gated 4096x5120 920 to 940 us, 1.5
-// PFLOP/s; 4096x8, 5120x2048 529 us (to 600, process by process). No
+// us, 4.4 TB/s of packed weights; 4096x8, gated 4096x5120 950 us, 1.4 PFLOP/s, and
+// 4096x8, 5120x2048 563 us (925 to 965 and 525 to 610, process by process; with rows
+// of C off 16 bytes, element by element: 1338 and 975, 333x8 368). The plain kernel
+// spills 56 bytes a thread of its copying and MMA warps, at 32 registers. No
 // unit is full: at 333x8 DRAM is 56 % busy, issue slots and the ALU 58 %, the tensor
 // core 21 %. What a stage costs is its hand-overs: copies and barriers alone, without
 // decoding, stores to tensor memory and seven of eight MMAs, take 290, 700 and 403
